@@ -67,6 +67,8 @@ enum {
 #define RETOPK_STATUS_NONFINITE   0x4u  /* a non-finite score was produced          */
 #define RETOPK_STATUS_TIMEOUT     0x8u  /* a bounded pipeline wait expired (the step's
                                            results are not valid)                  */
+#define RETOPK_STATUS_BAD_PAGE    0x20u /* a page-table entry outside [0, n_pages): its
+                                           rows are neither read nor written        */
 #define RETOPK_STATUS_GATHER      0x10u /* a gathered K/V row index outside [0, L) was
                                           skipped: checked by builds with
                                           RETOPK_CHECKED defined, and always by
@@ -372,6 +374,111 @@ int retopk_fidelity(retopk_ctx *ctx, const retopk_bf16 *q, const retopk_bf16 *k_
  * a diagnostic, not part of the decode step. */
 int retopk_support_overlap(const int32_t *S, const int32_t *others, int rows, int R, int K, float *out,
                            void *stream);
+
+/* ---- prompt side: rotated append, cache copy, chunk attention ------------- */
+
+/* Rows of a cache as these entry points see them (the retopk_* and exact_*
+ * calls above read contiguous bf16 caches only; retopk_cache_copy makes those
+ * from any other form and back). */
+#define RETOPK_CACHE_BF16 0
+#define RETOPK_CACHE_MX8  1   /* a row is 128 e4m3 codes and 4 scale bytes: value =
+                                 code * 2^(scale - 127) for each 32 elements.  Written
+                                 with the smallest scale that keeps the 32 values
+                                 within 448, codes rounded to nearest even once.  A
+                                 block with a NaN or an infinity gets scale 255 and
+                                 reads back as NaN; an all-zero block scale 0.       */
+
+/* The keys and values of B sequences: k and v are [n_pages, n_kv_heads,
+ * page_rows, 128] (bf16, or e4m3 bytes with k_scale / v_scale [n_pages,
+ * n_kv_heads, page_rows, 4]).  Row i of sequence b is row i % page_rows of page
+ * table[b * table_width + i / page_rows].  table == NULL: page b holds sequence
+ * b whole (n_pages >= B, page_rows = max_len) -- the contiguous layout of the
+ * calls above.  With a table, page_rows is a multiple of 16.  Sequences may share
+ * pages that no call writes.  The struct is host memory, read during the call; all its pointers
+ * are device memory, 16-byte aligned (table: 4-byte, scales: 4-byte). */
+typedef struct retopk_cache {
+    void *k, *v;
+    uint8_t *k_scale, *v_scale;   /* RETOPK_CACHE_MX8 only                        */
+    const int32_t *table;         /* [B, table_width], or NULL                    */
+    int32_t format;               /* RETOPK_CACHE_*                               */
+    int32_t n_pages, n_kv_heads, page_rows, table_width;
+} retopk_cache;
+
+/* What is done to a query or key head x before it is used:
+ *   norm      x <- x * rsqrt(mean(x^2) + eps) * weight     (weight NULL: none)
+ *   rotation  pairs (a, b) of the first rot_dim elements -- (j, j + rot_dim/2),
+ *             or (2j, 2j + 1) with `interleaved` -- turn by t = pos * inv_freq[j]:
+ *             a' = a cos t - b sin t,  b' = b cos t + a sin t
+ * in fp32 with one rounding at the end; the angle is reduced in 64 bits, so far
+ * positions lose nothing.  weights: bf16 [128]; inv_freq: fp32 [rot_dim / 2],
+ * NULL (and rot_dim 0) for no rotation.  rot_dim: a multiple of 16 up to 128. */
+typedef struct retopk_rope {
+    const retopk_bf16 *q_weight, *k_weight;
+    const float *inv_freq;
+    float eps;
+    int32_t rot_dim, interleaved;
+} retopk_rope;
+
+/* Ragged new tokens: row t of q / k / v belongs to sequence b when
+ * cu_tokens[b] <= t < cu_tokens[b + 1] (device int32 [B + 1], not decreasing; NULL: one
+ * token for each sequence, T == B).  Rows of [0, T) in no sequence are not
+ * read and their outputs are left as they were.  q [T, Hq, 128], k, v [T, Hkv, 128] bf16, a
+ * token's heads side by side, tokens q_stride / k_stride / v_stride elements
+ * apart (multiples of 8), so slices of one fused projection are taken as they are.
+ * Limits: 0 <= T <= 2^22, 1 <= B <= 65535, Hq / Hkv <= 16, Hq <= 1024.
+ * d_status: optional device word for RETOPK_STATUS_* bits (NULL: not reported).
+ *
+ * retopk_qk_rope: norm and rotation of the tokens' queries and keys at the
+ * positions seqlens[b], seqlens[b] + 1, ... (seqlens: rows before these
+ * tokens), into q_out [T, Hq, 128] and k_out [T, Hkv, 128].  With one token for
+ * each sequence its outputs are the q and k_new of retopk_decode_step_kv.
+ * q_out may be q and k_out may be k where the strides are the outputs'.
+ *
+ * retopk_qkv_append: the same, with the keys and the values written to rows
+ * seqlens[b] + i of the cache (bf16 or MX8), and seqlens_out[b] = seqlens[b] +
+ * the sequence's tokens.  seqlens_out may be seqlens (advanced in place, as
+ * retopk_append_kv does, by a second launch) or a separate buffer.  A sequence
+ * whose tokens do not fit sets RETOPK_STATUS_KV_FULL and keeps its rows and
+ * its length; its queries are still written. */
+int retopk_qk_rope(const retopk_rope *rope, const retopk_bf16 *q, int64_t q_stride, const retopk_bf16 *k,
+                   int64_t k_stride, const int32_t *cu_tokens, int T, int B, int Hq, int Hkv,
+                   const int32_t *seqlens, retopk_bf16 *q_out, retopk_bf16 *k_out, void *stream);
+int retopk_qkv_append(const retopk_rope *rope, const retopk_bf16 *q, int64_t q_stride, const retopk_bf16 *k,
+                      int64_t k_stride, const retopk_bf16 *v, int64_t v_stride, const int32_t *cu_tokens, int T,
+                      int B, int Hq, const retopk_cache *cache, const int32_t *seqlens, int32_t *seqlens_out,
+                      retopk_bf16 *q_out, uint32_t *d_status, void *stream);
+
+/* Rows [first[b], last[b]) of every sequence of `src` into the same rows of
+ * `dst` (device int32 [B]); both caches have the same n_kv_heads and may differ in
+ * format, paging and row capacity: quantised rows are read back into the cache
+ * that decoding reads, bf16 rows are parked in MX8 form, pages are gathered
+ * into contiguous rows.  Equal formats copy bits.  max_rows bounds last[b] -
+ * first[b] (it sizes the launch; rows beyond it are not copied); rows outside either cache's
+ * capacity are not copied and set RETOPK_STATUS_GATHER.  src and dst must not overlap. */
+int retopk_cache_copy(const retopk_cache *src, const retopk_cache *dst, const int32_t *first, const int32_t *last,
+                      int B, int max_rows, uint32_t *d_status, void *stream);
+
+/* Causal attention of ragged tokens over a cache that already holds them:
+ * seqlens[b] = L_b rows INCLUDING the sequence's n_b tokens (what qkv_append
+ * leaves in seqlens_out), token i at position p = L_b - n_b + i sees keys
+ * max(0, p - window + 1) .. p (window 0: all from 0):
+ *   s_j = scale q.k_j, with softcap > 0: softcap tanh(s_j / softcap)
+ *   out = sum_j softmax(s)_j v_j,   lse = log sum_j exp(s_j)
+ * q, out [T, Hq, 128] bf16, tokens q_stride / out_stride elements apart; lse
+ * [T, Hq] fp32 or NULL.  A token that sees no key (L_b < n_b, L_b = 0) gets
+ * zeros and lse = -inf.  The cache must be RETOPK_CACHE_BF16; rows at or past
+ * L_b are never used, whatever they hold.  A row below L_b that is not finite
+ * may reach every token of its sequence.  Lengths beyond the cache's capacity
+ * are clamped to it.  scale 0 means 1/sqrt(128).
+ * d_workspace: >= retopk_chunk_attention_workspace_bytes, 256-byte aligned;
+ * concurrent calls need one each.  Long histories of few tokens are split over the GPU
+ * and joined from it.  Results do not depend on the other sequences of the call beyond
+ * rounding.  Graph-capturable. */
+size_t retopk_chunk_attention_workspace_bytes(int T, int B, int Hq, int Hkv);
+int retopk_chunk_attention(const retopk_bf16 *q, int64_t q_stride, const retopk_cache *cache,
+                           const int32_t *cu_tokens, int T, int B, int Hq, const int32_t *seqlens, float scale,
+                           float softcap, int window, retopk_bf16 *out, int64_t out_stride, float *lse,
+                           void *d_workspace, size_t bytes, uint32_t *d_status, void *stream);
 
 /* ---- profiling ----------------------------------------------------------- */
 

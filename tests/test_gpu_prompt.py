@@ -1,0 +1,555 @@
+"""Rotated append, cache copy and chunk attention against plain 64-bit formulas (GPU).
+
+Tolerances.  u = 2^-24 is half a step of fp32, half a step of bf16 is 2^-8 and of e4m3 2^-4, relative to the value.
+  rotation   a' = a c - b s in fp32 from a norm of 128 terms: each of a, b is off by less than 16 u relative, c and s
+             by 2^-22, so a' is off by at most 2^-19 (|a| + |b|) <= 2^-18 of the head's largest element; then one
+             rounding to the output's type.
+  attention  a score is a sum of 128 products, off by at most 128 u sum|q k| scale <= 2^-17 times that sum, and the
+             exponential's argument and result by 2^-20 more: d; a capped score is off by no more.  The weights are rounded to bf16 once
+             (2^-8), the output once more: |out - exact| <= 2^-8 |exact| + (2^-8 + 2 d + 2^-14) sum_j p_j |v_j|.
+             lse is off by d + 2^-20 (1 + |lse|).
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from top_sparse_attention_exact_gb300 import retopk
+
+pytestmark = pytest.mark.gpu
+D = 128
+
+
+def gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def normal(g, *shape, scale=1.0):
+    return (torch.randn(*shape, generator=g, device="cuda") * scale).to(torch.bfloat16)
+
+
+def i32(x):
+    return torch.tensor(np.asarray(x, np.int32), device="cuda")
+
+
+def offsets(n):
+    return i32(np.concatenate([[0], np.cumsum(n)]))
+
+
+class Cache:
+    """A cache of B sequences with `rows` capacity, contiguous or in shuffled pages, filled with `fill`."""
+
+    def __init__(self, B, Hkv, rows, page=0, mx8=False, fill=float("nan"), seed=0):
+        self.page, self.mx8 = page, mx8
+        if page:
+            width = -(-rows // page)
+            perm = np.random.default_rng(seed).permutation(B * width + 2)[:B * width].reshape(B, width)
+            self.table, shape = i32(perm), (B * width + 2, Hkv, page, D)
+        else:
+            self.table, shape = None, (B, Hkv, rows, D)
+        if mx8:
+            self.k, self.v = (torch.full(shape, 0x55, dtype=torch.uint8, device="cuda") for _ in range(2))
+            self.ks, self.vs = (torch.full(shape[:3] + (4,), 0x66, dtype=torch.uint8, device="cuda") for _ in range(2))
+            self.h = retopk.KVCache(self.k, self.v, table=self.table, k_scale=self.ks, v_scale=self.vs)
+        else:
+            self.k, self.v = (torch.full(shape, fill, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+            self.ks = self.vs = None
+            self.h = retopk.KVCache(self.k, self.v, table=self.table)
+
+    def at(self, b, n):
+        pos = torch.arange(n, device="cuda")
+        return (self.table[b, pos // self.page].long(), pos % self.page) if self.page else (torch.full_like(pos, b), pos)
+
+    def put(self, b, k, v):
+        """Rows 0.. of sequence b (k, v: [n, Hkv, 128])."""
+        p, r = self.at(b, k.shape[0])
+        self.k[p, :, r], self.v[p, :, r] = k, v
+
+    def rows(self, b, n):
+        p, r = self.at(b, n)
+        out = []
+        for x, s in ((self.k, self.ks), (self.v, self.vs)):
+            y = x[p, :, r]
+            if self.mx8:
+                y = value8(y, s[p, :, r])
+            out.append(y.double())
+        return out
+
+    def snapshot(self):
+        return [x.clone() for x in (self.k, self.v, self.ks, self.vs) if x is not None]
+
+
+def value8(codes, scale):
+    s = torch.ldexp(torch.ones((), dtype=torch.float64), scale.cpu().int() - 127).cuda()
+    s = torch.where(scale == 255, torch.full_like(s, math.nan), s)
+    return (codes.view(torch.float8_e4m3fn).double().unflatten(-1, (4, 32)) * s[..., None]).flatten(-2)
+
+
+def scale8(x):
+    """The smallest e with max|x| <= 448 * 2^e for each 32 values of fp64 rows, by search over exact powers."""
+    top = x.unflatten(-1, (4, 32)).abs().amax(-1)
+    e = torch.frexp(top / 448.0)
+    return torch.where(top == 0, torch.full_like(e.exponent, -127),
+                       torch.where(e.mantissa == 0.5, e.exponent - 1, e.exponent).clamp(min=-127))
+
+
+# ---- rotated append --------------------------------------------------------------------------------------------------
+def rotated(x, w, inv_freq, pos, interleaved, eps):
+    """(exact rows, bound on the fp32 error) of [n, heads, 128] bf16 rows."""
+    x = x.double()
+    if w is not None:
+        x = x / (x.pow(2).mean(-1, keepdim=True) + eps).sqrt() * w.double()
+    top = x.abs().amax(-1, keepdim=True)
+    if inv_freq is not None:
+        m = inv_freq.numel()
+        t = pos.double()[:, None, None] * inv_freq.double()
+        i = torch.arange(m, device="cuda")
+        a, b = (2 * i, 2 * i + 1) if interleaved else (i, i + m)
+        y = x.clone()
+        y[..., a] = x[..., a] * t.cos() - x[..., b] * t.sin()
+        y[..., b] = x[..., b] * t.cos() + x[..., a] * t.sin()
+        x = y
+    return x, 2.0 ** -18 * top
+
+
+def freqs(rot, theta=1e6):
+    return (theta ** (-torch.arange(0, rot, 2, device="cuda").double() / rot)).float()
+
+
+APPEND = [  # tokens of each sequence, rows before, Hq, Hkv, page, rot, interleaved, norm, mx8
+    ([1], [0], 28, 4, 0, 128, False, True, False),
+    ([1], [8000000], 2, 1, 0, 128, False, True, False),            # a far position
+    ([1, 1, 1], [5, 127, 128], 8, 8, 16, 128, True, True, True),
+    ([7, 0, 1, 130], [0, 3, 16, 500], 7, 1, 48, 64, False, True, False),
+    ([7, 0, 1, 130], [0, 3, 16, 500], 7, 1, 48, 64, True, False, True),
+    ([300], [1], 32, 8, 0, 32, False, False, True),
+    ([33, 65], [100, 31], 16, 1, 64, 16, False, True, True),
+    ([20], [9], 3, 3, 32, 0, False, True, False),                  # norm alone
+    ([20], [9], 1, 1, 0, 0, False, False, True),                   # quantisation alone
+]
+
+
+@pytest.mark.parametrize("n,start,Hq,Hkv,page,rot,inter,norm,mx8", APPEND)
+@pytest.mark.parametrize("in_place", [False, True])
+def test_append(n, start, Hq, Hkv, page, rot, inter, norm, mx8, in_place):
+    g = gen(len(n) * 100 + Hq + rot)
+    B, T = len(n), sum(n)
+    pad = 3                                                        # rows behind the last sequence
+    proj = normal(g, T + pad, (Hq + 2 * Hkv) * D, scale=2.0)
+    q, k, v = (x.view(T + pad, -1, D) for x in proj.split([Hq * D, Hkv * D, Hkv * D], dim=1))
+    qw, kw = (normal(g, D) for _ in range(2)) if norm else (None, None)
+    inv = freqs(rot) if rot else None
+    c = Cache(B, Hkv, max(a + b for a, b in zip(n, start)) + 5, page, mx8, fill=3.0)
+    before = c.snapshot()
+    sl, st = i32(start), torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = sl if in_place else torch.full_like(sl, -1)
+    qo = torch.full((T + pad, Hq, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    rope = retopk.QKRope(inv, qw, kw, eps=1e-5, interleaved=inter)
+    retopk.qkv_append(rope, q, k, v, c.h, sl, None if in_place else out, qo, cu_tokens=offsets(n), status=st)
+    assert out.tolist() == [a + b for a, b in zip(n, start)] and st.item() == 0
+    if not in_place:
+        assert sl.tolist() == start
+    assert (qo[T:] == 7).all()
+    t0 = 0
+    for b in range(B):
+        sel = slice(t0, t0 + n[b])
+        t0 += n[b]
+        if n[b] == 0:
+            continue
+        pos = start[b] + torch.arange(n[b], device="cuda")
+        ref, tol = rotated(q[sel], qw, inv, pos, inter, 1e-5)
+        assert ((qo[sel].double() - ref).abs() <= 2.0 ** -8 * ref.abs() + tol).all()
+        ref, tol = rotated(k[sel], kw, inv, pos, inter, 1e-5)
+        p, r = c.at(b, start[b] + n[b])
+        p, r = p[start[b]:], r[start[b]:]
+        if not mx8:
+            assert ((c.k[p, :, r].double() - ref).abs() <= 2.0 ** -8 * ref.abs() + tol).all()
+            assert torch.equal(c.v[p, :, r].view(torch.int16), v[sel].contiguous().view(torch.int16))
+            continue
+        for x, exact, slack, codes, scale in ((k, ref, tol, c.k, c.ks), (v, v[sel].double(), 0.0 * tol, c.v, c.vs)):
+            e = scale8(exact)
+            near = ((scale8(exact * (1 + 2.0 ** -17)) != e) | (scale8(exact * (1 - 2.0 ** -17)) != e)) & (slack.amax() > 0)
+            got = scale[p, :, r].int() - 127
+            assert (got == e)[~near].all() and ((got - e).abs() <= 1).all()
+            y = value8(codes[p, :, r], scale[p, :, r])
+            step = torch.ldexp(torch.ones((), dtype=torch.float64), (got.cpu() - 10)).cuda().repeat_interleave(32, -1)
+            assert ((y - exact).abs() <= torch.maximum(2.0 ** -4 * exact.abs(), step) * (1 + 2.0 ** -10) + slack).all()
+    # what belongs to no new row is as it was
+    for now, old in zip(c.snapshot(), before):
+        for b in range(B):
+            p, r = c.at(b, start[b] + n[b])
+            now[p[start[b]:], :, r[start[b]:]] = old[p[start[b]:], :, r[start[b]:]]
+        assert torch.equal(now.view(torch.uint8), old.view(torch.uint8))
+
+
+def test_append_full_sequence_keeps_rows_and_length():
+    g = gen(5)
+    n, start = [4, 4, 4], [28, 29, 0]
+    q, k, v = normal(g, 12, 4, D), normal(g, 12, 2, D), normal(g, 12, 2, D)
+    c = Cache(3, 2, 32, 16, fill=1.0)
+    sl, st = i32(start), torch.zeros(1, dtype=torch.int32, device="cuda")
+    qo = retopk.qkv_append(retopk.QKRope(freqs(128)), q, k, v, c.h, sl, cu_tokens=offsets(n), status=st)
+    assert sl.tolist() == [32, 29, 4] and st.item() == retopk.STATUS_KV_FULL
+    assert (c.rows(1, 32)[0] == 1).all() and (c.rows(1, 32)[1] == 1).all()
+    ref, tol = rotated(q[4:8], None, freqs(128), 29 + torch.arange(4, device="cuda"), False, 0)
+    assert ((qo[4:8].double() - ref).abs() <= 2.0 ** -8 * ref.abs() + tol).all()
+
+
+def test_append_keeps_out_of_bad_pages():
+    g = gen(6)
+    q, k, v = normal(g, 40, 2, D), normal(g, 40, 1, D), normal(g, 40, 1, D)
+    c = Cache(2, 1, 48, 16, fill=1.0)
+    good = c.table.clone()
+    c.table[0, 1], c.table[1, 0] = c.k.shape[0], -1                # outside the pool on either side
+    before, st = c.snapshot(), torch.zeros(1, dtype=torch.int32, device="cuda")
+    sl = i32([0, 0])
+    retopk.qkv_append(retopk.QKRope(), q, k, v, c.h, sl, cu_tokens=offsets([33, 7]), status=st)
+    assert st.item() == retopk.STATUS_BAD_PAGE and sl.tolist() == [33, 7]
+    now = c.snapshot()
+    for page in range(c.k.shape[0]):
+        written = page in (good[0, 0].item(), good[0, 2].item())
+        assert torch.equal(now[0][page], before[0][page]) != written
+
+
+def test_append_of_blocks_that_are_not_finite_or_zero():
+    g = gen(7)
+    k, v, q = normal(g, 4, 1, D), normal(g, 4, 1, D), normal(g, 4, 1, D)
+    v[0, 0, 3], v[1, 0, 40], v[2, 0, 64:96] = float("inf"), float("nan"), 0.0
+    v[3, 0, :32] = 0
+    v[3, 0, 5] = 2.0 ** -133                                        # the smallest bf16
+    c = Cache(1, 1, 8, mx8=True)
+    retopk.qkv_append(retopk.QKRope(), q, k, v, c.h, i32([0]), cu_tokens=offsets([4]))
+    y = c.rows(0, 4)[1][:, 0]
+    assert y[0, :32].isnan().all() and y[1, 32:64].isnan().all() and not y[0, 32:].isnan().any()
+    assert (y[2, 64:96] == 0).all() and c.vs[0, 0, 2, 2] == 0 and c.vs[0, 0, 0, 0] == 255
+    assert y[3, 5] == 2.0 ** -133 and (y[3, :5] == 0).all()
+
+
+@pytest.mark.parametrize("rot,inter", [(128, False), (64, True)])
+def test_qk_rope_is_appends_rows_and_works_in_place(rot, inter):
+    g = gen(8)
+    B, Hq, Hkv = 5, 14, 2
+    q, k, v = normal(g, B, Hq, D), normal(g, B, Hkv, D), normal(g, B, Hkv, D)
+    qw, kw = normal(g, D), normal(g, D)
+    sl = i32([0, 1, 77, 4000, 12])
+    rope = retopk.QKRope(freqs(rot), qw, kw, interleaved=inter)
+    c = Cache(B, Hkv, 4096)
+    qo = retopk.qkv_append(rope, q, k, v, c.h, sl, torch.empty_like(sl))
+    q2, k2 = retopk.qk_rope(rope, q, k, sl)
+    assert torch.equal(q2, qo)
+    for b, pos in enumerate(sl.tolist()):
+        assert torch.equal(k2[b], c.k[b, :, pos])
+    retopk.qk_rope(rope, q, k, sl, q, k)
+    assert torch.equal(q, q2) and torch.equal(k, k2)
+
+
+def test_append_nothing_moves_lengths_over():
+    c = Cache(2, 2, 32)
+    e = torch.empty((0, 4, D), dtype=torch.bfloat16, device="cuda")
+    sl, out = i32([3, 9]), i32([0, 0])
+    retopk.qkv_append(retopk.QKRope(), e, e[:, :2], e[:, :2], c.h, sl, out, cu_tokens=i32([0, 0, 0]))
+    assert out.tolist() == [3, 9]
+
+
+# ---- cache copy ------------------------------------------------------------------------------------------------------
+def filled(g, B, Hkv, rows, page, mx8, seed):
+    c = Cache(B, Hkv, rows, page, mx8, seed=seed)
+    for x, s in ((c.k, c.ks), (c.v, c.vs)):
+        if mx8:
+            x.copy_(torch.randint(0, 256, x.shape, generator=g, device="cuda"))
+            x[(x & 127) == 127] = 0                                 # the two NaN codes are never written
+            s.copy_(torch.randint(0, 250, s.shape, generator=g, device="cuda"))
+        else:
+            size = torch.exp2(torch.randint(-40, 40, x.shape[:3] + (1,), generator=g, device="cuda").float())
+            x.copy_(torch.randn(x.shape, generator=g, device="cuda") * size)
+    return c
+
+
+@pytest.mark.parametrize("src8,dst8", [(True, False), (False, True), (False, False), (True, True)])
+@pytest.mark.parametrize("Hkv,sp,dp,first,last", [
+    (1, 0, 0, [0], [1]), (4, 16, 0, [0, 5, 200], [300, 5, 201]), (2, 0, 48, [1, 130], [128, 263]), (3, 64, 256, [0], [1025]),
+    (1, 128, 16, [7, 0, 0, 90], [90, 0, 513, 80])])
+def test_copy(src8, dst8, Hkv, sp, dp, first, last):
+    g = gen(sum(last) + Hkv)
+    B = len(first)
+    src = filled(g, B, Hkv, max(last) + 9, sp, src8, 1)
+    dst = Cache(B, Hkv, max(last) + 2, dp, dst8, fill=2.0, seed=2)
+    old = dst.snapshot()
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    retopk.cache_copy(src.h, dst.h, i32(first), i32(last), max(1, max(l - f for f, l in zip(first, last))), status=st)
+    assert st.item() == 0
+    now = dst.snapshot()
+    for b in range(B):
+        f, l = first[b], max(first[b], last[b])
+        (p, r), (u, w) = (x[f:l] for x in src.at(b, l)), (x[f:l] for x in dst.at(b, l))
+        for x, xs, y, ys in ((src.k, src.ks, dst.k, dst.ks), (src.v, src.vs, dst.v, dst.vs)):
+            if src8 == dst8:
+                assert torch.equal(y[u, :, w].view(torch.uint8), x[p, :, r].view(torch.uint8))
+                assert not src8 or torch.equal(ys[u, :, w], xs[p, :, r])
+            elif src8:     # representable in bf16 but for the last bits of the smallest scales
+                assert torch.equal(y[u, :, w], value8(x[p, :, r], xs[p, :, r]).to(torch.bfloat16))
+            else:
+                exact = x[p, :, r].double()
+                e = scale8(exact)
+                assert torch.equal(ys[u, :, w].int() - 127, e)
+                one = torch.ldexp(torch.ones((), dtype=torch.float64), -e.cpu()).cuda().repeat_interleave(32, -1)
+                assert torch.equal(y[u, :, w], (exact * one).float().to(torch.float8_e4m3fn).view(torch.uint8))
+        for new, was in zip(now, old):
+            new[u, :, w] = was[u, :, w]
+    for new, was in zip(now, old):
+        assert torch.equal(new.view(torch.uint8), was.view(torch.uint8))
+
+
+def test_copy_reports_rows_out_of_range_and_bad_pages():
+    src, dst = filled(gen(3), 2, 1, 64, 16, True, 1), Cache(2, 1, 40, fill=2.0)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    retopk.cache_copy(src.h, dst.h, i32([0, -3]), i32([60, 8]), 64, status=st)
+    assert st.item() == retopk.STATUS_GATHER
+    assert torch.equal(dst.rows(0, 40)[0], src.rows(0, 40)[0].to(torch.bfloat16).double())
+    st.zero_()
+    src.table[0, 0] = 1 << 30
+    dst.k.fill_(2.0)
+    retopk.cache_copy(src.h, dst.h, i32([0, 0]), i32([32, 0]), 64, status=st)
+    assert st.item() == retopk.STATUS_BAD_PAGE
+    assert (dst.k[0, 0, :16] == 2).all() and not (dst.k[0, 0, 16:32] == 2).all() and (dst.k[0, 0, 32:] == 2).all()
+
+
+# ---- chunk attention -------------------------------------------------------------------------------------------------
+def reference(q, k, v, first, scale, cap, window):
+    """(out, lse, sum p|v|, score error) in fp64 of q [n, Hq, 128] at positions first.., over k, v [L, Hkv, 128]."""
+    n, Hq, _ = q.shape
+    L, Hkv, _ = k.shape
+    q, k, v = q.double(), k.double().repeat_interleave(Hq // Hkv, 1), v.double().repeat_interleave(Hq // Hkv, 1)
+    s = torch.einsum("ihd,jhd->hij", q, k) * scale
+    size = torch.einsum("ihd,jhd->hij", q.abs(), k.abs()).amax((0, 1, 2)) * scale if L and n else torch.zeros(())
+    if cap:
+        s = cap * torch.tanh(s / cap)
+    pos, j = first + torch.arange(n, device="cuda")[:, None], torch.arange(L, device="cuda")[None]
+    seen = (j <= pos) & ((j > pos - window) if window else torch.ones_like(j <= pos))
+    s = s.masked_fill(~seen, -math.inf)
+    lse = torch.logsumexp(s, -1) if L else torch.full((Hq, n), -math.inf, dtype=torch.float64, device="cuda")
+    p = torch.nan_to_num(torch.exp(s - lse[..., None]), nan=0.0)
+    out, mass = (torch.einsum("hij,jhd->ihd", p, x) for x in (v, v.abs()))
+    return out, lse.transpose(0, 1), mass, 2.0 ** -17 * float(size) + 2.0 ** -20
+
+
+def check(q, qoff, n, lens, c, out, lse, scale, cap, window):
+    t = qoff
+    for b in range(len(n)):
+        L = max(0, lens[b])
+        k, v = c.rows(b, L)
+        sel = slice(t, t + n[b])
+        t += n[b]
+        if n[b] == 0:
+            continue
+        ref, rl, mass, d = reference(q[sel], k, v, L - n[b], scale, cap, window)
+        tol = 2.0 ** -8 * ref.abs() + (2.0 ** -8 + 2 * d + 2.0 ** -14) * mass
+        err = (out[sel].double() - ref).abs()
+        assert (err <= tol).all(), (b, float((err - tol).max()), float((err / (mass + 1e-30)).max()))
+        if lse is not None:
+            none = rl == -math.inf
+            assert torch.equal(lse[sel] == -math.inf, none)
+            assert ((lse[sel].double() - rl).abs() <= d + 2.0 ** -20 * (1 + rl.abs()))[~none].all()
+
+
+ATTEND = [  # tokens of each sequence, rows in all, Hq, Hkv, page, window, cap
+    ([1], [1], 1, 1, 0, 0, 0.0),                                    # a single key
+    ([1], [300], 28, 4, 0, 0, 0.0),
+    ([1], [129], 7, 1, 16, 0, 0.0),
+    ([1] * 9, [1, 2, 127, 128, 129, 255, 256, 257, 1000], 16, 1, 48, 0, 0.0),
+    ([1] * 5, [0, 5, 400, 17, 16], 32, 8, 64, 0, 50.0),             # a sequence without rows
+    ([3] * 4, [3, 64, 500, 2], 8, 8, 0, 0, 0.0),                    # the last: fewer rows than tokens
+    ([1, 1], [70001, 333], 28, 4, 256, 0, 0.0),                     # a long history beside a short one
+    ([5], [40000], 16, 2, 0, 0, 30.0),
+    ([1, 2], [9000, 9000], 12, 4, 0, 100, 0.0),
+    ([77], [77], 4, 2, 0, 0, 0.0),
+    ([300], [300], 28, 4, 128, 0, 0.0),
+    ([129], [1300], 16, 1, 16, 0, 0.0),
+    ([64, 0, 1, 200], [64, 50, 700, 900], 10, 2, 48, 0, 0.0),
+    ([200, 37], [1000, 37], 6, 6, 0, 33, 0.0),                      # a window inside one tile
+    ([150], [900], 14, 2, 64, 257, 20.0),
+    ([260], [100], 2, 1, 0, 0, 0.0),                                # tokens 0..159 see no key
+    ([700], [5000], 15, 5, 112, 1, 0.0),                            # each token sees itself only
+    ([513], [2050], 13, 1, 0, 0, 5.0),
+]
+
+
+def setup(n, lens, Hq, Hkv, page, seed, pad=2, qscale=2.0, strided=True):
+    g = gen(seed)
+    T = sum(n)
+    wide = normal(g, T + pad, Hq + 3, D, scale=qscale)
+    q = wide[:, :Hq] if strided else wide[:, :Hq].contiguous()
+    c = Cache(len(n), Hkv, max(max(lens), 1) + 7, page, seed=seed)  # rows past the lengths are NaN
+    for b, L in enumerate(lens):
+        c.put(b, normal(g, L, Hkv, D), normal(g, L, Hkv, D))
+    return q, c
+
+
+@pytest.mark.parametrize("n,lens,Hq,Hkv,page,window,cap", ATTEND)
+def test_attention(n, lens, Hq, Hkv, page, window, cap):
+    q, c = setup(n, lens, Hq, Hkv, page, sum(lens) + Hq)
+    T = sum(n)
+    wide = torch.full((T + 2, Hq + 1, D), 9.0, dtype=torch.bfloat16, device="cuda")
+    out, lse = wide[:, :Hq], torch.full((T + 2, Hq), 9.0, device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    retopk.chunk_attention(q, c.h, i32(lens), out, cu_tokens=offsets(n), softcap=cap, window=window, lse=lse, status=st)
+    assert st.item() == 0
+    check(q, 0, n, lens, c, out, lse, 1 / math.sqrt(D), cap, window)
+    # rows behind the last sequence and columns beside the heads are as they were
+    assert (wide[T:] == 9).all() and (lse[T:] == 9).all() and (wide[:, Hq:] == 9).all()
+
+
+@pytest.mark.parametrize("B,L", [(1, 260), (6, 1000)])
+def test_attention_one_token_each_without_offsets(B, L):
+    q, c = setup([1] * B, [L] * B, 8, 2, 0, B, pad=0, strided=False)
+    out = retopk.chunk_attention(q, c.h, i32([L] * B), scale=0.3)
+    check(q, 0, [1] * B, [L] * B, c, out, None, 0.3, 0.0, 0)
+
+
+def test_attention_large_and_tiny_scores():
+    # scores over a range of hundreds: one key takes all the weight; then all weights equal
+    q, c = setup([1, 40], [600, 600], 8, 2, 0, 3, qscale=60.0)
+    lse = torch.empty((43, 8), device="cuda")
+    out = retopk.chunk_attention(q, c.h, i32([600, 600]), cu_tokens=offsets([1, 40]), lse=lse)
+    check(q, 0, [1, 40], [600, 600], c, out, lse, 1 / math.sqrt(D), 0.0, 0)
+    zero = torch.zeros_like(q)
+    out = retopk.chunk_attention(zero, c.h, i32([600, 600]), cu_tokens=offsets([1, 40]), lse=lse)
+    check(zero, 0, [1, 40], [600, 600], c, out, lse, 1 / math.sqrt(D), 0.0, 0)
+
+
+def test_attention_scores_that_grow_along_the_history():
+    # every later tile raises the running maximum, so the accumulators are rescaled all along
+    n, L, Hq, Hkv = [200], [3000], 8, 1
+    q, c = setup(n, L, Hq, Hkv, 0, 4, qscale=1.0)
+    ramp = torch.linspace(0, 4, L[0], device="cuda")[:, None, None]
+    q.copy_(q.abs())
+    k = (torch.rand((L[0], Hkv, D), generator=gen(9), device="cuda") * ramp).to(torch.bfloat16)
+    c.put(0, k, normal(gen(10), L[0], Hkv, D))
+    out = retopk.chunk_attention(q, c.h, i32(L), cu_tokens=offsets(n))
+    check(q, 0, n, L, c, out, None, 1 / math.sqrt(D), 0.0, 0)
+
+
+def test_attention_lengths_beyond_the_capacity_are_clamped():
+    q, c = setup([1], [64], 4, 1, 0, 12, pad=0)
+    c.put(0, normal(gen(1), 71, 1, D), normal(gen(2), 71, 1, D))
+    out = retopk.chunk_attention(q, c.h, i32([5000]))
+    check(q, 0, [1], [71], c, out, None, 1 / math.sqrt(D), 0.0, 0)
+
+
+def test_attention_reports_bad_pages():
+    q, c = setup([1, 1], [100, 100], 4, 1, 16, 13, pad=0)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    good = retopk.chunk_attention(q, c.h, i32([100, 100]), status=st).clone()
+    c.table[0, 2], c.table[0, 3] = c.k.shape[0], -7
+    out = retopk.chunk_attention(q, c.h, i32([100, 100]), status=st)
+    assert st.item() == retopk.STATUS_BAD_PAGE
+    assert torch.equal(out[1], good[1]) and not out.isnan().any()
+
+
+def test_attention_shared_pages():
+    # two sequences with the same first pages
+    q, c = setup([1, 1], [200, 150], 4, 2, 16, 14, pad=0)
+    c.table[1, :9] = c.table[0, :9]
+    out = retopk.chunk_attention(q, c.h, i32([200, 150]))
+    check(q, 0, [1, 1], [200, 150], c, out, None, 1 / math.sqrt(D), 0.0, 0)
+
+
+def test_attention_captured_and_replayed_with_new_lengths():
+    lens, n = [900, 333], [1, 1]
+    q, c = setup(n, lens, 28, 4, 64, 15, pad=0, strided=False)
+    sl, out = i32([10, 20]), torch.empty_like(q)
+    ws = torch.empty(retopk.chunk_attention_workspace_bytes(2, 2, 28, 4) + 256, dtype=torch.uint8, device="cuda")
+    retopk.chunk_attention(q, c.h, sl, out, workspace=ws)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        retopk.chunk_attention(q, c.h, sl, out, workspace=ws)
+        retopk.chunk_attention(q, c.h, sl, out, workspace=ws)      # the same workspace, one after another
+    for L in (lens, [1, 2], [129, 128]):
+        sl.copy_(i32(L))
+        out.fill_(9.0)
+        g.replay()
+        for b in range(2):
+            k, v = c.rows(b, L[b])
+            ref, _, mass, d = reference(q[b:b + 1], k, v, L[b] - 1, 1 / math.sqrt(D), 0.0, 0)
+            assert ((out[b:b + 1].double() - ref).abs() <= 2.0 ** -8 * ref.abs() + (2.0 ** -8 + 2 * d + 2.0 ** -14) * mass).all()
+
+
+def test_attention_on_two_streams_at_once():
+    a, b = setup([1, 1], [5000, 100], 28, 4, 0, 16, pad=0), setup([300], [2000], 8, 8, 128, 17, pad=0)
+    la, lb, cu = i32([5000, 100]), i32([2000]), offsets([300])
+    one = [retopk.chunk_attention(a[0], a[1].h, la).clone(), retopk.chunk_attention(b[0], b[1].h, lb, cu_tokens=cu).clone()]
+    s = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        x = retopk.chunk_attention(a[0], a[1].h, la, stream=s[0])
+        y = retopk.chunk_attention(b[0], b[1].h, lb, cu_tokens=cu, stream=s[1])
+        torch.cuda.synchronize()
+        assert torch.equal(x, one[0]) and torch.equal(y, one[1])
+
+
+def test_attention_repeats_bit_for_bit():
+    q, c = setup([1, 90, 4], [30000, 2000, 700], 28, 4, 64, 18)
+    cu, sl = offsets([1, 90, 4]), i32([30000, 2000, 700])
+    first = retopk.chunk_attention(q, c.h, sl, cu_tokens=cu)[:95].clone()
+    for _ in range(4):
+        assert torch.equal(retopk.chunk_attention(q, c.h, sl, cu_tokens=cu)[:95], first)
+
+
+def test_calls_refuse_tensors_elsewhere():
+    q, c = setup([1], [10], 4, 1, 0, 19, pad=0)
+    with pytest.raises(retopk.RetopkError):
+        retopk.chunk_attention(q.cpu(), c.h, i32([10]))
+    with pytest.raises(retopk.RetopkError):
+        retopk.chunk_attention(q, c.h, i32([10]).cpu())
+    with pytest.raises(retopk.RetopkError):
+        retopk.chunk_attention(q, c.h, i32([10]), lse=torch.empty((2, 4), device="cuda"))
+
+
+# ---- together --------------------------------------------------------------------------------------------------------
+def test_prompt_in_chunks_then_sparse_decoding():
+    """A prompt is appended to pages and attended in chunks, gathered into the contiguous cache, and decoded with
+    retopk_decode_step_kv; the sequence is then parked in 8 bits and read back."""
+    g = gen(21)
+    B, Hq, Hkv, L0, K, C = 2, 8, 2, 700, 2000, 8
+    w = (torch.randn(2, D, generator=g, device="cuda") * 0.1 + 1).to(torch.bfloat16)
+    rope = retopk.QKRope(freqs(128, 1e4), w[0], w[1])
+    paged = Cache(B, Hkv, 800, 48, fill=0.0)
+    proj = normal(g, L0 + 4, B, (Hq + 2 * Hkv) * D)
+    sl = i32([0] * B)
+    qs = []
+    for f, l in ((0, 333), (333, 334), (334, 700)):
+        x = proj[f:l].transpose(0, 1).reshape(B * (l - f), -1)
+        q, k, v = (y.view(x.shape[0], -1, D) for y in x.split([Hq * D, Hkv * D, Hkv * D], dim=1))
+        cu = offsets([l - f] * B)
+        qr = retopk.qkv_append(rope, q, k, v, paged.h, sl, cu_tokens=cu)
+        out = retopk.chunk_attention(qr, paged.h, sl, cu_tokens=cu)
+        check(qr, 0, [l - f] * B, [l] * B, paged, out, None, 1 / math.sqrt(D), 0.0, 0)
+        qs.append(qr.view(B, l - f, Hq, D))
+    assert sl.tolist() == [L0] * B
+    flat = Cache(B, Hkv, 800, fill=0.0)
+    retopk.cache_copy(paged.h, flat.h, i32([0] * B), sl, 800)
+    for b in range(B):
+        assert all(torch.equal(x, y) for x, y in zip(paged.rows(b, L0), flat.rows(b, L0)))
+    # with K beyond every length the sparse step is dense attention: the two agree
+    ctx = retopk.ReTopK(B, Hq, Hkv, 800, K=K, C=C, W=8, R=2, T_r=1, tau=2.0)
+    q_last = torch.cat(qs, 1)[:, -C:].transpose(1, 2).contiguous()
+    ctx.retopk_init_cache(q_last, flat.k, sl)
+    for t in range(4):
+        x = proj[L0 + t].view(B, Hq + 2 * Hkv, D)
+        q, k = retopk.qk_rope(rope, x[:, :Hq], x[:, Hq:Hq + Hkv], sl)
+        sparse = torch.empty_like(q)
+        ctx.retopk_decode_step_kv(k, x[:, Hq + Hkv:].contiguous(), q, flat.k, flat.v, sl, sparse)
+        dense = retopk.chunk_attention(q, flat.h, sl)
+        check(q, 0, [1] * B, [L0 + t + 1] * B, flat, dense, None, 1 / math.sqrt(D), 0.0, 0)
+        check(q, 0, [1] * B, [L0 + t + 1] * B, flat, sparse, None, 1 / math.sqrt(D), 0.0, 0)
+    parked, back = Cache(B, Hkv, 800, 64, mx8=True, seed=5), Cache(B, Hkv, 800, fill=0.0)
+    zero = i32([0] * B)
+    retopk.cache_copy(flat.h, parked.h, zero, sl, 800)
+    retopk.cache_copy(parked.h, back.h, zero, sl, 800)
+    for b in range(B):
+        for x, y in zip(flat.rows(b, L0 + 4), back.rows(b, L0 + 4)):
+            top = x.unflatten(-1, (4, 32)).abs().amax(-1, keepdim=True).expand(-1, -1, 4, 32).flatten(-2)
+            assert ((x - y).abs() <= torch.maximum(2.0 ** -4 * x.abs(), top * 2.0 ** -17)).all()

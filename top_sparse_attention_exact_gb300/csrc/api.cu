@@ -18,6 +18,7 @@ cudaError_t configure_finish();
 size_t finish_smem_bytes_for(int max_len, int K, int RKW, int CL);
 cudaError_t configure_fidelity();
 cudaError_t configure_prefilter();
+cudaError_t configure_chunk_attention();
 }  // namespace retopk
 
 using namespace retopk;
@@ -64,14 +65,6 @@ struct Layout {
 
 thread_local cudaError_t g_last_cuda_error = cudaSuccess;
 
-int cuda_rc(cudaError_t e)
-{
-    if (e == cudaSuccess)
-        return RETOPK_OK;
-    g_last_cuda_error = e;
-    return RETOPK_ERR_CUDA;
-}
-
 // Both the SM count and the kernels' attributes (cudaFuncSetAttribute) belong
 // to a device: they are kept per device, for the device current at the call.
 constexpr int kMaxDevices = 64;
@@ -82,6 +75,18 @@ int current_device()
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices)
         return -1;
     return dev;
+}
+
+}  // namespace
+
+namespace retopk {
+
+int cuda_rc(cudaError_t e)
+{
+    if (e == cudaSuccess)
+        return RETOPK_OK;
+    g_last_cuda_error = e;
+    return RETOPK_ERR_CUDA;
 }
 
 int sm_count()
@@ -116,10 +121,16 @@ int ensure_configured()
             e = configure_fidelity();
         if (e == cudaSuccess)
             e = configure_prefilter();
+        if (e == cudaSuccess)
+            e = configure_chunk_attention();
         err[dev] = e;
     });
     return cuda_rc(err[dev]);
 }
+
+}  // namespace retopk
+
+namespace {
 
 bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 

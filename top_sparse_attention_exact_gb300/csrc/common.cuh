@@ -270,6 +270,11 @@ cudaError_t launch_prefilter(const Work &w, const int32_t *seqlens, cudaStream_t
 cudaError_t launch_selftest_wait(uint32_t *status, long long limit, cudaStream_t st);
 int scan_ctas_per_sm();
 
+// ---- shared by the files that hold entry points ----------------------------
+int cuda_rc(cudaError_t e);   // RETOPK_OK, or RETOPK_ERR_CUDA with the error kept for retopk_cuda_error_string
+int sm_count();               // of the current device
+int ensure_configured();      // the kernels' attributes on the current device
+
 enum { FIN_DECODE = 0, FIN_EXACT = 1, FIN_INIT = 2 };
 
 }  // namespace retopk

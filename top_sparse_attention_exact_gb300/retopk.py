@@ -20,6 +20,8 @@ _lib = None
 
 RETOPK_PATH_REUSE, RETOPK_PATH_FALLBACK, RETOPK_PATH_REFRESH = 0, 1, 2
 STATUS_BAD_INDEX, STATUS_KV_FULL, STATUS_NONFINITE, STATUS_TIMEOUT, STATUS_GATHER = 0x1, 0x2, 0x4, 0x8, 0x10
+STATUS_BAD_PAGE = 0x20
+CACHE_BF16, CACHE_MX8 = 0, 1
 
 EXPORTED = ("retopk_workspace_bytes", "retopk_create", "retopk_destroy", "retopk_init_cache",
             "retopk_append_kv", "retopk_decode_step", "retopk_decode_step_kv", "retopk_get_diagnostics",
@@ -29,7 +31,9 @@ EXPORTED = ("retopk_workspace_bytes", "retopk_create", "retopk_destroy", "retopk
             "retopk_profile_enable", "retopk_profile_read", "retopk_profile_reset",
             "retopk_selftest_wait", "exact_topk_attention_step_noalloc", "retopk_fidelity",
             "retopk_decode_step_host", "retopk_support_overlap", "exact_topk_scan", "exact_topk_select",
-            "retopk_state_workspace_bytes", "retopk_scratch_bytes", "retopk_create_shared")
+            "retopk_state_workspace_bytes", "retopk_scratch_bytes", "retopk_create_shared",
+            "retopk_qk_rope", "retopk_qkv_append", "retopk_cache_copy",
+            "retopk_chunk_attention_workspace_bytes", "retopk_chunk_attention")
 
 PROF_KERNELS = ("append", "finish", "scan", "select", "clear", "decide")
 
@@ -44,6 +48,18 @@ class retopk_config(ctypes.Structure):
                 ("max_len", ctypes.c_int32), ("K", ctypes.c_int32), ("C", ctypes.c_int32),
                 ("W", ctypes.c_int32), ("R", ctypes.c_int32), ("T_r", ctypes.c_int32),
                 ("tau", ctypes.c_float), ("retrieval", ctypes.c_int32), ("cluster", ctypes.c_int32)]
+
+
+class retopk_cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("table", ctypes.c_void_p), ("format", ctypes.c_int32),
+                ("n_pages", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32), ("page_rows", ctypes.c_int32),
+                ("table_width", ctypes.c_int32)]
+
+
+class retopk_rope(ctypes.Structure):
+    _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("inv_freq", ctypes.c_void_p),
+                ("eps", ctypes.c_float), ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
 
 
 _P, _S, _I = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int
@@ -88,6 +104,13 @@ def _declare(lib):
     lib.retopk_support_overlap.argtypes = [_P, _P, _I, _I, _I, _P, _P]
     lib.exact_topk_scan.argtypes = [_P, _P, _P] + [_I] * 6 + [_P, _S, _P]
     lib.exact_topk_select.argtypes = [_P, _P, _P] + [_I] * 6 + [_P, _P, _P, _S, _P]
+    L, F = ctypes.c_int64, ctypes.c_float
+    lib.retopk_qk_rope.argtypes = [_P, _P, L, _P, L, _P] + [_I] * 4 + [_P] * 4
+    lib.retopk_qkv_append.argtypes = [_P, _P, L, _P, L, _P, L, _P] + [_I] * 3 + [_P] * 6
+    lib.retopk_cache_copy.argtypes = [_P] * 4 + [_I, _I, _P, _P]
+    lib.retopk_chunk_attention_workspace_bytes.argtypes = [_I] * 4
+    lib.retopk_chunk_attention_workspace_bytes.restype = _S
+    lib.retopk_chunk_attention.argtypes = ([_P, L, _P, _P] + [_I] * 3 + [_P, F, F, _I, _P, L, _P, _P, _S, _P, _P])
     for name in EXPORTED:
         getattr(lib, name).restype = getattr(lib, name).restype or ctypes.c_int
     return lib
@@ -258,6 +281,200 @@ def profile_read() -> dict:
 
 def profile_reset():
     _check(load().retopk_profile_reset(), "retopk_profile_reset")
+
+
+# ---- prompt side: rotated append, cache copy, chunk attention ------------------
+
+def _call_stream(stream, tensors):
+    """The raw stream of a call; every tensor (None passes) has to be on the current device, and so has the stream."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise RetopkError(f"expected CUDA tensors on the current device (cuda:{dev}), got one on {t.device}")
+    if stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    if stream.device_index != dev:
+        raise RetopkError(f"stream of device {stream.device_index} while cuda:{dev} is current")
+    return stream.cuda_stream
+
+
+def _empty(shape, dtype, device, stream):
+    """Memory for a call on `stream`, allocated there so that the allocator's reuse follows that stream's order."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _tokens(t: torch.Tensor, what: str) -> int:
+    """The token stride of a bf16 [T, heads, 128] tensor whose heads lie side by side."""
+    if t.dtype not in _BF16_TYPES or t.dim() != 3 or t.shape[2] != 128:
+        raise RetopkError(f"{what}: a bf16 [T, heads, 128] tensor expected, got {t.dtype} {tuple(t.shape)}")
+    T, h, _ = t.shape
+    st, sh, sd = t.stride()
+    if sd != 1 or (h > 1 and sh != 128):
+        raise RetopkError(f"{what}: a token's heads have to lie side by side, got strides {t.stride()}")
+    return st if T > 1 else max(st, h * 128)
+
+
+def _lens(t: torch.Tensor | None, n: int, what: str):
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or t.dim() != 1 or t.numel() != n or not t.is_contiguous():
+        raise RetopkError(f"{what}: a contiguous int32 [{n}] tensor expected, got {t.dtype} {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _status(t: torch.Tensor | None):
+    if t is None:
+        return None
+    if t.element_size() != 4 or t.is_floating_point() or t.numel() < 1:
+        raise RetopkError("status: a 32-bit integer tensor expected")
+    return t.data_ptr()
+
+
+def _same(t: torch.Tensor, shape, what: str):
+    if t.dtype not in _BF16_TYPES or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise RetopkError(f"{what}: a contiguous bf16 {tuple(shape)} tensor expected, got {t.dtype} {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+class KVCache:
+    """The keys and values of some sequences, as the prompt-side calls see them (struct retopk_cache).
+
+    k, v: [pages, Hkv, rows, 128], bf16, or uint8 e4m3 codes with k_scale, v_scale uint8 [pages, Hkv, rows, 4].
+    table: int32 [B, width], the pages of each sequence in order (rows a multiple of 16); None: page b holds
+    sequence b whole, the [B, Hkv, max_len, 128] layout of the decode calls.  Keeps the tensors alive."""
+
+    def __init__(self, k, v, table=None, k_scale=None, v_scale=None):
+        mx8 = k.dtype == torch.uint8
+        for what, t in (("k", k), ("v", v)):
+            if t.dim() != 4 or t.shape != k.shape or t.shape[3] != 128 or t.dtype != k.dtype or not t.is_contiguous():
+                raise RetopkError(f"{what}: contiguous k and v of one type, [pages, Hkv, rows, 128], expected")
+        if not mx8:
+            _bf16(k)
+        scales = (k_scale, v_scale)
+        if mx8 != all(t is not None for t in scales) or (not mx8 and any(t is not None for t in scales)):
+            raise RetopkError("k_scale and v_scale belong to uint8 caches, and only to those")
+        for t in scales:
+            if t is not None and (t.dtype != torch.uint8 or tuple(t.shape) != (*k.shape[:3], 4) or not t.is_contiguous()):
+                raise RetopkError("scales: contiguous uint8 [pages, Hkv, rows, 4] tensors expected")
+        if table is not None and (table.dtype != torch.int32 or table.dim() != 2 or not table.is_contiguous()):
+            raise RetopkError("table: a contiguous int32 [B, width] tensor expected")
+        self.tensors = (k, v, table, k_scale, v_scale)
+        for t in self.tensors:
+            if t is not None and t.device != k.device:
+                raise RetopkError("the tensors of a cache are on one device")
+        self.k, self.v, self.table, self.k_scale, self.v_scale = self.tensors
+        p = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+        pages, Hkv, rows, _ = k.shape
+        self.Hkv, self.B = Hkv, pages if table is None else table.shape[0]
+        self.rows = rows if table is None else rows * table.shape[1]
+        self.struct = retopk_cache(p(k), p(v), p(k_scale), p(v_scale), p(table), CACHE_MX8 if mx8 else CACHE_BF16,
+                                   pages, Hkv, rows, 0 if table is None else table.shape[1])
+        self._ref = ctypes.addressof(self.struct)
+
+    def _holds(self, B, what):
+        if self.B < B:
+            raise RetopkError(f"{what}: a cache for {self.B} sequences, {B} asked")
+        return self._ref
+
+
+class QKRope:
+    """What is done to query and key heads before their use (struct retopk_rope): RMS norm where weights (bf16
+    [128]) are given, rotation of the first 2 * len(inv_freq) elements where inv_freq (fp32) is."""
+
+    def __init__(self, inv_freq=None, q_weight=None, k_weight=None, eps=1e-6, interleaved=False):
+        for w in (q_weight, k_weight):
+            if w is not None and (w.dtype not in _BF16_TYPES or tuple(w.shape) != (128,) or not w.is_contiguous()):
+                raise RetopkError("norm weights: contiguous bf16 [128] tensors expected")
+        if inv_freq is not None and (inv_freq.dtype != torch.float32 or inv_freq.dim() != 1 or not inv_freq.is_contiguous()):
+            raise RetopkError("inv_freq: a contiguous fp32 [rot_dim / 2] tensor expected")
+        self.tensors = (inv_freq, q_weight, k_weight)
+        p = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+        self.struct = retopk_rope(p(q_weight), p(k_weight), p(inv_freq), eps,
+                                  0 if inv_freq is None else 2 * inv_freq.numel(), 1 if interleaved else 0)
+        self._ref = ctypes.addressof(self.struct)
+
+
+def qk_rope(rope: QKRope, q, k, seqlens, q_out=None, k_out=None, cu_tokens=None, stream=None):
+    """Norm and rotation of q [T, Hq, 128] and k [T, Hkv, 128] at positions seqlens[b] + i; returns (q_out, k_out).
+    cu_tokens: int32 [B + 1] offsets of each sequence's tokens (None: one token each)."""
+    T, Hq, Hkv = q.shape[0], q.shape[1], k.shape[1]
+    B = seqlens.numel()
+    q_out = _empty((T, Hq, 128), q.dtype, q.device, stream) if q_out is None else q_out
+    k_out = _empty((T, Hkv, 128), k.dtype, k.device, stream) if k_out is None else k_out
+    st = _call_stream(stream, (q, k, seqlens, q_out, k_out, cu_tokens, *rope.tensors))
+    if k.shape[0] != T:
+        raise RetopkError(f"q has {T} tokens, k {k.shape[0]}")
+    rc = load().retopk_qk_rope(rope._ref, q.data_ptr(), _tokens(q, "q"), k.data_ptr(), _tokens(k, "k"),
+                               _lens(cu_tokens, B + 1, "cu_tokens"), T, B, Hq, Hkv, _lens(seqlens, B, "seqlens"),
+                               _same(q_out, (T, Hq, 128), "q_out"), _same(k_out, (T, Hkv, 128), "k_out"), st)
+    _check(rc, "retopk_qk_rope")
+    return q_out, k_out
+
+
+def qkv_append(rope: QKRope, q, k, v, cache: KVCache, seqlens, seqlens_out=None, q_out=None, cu_tokens=None,
+               status=None, stream=None):
+    """qk_rope with the keys and values written to rows seqlens[b] + i of the cache; returns q_out.  The lengths go to
+    seqlens_out (None: seqlens itself advances).  q, k, v may be slices of one fused projection."""
+    T, Hq, Hkv = q.shape[0], q.shape[1], cache.Hkv
+    B = seqlens.numel()
+    q_out = _empty((T, Hq, 128), q.dtype, q.device, stream) if q_out is None else q_out
+    seqlens_out = seqlens if seqlens_out is None else seqlens_out
+    st = _call_stream(stream, (q, k, v, cache.k, seqlens, seqlens_out, q_out, cu_tokens, status, *rope.tensors))
+    if tuple(k.shape) != (T, Hkv, 128) or k.shape != v.shape:
+        raise RetopkError(f"k and v: [{T}, {Hkv}, 128] expected, got {tuple(k.shape)} and {tuple(v.shape)}")
+    rc = load().retopk_qkv_append(
+        rope._ref, q.data_ptr(), _tokens(q, "q"), k.data_ptr(), _tokens(k, "k"), v.data_ptr(), _tokens(v, "v"),
+        _lens(cu_tokens, B + 1, "cu_tokens"), T, B, Hq, cache._holds(B, "qkv_append"), _lens(seqlens, B, "seqlens"),
+        _lens(seqlens_out, B, "seqlens_out"), _same(q_out, (T, Hq, 128), "q_out"), _status(status), st)
+    _check(rc, "retopk_qkv_append")
+    return q_out
+
+
+def cache_copy(src: KVCache, dst: KVCache, first, last, max_rows: int | None = None, status=None, stream=None):
+    """Rows [first[b], last[b]) of every sequence from src to the same rows of dst, converted where the formats differ.
+    max_rows bounds last - first (None: the smaller capacity)."""
+    B = first.numel()
+    st = _call_stream(stream, (src.k, dst.k, first, last, status))
+    rc = load().retopk_cache_copy(src._holds(B, "cache_copy"), dst._holds(B, "cache_copy"), _lens(first, B, "first"),
+                                  _lens(last, B, "last"), B, min(src.rows, dst.rows) if max_rows is None else max_rows,
+                                  _status(status), st)
+    _check(rc, "retopk_cache_copy")
+
+
+def chunk_attention_workspace_bytes(T, B, Hq, Hkv) -> int:
+    n = load().retopk_chunk_attention_workspace_bytes(T, B, Hq, Hkv)
+    if n == 0:
+        raise RetopkError("chunk_attention_workspace_bytes: invalid sizes")
+    return int(n)
+
+
+def chunk_attention(q, cache: KVCache, seqlens, out=None, cu_tokens=None, scale=None, softcap=0.0, window=0, lse=None,
+                    workspace=None, status=None, stream=None):
+    """Causal attention of q [T, Hq, 128] over a bf16 cache that holds the tokens' own rows (seqlens: rows in all);
+    returns out.  cu_tokens: offsets of each sequence's tokens (None: one token each, dense decoding).  lse: optional
+    fp32 [T, Hq].  workspace: uint8, chunk_attention_workspace_bytes(...) + 256 (None: allocated for the call)."""
+    T, Hq, Hkv = q.shape[0], q.shape[1], cache.Hkv
+    B = seqlens.numel()
+    out = _empty((T, Hq, 128), q.dtype, q.device, stream) if out is None else out
+    st = _call_stream(stream, (q, cache.k, seqlens, out, cu_tokens, lse, workspace, status))
+    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (T, Hq) or not lse.is_contiguous()):
+        raise RetopkError(f"lse: a contiguous fp32 [{T}, {Hq}] tensor expected")
+    if out.shape != q.shape:
+        raise RetopkError(f"out: {tuple(q.shape)} expected, got {tuple(out.shape)}")
+    if workspace is None:
+        workspace = _empty(chunk_attention_workspace_bytes(T, B, Hq, Hkv) + 256, torch.uint8, q.device, stream)
+    wp = workspace.data_ptr()
+    up = -wp % 256
+    rc = load().retopk_chunk_attention(
+        q.data_ptr(), _tokens(q, "q"), cache._holds(B, "chunk_attention"), _lens(cu_tokens, B + 1, "cu_tokens"), T, B,
+        Hq, _lens(seqlens, B, "seqlens"), 0.0 if scale is None else scale, softcap, window, out.data_ptr(),
+        _tokens(out, "out"), None if lse is None else lse.data_ptr(), wp + up,
+        max(0, workspace.numel() * workspace.element_size() - up), _status(status), st)
+    _check(rc, "retopk_chunk_attention")
+    return out
 
 
 class ReTopK:
