@@ -24,7 +24,8 @@ int check_cache(const retopk_cache *c, int B)
         return RETOPK_ERR_INVALID;
     if (c->table ? c->table_width < 1 || c->page_rows % 16 != 0 : c->n_pages < B)
         return RETOPK_ERR_INVALID;
-    if (c->n_kv_heads > kMaxHeads || cache_capacity(*c) > kMaxLen)
+    if (c->n_kv_heads > kMaxHeads || cache_capacity(*c) > kMaxLen ||
+        (long long)c->n_pages * c->n_kv_heads >= INT32_MAX)
         return RETOPK_ERR_UNSUPPORTED;
     if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->table, 4) ||
         (c->format == RETOPK_CACHE_MX8 && (!aligned(c->k_scale, 4) || !aligned(c->v_scale, 4))))

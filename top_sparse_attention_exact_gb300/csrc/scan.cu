@@ -35,6 +35,7 @@
 #include <algorithm>
 
 #include "common.cuh"
+#include "tensor_map.cuh"
 
 namespace retopk {
 
@@ -434,26 +435,6 @@ static int stages_for(int G)
 static size_t scan_smem_bytes(int G) { return 1024 + (size_t)stages_for(G) * kStageBytes + hist_bytes(G); }
 
 int scan_ctas_per_sm() { return 1; }
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-static EncodeTiledFn encode_fn()
-{
-    static EncodeTiledFn fn = nullptr;
-    static bool tried = false;
-    if (!tried) {
-        tried = true;
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(p);
-    }
-    return fn;
-}
 
 // K cache viewed as a 2-D tensor of 128-byte half rows: [2*B*Hkv*max_len, 64
 // elements].  One box of 256 half rows is one contiguous 32 KiB tile.
