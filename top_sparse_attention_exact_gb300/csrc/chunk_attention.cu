@@ -11,10 +11,12 @@
 // one KV head (the row of token t, head g is t G + g), so every head of the group uses
 // the K / V rows that were loaded once.
 //
-// Roles (10 warps, one CTA per SM): two groups of four softmax warps, each
-// thread one row of its tile; one thread that issues the matrix instructions
-// (S = Q K^T from shared memory, O += P V with P in tensor memory); one warp that
-// issues the copies.  Tensor memory: S_0, S_1 (P_i takes the first half of
+// Roles (12 warps, one CTA per SM; two of them idle): two groups of four softmax
+// warps, each thread one row of its tile, whose 128 scores stay in registers; one
+// thread that issues the matrix instructions (S = Q K^T from shared memory, O += P V
+// with P in tensor memory); one warp that issues the copies.  Shared memory leaves
+// the L1 no room, so a spilled register costs a trip to the L2: what a warp keeps
+// between tiles is small, and its place in the share lies in shared memory.  Tensor memory: S_0, S_1 (P_i takes the first half of
 // S_i's columns), O_0, O_1, 128 columns each.
 //   two tiles    (TWO):  the groups hold neighbouring tiles of tokens and share
 //                every K / V tile.  For prompts.
@@ -39,9 +41,10 @@ constexpr int kTile = 128;                       // rows and keys of a tile
 constexpr int kAttnStages = 5;                   // K / V tiles in flight
 constexpr int kAttnStageBytes = kTile * kD * 2;  // 32 KiB: [half of d][key][64]
 constexpr int kHalfBytes = kAttnStageBytes / 2;
-constexpr int kAttnThreads = 10 * 32;
+constexpr int kAttnThreads = 12 * 32;
 constexpr int kMmaWarp = 8, kLoadWarp = 9;
-constexpr size_t kAttnSmem = 1024 + (2 + kAttnStages) * (size_t)kAttnStageBytes;
+// registers of a thread after the split: 2 x 128 x 208 + 128 x 88 = 384 x 168, what the block is launched with
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
 constexpr float kLazy = 8.f;                     // growth of m, in powers of two, that is left to the accumulators
 
 // Where a share begins: an item and the number of its K / V tiles that belong
@@ -56,8 +59,9 @@ __device__ __forceinline__ bool same_item(const Place &x, const Place &y)
 }
 
 struct Plan {
-    int tokens;      // tokens of a block (two tiles', or one tile's)
-    int overhead;    // weight of an item beside its keys
+    int tokens;                    // tokens of a block (two tiles', or one tile's)
+    int overhead;                  // weight of an item beside its keys
+    unsigned long long inverse;    // 2^64 / shares
 };
 
 // Tokens, first token and rows of a sequence.
@@ -93,10 +97,15 @@ __device__ __forceinline__ int blocks_of(const Plan &p, const Seq &s) { return (
 // last key's position, bounded by the window.
 __device__ __forceinline__ long long weight(const AttnArgs &a, const Plan &p, const Seq &s, int k)
 {
-    const long long first = (long long)max(0, s.L - s.n) + min(p.tokens, s.n) + p.overhead;
-    const long long most = a.window > 0 ? (long long)a.window + p.tokens + kTile + p.overhead : 1ll << 40;
-    const long long grow = most <= first ? 0 : min((long long)k, (most - first) / p.tokens + 1);
-    return grow * first + p.tokens * (grow * (grow - 1) / 2) + (k - grow) * most;
+    const int first = max(0, s.L - s.n) + min(p.tokens, s.n) + p.overhead;
+    int grow = k;
+    long long flat = 0;
+    if (a.window > 0 && a.window < kMaxLen) {
+        const int most = a.window + p.tokens + kTile + p.overhead;
+        grow = most <= first ? 0 : min(k, (most - first) / p.tokens + 1);
+        flat = (long long)(k - grow) * most;
+    }
+    return (long long)grow * first + (long long)p.tokens * grow * (grow - 1) / 2 + flat;
 }
 
 // The place u units behind the beginning of sequence b.
@@ -104,8 +113,14 @@ __device__ Place place_in(const AttnArgs &a, const Plan &p, const Seq &s, int b,
 {
     const int nb = blocks_of(p, s);
     const long long each = weight(a, p, s, nb);
-    Place r{b, (int)(u / each), 0, 0};
-    u -= r.hk * each;
+    Place r{b, 0, 0, 0};
+    if (a.cache.n_kv_heads > 32) {
+        r.hk = (int)(u / each);
+        u -= r.hk * each;
+    } else {
+        for (; u >= each; u -= each)
+            ++r.hk;
+    }
     int top = nb - 1;
     while (r.k < top) {   // the last block that begins at or before u
         const int mid = (r.k + top + 1) / 2;
@@ -116,10 +131,10 @@ __device__ Place place_in(const AttnArgs &a, const Plan &p, const Seq &s, int b,
     }
     int lo, hi;
     tiles_of(a, p, s, r.k, lo, hi);
-    const long long begin = weight(a, p, s, r.k), all = weight(a, p, s, r.k + 1) - begin;
+    const long long begin = weight(a, p, s, r.k);
     // short items are cut into no small parts: joining costs more than it gives
     const int nt = hi - lo, grain = nt >= 64 ? 1 : nt >= 16 ? 2 : 4;
-    const int x = (int)((u - begin) * nt / all);
+    const int x = (int)(__fdividef((float)(int)(u - begin), (float)(int)(weight(a, p, s, r.k + 1) - begin)) * nt);
     r.cut = (x + grain / 2) / grain * grain;
     if (r.cut >= nt) {   // the beginning of the next item
         r.cut = 0;
@@ -134,18 +149,91 @@ __device__ Place place_in(const AttnArgs &a, const Plan &p, const Seq &s, int b,
     return r;
 }
 
+// ---- the walk over a share ---------------------------------------------------------
+struct Walk {
+    Place at, end;
+    Seq seq;
+    int loaded;   // sequence that seq describes
+};
+
+struct Segment {
+    int b, hk, k;
+    int lo, j0, j1, hi;   // K / V tiles [j0, j1) of the item's [lo, hi)
+    Seq seq;
+    int more;             // 0: the share is done
+};
+
+__device__ __forceinline__ bool next_segment(const AttnArgs &a, const Plan &p, Walk &w, Segment &s)
+{
+    for (;;) {
+        if (w.at.b > w.end.b || w.at.b >= a.B ||
+            (w.at.b == w.end.b &&
+             (w.at.hk > w.end.hk || (w.at.hk == w.end.hk && (w.at.k > w.end.k || (w.at.k == w.end.k && w.at.cut >= w.end.cut))))))
+            return false;
+        if (w.loaded != w.at.b) {
+            w.seq = sequence(a, w.at.b);
+            w.loaded = w.at.b;
+        }
+        const int nb = blocks_of(p, w.seq);
+        if (nb == 0) {
+            w.at = Place{w.at.b + 1, 0, 0, 0};
+            continue;
+        }
+        s.b = w.at.b;
+        s.hk = w.at.hk;
+        s.k = w.at.k;
+        tiles_of(a, p, w.seq, s.k, s.lo, s.hi);
+        s.j0 = s.lo + w.at.cut;
+        s.j1 = same_item(w.at, w.end) ? s.lo + w.end.cut : s.hi;
+        w.at.cut = 0;
+        if (++w.at.k == nb) {
+            w.at.k = 0;
+            if (++w.at.hk == a.cache.n_kv_heads) {
+                w.at.hk = 0;
+                ++w.at.b;
+            }
+        }
+        if (s.j1 > s.j0) {
+            s.seq = w.seq;
+            return true;
+        }
+    }
+}
+
+// A warp's place in its share, in shared memory.
+struct WarpWalk {
+    Walk w;
+    Segment s;
+};
+
+// The next segment, found by one lane for its warp (all lanes call).
+__device__ __forceinline__ bool next_of_warp(const AttnArgs &a, const Plan &p, WarpWalk &x)
+{
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0)
+        x.s.more = next_segment(a, p, x.w, x.s);
+    __syncwarp();
+    return x.s.more != 0;
+}
+
+
 struct AttnShared {
     uint64_t kv_full[kAttnStages], kv_empty[kAttnStages];
     uint64_t q_full, q_empty;
-    uint64_t s_full[2], p_full[2], o_full[2];
+    uint64_t s_full[2], p_full[2][2], o_full[2];
     uint64_t x_full, x_empty;   // the streams' join in shared memory
     uint64_t drained;
     Place bound[2];
+    Seq first;                 // the sequence that bound[0] was found in
+    int first_b;
+    WarpWalk walk[kLoadWarp + 1];
     long long sums[kAttnThreads / 32 + 1];
     uint32_t tmem;
     int failed;
-    float ml[2][kTile];   // stream 1's maximum and sum, for the join in shared memory
 };
+// two Q tiles, the ring, AttnShared; with one Q tile the second's place serves the streams' join
+constexpr size_t kAttnSmem = (2 + kAttnStages) * (size_t)kAttnStageBytes + sizeof(AttnShared);
+static_assert(kAttnSmem <= kMaxDynSmem, "one CTA's shared memory");
 
 // ---- waits -------------------------------------------------------------------
 // Bounded; once one has run out every other gives up at once.
@@ -208,6 +296,21 @@ __device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t *x)
         W16(x, 0), W16(x, 16)
         : "memory");
 }
+__device__ __forceinline__ void tc_ld16(uint32_t addr, uint32_t *x)
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+                 : R16(x, 0)
+                 : "r"(addr));
+}
+
+__device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t *x)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(
+            addr),
+        W16(x, 0)
+        : "memory");
+}
 #undef R4
 #undef R16
 #undef W4
@@ -268,57 +371,28 @@ __device__ __forceinline__ float rcp(float x)
     return y;
 }
 
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(reinterpret_cast<uint64_t &>(d))
+        : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)), "l"(reinterpret_cast<uint64_t &>(c)));
+    return d;
+}
+
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    float2 d;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<uint64_t &>(d))
+        : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)));
+    return d;
+}
+
 // softcap tanh(s / softcap) in powers of two, with tanh(y) = 1 - 2 / (1 + e^2y).
 __device__ __forceinline__ float capped(float s, float in, float cap2)
 {
     return fmaf(-2.f * cap2, rcp(1.f + ex2(s * in)), cap2);
-}
-
-// ---- the walk over a share ---------------------------------------------------------
-struct Walk {
-    Place at, end;
-    Seq seq;
-    int loaded;   // sequence that seq describes
-};
-
-struct Segment {
-    int b, hk, k;
-    int lo, j0, j1, hi;   // K / V tiles [j0, j1) of the item's [lo, hi)
-};
-
-__device__ __forceinline__ bool next_segment(const AttnArgs &a, const Plan &p, Walk &w, Segment &s)
-{
-    for (;;) {
-        if (w.at.b > w.end.b || w.at.b >= a.B ||
-            (w.at.b == w.end.b &&
-             (w.at.hk > w.end.hk || (w.at.hk == w.end.hk && (w.at.k > w.end.k || (w.at.k == w.end.k && w.at.cut >= w.end.cut))))))
-            return false;
-        if (w.loaded != w.at.b) {
-            w.seq = sequence(a, w.at.b);
-            w.loaded = w.at.b;
-        }
-        const int nb = blocks_of(p, w.seq);
-        if (nb == 0) {
-            w.at = Place{w.at.b + 1, 0, 0, 0};
-            continue;
-        }
-        s.b = w.at.b;
-        s.hk = w.at.hk;
-        s.k = w.at.k;
-        tiles_of(a, p, w.seq, s.k, s.lo, s.hi);
-        s.j0 = s.lo + w.at.cut;
-        s.j1 = same_item(w.at, w.end) ? s.lo + w.end.cut : s.hi;
-        w.at.cut = 0;
-        if (++w.at.k == nb) {
-            w.at.k = 0;
-            if (++w.at.hk == a.cache.n_kv_heads) {
-                w.at.hk = 0;
-                ++w.at.b;
-            }
-        }
-        if (s.j1 > s.j0)
-            return true;
-    }
 }
 
 // Order in which a segment's K and V tiles go through the ring.
@@ -351,19 +425,419 @@ struct AttnLaunch {
     int chunk;   // rows of one K / V copy (a page's, 128 at most)
 };
 
+// ---- the copies --------------------------------------------------------------------
+template <bool TWO>
+__device__ __forceinline__ void copies(const AttnLaunch &c, AttnShared &sh, WarpWalk &walk, const CUtensorMap &qmap,
+                                       const CUtensorMap &kmap, const CUtensorMap &vmap, uint32_t qbuf, uint32_t ring,
+                                       int lane)
+{
+    const AttnArgs &a = c.a;
+    const Segment &s = walk.s;
+    const int Hkv = a.cache.n_kv_heads, tile_tokens = kTile / a.G;
+    const int half = lane & 1, piece = lane >> 1, pieces = kTile / c.chunk;   // this lane's copy
+    bool ok = true;
+    uint32_t used = 0, issued = 0, segs = 0;   // ring slots before this segment, copied so far; Q copies
+    while (ok && next_of_warp(a, c.plan, walk)) {
+        const int nt = s.j1 - s.j0, L = s.seq.L, j0 = s.j0, hk = s.hk, b = s.b;
+        if (lane == 0) {
+            ok = segs == 0 || wait(sh, &sh.q_empty, (segs - 1) & 1, a.status);
+            if (ok) {
+                const int t0 = s.seq.t0 + s.k * c.plan.tokens;
+                mbar_expect_tx(&sh.q_full, (TWO ? 2 : 1) * tile_tokens * a.G * kD * 2);
+                for (int i = 0; i < (TWO ? 2 : 1); ++i)
+                    for (int h = 0; h < 2; ++h)
+                        load_3d(qbuf + i * kAttnStageBytes + h * kHalfBytes, &qmap, h * 64, hk * a.G, t0 + i * tile_tokens,
+                                &sh.q_full);
+                ++segs;
+            }
+        }
+        ok = __shfl_sync(0xffffffffu, (int)ok, 0);
+        segs = __shfl_sync(0xffffffffu, segs, 0);
+        // the ring's order: K ahead of V by one tile (or two, one for each stream)
+        const int ahead = TWO ? 1 : 2;
+        for (int x = -ahead; x < nt && ok; ++x) {
+#pragma unroll
+            for (int isk = 0; isk < 2; ++isk) {
+                const int t = isk ? x + ahead : x;
+                if (t < 0 || t >= nt || !ok)
+                    continue;
+                const uint32_t u = used + (isk ? ring_k<TWO>(t) : ring_v<TWO>(t, nt));
+                const int st = u % kAttnStages;
+                const int pos = (j0 + t) * kTile + piece * c.chunk;
+                int z = a.cache.n_pages * Hkv, y = 0;   // outside: read as zeros
+                if (piece < pieces && pos < L) {
+                    int page = b;
+                    y = pos;
+                    if (a.cache.table) {
+                        page = a.cache.table[(long long)b * a.cache.table_width + pos / a.cache.page_rows];
+                        y = pos % a.cache.page_rows;
+                    }
+                    if ((uint32_t)page < (uint32_t)a.cache.n_pages)
+                        z = page * Hkv + hk;
+                    else if (a.status)
+                        atomicOr(a.status, RETOPK_STATUS_BAD_PAGE);
+                }
+                int good = 1;
+                if (lane == 0) {
+                    if (u >= kAttnStages)
+                        good = wait(sh, &sh.kv_empty[st], (u / kAttnStages - 1) & 1, a.status);
+                    if (good)
+                        mbar_expect_tx(&sh.kv_full[st], kAttnStageBytes);
+                }
+                ok = __shfl_sync(0xffffffffu, good, 0);
+                if (ok) {
+                    issued = u + 1;
+                    if (piece < pieces)
+                        load_3d(ring + st * kAttnStageBytes + half * kHalfBytes + piece * c.chunk * 128,
+                                isk ? &kmap : &vmap, half * 64, y, z, &sh.kv_full[st]);
+                }
+            }
+        }
+        used += 2 * nt;
+    }
+    // a wait ran out: the copies in flight are waited for before the memory goes
+    if (*reinterpret_cast<volatile int *>(&sh.failed) && lane == 0) {
+        const long long t0 = clock64();
+        for (uint32_t u = issued > kAttnStages ? issued - kAttnStages : 0; u < issued; ++u)
+            while (!mbar_try_wait(&sh.kv_full[u % kAttnStages], (u / kAttnStages) & 1) && clock64() - t0 < kWaitCycles)
+                ;
+        while (segs && !mbar_try_wait(&sh.q_full, (segs - 1) & 1) && clock64() - t0 < kWaitCycles)
+            ;
+    }
+    __syncwarp();
+}
+
+// ---- the matrix instructions: one lane's ----------------------------------------------
+template <bool TWO>
+__device__ __forceinline__ void matrices(const AttnLaunch &c, AttnShared &sh, WarpWalk &walk, uint32_t qbuf, uint32_t ring,
+                                         uint32_t tmem, int lane)
+{
+    const AttnArgs &a = c.a;
+    bool ok = true;
+    uint32_t used = 0, segs = 0, done[2] = {0, 0};   // done: tiles of each group before this segment
+    // S_i of the segment's tile t
+    auto scores = [&](int i, int t) {
+        const uint32_t u = used + ring_k<TWO>(t);
+        const int st = u % kAttnStages;
+        if (!wait(sh, &sh.kv_full[st], (u / kAttnStages) & 1, a.status))
+            return false;
+        tc_fence_after();
+        const uint32_t qa = qbuf + (TWO ? i * kAttnStageBytes : 0), ka = ring + st * kAttnStageBytes;
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+            const uint32_t o = (x >> 2) * kHalfBytes + (x & 3) * 32;
+            mma_ss(tmem + i * kTile, operand(qa + o, 0), operand(ka + o, 0), x > 0);
+        }
+        tc_commit(&sh.s_full[i]);
+        if (!TWO || i == 1)
+            tc_commit(&sh.kv_empty[st]);
+        return true;
+    };
+    while (__any_sync(0xffffffffu, ok) && next_of_warp(a, c.plan, walk)) {
+        if (lane == 0) {
+            const int nt = walk.s.j1 - walk.s.j0;
+            const int m[2] = {TWO ? nt : (nt + 1) / 2, TWO ? nt : nt / 2};
+            auto tile = [&](int i, int t) { return TWO ? t : 2 * t + i; };
+            ok = wait(sh, &sh.q_full, segs & 1, a.status);
+            for (int i = 0; i < 2 && ok; ++i)
+                if (m[i] > 0)
+                    ok = scores(i, tile(i, 0));
+            if (ok && m[0] == 1)
+                tc_commit(&sh.q_empty);
+            for (int t = 0; t < m[0] && ok; ++t) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    if (t >= m[i] || !ok)
+                        continue;
+                    const uint32_t u = used + ring_v<TWO>(tile(i, t), nt);
+                    const int st = u % kAttnStages;
+                    const uint32_t va = ring + st * kAttnStageBytes;
+                    ok = wait(sh, &sh.kv_full[st], (u / kAttnStages) & 1, a.status);
+                    // P comes in halves, so that the product begins while the second is made
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        ok = ok && wait(sh, &sh.p_full[i][h], (done[i] + t) & 1, a.status);
+                        if (!ok)
+                            break;
+                        tc_fence_after();
+#pragma unroll
+                        for (int x = 4 * h; x < 4 * h + 4; ++x)
+                            mma_ts(tmem + (2 + i) * kTile, tmem + i * kTile + x * 8, operand(va + x * 2048, kHalfBytes),
+                                   t > 0 || x > 0);
+                    }
+                    if (!ok)
+                        continue;
+                    tc_commit(&sh.o_full[i]);
+                    if (!TWO || i == 1)
+                        tc_commit(&sh.kv_empty[st]);
+                    if (t + 1 < m[i])
+                        ok = scores(i, tile(i, t + 1));
+                }
+                // the last use of Q
+                if (ok && t + 2 == m[0])
+                    tc_commit(&sh.q_empty);
+            }
+            used += 2 * nt;
+            done[0] += m[0];
+            done[1] += m[1];
+            ++segs;
+        } else {
+            ok = false;   // lane 0 alone says whether there is more to do
+        }
+    }
+    if (lane == 0 && !ok) {   // a wait ran out: the instructions in flight end before the tensor memory goes
+        tc_commit(&sh.drained);
+        const long long t0 = clock64();
+        while (!mbar_try_wait(&sh.drained, 0) && clock64() - t0 < kWaitCycles)
+            ;
+    }
+    __syncwarp();
+}
+
+// ---- softmax: group i, row r --------------------------------------------------------------
+template <bool TWO, bool CAP>
+__device__ __forceinline__ void softmax(const AttnLaunch &c, AttnShared &sh, WarpWalk &walk, float *other, uint32_t ring,
+                                        uint32_t tmem, int warp, int lane)
+{
+    const AttnArgs &a = c.a;
+    const Segment &s = walk.s;
+    const int i = warp >> 2, r = (warp & 3) * 32 + lane, G = a.G;
+    const uint32_t s_addr = tmem + i * kTile + ((uint32_t)(warp & 3) << 21), o_addr = s_addr + 2 * kTile;
+    const float scale2 = a.scale * 1.4426950408889634f;     // scores in powers of two
+    const float cap2 = a.softcap * 1.4426950408889634f;
+    const float cap_in = CAP ? 2.f * scale2 / a.softcap : 0.f;   // e^2y = 2^(cap_in s)
+    bool ok = true;
+    uint32_t used = 0, done = 0, segs = 0;
+    while (ok && next_of_warp(a, c.plan, walk)) {
+        const int nt = s.j1 - s.j0, m_tiles = TWO ? nt : (nt + 1 - i) / 2;
+        const int tok = s.k * c.plan.tokens + (TWO ? i * (kTile / G) : 0) + r / G;   // in the sequence
+        const bool valid = r < kTile / G * G && tok < s.seq.n;
+        const bool work = __any_sync(0xffffffffu, valid);
+        float m = -INFINITY, l = 0.f;
+        {
+            const int pos = s.seq.L - s.seq.n + tok;
+            const int low = a.window > 0 ? pos - a.window + 1 : 0;
+            // the positions up to which, and from which, all rows of the warp see every key
+            const int all_hi = __reduce_min_sync(0xffffffffu, valid ? pos : INT32_MAX);
+            const int all_lo = __reduce_max_sync(0xffffffffu, valid ? low : 0);
+            int j = s.j0 + (TWO ? 0 : i);
+            for (int t = 0; t < m_tiles; ++t, j += TWO ? 1 : 2) {
+                ok = warp_wait(sh, &sh.s_full[i], (done + t) & 1, a.status);
+                if (!ok)
+                    break;
+                tc_fence_after();
+                // V rows past the length may hold anything, and 0 times that is not 0: they are
+                // cleared where the tile is used first
+                if ((!TWO || i == 0) && (j + 1) * kTile > s.seq.L) {
+                    const uint32_t u = used + ring_v<TWO>(j - s.j0, nt);
+                    const int st = u % kAttnStages;
+                    ok = warp_wait(sh, &sh.kv_full[st], (u / kAttnStages) & 1, a.status);
+                    if (!ok)
+                        break;
+                    if (j * kTile + r >= s.seq.L) {
+#pragma unroll 1
+                        for (int q = 0; q < 16; ++q)
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                             ring + st * kAttnStageBytes + (q >> 3) * kHalfBytes + r * 128 + (q & 7) * 16),
+                                         "r"(0)
+                                         : "memory");
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                }
+                if (work) {
+                    uint32_t x[kTile];
+                    float *f = reinterpret_cast<float *>(x);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        tc_ld32(s_addr + 32 * q, x + 32 * q);
+                    tc_wait_ld();
+                    if (CAP) {
+#pragma unroll
+                        for (int e = 0; e < kTile; ++e)
+                            f[e] = capped(f[e], cap_in, cap2);
+                    }
+                    if (j * kTile + kTile - 1 > all_hi || j * kTile < all_lo) {
+                        const int top = pos - j * kTile, bottom = low - j * kTile;
+#pragma unroll
+                        for (int e = 0; e < kTile; ++e)
+                            f[e] = e <= top && e >= bottom ? f[e] : -INFINITY;
+                    }
+                    float mx[4] = {f[0], f[1], f[2], f[3]};
+#pragma unroll
+                    for (int e = 4; e + 4 < kTile; e += 8) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            mx[q] = fmaxf(mx[q], fmaxf(f[e + q], f[e + 4 + q]));
+                    }
+                    float top = fmaxf(fmaxf(fmaxf(mx[0], f[124]), fmaxf(mx[1], f[125])),
+                                      fmaxf(fmaxf(mx[2], f[126]), fmaxf(mx[3], f[127])));
+                    if (!CAP)
+                        top *= scale2;
+                    // The maximum that the weights are taken against follows the true one only
+                    // when it has grown by more than 2^8: until then the weights are at most 256, and
+                    // the accumulators need no pass over them.
+                    const bool grow = m != -INFINITY && top > m + kLazy;
+                    if (__any_sync(0xffffffffu, grow)) {
+                        ok = warp_wait(sh, &sh.o_full[i], (done + t - 1) & 1, a.status);
+                        if (!ok)
+                            break;
+                        tc_fence_after();
+                        const float f2 = grow ? ex2(m - top) : 1.f;
+                        l *= f2;
+#pragma unroll 1
+                        for (int q = 0; q < 8; ++q) {
+                            uint32_t o[16];
+                            tc_ld16(o_addr + 16 * q, o);
+                            tc_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                o[e] = __float_as_uint(__uint_as_float(o[e]) * f2);
+                            tc_st16(o_addr + 16 * q, o);
+                        }
+                    }
+                    if (grow || m == -INFINITY)
+                        m = top;
+                    const float base = m == -INFINITY ? 0.f : m;
+                    float2 sum[4] = {};
+                    // weights of keys 16 q .. 16 q + 15
+                    auto weights = [&](int q) {
+#pragma unroll
+                        for (int e = 16 * q; e < 16 * q + 16; e += 2) {
+                            float2 y = make_float2(f[e], f[e + 1]);
+                            y = CAP ? add2(y, make_float2(-base, -base))
+                                    : fma2(y, make_float2(scale2, scale2), make_float2(-base, -base));
+                            y.x = ex2(y.x);
+                            y.y = ex2(y.y);
+                            sum[e >> 1 & 3] = add2(sum[e >> 1 & 3], y);
+                            x[e >> 1] = bf16x2(y.x, y.y);
+                        }
+                    };
+                    // P takes the columns of scores that are in registers
+                    weights(0), weights(1), weights(2), weights(3);
+                    tc_st32(s_addr, x);
+                    weights(4), weights(5);
+                    tc_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(&sh.p_full[i][0]);
+                    weights(6), weights(7);
+                    tc_st32(s_addr + 32, x + 32);
+                    const float2 both = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
+                    l += both.x + both.y;
+                    tc_wait_st();
+                } else if (lane == 0) {
+                    mbar_arrive(&sh.p_full[i][0]);
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&sh.p_full[i][1]);
+            }
+        }
+        done += m_tiles;
+        if (ok && m_tiles > 0)
+            ok = warp_wait(sh, &sh.o_full[i], (done - 1) & 1, a.status);
+        tc_fence_after();
+        // ---- the rows' end: a share's part, or the output
+        const bool whole = s.j0 == s.lo && s.j1 == s.hi;
+        const size_t part = (size_t)(2 * blockIdx.x + (s.j0 == s.lo)) * c.parts.rows + (TWO ? i * kTile : 0) + r;
+        const size_t t = s.seq.t0 + tok;
+        const int head = s.hk * G + r % G;
+        // stream 1's rows join stream 0's through shared memory, 32 columns at a time
+        float *const ml = other + 32 * kTile;
+        float f0 = 1.f, f1 = 0.f;
+#pragma unroll 1
+        for (int h = 0; h < 4; ++h) {
+            if (!TWO && i == 1) {
+                // (four phases a segment, so the parities stay)
+                if (ok && (h > 0 || segs > 0))
+                    ok = warp_wait(sh, &sh.x_empty, (h & 1) ^ 1, a.status);
+                if (h == 0) {
+                    ml[r] = m;
+                    ml[kTile + r] = l;
+                }
+            }
+            uint32_t x[32];
+            float *y = reinterpret_cast<float *>(x);
+            if (work) {
+                tc_ld32(o_addr + 32 * h, x);
+                tc_wait_ld();
+            }
+            if (!TWO && i == 1) {
+                if (work && nt > 1) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        other[e * kTile + r] = y[e];
+                }
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&sh.x_full);
+                continue;
+            }
+            if (!TWO) {
+                if (ok)
+                    ok = warp_wait(sh, &sh.x_full, h & 1, a.status);
+                if (nt > 1) {
+                    if (h == 0) {
+                        const float m1 = ml[r], mm = fmaxf(m, m1), b0 = mm == -INFINITY ? 0.f : mm;
+                        f0 = ex2(m - b0);
+                        f1 = ex2(m1 - b0);
+                        l = l * f0 + ml[kTile + r] * f1;
+                        m = mm;
+                    }
+                    if (work) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            y[e] = fmaf(other[e * kTile + r], f1, y[e] * f0);
+                    }
+                }
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&sh.x_empty);
+            }
+            if (valid && ok) {
+                if (whole) {
+                    const float inv = l > 0.f ? 1.f / l : 0.f;
+                    uint16_t *const dst = a.out + t * a.out_stride + head * kD + h * 32;
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8)
+                        *reinterpret_cast<uint4 *>(dst + e) =
+                            make_uint4(bf16x2(y[e] * inv, y[e + 1] * inv), bf16x2(y[e + 2] * inv, y[e + 3] * inv),
+                                       bf16x2(y[e + 4] * inv, y[e + 5] * inv), bf16x2(y[e + 6] * inv, y[e + 7] * inv));
+                } else {
+                    float *const dst = c.parts.o + part * kD + h * 32;
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4)
+                        *reinterpret_cast<float4 *>(dst + e) = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+                }
+            }
+        }
+        if (valid && ok && (TWO || i == 0)) {
+            if (!whole)
+                c.parts.ml[part] = make_float2(m, l);
+            else if (a.lse)
+                a.lse[t * a.Hq + head] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+        }
+        used += 2 * nt;
+        ++segs;
+        tc_fence_before();
+    }
+}
+
 template <bool TWO, bool CAP>
 __global__ void __launch_bounds__(kAttnThreads, 1)
     chunk_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                            const __grid_constant__ CUtensorMap vmap, const AttnLaunch c)
 {
-    extern __shared__ unsigned char attn_smem[];
-    __shared__ AttnShared sh;
+    extern __shared__ __align__(1024) unsigned char attn_smem[];
+    AttnShared &sh = *reinterpret_cast<AttnShared *>(attn_smem + (2 + kAttnStages) * kAttnStageBytes);
     const AttnArgs &a = c.a;
     const Plan &plan = c.plan;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const uint32_t qbuf = (smem_u32(attn_smem) + 1023) & ~1023u;   // two Q tiles, then the ring
+    const uint32_t qbuf = smem_u32(attn_smem);   // 1024-byte aligned, as the swizzle wants it
     const uint32_t ring = qbuf + 2 * kAttnStageBytes;
-    const int G = a.G, tile_tokens = kTile / G, Hkv = a.cache.n_kv_heads;
+    const int Hkv = a.cache.n_kv_heads;
 
     if (tid == 0) {
         for (int s = 0; s < kAttnStages; ++s) {
@@ -374,7 +848,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         mbar_init(&sh.q_empty, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.s_full[i], 1);
-            mbar_init(&sh.p_full[i], 4);
+            mbar_init(&sh.p_full[i][0], 4);
+            mbar_init(&sh.p_full[i][1], 4);
             mbar_init(&sh.o_full[i], 1);
         }
         mbar_init(&sh.x_full, 4);
@@ -383,6 +858,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         sh.failed = 0;
         sh.bound[0] = sh.bound[1] = Place{a.B, 0, 0, 0};
+        sh.first_b = -1;
+        for (const CUtensorMap *map : {&qmap, &kmap, &vmap})
+            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
     }
     if (warp == kMmaWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sh.tmem))
@@ -392,56 +870,85 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     pdl_wait();
     pdl_trigger();
 
-    // ---- this CTA's share: the sum of all weights, then the places of its two bounds
-    long long total = 0;
-    for (int base = 0; base < a.B; base += kAttnThreads) {
-        const int b = base + tid;
-        if (b < a.B) {
-            const Seq s = sequence(a, b);
-            total += Hkv * weight(a, plan, s, blocks_of(plan, s));
-        }
+    // ---- this CTA's share: the sum of all weights, then the places of its two
+    //      bounds.  Up to 384 sequences stay in the threads' registers.
+    auto of_sequence = [&](int b, Seq &q) {
+        if (b >= a.B)
+            return 0ll;
+        q = sequence(a, b);
+        return Hkv * weight(a, plan, q, blocks_of(plan, q));
+    };
+    Seq mine{0, 0, 0};
+    const long long my_weight = of_sequence(tid, mine);
+    long long total = my_weight;
+    for (int b = tid + kAttnThreads; b < a.B; b += kAttnThreads) {
+        Seq q;
+        total += of_sequence(b, q);
     }
+    long long up = my_weight;   // of the first round: the running sum within the warp
 #pragma unroll
-    for (int o = 16; o; o >>= 1)
-        total += __shfl_xor_sync(0xffffffffu, total, o);
-    if (lane == 0)
-        sh.sums[warp] = total;
-    __syncthreads();
-    total = 0;
-    for (int i = 0; i < kAttnThreads / 32; ++i)
-        total += sh.sums[i];
-    const long long u0 = total * blockIdx.x / gridDim.x, u1 = total * (blockIdx.x + 1) / gridDim.x;
-    long long before = 0;
-    for (int base = 0; base < a.B; base += kAttnThreads) {
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, up, o);
+        if (lane >= o)
+            up += y;
+    }
+    if (a.B > kAttnThreads) {
+#pragma unroll
+        for (int o = 16; o; o >>= 1)
+            total += __shfl_xor_sync(0xffffffffu, total, o);
+        if (lane == 0)
+            sh.sums[warp] = total;
         __syncthreads();
-        const int b = base + tid;
-        long long w = 0;
-        Seq s{0, 0, 0};
-        if (b < a.B) {
-            s = sequence(a, b);
-            w = Hkv * weight(a, plan, s, blocks_of(plan, s));
+        total = 0;
+        for (int i = 0; i < kAttnThreads / 32; ++i)
+            total += sh.sums[i];
+        __syncthreads();
+    }
+    if (lane == 31)
+        sh.sums[warp] = up;
+    __syncthreads();
+    long long off = 0, round = 0;
+#pragma unroll
+    for (int i = 0; i < kAttnThreads / 32; ++i) {
+        const long long x = sh.sums[i];
+        off += i < warp ? x : 0;
+        round += x;
+    }
+    if (a.B <= kAttnThreads)
+        total = round;
+    const long long share = (long long)__umul64hi((unsigned long long)total, plan.inverse) + 1;
+    const long long u0 = min(share * blockIdx.x, total), u1 = min(share * (blockIdx.x + 1), total);
+    auto find = [&](int b, const Seq &q, long long from, long long weight_of) {
+        if (weight_of > 0 && u0 >= from && u0 < from + weight_of) {
+            sh.bound[0] = place_in(a, plan, q, b, u0 - from);
+            sh.first = q;
+            sh.first_b = b;
         }
-        long long up = w;
+        if (weight_of > 0 && u1 >= from && u1 < from + weight_of)
+            sh.bound[1] = place_in(a, plan, q, b, u1 - from);
+    };
+    find(tid, mine, off + up - my_weight, my_weight);
+    for (int base = kAttnThreads; base < a.B; base += kAttnThreads) {
+        const long long before = round;
+        Seq q{0, 0, 0};
+        const long long x = of_sequence(base + tid, q);
+        up = x;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const long long y = __shfl_up_sync(0xffffffffu, up, o);
             if (lane >= o)
                 up += y;
         }
+        __syncthreads();
         if (lane == 31)
             sh.sums[warp] = up;
         __syncthreads();
-        long long off = before;
+        off = before;
         for (int i = 0; i < kAttnThreads / 32; ++i) {
-            if (i < warp)
-                off += sh.sums[i];
-            before += sh.sums[i];
+            off += i < warp ? sh.sums[i] : 0;
+            round += sh.sums[i];
         }
-        const long long from = off + up - w;
-        if (w > 0 && u0 >= from && u0 < from + w)
-            sh.bound[0] = place_in(a, plan, s, b, u0 - from);
-        if (w > 0 && u1 >= from && u1 < from + w)
-            sh.bound[1] = place_in(a, plan, s, b, u1 - from);
+        find(base + tid, q, off + up - x, x);
     }
     tc_fence_before();
     __syncthreads();
@@ -452,404 +959,17 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         if (blockIdx.x == gridDim.x - 1)
             c.parts.bound[gridDim.x] = sh.bound[1];
     }
-    Walk w{sh.bound[0], sh.bound[1], Seq{0, 0, 0}, -1};
-    Segment s;
-    uint32_t used = 0;   // ring slots before this segment
-    uint32_t segs = 0;
-
-    if (warp == kLoadWarp) {
-        // ================= copies =================
-        bool ok = true;
-        uint32_t issued = 0, q_issued = 0;
-        const int pieces = kTile / c.chunk;   // per half
-        while (ok && next_segment(a, plan, w, s)) {
-            const int nt = s.j1 - s.j0, L = w.seq.L;
-            if (lane == 0) {
-                ok = segs == 0 || wait(sh, &sh.q_empty, (segs - 1) & 1, a.status);
-                if (ok) {
-                    const int rows = tile_tokens * G, t0 = w.seq.t0 + s.k * plan.tokens;
-                    mbar_expect_tx(&sh.q_full, (TWO ? 2 : 1) * rows * kD * 2);
-                    for (int i = 0; i < (TWO ? 2 : 1); ++i)
-                        for (int h = 0; h < 2; ++h)
-                            load_3d(qbuf + i * kAttnStageBytes + h * kHalfBytes, &qmap, h * 64, s.hk * G,
-                                    t0 + i * tile_tokens, &sh.q_full);
-                    ++q_issued;
-                }
-            }
-            ok = __shfl_sync(0xffffffffu, (int)ok, 0);
-            // the ring's order: K ahead of V by one tile (or two, one for each stream)
-            const int ahead = TWO ? 1 : 2;
-            for (int x = -ahead; x < nt && ok; ++x) {
-#pragma unroll
-                for (int isk = 0; isk < 2; ++isk) {
-                    const int t = isk ? x + ahead : x;
-                    if (t < 0 || t >= nt || !ok)
-                        continue;
-                    const uint32_t u = used + (isk ? ring_k<TWO>(t) : ring_v<TWO>(t, nt));
-                    const int st = u % kAttnStages;
-                    // rows of this lane's copy
-                    const int half = lane & 1, piece = lane >> 1, pos = (s.j0 + t) * kTile + piece * c.chunk;
-                    int z = a.cache.n_pages * Hkv, y = 0;   // outside: read as zeros
-                    if (piece < pieces && pos < L) {
-                        int page = s.b;
-                        y = pos;
-                        if (a.cache.table) {
-                            page = a.cache.table[(long long)s.b * a.cache.table_width + pos / a.cache.page_rows];
-                            y = pos % a.cache.page_rows;
-                        }
-                        if ((uint32_t)page < (uint32_t)a.cache.n_pages)
-                            z = page * Hkv + s.hk;
-                        else if (a.status)
-                            atomicOr(a.status, RETOPK_STATUS_BAD_PAGE);
-                    }
-                    int good = 1;
-                    if (lane == 0) {
-                        if (u >= kAttnStages)
-                            good = wait(sh, &sh.kv_empty[st], (u / kAttnStages - 1) & 1, a.status);
-                        if (good)
-                            mbar_expect_tx(&sh.kv_full[st], kAttnStageBytes);
-                    }
-                    ok = __shfl_sync(0xffffffffu, good, 0);
-                    if (ok) {
-                        issued = u + 1;
-                        if (piece < pieces)
-                            load_3d(ring + st * kAttnStageBytes + half * kHalfBytes + piece * c.chunk * 128,
-                                    isk ? &kmap : &vmap, half * 64, y, z, &sh.kv_full[st]);
-                    }
-                }
-            }
-            used += 2 * nt;
-            ++segs;
-        }
-        // a wait ran out: the copies in flight are waited for before the memory goes
-        if (*reinterpret_cast<volatile int *>(&sh.failed) && lane == 0) {
-            const long long t0 = clock64();
-            for (uint32_t u = issued > kAttnStages ? issued - kAttnStages : 0; u < issued; ++u)
-                while (!mbar_try_wait(&sh.kv_full[u % kAttnStages], (u / kAttnStages) & 1) && clock64() - t0 < kWaitCycles)
-                    ;
-            while (q_issued && !mbar_try_wait(&sh.q_full, (q_issued - 1) & 1) && clock64() - t0 < kWaitCycles)
-                ;
-        }
-    } else if (warp == kMmaWarp) {
-        // ================= matrix instructions =================
-        if (lane == 0) {
-            bool ok = true;
-            uint32_t done[2] = {0, 0};   // tiles of each group before this segment
-            // S_i of the segment's tile t
-            auto scores = [&](int i, int t) {
-                const uint32_t u = used + ring_k<TWO>(t);
-                const int st = u % kAttnStages;
-                if (!wait(sh, &sh.kv_full[st], (u / kAttnStages) & 1, a.status))
-                    return false;
-                tc_fence_after();
-                const uint32_t qa = qbuf + (TWO ? i * kAttnStageBytes : 0), ka = ring + st * kAttnStageBytes;
-#pragma unroll
-                for (int x = 0; x < 8; ++x) {
-                    const uint32_t o = (x >> 2) * kHalfBytes + (x & 3) * 32;
-                    mma_ss(tmem + i * kTile, operand(qa + o, 0), operand(ka + o, 0), x > 0);
-                }
-                tc_commit(&sh.s_full[i]);
-                if (!TWO || i == 1)
-                    tc_commit(&sh.kv_empty[st]);
-                return true;
-            };
-            while (ok && next_segment(a, plan, w, s)) {
-                const int nt = s.j1 - s.j0;
-                const int m[2] = {TWO ? nt : (nt + 1) / 2, TWO ? nt : nt / 2};
-                auto tile = [&](int i, int t) { return TWO ? t : 2 * t + i; };
-                ok = wait(sh, &sh.q_full, segs & 1, a.status);
-                for (int i = 0; i < 2 && ok; ++i)
-                    if (m[i] > 0)
-                        ok = scores(i, tile(i, 0));
-                if (ok && m[0] == 1)
-                    tc_commit(&sh.q_empty);
-                for (int t = 0; t < m[0] && ok; ++t) {
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        if (t >= m[i] || !ok)
-                            continue;
-                        const uint32_t u = used + ring_v<TWO>(tile(i, t), nt);
-                        const int st = u % kAttnStages;
-                        ok = wait(sh, &sh.kv_full[st], (u / kAttnStages) & 1, a.status) &&
-                             wait(sh, &sh.p_full[i], (done[i] + t) & 1, a.status);
-                        if (!ok)
-                            continue;
-                        tc_fence_after();
-                        const uint32_t va = ring + st * kAttnStageBytes;
-#pragma unroll
-                        for (int x = 0; x < 8; ++x)
-                            mma_ts(tmem + (2 + i) * kTile, tmem + i * kTile + x * 8, operand(va + x * 2048, kHalfBytes),
-                                   t > 0 || x > 0);
-                        tc_commit(&sh.o_full[i]);
-                        if (!TWO || i == 1)
-                            tc_commit(&sh.kv_empty[st]);
-                        if (t + 1 < m[i])
-                            ok = scores(i, tile(i, t + 1));
-                    }
-                    // the last use of Q
-                    if (ok && t + 2 == m[0])
-                        tc_commit(&sh.q_empty);
-                }
-                used += 2 * nt;
-                done[0] += m[0];
-                done[1] += m[1];
-                ++segs;
-            }
-            if (!ok) {   // a wait ran out: the instructions in flight end before the tensor memory goes
-                tc_commit(&sh.drained);
-                const long long t0 = clock64();
-                while (!mbar_try_wait(&sh.drained, 0) && clock64() - t0 < kWaitCycles)
-                    ;
-            }
-        }
-        __syncwarp();
-    } else if (warp < kMmaWarp) {
-        // ================= softmax =================
-        const int i = warp >> 2, r = tid & (kTile - 1);
-        const uint32_t quarter = (uint32_t)(warp & 3) << 21;   // this warp's lanes of the tensor memory
-        const uint32_t s_addr = tmem + i * kTile + quarter, o_addr = tmem + (2 + i) * kTile + quarter;
-        const float scale2 = a.scale * 1.4426950408889634f;     // scores in powers of two
-        const float cap2 = a.softcap * 1.4426950408889634f;
-        const float cap_in = CAP ? 2.f * scale2 / a.softcap : 0.f;   // e^2y = 2^(cap_in s)
-        bool ok = true;
-        uint32_t done = 0;
-        while (ok && next_segment(a, plan, w, s)) {
-            const int nt = s.j1 - s.j0, m_tiles = TWO ? nt : (nt + 1 - i) / 2;
-            const int tok = s.k * plan.tokens + (TWO ? i * tile_tokens : 0) + r / G;   // in the sequence
-            const bool valid = r < tile_tokens * G && tok < w.seq.n;
-            const bool work = __any_sync(0xffffffffu, valid);
-            const int pos = w.seq.L - w.seq.n + tok;
-            const int low = a.window > 0 ? pos - a.window + 1 : 0;
-            // every key of tiles [lowest / 128 rounded up, highest / 128) is seen by all rows of the warp
-            const int all_hi = __reduce_min_sync(0xffffffffu, valid ? pos : INT32_MAX);
-            const int all_lo = __reduce_max_sync(0xffffffffu, valid ? low : 0);
-            float m = -INFINITY, l = 0.f;
-            for (int t = 0; t < m_tiles && ok; ++t) {
-                const int j = s.j0 + (TWO ? t : 2 * t + i);
-                ok = warp_wait(sh, &sh.s_full[i], (done + t) & 1, a.status);
-                if (!ok)
-                    break;
-                tc_fence_after();
-                if (work) {
-                    // The scores are read twice, half a row at a time (64 registers): for the maximum, then for the weights.
-                    const bool part = j * kTile + kTile - 1 > all_hi || j * kTile < all_lo;
-                    const int top = pos - j * kTile, bottom = low - j * kTile;
-                    float mx = -INFINITY;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t x[64];
-                        tc_ld32(s_addr + 64 * h, x);
-                        tc_ld32(s_addr + 64 * h + 32, x + 32);
-                        tc_wait_ld();
-                        float *f = reinterpret_cast<float *>(x);
-                        if (part) {
-#pragma unroll
-                            for (int e = 0; e < 64; ++e)
-                                f[e] = 64 * h + e <= top && 64 * h + e >= bottom ? f[e] : -INFINITY;
-                        }
-#pragma unroll
-                        for (int e = 0; e < 64; e += 2)
-                            mx = fmaxf(mx, fmaxf(f[e], f[e + 1]));
-                    }
-                    // (the cap does not change the order of scores)
-                    mx = CAP && mx != -INFINITY ? capped(mx, cap_in, cap2) : mx * scale2;
-                    // The maximum that the weights are taken against follows the true one only
-                    // when it has grown by more than 2^8: until then the weights are at most 256, and the
-                    // accumulators need no pass over them.
-                    const bool grow = m != -INFINITY && mx > m + kLazy;
-                    if (__any_sync(0xffffffffu, grow)) {
-                        ok = warp_wait(sh, &sh.o_full[i], (done + t - 1) & 1, a.status);
-                        if (!ok)
-                            break;
-                        tc_fence_after();
-                        const float f2 = grow ? ex2(m - mx) : 1.f;
-                        l *= f2;
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            uint32_t o[32];
-                            tc_ld32(o_addr + 32 * q, o);
-                            tc_wait_ld();
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                o[e] = __float_as_uint(__uint_as_float(o[e]) * f2);
-                            tc_st32(o_addr + 32 * q, o);
-                        }
-                    }
-                    if (grow || m == -INFINITY)
-                        m = mx;
-                    const float base = m == -INFINITY ? 0.f : m;
-                    float sum[4] = {};
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t x[64];
-                        tc_ld32(s_addr + 64 * h, x);
-                        tc_ld32(s_addr + 64 * h + 32, x + 32);
-                        tc_wait_ld();
-                        float *f = reinterpret_cast<float *>(x);
-#pragma unroll
-                        for (int e = 0; e < 64; ++e)
-                            f[e] = CAP ? capped(f[e], cap_in, cap2) - base : fmaf(f[e], scale2, -base);
-                        if (part) {
-#pragma unroll
-                            for (int e = 0; e < 64; ++e)
-                                f[e] = 64 * h + e <= top && 64 * h + e >= bottom ? f[e] : -INFINITY;
-                        }
-#pragma unroll
-                        for (int e = 0; e < 64; e += 2) {
-                            f[e] = ex2(f[e]);
-                            f[e + 1] = ex2(f[e + 1]);
-                            sum[(e >> 1) & 3] += f[e] + f[e + 1];
-                            x[e >> 1] = bf16x2(f[e], f[e + 1]);
-                        }
-                        // P takes the columns of scores that are done with
-                        tc_st32(s_addr + 32 * h, x);
-                    }
-                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                    tc_wait_st();
-                }
-                // V rows past the length may hold anything, and 0 times that is not 0: they are
-                // cleared where the tile is used first
-                if ((!TWO || i == 0) && (j + 1) * kTile > w.seq.L) {
-                    const uint32_t u = used + ring_v<TWO>(j - s.j0, nt);
-                    const int st = u % kAttnStages;
-                    ok = warp_wait(sh, &sh.kv_full[st], (u / kAttnStages) & 1, a.status);
-                    if (!ok)
-                        break;
-                    if (j * kTile + r >= w.seq.L) {
-#pragma unroll
-                        for (int q = 0; q < 16; ++q)
-                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
-                                             ring + st * kAttnStageBytes + (q >> 3) * kHalfBytes + r * 128 + (q & 7) * 16),
-                                         "r"(0)
-                                         : "memory");
-                    }
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(&sh.p_full[i]);
-            }
-            done += m_tiles;
-            if (ok && m_tiles > 0)
-                ok = warp_wait(sh, &sh.o_full[i], (done - 1) & 1, a.status);
-            tc_fence_after();
-            // ---- the rows' end: a share's part, or the output
-            const bool whole = s.j0 == s.lo && s.j1 == s.hi;
-            if (!TWO) {
-                // stream 1's half joins stream 0's through shared memory, 64 columns at a time
-                float *const other = reinterpret_cast<float *>(attn_smem + (qbuf - smem_u32(attn_smem)) + kAttnStageBytes);
-                float f0 = 1.f, f1 = 0.f;
-                for (int h = 0; h < 2; ++h) {
-                    // (each of the two halves is one phase, so a segment takes two and the parities stay)
-                    if (i == 1 && ok && (h == 1 || segs > 0))
-                        ok = warp_wait(sh, &sh.x_empty, h ^ 1, a.status);
-                    if (h == 0 && i == 1 && ok) {
-                        sh.ml[0][r] = m;
-                        sh.ml[1][r] = l;
-                    }
-                    if (i == 1 && work && ok) {
-#pragma unroll
-                        for (int q = 0; q < 2; ++q) {
-                            uint32_t o[32];
-                            tc_ld32(o_addr + h * 64 + 32 * q, o);
-                            tc_wait_ld();
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                other[(q * 32 + e) * kTile + r] = __uint_as_float(o[e]);
-                        }
-                    }
-                    if (i == 1) {
-                        __syncwarp();
-                        if (lane == 0)
-                            mbar_arrive(&sh.x_full);
-                    } else if (ok) {
-                        ok = warp_wait(sh, &sh.x_full, h, a.status);
-                    }
-                    if (i == 0 && work && ok) {
-                        if (h == 0) {
-                            const float m1 = sh.ml[0][r], mm = fmaxf(m, m1), b0 = mm == -INFINITY ? 0.f : mm;
-                            f0 = ex2(m - b0);
-                            f1 = ex2(m1 - b0);
-                            l = l * f0 + (nt > 1 ? sh.ml[1][r] * f1 : 0.f);
-                            m = mm;
-                        }
-                        const float inv = whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
-#pragma unroll
-                        for (int q = 0; q < 2; ++q) {
-                            uint32_t o[32];
-                            tc_ld32(o_addr + h * 64 + 32 * q, o);
-                            tc_wait_ld();
-                            float y[32];
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) {
-                                y[e] = __uint_as_float(o[e]) * f0;
-                                if (nt > 1)
-                                    y[e] = fmaf(other[(q * 32 + e) * kTile + r], f1, y[e]);
-                                y[e] *= inv;
-                            }
-                            if (!valid)
-                                continue;
-                            const int col = h * 64 + q * 32;
-                            if (whole) {
-                                uint16_t *dst = a.out + (w.seq.t0 + tok) * a.out_stride + (s.hk * G + r % G) * kD + col;
-#pragma unroll
-                                for (int e = 0; e < 32; e += 8)
-                                    *reinterpret_cast<uint4 *>(dst + e) =
-                                        make_uint4(bf16x2(y[e], y[e + 1]), bf16x2(y[e + 2], y[e + 3]),
-                                                   bf16x2(y[e + 4], y[e + 5]), bf16x2(y[e + 6], y[e + 7]));
-                            } else {
-                                float *dst = c.parts.o + ((size_t)(2 * blockIdx.x + (s.j0 == s.lo)) * c.parts.rows + r) * kD + col;
-#pragma unroll
-                                for (int e = 0; e < 32; e += 4)
-                                    *reinterpret_cast<float4 *>(dst + e) = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
-                            }
-                        }
-                    }
-                    if (i == 0) {
-                        __syncwarp();
-                        if (lane == 0)
-                            mbar_arrive(&sh.x_empty);
-                    }
-                }
-            } else if (work && ok) {
-                const float inv = whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    uint32_t o[32];
-                    tc_ld32(o_addr + 32 * q, o);
-                    tc_wait_ld();
-                    if (!valid)
-                        continue;
-                    float *y = reinterpret_cast<float *>(o);
-                    if (whole) {
-                        uint16_t *dst = a.out + (w.seq.t0 + tok) * a.out_stride + (s.hk * G + r % G) * kD + q * 32;
-#pragma unroll
-                        for (int e = 0; e < 32; e += 8)
-                            *reinterpret_cast<uint4 *>(dst + e) =
-                                make_uint4(bf16x2(y[e] * inv, y[e + 1] * inv), bf16x2(y[e + 2] * inv, y[e + 3] * inv),
-                                           bf16x2(y[e + 4] * inv, y[e + 5] * inv), bf16x2(y[e + 6] * inv, y[e + 7] * inv));
-                    } else {
-                        float *dst = c.parts.o +
-                                     ((size_t)(2 * blockIdx.x + (s.j0 == s.lo)) * c.parts.rows + i * kTile + r) * kD + q * 32;
-#pragma unroll
-                        for (int e = 0; e < 32; e += 4)
-                            *reinterpret_cast<float4 *>(dst + e) = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
-                    }
-                }
-            }
-            if (valid && ok && (TWO || i == 0)) {
-                if (!whole)
-                    c.parts.ml[(size_t)(2 * blockIdx.x + (s.j0 == s.lo)) * c.parts.rows + (TWO ? i * kTile : 0) + r] =
-                        make_float2(m, l);
-                else if (a.lse)
-                    a.lse[(size_t)(w.seq.t0 + tok) * a.Hq + s.hk * G + r % G] =
-                        l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
-            }
-            used += 2 * nt;
-            ++segs;
-            tc_fence_before();
-        }
+    if (lane == 0 && warp <= kLoadWarp)
+        sh.walk[warp].w = Walk{sh.bound[0], sh.bound[1], sh.first, sh.first_b};
+    if (warp < kMmaWarp) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+        softmax<TWO, CAP>(c, sh, sh.walk[warp], reinterpret_cast<float *>(attn_smem + kAttnStageBytes), ring, tmem, warp, lane);
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        if (warp == kLoadWarp)
+            copies<TWO>(c, sh, sh.walk[warp], qmap, kmap, vmap, qbuf, ring, lane);
+        else if (warp == kMmaWarp)
+            matrices<TWO>(c, sh, sh.walk[warp], qbuf, ring, tmem, lane);
     }
     tc_fence_before();
     __syncthreads();
@@ -870,9 +990,12 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnLaunch c, int share
     if (at.cut == 0 || (same_item(at, prev) && prev.cut > 0))
         return;
     // parts: share x - 1's part 1, then part 0 of shares x, x + 1, ... while they begin in the item
-    int end = x + 1;
-    while (end < shares && same_item(c.parts.bound[end], at))
-        ++end;
+    int end = x + 1, more;
+    do {
+        const int y = end + (int)threadIdx.x;
+        more = __syncthreads_count(y < shares && same_item(c.parts.bound[y], at));
+        end += more;
+    } while (more == 256);
     const Seq s = sequence(a, at.b);
     const int tile_tokens = kTile / a.G, per_tile = tile_tokens * a.G;
     const int rows = TWO ? kTile + per_tile : per_tile;
@@ -910,13 +1033,12 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnLaunch c, int share
 #pragma unroll 8
             for (int i = 0; i < most; ++i) {
                 const float fi = __shfl_sync(0xffffffffu, f, i);
-                if (fi != 0.f) {   // (parts without a row's keys, and those that are not there)
-                    const float4 o = reinterpret_cast<const float4 *>(c.parts.o + index(i0 + i) * kD)[lane];
-                    acc.x = fmaf(fi, o.x, acc.x);
-                    acc.y = fmaf(fi, o.y, acc.y);
-                    acc.z = fmaf(fi, o.z, acc.z);
-                    acc.w = fmaf(fi, o.w, acc.w);
-                }
+                const float4 o = reinterpret_cast<const float4 *>(c.parts.o + index(i0 + i) * kD)[lane];
+                // (parts without a row's keys, and those that are not there, may hold anything)
+                acc.x = fi != 0.f ? fmaf(fi, o.x, acc.x) : acc.x;
+                acc.y = fi != 0.f ? fmaf(fi, o.y, acc.y) : acc.y;
+                acc.z = fi != 0.f ? fmaf(fi, o.z, acc.z) : acc.z;
+                acc.w = fi != 0.f ? fmaf(fi, o.w, acc.w) : acc.w;
             }
         }
         l = warp_sum(l);
@@ -989,6 +1111,7 @@ cudaError_t launch_chunk_attention(const AttnArgs &a, cudaStream_t st)
     const bool two = two_tiles(a.T, a.B, a.G);
     c.plan.tokens = two ? 2 * tokens : tokens;
     c.plan.overhead = two ? 128 : 256;
+    c.plan.inverse = ~0ull / (unsigned long long)sm_count();
     carve(a.T, a.B, a.Hq, Hkv, static_cast<char *>(a.ws), &c.parts);
     c.chunk = kTile;
     if (a.cache.table)
