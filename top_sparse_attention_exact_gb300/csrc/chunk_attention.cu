@@ -264,7 +264,6 @@ __device__ __forceinline__ bool warp_wait(AttnShared &sh, uint64_t *bar, uint32_
 // ---- tensor memory and matrix instructions (inline PTX) -------------------------
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ void tc_commit(uint64_t *bar)
@@ -275,6 +274,8 @@ __device__ __forceinline__ void tc_commit(uint64_t *bar)
 
 #define R4(x, i) "=r"(x[i]), "=r"(x[i + 1]), "=r"(x[i + 2]), "=r"(x[i + 3])
 #define R16(x, i) R4(x, i), R4(x, i + 4), R4(x, i + 8), R4(x, i + 12)
+#define RW4(x, i) "+r"(x[i]), "+r"(x[i + 1]), "+r"(x[i + 2]), "+r"(x[i + 3])
+#define RW16(x, i) RW4(x, i), RW4(x, i + 4), RW4(x, i + 8), RW4(x, i + 12)
 #define W4(x, i) "r"(x[i]), "r"(x[i + 1]), "r"(x[i + 2]), "r"(x[i + 3])
 #define W16(x, i) W4(x, i), W4(x, i + 4), W4(x, i + 8), W4(x, i + 12)
 
@@ -286,6 +287,16 @@ __device__ __forceinline__ void tc_ld32(uint32_t addr, uint32_t *x)
         "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
         : R16(x, 0), R16(x, 16)
         : "r"(addr));
+}
+
+// The wait for loads, with the registers that they fill: nothing may read these before it.
+__device__ __forceinline__ void tc_wait_ld32(uint32_t *x)
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : RW16(x, 0), RW16(x, 16)::"memory");
+}
+__device__ __forceinline__ void tc_wait_ld16(uint32_t *x)
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : RW16(x, 0)::"memory");
 }
 
 __device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t *x)
@@ -313,39 +324,47 @@ __device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t *x)
 }
 #undef R4
 #undef R16
+#undef RW4
+#undef RW16
 #undef W4
 #undef W16
 
 // Shared-memory operand descriptor, 128-byte swizzle.  K-major operands (Q, K:
 // [half of d][row][64]) step 1024 bytes from one 8-row group to the next; V is read
 // MN-major ([half of d][key][64], d being N): 1024 bytes from one group of 8 keys
-// to the next, a half's size from one block of 64 columns to the next.
-__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lead)
-{
-    return (uint64_t)((addr & 0x3ffff) >> 4) | (uint64_t)(lead >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 | 1ull << 46 |
-           2ull << 61;
-}
+// to the next, a half's size from one block of 64 columns to the next.  The address
+// is all that changes, in the low word.
+constexpr uint32_t kDescHigh = (1024 >> 4) | 1u << 14 | 2u << 29;
+constexpr uint32_t kDescLead = (uint32_t)(kHalfBytes >> 4) << 16;   // V's block of columns
 
 // fp32 accumulators, bf16 operands, M = N = 128.
 constexpr uint32_t kIdescS = 1u << 4 | 1u << 7 | 1u << 10 | (kTile / 8) << 17 | (kTile / 16) << 24;
 constexpr uint32_t kIdescO = kIdescS | 1u << 16;   // B (V) is MN-major
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t accumulate)
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t accumulate)
 {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-        "l"(a), "l"(b), "r"(kIdescS), "r"(accumulate)
+        "{\n .reg .pred p;\n .reg .b64 x, y;\n setp.ne.u32 p, %5, 0;\n mov.b64 x, {%1, %3};\n mov.b64 y, {%2, %3};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, p;\n}\n" ::"r"(d),
+        "r"(a), "r"(b), "r"(kDescHigh), "r"(kIdescS), "r"(accumulate)
         : "memory");
 }
 
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t accumulate)
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t accumulate)
 {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-        "r"(a), "l"(b), "r"(kIdescO), "r"(accumulate)
+        "{\n .reg .pred p;\n .reg .b64 y;\n setp.ne.u32 p, %5, 0;\n mov.b64 y, {%2, %3};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n}\n" ::"r"(d),
+        "r"(a), "r"(b), "r"(kDescHigh), "r"(kIdescO), "r"(accumulate)
         : "memory");
+}
+
+// One lane of the (converged) warp, the same each time.
+__device__ __forceinline__ bool elected()
+{
+    uint32_t x;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(x));
+    return x != 0;
 }
 
 __device__ __forceinline__ void load_3d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar)
@@ -369,6 +388,13 @@ __device__ __forceinline__ float rcp(float x)
     float y;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
 }
 
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
@@ -507,85 +533,89 @@ __device__ __forceinline__ void copies(const AttnLaunch &c, AttnShared &sh, Warp
     __syncwarp();
 }
 
-// ---- the matrix instructions: one lane's ----------------------------------------------
+// ---- the matrix instructions ------------------------------------------------------------
+// The whole warp walks and waits, one lane issues: what addresses the operands
+// stays the same for all lanes, so that it can live in uniform registers (an
+// instruction issued from a divergent branch cost 110 cycles in place of 64).
 template <bool TWO>
 __device__ __forceinline__ void matrices(const AttnLaunch &c, AttnShared &sh, WarpWalk &walk, uint32_t qbuf, uint32_t ring,
-                                         uint32_t tmem, int lane)
+                                         uint32_t tmem_any)
 {
     const AttnArgs &a = c.a;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_any, 0);
     bool ok = true;
-    uint32_t used = 0, segs = 0, done[2] = {0, 0};   // done: tiles of each group before this segment
+    uint32_t used = 0, segs = 0, done0 = 0, done1 = 0;   // done: tiles of each group before this segment
     // S_i of the segment's tile t
     auto scores = [&](int i, int t) {
-        const uint32_t u = used + ring_k<TWO>(t);
-        const int st = u % kAttnStages;
-        if (!wait(sh, &sh.kv_full[st], (u / kAttnStages) & 1, a.status))
+        const uint32_t u = used + ring_k<TWO>(t), st = u % kAttnStages;
+        if (!warp_wait(sh, &sh.kv_full[st], (u / kAttnStages) & 1, a.status))
             return false;
         tc_fence_after();
-        const uint32_t qa = qbuf + (TWO ? i * kAttnStageBytes : 0), ka = ring + st * kAttnStageBytes;
+        if (elected()) {
+            const uint32_t q = (qbuf + (TWO ? i * kAttnStageBytes : 0)) >> 4, k = (ring + st * kAttnStageBytes) >> 4;
 #pragma unroll
-        for (int x = 0; x < 8; ++x) {
-            const uint32_t o = (x >> 2) * kHalfBytes + (x & 3) * 32;
-            mma_ss(tmem + i * kTile, operand(qa + o, 0), operand(ka + o, 0), x > 0);
+            for (int x = 0; x < 8; ++x) {
+                const uint32_t o = ((x >> 2) * kHalfBytes + (x & 3) * 32) >> 4;
+                mma_ss(tmem + i * kTile, q + o, k + o, x > 0);
+            }
+            tc_commit(&sh.s_full[i]);
+            if (!TWO || i == 1)
+                tc_commit(&sh.kv_empty[st]);
         }
-        tc_commit(&sh.s_full[i]);
-        if (!TWO || i == 1)
-            tc_commit(&sh.kv_empty[st]);
+        __syncwarp();
         return true;
     };
-    while (__any_sync(0xffffffffu, ok) && next_of_warp(a, c.plan, walk)) {
-        if (lane == 0) {
-            const int nt = walk.s.j1 - walk.s.j0;
-            const int m[2] = {TWO ? nt : (nt + 1) / 2, TWO ? nt : nt / 2};
-            auto tile = [&](int i, int t) { return TWO ? t : 2 * t + i; };
-            ok = wait(sh, &sh.q_full, segs & 1, a.status);
-            for (int i = 0; i < 2 && ok; ++i)
-                if (m[i] > 0)
-                    ok = scores(i, tile(i, 0));
-            if (ok && m[0] == 1)
-                tc_commit(&sh.q_empty);
-            for (int t = 0; t < m[0] && ok; ++t) {
+    while (ok && next_of_warp(a, c.plan, walk)) {
+        const int nt = __shfl_sync(0xffffffffu, walk.s.j1 - walk.s.j0, 0);
+        const int m0 = TWO ? nt : (nt + 1) / 2, m1 = TWO ? nt : nt / 2;
+        auto tile = [&](int i, int t) { return TWO ? t : 2 * t + i; };
+        ok = warp_wait(sh, &sh.q_full, segs & 1, a.status);
+        if (ok)
+            ok = scores(0, tile(0, 0));
+        if (ok && m1 > 0)
+            ok = scores(1, tile(1, 0));
+        if (ok && m0 == 1 && elected())
+            tc_commit(&sh.q_empty);
+        for (int t = 0; t < m0 && ok; ++t) {
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    if (t >= m[i] || !ok)
-                        continue;
-                    const uint32_t u = used + ring_v<TWO>(tile(i, t), nt);
-                    const int st = u % kAttnStages;
-                    const uint32_t va = ring + st * kAttnStageBytes;
-                    ok = wait(sh, &sh.kv_full[st], (u / kAttnStages) & 1, a.status);
-                    // P comes in halves, so that the product begins while the second is made
+            for (int i = 0; i < 2; ++i) {
+                if (t >= (i ? m1 : m0) || !ok)
+                    continue;
+                const uint32_t u = used + ring_v<TWO>(tile(i, t), nt), st = u % kAttnStages;
+                ok = warp_wait(sh, &sh.kv_full[st], (u / kAttnStages) & 1, a.status);
+                // P comes in halves, so that the product begins while the second is made
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        ok = ok && wait(sh, &sh.p_full[i][h], (done[i] + t) & 1, a.status);
-                        if (!ok)
-                            break;
-                        tc_fence_after();
+                for (int h = 0; h < 2; ++h) {
+                    ok = ok && warp_wait(sh, &sh.p_full[i][h], ((i ? done1 : done0) + t) & 1, a.status);
+                    if (!ok)
+                        break;
+                    tc_fence_after();
+                    if (elected()) {
+                        const uint32_t v = (ring + st * kAttnStageBytes) >> 4 | kDescLead;
 #pragma unroll
                         for (int x = 4 * h; x < 4 * h + 4; ++x)
-                            mma_ts(tmem + (2 + i) * kTile, tmem + i * kTile + x * 8, operand(va + x * 2048, kHalfBytes),
-                                   t > 0 || x > 0);
+                            mma_ts(tmem + (2 + i) * kTile, tmem + i * kTile + x * 8, v + (x * 2048 >> 4), t > 0 || x > 0);
+                        if (h == 1) {
+                            tc_commit(&sh.o_full[i]);
+                            if (!TWO || i == 1)
+                                tc_commit(&sh.kv_empty[st]);
+                        }
                     }
-                    if (!ok)
-                        continue;
-                    tc_commit(&sh.o_full[i]);
-                    if (!TWO || i == 1)
-                        tc_commit(&sh.kv_empty[st]);
-                    if (t + 1 < m[i])
-                        ok = scores(i, tile(i, t + 1));
+                    __syncwarp();
                 }
-                // the last use of Q
-                if (ok && t + 2 == m[0])
-                    tc_commit(&sh.q_empty);
+                if (ok && t + 1 < (i ? m1 : m0))
+                    ok = scores(i, tile(i, t + 1));
             }
-            used += 2 * nt;
-            done[0] += m[0];
-            done[1] += m[1];
-            ++segs;
-        } else {
-            ok = false;   // lane 0 alone says whether there is more to do
+            // the last use of Q
+            if (ok && t + 2 == m0 && elected())
+                tc_commit(&sh.q_empty);
         }
+        used += 2 * nt;
+        done0 += m0;
+        done1 += m1;
+        ++segs;
     }
-    if (lane == 0 && !ok) {   // a wait ran out: the instructions in flight end before the tensor memory goes
+    if (!ok && elected()) {   // a wait ran out: the instructions in flight end before the tensor memory goes
         tc_commit(&sh.drained);
         const long long t0 = clock64();
         while (!mbar_try_wait(&sh.drained, 0) && clock64() - t0 < kWaitCycles)
@@ -647,32 +677,31 @@ __device__ __forceinline__ void softmax(const AttnLaunch &c, AttnShared &sh, War
                 if (work) {
                     uint32_t x[kTile];
                     float *f = reinterpret_cast<float *>(x);
+                    // the maximum of each quarter is taken while the next is on its way (of the raw scores:
+                    // neither scale nor cap changes their order)
+                    const bool part = j * kTile + kTile - 1 > all_hi || j * kTile < all_lo;
+                    const int last = pos - j * kTile, first = low - j * kTile;
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    tc_ld32(s_addr, x);
 #pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        tc_ld32(s_addr + 32 * q, x + 32 * q);
-                    tc_wait_ld();
-                    if (CAP) {
+                    for (int q = 0; q < 4; ++q) {
+                        tc_wait_ld32(x + 32 * q);
+                        if (q < 3)
+                            tc_ld32(s_addr + 32 * (q + 1), x + 32 * (q + 1));
+                        if (part) {
 #pragma unroll
-                        for (int e = 0; e < kTile; ++e)
-                            f[e] = capped(f[e], cap_in, cap2);
+                            for (int e = 32 * q; e < 32 * q + 32; ++e)
+                                f[e] = e <= last && e >= first ? f[e] : -INFINITY;
+                        }
+#pragma unroll
+                        for (int e = 32 * q; e < 32 * q + 32; e += 8) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                mx[k] = max3(mx[k], f[e + k], f[e + 4 + k]);
+                        }
                     }
-                    if (j * kTile + kTile - 1 > all_hi || j * kTile < all_lo) {
-                        const int top = pos - j * kTile, bottom = low - j * kTile;
-#pragma unroll
-                        for (int e = 0; e < kTile; ++e)
-                            f[e] = e <= top && e >= bottom ? f[e] : -INFINITY;
-                    }
-                    float mx[4] = {f[0], f[1], f[2], f[3]};
-#pragma unroll
-                    for (int e = 4; e + 4 < kTile; e += 8) {
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            mx[q] = fmaxf(mx[q], fmaxf(f[e + q], f[e + 4 + q]));
-                    }
-                    float top = fmaxf(fmaxf(fmaxf(mx[0], f[124]), fmaxf(mx[1], f[125])),
-                                      fmaxf(fmaxf(mx[2], f[126]), fmaxf(mx[3], f[127])));
-                    if (!CAP)
-                        top *= scale2;
+                    float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
+                    top = !CAP ? top * scale2 : top == -INFINITY ? top : capped(top, cap_in, cap2);
                     // The maximum that the weights are taken against follows the true one only
                     // when it has grown by more than 2^8: until then the weights are at most 256, and
                     // the accumulators need no pass over them.
@@ -688,7 +717,7 @@ __device__ __forceinline__ void softmax(const AttnLaunch &c, AttnShared &sh, War
                         for (int q = 0; q < 8; ++q) {
                             uint32_t o[16];
                             tc_ld16(o_addr + 16 * q, o);
-                            tc_wait_ld();
+                            tc_wait_ld16(o);
 #pragma unroll
                             for (int e = 0; e < 16; ++e)
                                 o[e] = __float_as_uint(__uint_as_float(o[e]) * f2);
@@ -698,32 +727,56 @@ __device__ __forceinline__ void softmax(const AttnLaunch &c, AttnShared &sh, War
                     if (grow || m == -INFINITY)
                         m = top;
                     const float base = m == -INFINITY ? 0.f : m;
-                    float2 sum[4] = {};
-                    // weights of keys 16 q .. 16 q + 15
-                    auto weights = [&](int q) {
+                    // The weights, two keys at a time, in three steps that overlap: the exponents of
+                    // pair n + kLead, the exponentials of pair n, the sum and the rounding of pair n - kLead.
+                    float2 sum[2] = {};
+                    const float2 mul = make_float2(scale2, scale2), add = CAP ? make_float2(cap2 - base, cap2 - base) : make_float2(-base, -base);
+                    constexpr int kLead = 4, kPairs = kTile / 2;
 #pragma unroll
-                        for (int e = 16 * q; e < 16 * q + 16; e += 2) {
-                            float2 y = make_float2(f[e], f[e + 1]);
-                            y = CAP ? add2(y, make_float2(-base, -base))
-                                    : fma2(y, make_float2(scale2, scale2), make_float2(-base, -base));
-                            y.x = ex2(y.x);
-                            y.y = ex2(y.y);
-                            sum[e >> 1 & 3] = add2(sum[e >> 1 & 3], y);
-                            x[e >> 1] = bf16x2(y.x, y.y);
+                    for (int n = -kLead; n < kPairs + kLead; ++n) {
+                        if (n + kLead < kPairs) {
+                            const int e = 2 * (n + kLead);
+                            if (!CAP) {
+                                const float2 y = fma2(make_float2(f[e], f[e + 1]), mul, add);
+                                f[e] = y.x, f[e + 1] = y.y;
+                            } else {   // 1 + e^2y (beyond 2^60 the cap is reached)
+                                f[e] = 1.f + ex2(fminf(f[e] * cap_in, 60.f));
+                                f[e + 1] = 1.f + ex2(fminf(f[e + 1] * cap_in, 60.f));
+                            }
                         }
-                    };
-                    // P takes the columns of scores that are in registers
-                    weights(0), weights(1), weights(2), weights(3);
-                    tc_st32(s_addr, x);
-                    weights(4), weights(5);
-                    tc_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive(&sh.p_full[i][0]);
-                    weights(6), weights(7);
+                        if (n >= 0 && n < kPairs) {
+                            const int e = 2 * n;
+                            if (CAP) {   // both reciprocals from one
+                                const float both = rcp(f[e] * f[e + 1]), r0 = both * f[e + 1], r1 = both * f[e];
+                                f[e] = fmaf(-2.f * cap2, r0, add.x);
+                                f[e + 1] = fmaf(-2.f * cap2, r1, add.x);
+                                if (part) {
+                                    f[e] = e <= last && e >= first ? f[e] : -INFINITY;
+                                    f[e + 1] = e + 1 <= last && e + 1 >= first ? f[e + 1] : -INFINITY;
+                                }
+                            }
+                            f[e] = ex2(f[e]);
+                            f[e + 1] = ex2(f[e + 1]);
+                        }
+                        if (n >= kLead) {
+                            const int e = 2 * (n - kLead);
+                            sum[n & 1] = add2(sum[n & 1], make_float2(f[e], f[e + 1]));
+                            x[e >> 1] = bf16x2(f[e], f[e + 1]);
+                        }
+                        // P takes the columns of scores that are in registers; the first half is handed
+                        // over while the second is made
+                        if (n == kPairs / 2 + kLead - 1)
+                            tc_st32(s_addr, x);
+                        if (n == kPairs * 3 / 4) {
+                            tc_wait_st();
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0)
+                                mbar_arrive(&sh.p_full[i][0]);
+                        }
+                    }
                     tc_st32(s_addr + 32, x + 32);
-                    const float2 both = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
+                    const float2 both = add2(sum[0], sum[1]);
                     l += both.x + both.y;
                     tc_wait_st();
                 } else if (lane == 0) {
@@ -762,7 +815,7 @@ __device__ __forceinline__ void softmax(const AttnLaunch &c, AttnShared &sh, War
             float *y = reinterpret_cast<float *>(x);
             if (work) {
                 tc_ld32(o_addr + 32 * h, x);
-                tc_wait_ld();
+                tc_wait_ld32(x);
             }
             if (!TWO && i == 1) {
                 if (work && nt > 1) {
@@ -969,7 +1022,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         if (warp == kLoadWarp)
             copies<TWO>(c, sh, sh.walk[warp], qmap, kmap, vmap, qbuf, ring, lane);
         else if (warp == kMmaWarp)
-            matrices<TWO>(c, sh, sh.walk[warp], qbuf, ring, tmem, lane);
+            matrices<TWO>(c, sh, sh.walk[warp], qbuf, ring, tmem);
     }
     tc_fence_before();
     __syncthreads();
