@@ -222,7 +222,7 @@ struct AttnShared {
     uint64_t q_full, q_empty;
     uint64_t s_full[2], p_full[2][2], o_full[2];
     uint64_t x_full, x_empty;   // the streams' join in shared memory
-    uint64_t drained;
+    uint64_t drained, nobody[2];
     Place bound[2];
     Seq first;                 // the sequence that bound[0] was found in
     int first_b;
@@ -435,12 +435,12 @@ __device__ __forceinline__ int ring_v(int t, int nt)
 
 // ---- workspace ----------------------------------------------------------------------
 // Places of the n + 1 bounds, then for each CTA two parts (0: of an item that began in an
-// earlier share, 1: of an item that goes on in the next) of `rows` rows: (m, l) pairs and
-// 128 accumulators each.
+// earlier share, 1: of an item that goes on in the next) of `rows` rows: (m, l) pairs, and
+// the accumulators as [column / 4][row][4], so that a warp's rows lie side by side.
 struct Parts {
     Place *bound;
     float2 *ml;
-    float *o;
+    float4 *o;
     int rows;
 };
 
@@ -650,15 +650,22 @@ __device__ __forceinline__ void softmax(const AttnLaunch &c, AttnShared &sh, War
             // the positions up to which, and from which, all rows of the warp see every key
             const int all_hi = __reduce_min_sync(0xffffffffu, valid ? pos : INT32_MAX);
             const int all_lo = __reduce_max_sync(0xffffffffu, valid ? low : 0);
-            int j = s.j0 + (TWO ? 0 : i);
-            for (int t = 0; t < m_tiles; ++t, j += TWO ? 1 : 2) {
-                ok = warp_wait(sh, &sh.s_full[i], (done + t) & 1, a.status);
+            // Before the first tile the steps are gone through once for nothing (P goes to where O will
+            // be, and to no waiter): it brings their instructions in, 3 us when cold, while the first
+            // keys are on their way.
+            int t = segs == 0 && m_tiles > 0 ? -1 : 0, j = s.j0 + (TWO ? t : 2 * t + i);
+            for (; t < m_tiles; ++t, j += TWO ? 1 : 2) {
+                const bool live = t >= 0;
+                if (live)
+                    ok = warp_wait(sh, &sh.s_full[i], (done + t) & 1, a.status);
                 if (!ok)
                     break;
                 tc_fence_after();
+                const uint32_t p_addr = live ? s_addr : o_addr;
+                uint64_t *const p_bar = live ? sh.p_full[i] : sh.nobody;
                 // V rows past the length may hold anything, and 0 times that is not 0: they are
                 // cleared where the tile is used first
-                if ((!TWO || i == 0) && (j + 1) * kTile > s.seq.L) {
+                if (live && (!TWO || i == 0) && (j + 1) * kTile > s.seq.L) {
                     const uint32_t u = used + ring_v<TWO>(j - s.j0, nt);
                     const int st = u % kAttnStages;
                     ok = warp_wait(sh, &sh.kv_full[st], (u / kAttnStages) & 1, a.status);
@@ -677,31 +684,52 @@ __device__ __forceinline__ void softmax(const AttnLaunch &c, AttnShared &sh, War
                 if (work) {
                     uint32_t x[kTile];
                     float *f = reinterpret_cast<float *>(x);
-                    // the maximum of each quarter is taken while the next is on its way (of the raw scores:
+                    // the maximum of the first half is taken while the second is on its way (of the raw scores:
                     // neither scale nor cap changes their order)
                     const bool part = j * kTile + kTile - 1 > all_hi || j * kTile < all_lo;
                     const int last = pos - j * kTile, first = low - j * kTile;
                     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
                     tc_ld32(s_addr, x);
+                    tc_ld32(s_addr + 32, x + 32);
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        tc_wait_ld32(x + 32 * q);
-                        if (q < 3)
-                            tc_ld32(s_addr + 32 * (q + 1), x + 32 * (q + 1));
+                    for (int q = 0; q < 2; ++q) {
+                        tc_wait_ld32(x + 64 * q);
+                        tc_wait_ld32(x + 64 * q + 32);
+                        if (q == 0) {
+                            tc_ld32(s_addr + 64, x + 64);
+                            tc_ld32(s_addr + 96, x + 96);
+                        }
                         if (part) {
 #pragma unroll
-                            for (int e = 32 * q; e < 32 * q + 32; ++e)
+                            for (int e = 64 * q; e < 64 * q + 64; ++e)
                                 f[e] = e <= last && e >= first ? f[e] : -INFINITY;
                         }
 #pragma unroll
-                        for (int e = 32 * q; e < 32 * q + 32; e += 8) {
+                        for (int e = 64 * q; e < 64 * q + 64; e += 8) {
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
                                 mx[k] = max3(mx[k], f[e + k], f[e + 4 + k]);
                         }
                     }
                     float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
-                    top = !CAP ? top * scale2 : top == -INFINITY ? top : capped(top, cap_in, cap2);
+                    if (CAP) {
+                        top = top == -INFINITY ? top : capped(top, cap_in, cap2);
+                        // cap tanh(s / cap) of all scores, two reciprocals from one (beyond 2^60 the cap is reached)
+#pragma unroll
+                        for (int e = 0; e < kTile; e += 2) {
+                            const float d0 = 1.f + ex2(fminf(f[e] * cap_in, 60.f)), d1 = 1.f + ex2(fminf(f[e + 1] * cap_in, 60.f));
+                            const float both = rcp(d0 * d1);
+                            f[e] = fmaf(-2.f * cap2, both * d1, cap2);
+                            f[e + 1] = fmaf(-2.f * cap2, both * d0, cap2);
+                        }
+                        if (part) {
+#pragma unroll
+                            for (int e = 0; e < kTile; ++e)
+                                f[e] = e <= last && e >= first ? f[e] : -INFINITY;
+                        }
+                    } else {
+                        top *= scale2;
+                    }
                     // The maximum that the weights are taken against follows the true one only
                     // when it has grown by more than 2^8: until then the weights are at most 256, and
                     // the accumulators need no pass over them.
@@ -730,33 +758,18 @@ __device__ __forceinline__ void softmax(const AttnLaunch &c, AttnShared &sh, War
                     // The weights, two keys at a time, in three steps that overlap: the exponents of
                     // pair n + kLead, the exponentials of pair n, the sum and the rounding of pair n - kLead.
                     float2 sum[2] = {};
-                    const float2 mul = make_float2(scale2, scale2), add = CAP ? make_float2(cap2 - base, cap2 - base) : make_float2(-base, -base);
+                    const float2 mul = make_float2(scale2, scale2), add = make_float2(-base, -base);
                     constexpr int kLead = 4, kPairs = kTile / 2;
 #pragma unroll
                     for (int n = -kLead; n < kPairs + kLead; ++n) {
                         if (n + kLead < kPairs) {
                             const int e = 2 * (n + kLead);
-                            if (!CAP) {
-                                const float2 y = fma2(make_float2(f[e], f[e + 1]), mul, add);
-                                f[e] = y.x, f[e + 1] = y.y;
-                            } else {   // 1 + e^2y (beyond 2^60 the cap is reached)
-                                f[e] = 1.f + ex2(fminf(f[e] * cap_in, 60.f));
-                                f[e + 1] = 1.f + ex2(fminf(f[e + 1] * cap_in, 60.f));
-                            }
+                            const float2 y = CAP ? add2(make_float2(f[e], f[e + 1]), add) : fma2(make_float2(f[e], f[e + 1]), mul, add);
+                            f[e] = y.x, f[e + 1] = y.y;
                         }
                         if (n >= 0 && n < kPairs) {
-                            const int e = 2 * n;
-                            if (CAP) {   // both reciprocals from one
-                                const float both = rcp(f[e] * f[e + 1]), r0 = both * f[e + 1], r1 = both * f[e];
-                                f[e] = fmaf(-2.f * cap2, r0, add.x);
-                                f[e + 1] = fmaf(-2.f * cap2, r1, add.x);
-                                if (part) {
-                                    f[e] = e <= last && e >= first ? f[e] : -INFINITY;
-                                    f[e + 1] = e + 1 <= last && e + 1 >= first ? f[e + 1] : -INFINITY;
-                                }
-                            }
-                            f[e] = ex2(f[e]);
-                            f[e + 1] = ex2(f[e + 1]);
+                            f[2 * n] = ex2(f[2 * n]);
+                            f[2 * n + 1] = ex2(f[2 * n + 1]);
                         }
                         if (n >= kLead) {
                             const int e = 2 * (n - kLead);
@@ -766,26 +779,27 @@ __device__ __forceinline__ void softmax(const AttnLaunch &c, AttnShared &sh, War
                         // P takes the columns of scores that are in registers; the first half is handed
                         // over while the second is made
                         if (n == kPairs / 2 + kLead - 1)
-                            tc_st32(s_addr, x);
+                            tc_st32(p_addr, x);
                         if (n == kPairs * 3 / 4) {
                             tc_wait_st();
                             tc_fence_before();
                             __syncwarp();
                             if (lane == 0)
-                                mbar_arrive(&sh.p_full[i][0]);
+                                mbar_arrive(p_bar);
                         }
                     }
-                    tc_st32(s_addr + 32, x + 32);
+                    tc_st32(p_addr + 32, x + 32);
                     const float2 both = add2(sum[0], sum[1]);
-                    l += both.x + both.y;
+                    l = live ? l + both.x + both.y : 0.f;
+                    m = live ? m : -INFINITY;
                     tc_wait_st();
                 } else if (lane == 0) {
-                    mbar_arrive(&sh.p_full[i][0]);
+                    mbar_arrive(p_bar);
                 }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0)
-                    mbar_arrive(&sh.p_full[i][1]);
+                    mbar_arrive(p_bar + 1);
             }
         }
         done += m_tiles;
@@ -794,7 +808,8 @@ __device__ __forceinline__ void softmax(const AttnLaunch &c, AttnShared &sh, War
         tc_fence_after();
         // ---- the rows' end: a share's part, or the output
         const bool whole = s.j0 == s.lo && s.j1 == s.hi;
-        const size_t part = (size_t)(2 * blockIdx.x + (s.j0 == s.lo)) * c.parts.rows + (TWO ? i * kTile : 0) + r;
+        const size_t part = 2 * blockIdx.x + (s.j0 == s.lo);
+        const int row = (TWO ? i * kTile : 0) + r;
         const size_t t = s.seq.t0 + tok;
         const int head = s.hk * G + r % G;
         // stream 1's rows join stream 0's through shared memory, 32 columns at a time
@@ -859,16 +874,16 @@ __device__ __forceinline__ void softmax(const AttnLaunch &c, AttnShared &sh, War
                             make_uint4(bf16x2(y[e] * inv, y[e + 1] * inv), bf16x2(y[e + 2] * inv, y[e + 3] * inv),
                                        bf16x2(y[e + 4] * inv, y[e + 5] * inv), bf16x2(y[e + 6] * inv, y[e + 7] * inv));
                 } else {
-                    float *const dst = c.parts.o + part * kD + h * 32;
 #pragma unroll
                     for (int e = 0; e < 32; e += 4)
-                        *reinterpret_cast<float4 *>(dst + e) = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+                        c.parts.o[(part * (kD / 4) + h * 8 + e / 4) * c.parts.rows + row] =
+                            make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
                 }
             }
         }
         if (valid && ok && (TWO || i == 0)) {
             if (!whole)
-                c.parts.ml[part] = make_float2(m, l);
+                c.parts.ml[part * c.parts.rows + row] = make_float2(m, l);
             else if (a.lse)
                 a.lse[t * a.Hq + head] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
         }
@@ -908,6 +923,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         mbar_init(&sh.x_full, 4);
         mbar_init(&sh.x_empty, 4);
         mbar_init(&sh.drained, 1);
+        mbar_init(&sh.nobody[0], 1 << 16);
+        mbar_init(&sh.nobody[1], 1 << 16);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         sh.failed = 0;
         sh.bound[0] = sh.bound[1] = Place{a.B, 0, 0, 0};
@@ -1031,77 +1048,81 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
-// Joins the parts of the item that bound blockIdx.x + 1 cuts first: a warp a row.
+// Joins the parts of the item that bound blockIdx.x + 1 cuts first.  A warp takes a
+// row, or, where a row has many parts, the block takes it and shares them out.
 template <bool TWO>
 __global__ void __launch_bounds__(256) join_kernel(const AttnLaunch c, int shares)
 {
+    __shared__ float4 sum[8][32];
+    __shared__ float2 ml_of[8];
     pdl_wait();
     pdl_trigger();
     const AttnArgs &a = c.a;
-    const int x = blockIdx.x + 1, lane = threadIdx.x & 31;
+    const int x = blockIdx.x + 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const Place at = c.parts.bound[x], prev = c.parts.bound[x - 1];
     if (at.cut == 0 || (same_item(at, prev) && prev.cut > 0))
         return;
     // parts: share x - 1's part 1, then part 0 of shares x, x + 1, ... while they begin in the item
+    const Seq s = sequence(a, at.b);
     int end = x + 1, more;
     do {
         const int y = end + (int)threadIdx.x;
         more = __syncthreads_count(y < shares && same_item(c.parts.bound[y], at));
         end += more;
     } while (more == 256);
-    const Seq s = sequence(a, at.b);
-    const int tile_tokens = kTile / a.G, per_tile = tile_tokens * a.G;
-    const int rows = TWO ? kTile + per_tile : per_tile;
-    for (int r = blockIdx.y * 8 + threadIdx.x / 32; r < rows; r += gridDim.y * 8) {
-        const int in = r & (kTile - 1);
-        const int tok = at.k * c.plan.tokens + (r >= kTile ? tile_tokens : 0) + in / a.G;
-        if (in >= per_tile || tok >= s.n)
-            continue;
-        auto index = [&](int i) { return (size_t)(2 * (x - 1 + i) + (i == 0)) * c.parts.rows + r; };
-        // a share between two equal cuts has no part
-        auto there = [&](int i) {
-            const int y = x - 1 + i;
-            return i == 0 || y + 1 > shares || !same_item(c.parts.bound[y + 1], at) ||
-                   c.parts.bound[y + 1].cut > c.parts.bound[y].cut;
-        };
-        const int n = end - x + 1;
-        float mm = -INFINITY;
-        for (int i = lane; i < n; i += 32)
-            if (there(i))
-                mm = fmaxf(mm, c.parts.ml[index(i)].x);
-#pragma unroll
-        for (int o = 16; o; o >>= 1)
-            mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
-        const float base = mm == -INFINITY ? 0.f : mm;
-        float l = 0.f;
+    const int n = end - x + 1;
+    const bool together = n > 8;
+    const int tile_tokens = kTile / a.G, per_tile = tile_tokens * a.G, first = at.k * c.plan.tokens;
+    const int rows = min(TWO ? 2 * per_tile : per_tile, (s.n - first) * a.G);
+    const int step = together ? 1 : 8;   // parts and rows of a warp
+    for (int r0 = blockIdx.y * step + (together ? 0 : warp); r0 < rows; r0 += gridDim.y * step) {
+        const int second = r0 >= per_tile, in = r0 - second * per_tile;
+        const int r = second * kTile + in, tok = first + second * tile_tokens + in / a.G;
+        auto part = [&](int i) { return (size_t)(2 * (x - 1 + i) + (i == 0)); };
+        float m = -INFINITY, l = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int i0 = 0; i0 < n; i0 += 32) {
-            float f = 0.f;
-            if (i0 + lane < n && there(i0 + lane)) {
-                const float2 ml = c.parts.ml[index(i0 + lane)];
-                f = ex2(ml.x - base);
-                l += f * ml.y;
-            }
-            const int most = min(32, n - i0);
-#pragma unroll 8
-            for (int i = 0; i < most; ++i) {
-                const float fi = __shfl_sync(0xffffffffu, f, i);
-                const float4 o = reinterpret_cast<const float4 *>(c.parts.o + index(i0 + i) * kD)[lane];
-                // (parts without a row's keys, and those that are not there, may hold anything)
-                acc.x = fi != 0.f ? fmaf(fi, o.x, acc.x) : acc.x;
-                acc.y = fi != 0.f ? fmaf(fi, o.y, acc.y) : acc.y;
-                acc.z = fi != 0.f ? fmaf(fi, o.z, acc.z) : acc.z;
-                acc.w = fi != 0.f ? fmaf(fi, o.w, acc.w) : acc.w;
-            }
+        auto add = [&](float m2, float l2, float4 o) {
+            const float mm = fmaxf(m, m2), base = mm == -INFINITY ? 0.f : mm;
+            const float f1 = ex2(m - base), f2 = m2 == -INFINITY ? 0.f : ex2(m2 - base);
+            l = l * f1 + l2 * f2;
+            // (a part without a row's keys may hold anything)
+            acc.x = fmaf(acc.x, f1, f2 != 0.f ? o.x * f2 : 0.f);
+            acc.y = fmaf(acc.y, f1, f2 != 0.f ? o.y * f2 : 0.f);
+            acc.z = fmaf(acc.z, f1, f2 != 0.f ? o.z * f2 : 0.f);
+            acc.w = fmaf(acc.w, f1, f2 != 0.f ? o.w * f2 : 0.f);
+            m = mm;
+        };
+#pragma unroll 4
+        for (int i = together ? warp : 0; i < n; i += together ? 8 : 1) {
+            // a share between two equal cuts has no part
+            const int y = x - 1 + i;
+            const Place p0 = c.parts.bound[y], p1 = c.parts.bound[y + 1];
+            const bool there = i == 0 || !same_item(p1, at) || p1.cut > p0.cut;
+            const float2 ml = c.parts.ml[part(i) * c.parts.rows + r];
+            const float4 o = c.parts.o[(part(i) * (kD / 4) + lane) * c.parts.rows + r];
+            add(there ? ml.x : -INFINITY, there ? ml.y : 0.f, o);
         }
-        l = warp_sum(l);
+        if (together) {
+            sum[warp][lane] = acc;
+            if (lane == 0)
+                ml_of[warp] = make_float2(m, l);
+            __syncthreads();
+            if (warp == 0) {
+                m = -INFINITY, l = 0.f, acc = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int i = 0; i < 8; ++i)
+                    add(ml_of[i].x, ml_of[i].y, sum[i][lane]);
+            }
+            __syncthreads();
+            if (warp != 0)
+                continue;
+        }
         const float inv = l > 0.f ? 1.f / l : 0.f;
         const size_t t = s.t0 + tok;
         const int h = at.hk * a.G + in % a.G;
         *reinterpret_cast<uint2 *>(a.out + t * a.out_stride + h * kD + lane * 4) =
             make_uint2(bf16x2(acc.x * inv, acc.y * inv), bf16x2(acc.z * inv, acc.w * inv));
         if (a.lse && lane == 0)
-            a.lse[t * a.Hq + h] = l > 0.f ? (mm + log2f(l)) * 0.6931471805599453f : -INFINITY;
+            a.lse[t * a.Hq + h] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
     }
 }
 
@@ -1125,7 +1146,7 @@ static size_t carve(int T, int B, int Hq, int Hkv, char *ws, Parts *p)
     if (p) {
         p->bound = reinterpret_cast<Place *>(ws);
         p->ml = reinterpret_cast<float2 *>(ws + o_ml);
-        p->o = reinterpret_cast<float *>(ws + o_o);
+        p->o = reinterpret_cast<float4 *>(ws + o_o);
         p->rows = (int)rows;
     }
     return o_o + 2 * n * rows * kD * sizeof(float);
@@ -1153,7 +1174,7 @@ static cudaError_t launch_mode(const CUtensorMap &qm, const CUtensorMap &km, con
     cudaError_t e = launch_pdl(kernel, dim3(n), dim3(kAttnThreads), kAttnSmem, st, 1, qm, km, vm, c);
     if (e != cudaSuccess || n < 2)
         return e;
-    return launch_pdl(join_kernel<TWO>, dim3(n - 1, TWO ? 4 : (c.parts.rows + 7) / 8), dim3(256), 0, st, 1, c, n);
+    return launch_pdl(join_kernel<TWO>, dim3(n - 1, TWO ? 16 : 8), dim3(256), 0, st, 1, c, n);
 }
 
 cudaError_t launch_chunk_attention(const AttnArgs &a, cudaStream_t st)

@@ -287,12 +287,13 @@ def profile_reset():
 
 def _call_stream(stream, tensors):
     """The raw stream of a call; every tensor (None passes) has to be on the current device, and so has the stream."""
-    dev = torch.cuda.current_device()
+    s = stream if stream is not None else torch.cuda.current_stream()
+    dev = s.device_index if stream is None else torch.cuda.current_device()
     for t in tensors:
         if t is not None and t.get_device() != dev:
             raise RetopkError(f"expected CUDA tensors on the current device (cuda:{dev}), got one on {t.device}")
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        return s.cuda_stream
     if stream.device_index != dev:
         raise RetopkError(f"stream of device {stream.device_index} while cuda:{dev} is current")
     return stream.cuda_stream
