@@ -421,11 +421,11 @@ typedef struct retopk_rope {
 
 /* Ragged new tokens: row t of q / k / v belongs to sequence b when
  * cu_tokens[b] <= t < cu_tokens[b + 1] (device int32 [B + 1], not decreasing; NULL: one
- * token for each sequence, T == B).  Rows of [0, T) in no sequence are not
- * read and their outputs are left as they were.  q [T, Hq, 128], k, v [T, Hkv, 128] bf16, a
+ * token for each sequence, T == B).  What rows of [0, T) in no sequence
+ * hold does not matter, and their outputs are left as they were.  q [T, Hq, 128], k, v [T, Hkv, 128] bf16, a
  * token's heads side by side, tokens q_stride / k_stride / v_stride elements
  * apart (multiples of 8), so slices of one fused projection are taken as they are.
- * Limits: 0 <= T <= 2^22, 1 <= B <= 65535, Hq / Hkv <= 16, Hq <= 1024.
+ * Limits: 0 <= T <= 2^22, 1 <= B <= 65535, Hq / Hkv <= 16, Hq <= 1024, T (Hq + 2 Hkv) <= 2^30.
  * d_status: optional device word for RETOPK_STATUS_* bits (NULL: not reported).
  *
  * retopk_qk_rope: norm and rotation of the tokens' queries and keys at the

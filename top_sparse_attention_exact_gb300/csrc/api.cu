@@ -19,6 +19,7 @@ size_t finish_smem_bytes_for(int max_len, int K, int RKW, int CL);
 cudaError_t configure_fidelity();
 cudaError_t configure_prefilter();
 cudaError_t configure_chunk_attention();
+cudaError_t configure_rope();
 }  // namespace retopk
 
 using namespace retopk;
@@ -123,6 +124,8 @@ int ensure_configured()
             e = configure_prefilter();
         if (e == cudaSuccess)
             e = configure_chunk_attention();
+        if (e == cudaSuccess)
+            e = configure_rope();
         err[dev] = e;
     });
     return cuda_rc(err[dev]);

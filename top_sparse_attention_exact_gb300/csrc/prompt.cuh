@@ -36,6 +36,22 @@ __device__ __forceinline__ long long cache_row(const retopk_cache &c, int b, int
     return ((long long)page * c.n_kv_heads + hk) * c.page_rows + r;
 }
 
+// Bounded wait; false (and RETOPK_STATUS_TIMEOUT, where there is a status word) on expiry.
+__device__ __forceinline__ bool wait_full(uint64_t *bar, uint32_t parity, uint32_t *status)
+{
+    if (mbar_try_wait(bar, parity))
+        return true;
+    const long long t0 = clock64();
+    while (!mbar_try_wait(bar, parity)) {
+        if (clock64() - t0 > kWaitCycles) {
+            if (status)
+                atomicOr(status, RETOPK_STATUS_TIMEOUT);
+            return false;
+        }
+    }
+    return true;
+}
+
 // ---- 8-bit rows: e4m3 codes with one power-of-two scale for 32 elements -----
 // Scale byte of a block from the largest |x| (its fp32 bits): the smallest e
 // with amax <= 448 * 2^e, e = byte - 127.  448 = 1.75 * 2^8, so e is the
@@ -82,6 +98,34 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi)
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
+}
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(reinterpret_cast<uint64_t &>(d))
+        : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)), "l"(reinterpret_cast<uint64_t &>(c)));
+    return d;
+}
+
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    float2 d;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<uint64_t &>(d))
+        : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)));
+    return d;
+}
+
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    float2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<uint64_t &>(d))
+        : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)));
+    return d;
 }
 
 __device__ __forceinline__ void unpack8(const uint4 &u, float (&x)[8])

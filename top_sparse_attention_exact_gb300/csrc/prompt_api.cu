@@ -11,6 +11,7 @@ namespace {
 constexpr int kMaxTokens = 1 << 22;
 constexpr int kMaxBatch = 65535;
 constexpr int kMaxHeads = 1024;
+constexpr long long kMaxTokenHeads = 1ll << 30;   // heads of all tokens: 256 GB of rows
 
 bool aligned(const void *p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
 
@@ -37,7 +38,8 @@ int check_tokens(int T, int B, int Hq, int Hkv, const int32_t *cu, const int32_t
 {
     if (T < 0 || B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || !seqlens || (!cu && T != B))
         return RETOPK_ERR_INVALID;
-    if (T > kMaxTokens || B > kMaxBatch || Hq > kMaxHeads || Hq / Hkv > kMaxGroup)
+    if (T > kMaxTokens || B > kMaxBatch || Hq > kMaxHeads || Hq / Hkv > kMaxGroup ||
+        (long long)T * (Hq + 2 * Hkv) > kMaxTokenHeads)
         return RETOPK_ERR_UNSUPPORTED;
     if (!aligned(cu, 4) || !aligned(seqlens, 4))
         return RETOPK_ERR_ALIGN;
@@ -82,6 +84,8 @@ int retopk_qk_rope(const retopk_rope *rope, const retopk_bf16 *q, int64_t q_stri
         return RETOPK_ERR_INVALID;
     if (!aligned(q_out, 16) || !aligned(k_out, 16))
         return RETOPK_ERR_ALIGN;
+    if ((e = ensure_configured()))
+        return e;
     RopeArgs a{};
     a.q = q;
     a.k = k;
@@ -122,6 +126,8 @@ int retopk_qkv_append(const retopk_rope *rope, const retopk_bf16 *q, int64_t q_s
         if (!aligned(q_out, 16))
             return RETOPK_ERR_ALIGN;
     }
+    if ((e = ensure_configured()))
+        return e;
     RopeArgs a{};
     a.q = q;
     a.k = k;

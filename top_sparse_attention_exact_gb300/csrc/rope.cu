@@ -4,11 +4,13 @@
 // Per head x (128 elements): x <- x * rsqrt(mean(x^2) + eps) * w, then the
 // pairs (a, b) turn by t = pos * inv_freq: a cos t - b sin t, b cos t + a sin t.
 // Each element is read and written once, so the memory bounds it; what has to be
-// kept small is the work for each.  A warp takes a token (or, where tokens are
-// few, some of a token's heads), two heads at a time, 16 lanes a head: a lane
-// holds two runs of four elements that are each other's partners, so the rotation
-// needs no exchange, its cosines and sines stay in registers for all heads of the token,
-// and so do its norm weights.
+// kept small is the work for each, and what has to be kept large the bytes on
+// their way.  Batches of eight heads are shared out evenly, in the order of tokens,
+// queries, keys, values, over the warps that fit on the GPU.  A warp has a ring of its
+// own in shared memory, into which bulk copies bring up to four batches ahead.  It
+// takes four heads at once, 8 lanes a head: a lane holds two runs of eight elements
+// that are each other's partners, so the rotation needs no exchange, and its
+// factors, weights included, stay in registers for all heads of the token.
 //
 // Angles.  pos is whole, so only the fraction of inv_freq / 2 pi counts: it is kept
 // as a 64-bit fixed-point number, and pos times it, modulo 2^64, is the fraction of the
@@ -20,8 +22,9 @@
 
 namespace retopk {
 
-constexpr int kRopeWarps = 8;
-constexpr int kRopeBatch = 4;   // pairs of heads in flight in a warp
+constexpr int kRopeWarps = 8, kRopeBlocks = 2;   // of a block; of an SM
+constexpr int kRopeHeads = 8;    // heads of a batch
+constexpr int kRopeStages = 4;   // batches of a warp's ring
 
 // The sequence that token t belongs to: the number of sequences that end at or
 // before t, found by the warp in steps of 32.
@@ -51,10 +54,10 @@ enum { TO_ROWS = 0, TO_BF16 = 1, TO_MX8 = 2 };   // k_out (no values), a bf16 ca
 // A lane's part of the norm and the rotation, with the weights in it: partners a, b
 // become f (a ac - b bs) and f (b bc + a as), f the norm's factor.
 struct Turn {
-    float ac[4], bs[4], bc[4], as[4];
+    float ac[8], bs[8], bc[8], as[8];
 };
 
-// Element numbers of a lane's partners: in its two runs, or side by side.
+// Element numbers of a lane's partners: side by side, or in its two runs.
 template <bool INTER>
 __device__ __forceinline__ constexpr int first_of(int e)
 {
@@ -63,40 +66,77 @@ __device__ __forceinline__ constexpr int first_of(int e)
 template <bool INTER>
 __device__ __forceinline__ constexpr int second_of(int e)
 {
-    return INTER ? 2 * e + 1 : e + 4;
+    return INTER ? 2 * e + 1 : e + 8;
 }
 
-__device__ __forceinline__ void unpack4(const uint2 (&u)[2], float (&x)[8])
+struct __align__(16) RopeWarp {
+    uint8_t ring[kRopeStages][kRopeHeads * kD * 2];
+    float2 turns[kD / 2];      // (cos, sin) of the token
+    uint32_t tops[4][16];      // largest |x| of runs of eight, for the scales
+    uint64_t full[kRopeStages];
+};
+
+__device__ __forceinline__ void unpack16(const uint4 &u, const uint4 &v, float (&x)[16])
 {
-    x[0] = bf16lo(u[0].x), x[1] = bf16hi(u[0].x), x[2] = bf16lo(u[0].y), x[3] = bf16hi(u[0].y);
-    x[4] = bf16lo(u[1].x), x[5] = bf16hi(u[1].x), x[6] = bf16lo(u[1].y), x[7] = bf16hi(u[1].y);
+    float lo[8], hi[8];
+    unpack8(u, lo);
+    unpack8(v, hi);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        x[e] = lo[e], x[8 + e] = hi[e];
 }
 
-// `groups` warps share a token's heads; a warp takes `tokens` tokens one after
-// another: its share of the query heads, then of the keys', then of the values'.
+// A warp takes `each` batches of the tokens' `T * all`.
 template <bool INTER, int TO>
-__global__ void __launch_bounds__(kRopeWarps * 32, 4) rope_kernel(const __grid_constant__ RopeArgs a, int groups, int tokens)
+__global__ void __launch_bounds__(kRopeWarps * 32, kRopeBlocks) rope_kernel(const __grid_constant__ RopeArgs a, int each)
 {
-    __shared__ float2 turns[kRopeWarps][kD / 2];                  // (cos, sin) of the warp's token
-    __shared__ __align__(16) uint32_t tops[kRopeWarps][2][32];    // largest |x| of runs of four, for the scales
+    extern __shared__ __align__(16) unsigned char rope_smem[];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane & 7, which = lane >> 3;
+    RopeWarp &sh = reinterpret_cast<RopeWarp *>(rope_smem)[warp];
+    if (lane == 0) {
+        for (int i = 0; i < kRopeStages; ++i)
+            mbar_init(&sh.full[i], 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncwarp();
     pdl_wait();
     pdl_trigger();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane & 15, second = lane >> 4;
     if (a.seqlens_out)   // the lengths after this call (a separate buffer)
         for (int b = blockIdx.x * blockDim.x + threadIdx.x; b < a.B; b += gridDim.x * blockDim.x)
             a.seqlens_out[b] = advanced(a, b);
-    const int unit = blockIdx.x * kRopeWarps + warp;
-    const int nq = (a.Hq + 1) / 2, nk = (a.Hkv + 1) / 2, all = nq + nk + (TO ? nk : 0), each = (all + groups - 1) / groups;
-    const int p0 = unit % groups * each, p1 = min(all, p0 + each);   // pairs of heads
-    const int t0 = unit / groups * tokens, t1 = min(a.T, t0 + tokens);
-    // this lane's two runs of four: partners in the rotation
+    const int nq = (a.Hq + kRopeHeads - 1) / kRopeHeads, nk = (a.Hkv + kRopeHeads - 1) / kRopeHeads;
+    const int all = nq + nk + (TO ? nk : 0);
+    const int i0 = min((long long)(blockIdx.x * kRopeWarps + warp) * each, (long long)a.T * all), i1 = min((long long)i0 + each, (long long)a.T * all);
+    if (i0 >= i1)
+        return;
+    // batch `p` of token `t` into the ring (one lane)
+    int ahead_t = i0 / all, ahead_p = i0 % all;
+    uint32_t ahead = 0;
+    auto copy_next = [&] {
+        if (i0 + (int)ahead >= i1)
+            return;
+        const int p = ahead_p, stage = ahead % kRopeStages;
+        const int first = (p < nq ? p : p < nq + nk ? p - nq : p - nq - nk) * kRopeHeads;
+        const uint16_t *src = (p < nq ? a.q + ahead_t * a.q_stride : p < nq + nk ? a.k + ahead_t * a.k_stride : a.v + ahead_t * a.v_stride);
+        const uint32_t bytes = min(kRopeHeads, (p < nq ? a.Hq : a.Hkv) - first) * kD * 2;
+        mbar_expect_tx(&sh.full[stage], bytes);
+        bulk_load(sh.ring[stage], src + first * kD, bytes, &sh.full[stage]);
+        ++ahead;
+        if (++ahead_p == all) {
+            ahead_p = 0;
+            ++ahead_t;
+        }
+    };
+    if (lane == 0)
+        for (int i = 0; i < kRopeStages; ++i)
+            copy_next();
+    // this lane's two runs of eight: partners in the rotation
     const int half = a.rope.rot_dim / 2;
-    const bool turned = 4 * l < half;
-    const int c0 = INTER ? 2 * l : turned ? l : half / 4 + l;
-    const int c1 = INTER ? 2 * l + 1 : turned ? l + half / 4 : l + 16;
+    const bool turned = 8 * l < half;
+    const int c0 = INTER ? 2 * l : turned ? l : half / 8 + l;
+    const int c1 = INTER ? 2 * l + 1 : turned ? l + half / 8 : l + 8;
     // turns of pairs lane and lane + 32 by one position
     uint64_t phase[2] = {0, 0};
-    if (p0 < nq + nk)
 #pragma unroll
         for (int i = 0; i < 2; ++i)
             if (lane + 32 * i < half) {
@@ -104,8 +144,12 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 4) rope_kernel(const __grid_c
                 phase[i] = (uint64_t)(int64_t)((f - rint(f)) * 4611686018427387904.0) << 2;   // 2^62, then 2^2
             }
     int b = -1, begin = 0, end = -1, L = 0;
-    bool fits = false;
-    for (int t = t0; t < t1; ++t) {
+    bool fits = false, ok = true;
+    long long at = -1;     // the row of the token in the cache, of head 0
+    int in_page = 0;       // its row in the page; 0: to be looked up
+    uint32_t used = 0;
+    for (int i = i0, t = i0 / all; i < i1 && ok; i = ++t * all) {
+        const int p0 = i - t * all, p1 = min(all, i1 - t * all);   // batches of this token
         if (t >= end) {
             if (!a.cu || (t < a.B && a.cu[t] == t && a.cu[t + 1] == t + 1)) {
                 b = begin = t;
@@ -119,145 +163,178 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 4) rope_kernel(const __grid_c
                 L = a.seqlens[b];
                 fits = L >= 0 && (long long)L + (end - begin) <= a.capacity;
             }
+            in_page = 0;
         }
-        if (begin > t || t >= end) {   // in no sequence
-            end = -1;
-            continue;
-        }
-        const int pos = L + (t - begin);
-        if (TO && !fits && t == begin && p0 == 0 && lane == 0 && a.status)
-            atomicOr(a.status, RETOPK_STATUS_KV_FULL);
-        if (p0 < nq + nk && half) {
-            __syncwarp();
+        const bool in = begin <= t && t < end;
+        if (in) {
+            const int pos = L + (t - begin);
+            if (TO && !fits && t == begin && p0 == 0 && lane == 0 && a.status)
+                atomicOr(a.status, RETOPK_STATUS_KV_FULL);
+            if (p0 < nq + nk) {
+                __syncwarp();
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-                if (lane + 32 * i < half) {
-                    float s, c;
-                    sincospif((float)(int32_t)(phase[i] * (uint64_t)(int64_t)pos >> 32) * 0x1p-31f, &s, &c);
-                    turns[warp][lane + 32 * i] = make_float2(c, s);
+                for (int i = 0; i < 2; ++i)
+                    if (lane + 32 * i < half) {
+                        float s, c;
+                        sincospif((float)(int32_t)(phase[i] * (uint64_t)(int64_t)pos >> 32) * 0x1p-31f, &s, &c);
+                        sh.turns[lane + 32 * i] = make_float2(c, s);
+                    }
+                __syncwarp();
+            }
+            if (TO && p1 > nq) {
+                if (in_page == 0 || in_page == a.cache.page_rows) {
+                    in_page = pos % a.cache.page_rows;
+                    at = fits ? cache_row(a.cache, b, 0, pos, a.status) : -1;
+                } else {
+                    at += at >= 0;
                 }
-            __syncwarp();
+                ++in_page;
+            }
+        } else {
+            end = -1;
         }
-        // the row of this token in the cache, of head 0
-        long long at = -1;
-        if (TO && fits && p1 > nq)
-            at = cache_row(a.cache, b, 0, pos, a.status);
 
-        // heads 2 lo .. 2 hi of the queries (0), keys (1) or values (2)
+        // batches lo .. hi of the queries (0), keys (1) or values (2)
         auto heads = [&](auto kind_, int lo, int hi) {
             constexpr int kind = decltype(kind_)::value;
             constexpr bool cached = TO && kind > 0, mx8 = TO == TO_MX8 && kind > 0;
             const int H = kind ? a.Hkv : a.Hq;
-            const uint16_t *const src = (kind == 0 ? a.q + t * a.q_stride : kind == 1 ? a.k + t * a.k_stride : a.v + t * a.v_stride);
+            const bool there = in && (!cached || at >= 0);
             const uint16_t *const w = kind == 2 ? nullptr : kind == 0 ? a.rope.q_weight : a.rope.k_weight;
             Turn tn;
-            if (kind < 2) {
-                float wx[8];
-                uint2 u[2] = {make_uint2(0x3f803f80u, 0x3f803f80u), make_uint2(0x3f803f80u, 0x3f803f80u)};   // ones
+            if (kind < 2 && there) {
+                float wx[16];
+                uint4 u = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u), v = u;   // ones
                 if (w) {
-                    u[0] = *reinterpret_cast<const uint2 *>(w + 4 * c0);
-                    u[1] = *reinterpret_cast<const uint2 *>(w + 4 * c1);
+                    u = reinterpret_cast<const uint4 *>(w)[c0];
+                    v = reinterpret_cast<const uint4 *>(w)[c1];
                 }
-                unpack4(u, wx);
+                unpack16(u, v, wx);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 cs = turned ? turns[warp][4 * l + e] : make_float2(1.f, 0.f);
+                for (int e = 0; e < 8; ++e) {
+                    const float2 cs = turned ? sh.turns[8 * l + e] : make_float2(1.f, 0.f);
                     const float wa = wx[first_of<INTER>(e)], wb = wx[second_of<INTER>(e)];
                     tn.ac[e] = wa * cs.x, tn.bs[e] = wb * cs.y, tn.bc[e] = wb * cs.x, tn.as[e] = wa * cs.y;
                 }
             }
-            for (int p = lo; p < hi; p += kRopeBatch) {
-                uint2 u[kRopeBatch][2];
-#pragma unroll
-                for (int i = 0; i < kRopeBatch; ++i) {
-                    const uint16_t *row = src + min(2 * (p + i) + second, H - 1) * kD;
-                    u[i][0] = *reinterpret_cast<const uint2 *>(row + 4 * c0);
-                    u[i][1] = *reinterpret_cast<const uint2 *>(row + 4 * c1);
-                }
-#pragma unroll
-                for (int i = 0; i < kRopeBatch; ++i) {
-                    const int h = 2 * (p + i) + second;
-                    const bool real = p + i < hi && h < H;
-                    float y[8];
-                    if (kind < 2 || mx8) {
-                        float x[8];
-                        unpack4(u[i], x);
-                        if (kind == 2) {
-#pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                y[e] = x[e];
-                        } else {
-                            float f = 1.f;
-                            if (w) {
-                                float sum = x[0] * x[0];
-#pragma unroll
-                                for (int e = 1; e < 8; ++e)
-                                    sum = fmaf(x[e], x[e], sum);
-#pragma unroll
-                                for (int o = 8; o; o >>= 1)
-                                    sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                                f = rsqrtf(fmaf(sum, 1.f / kD, a.rope.eps));
-                            }
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const float xa = x[first_of<INTER>(e)], xb = x[second_of<INTER>(e)];
-                                y[first_of<INTER>(e)] = f * fmaf(xa, tn.ac[e], -(xb * tn.bs[e]));
-                                y[second_of<INTER>(e)] = f * fmaf(xb, tn.bc[e], xa * tn.as[e]);
-                            }
-                        }
+            // four heads of a batch, one for each quarter of the warp
+            auto four = [&](const uint8_t *from, uint8_t *to, uint8_t *sc, bool real) {
+                const uint4 u = *reinterpret_cast<const uint4 *>(from), v = *reinterpret_cast<const uint4 *>(from + 16 * (c1 - c0));
+                if (kind == 2 && !mx8) {
+                    if (real) {
+                        *reinterpret_cast<uint4 *>(to) = u;
+                        *reinterpret_cast<uint4 *>(to + 16 * (c1 - c0)) = v;
                     }
-                    if (mx8) {
-                        // the largest of each 32 elements: eight runs of four
-                        uint32_t m0 = 0, m1 = 0;
+                    return;
+                }
+                float y[16];
+                unpack16(u, v, y);
+                if (kind < 2) {
+                    float f = 1.f;
+                    if (w) {
+                        float sum[4] = {};
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            m0 = max(m0, __float_as_uint(y[e]) & 0x7fffffffu);
-                            m1 = max(m1, __float_as_uint(y[4 + e]) & 0x7fffffffu);
-                        }
-                        __syncwarp();
-                        tops[warp][second][c0] = m0;
-                        tops[warp][second][c1] = m1;
-                        __syncwarp();
-                        auto scale = [&](int c) {
-                            const uint4 *q = reinterpret_cast<const uint4 *>(&tops[warp][second][c & 24]);
-                            const uint4 v = q[0], z = q[1];
-                            return mx_scale(max(max(max(v.x, v.y), max(v.z, v.w)), max(max(z.x, z.y), max(z.z, z.w))));
-                        };
-                        const uint32_t s0 = scale(c0), s1 = scale(c1);
-                        const float f0 = mx_inverse(s0), f1 = mx_inverse(s1);
-                        if (real && at >= 0) {
-                            const long long row = at + (long long)h * a.cache.page_rows;
-                            uint8_t *dst = static_cast<uint8_t *>(kind == 2 ? a.cache.v : a.cache.k) + row * kD;
-                            uint8_t *sc = (kind == 2 ? a.cache.v_scale : a.cache.k_scale) + row * kMxScales;
-                            *reinterpret_cast<uint32_t *>(dst + 4 * c0) = e4m3x2(y[0] * f0, y[1] * f0) | e4m3x2(y[2] * f0, y[3] * f0) << 16;
-                            *reinterpret_cast<uint32_t *>(dst + 4 * c1) = e4m3x2(y[4] * f1, y[5] * f1) | e4m3x2(y[6] * f1, y[7] * f1) << 16;
-                            if ((c0 & 7) == 0)
-                                sc[c0 / 8] = (uint8_t)s0;
-                            if ((c1 & 7) == 0)
-                                sc[c1 / 8] = (uint8_t)s1;
-                        }
-                    } else if (real && (!cached || at >= 0)) {
-                        if (kind < 2) {
-                            u[i][0] = make_uint2(bf16x2(y[0], y[1]), bf16x2(y[2], y[3]));
-                            u[i][1] = make_uint2(bf16x2(y[4], y[5]), bf16x2(y[6], y[7]));
-                        }
-                        uint16_t *dst = kind == 0 ? a.q_out + ((size_t)t * a.Hq + h) * kD
-                                        : !cached ? a.k_out + ((size_t)t * a.Hkv + h) * kD
-                                                  : static_cast<uint16_t *>(kind == 2 ? a.cache.v : a.cache.k) +
-                                                        (at + (long long)h * a.cache.page_rows) * kD;
-                        *reinterpret_cast<uint2 *>(dst + 4 * c0) = u[i][0];
-                        *reinterpret_cast<uint2 *>(dst + 4 * c1) = u[i][1];
+                        for (int e = 0; e < 16; ++e)
+                            sum[e & 3] = fmaf(y[e], y[e], sum[e & 3]);
+                        sum[0] = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+#pragma unroll
+                        for (int o = 4; o; o >>= 1)
+                            sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], o);
+                        f = rsqrtf(fmaf(sum[0], 1.f / kD, a.rope.eps));
+                    }
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float xa = y[first_of<INTER>(e)], xb = y[second_of<INTER>(e)];
+                        float pa = xa, pb = xb;
+                        if (half < kD / 2)   // elements that do not turn have no partner
+                            pa = turned ? pa : 0.f, pb = turned ? pb : 0.f;
+                        y[first_of<INTER>(e)] = fmaf(xa, tn.ac[e], -(pb * tn.bs[e])) * f;
+                        y[second_of<INTER>(e)] = fmaf(xb, tn.bc[e], pa * tn.as[e]) * f;
                     }
                 }
+                if (mx8) {
+                    // the largest of each 32 elements: four runs of eight
+                    uint32_t m0 = 0, m1 = 0;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        m0 = max(m0, __float_as_uint(y[e]) & 0x7fffffffu);
+                        m1 = max(m1, __float_as_uint(y[8 + e]) & 0x7fffffffu);
+                    }
+                    __syncwarp();
+                    sh.tops[which][c0] = m0;
+                    sh.tops[which][c1] = m1;
+                    __syncwarp();
+                    auto scale = [&](int c) {
+                        const uint4 m = *reinterpret_cast<const uint4 *>(&sh.tops[which][c & 12]);
+                        return mx_scale(max(max(m.x, m.y), max(m.z, m.w)));
+                    };
+                    const uint32_t s0 = scale(c0), s1 = scale(c1);
+                    const float f0 = mx_inverse(s0), f1 = mx_inverse(s1);
+                    if (real) {
+                        *reinterpret_cast<uint2 *>(to) =
+                            make_uint2(e4m3x2(y[0] * f0, y[1] * f0) | e4m3x2(y[2] * f0, y[3] * f0) << 16,
+                                       e4m3x2(y[4] * f0, y[5] * f0) | e4m3x2(y[6] * f0, y[7] * f0) << 16);
+                        *reinterpret_cast<uint2 *>(to + 8 * (c1 - c0)) =
+                            make_uint2(e4m3x2(y[8] * f1, y[9] * f1) | e4m3x2(y[10] * f1, y[11] * f1) << 16,
+                                       e4m3x2(y[12] * f1, y[13] * f1) | e4m3x2(y[14] * f1, y[15] * f1) << 16);
+                        if ((c0 & 3) == 0)
+                            sc[c0 / 4] = (uint8_t)s0;
+                        if ((c1 & 3) == 0)
+                            sc[c1 / 4] = (uint8_t)s1;
+                    }
+                } else if (real) {
+                    *reinterpret_cast<uint4 *>(to) = make_uint4(bf16x2(y[0], y[1]), bf16x2(y[2], y[3]), bf16x2(y[4], y[5]), bf16x2(y[6], y[7]));
+                    *reinterpret_cast<uint4 *>(to + 16 * (c1 - c0)) =
+                        make_uint4(bf16x2(y[8], y[9]), bf16x2(y[10], y[11]), bf16x2(y[12], y[13]), bf16x2(y[14], y[15]));
+                }
+            };
+            // where this lane's elements of the first four heads go, and the step to the next four
+            constexpr int size = mx8 ? 1 : 2;
+            const long long first_row = cached ? at + (long long)(lo * kRopeHeads + which) * a.cache.page_rows
+                                               : (long long)t * H + lo * kRopeHeads + which;
+            uint8_t *to = static_cast<uint8_t *>(kind == 0 ? a.q_out : kind == 2 ? a.cache.v : TO ? a.cache.k : a.k_out) +
+                          first_row * (kD * size) + 8 * size * c0;
+            uint8_t *sc = mx8 ? (kind == 2 ? a.cache.v_scale : a.cache.k_scale) + first_row * kMxScales : nullptr;
+            const long long step = (cached ? a.cache.page_rows : 1) * 4ll * kD * size;
+            for (int p = lo; p < hi; ++p) {
+                const int stage = used % kRopeStages;
+                ok = __all_sync(0xffffffffu, wait_full(&sh.full[stage], (used / kRopeStages) & 1, a.status));
+                if (!ok)
+                    return;
+                ++used;
+                const int left = min(kRopeHeads, H - p * kRopeHeads);   // heads of the batch
+                const uint8_t *from = sh.ring[stage] + which * kD * 2 + 16 * c0;
+                if (there) {
+                    if (left == kRopeHeads) {
+#pragma unroll
+                        for (int i = 0; i < kRopeHeads / 4; ++i)
+                            four(from + i * 8 * kD, to + i * step, sc + i * (step / (kD / kMxScales)), true);
+                    } else {
+                        for (int i = 0; 4 * i < left; ++i)
+                            four(from + i * 8 * kD, to + i * step, sc + i * (step / (kD / kMxScales)), 4 * i + which < left);
+                    }
+                    to += kRopeHeads / 4 * step;
+                    sc += kRopeHeads / 4 * (step / (kD / kMxScales));
+                }
+                __syncwarp();   // all lanes have read the batch
+                if (lane == 0)
+                    copy_next();
             }
         };
         if (p0 < nq)
             heads(std::integral_constant<int, 0>{}, p0, min(p1, nq));
-        if (p0 < nq + nk && p1 > nq)
+        if (p0 < nq + nk && p1 > nq && ok)
             heads(std::integral_constant<int, 1>{}, max(p0, nq) - nq, min(p1, nq + nk) - nq);
-        if (TO && p1 > nq + nk)
+        if (TO && p1 > nq + nk && ok)
             heads(std::integral_constant<int, 2>{}, max(p0, nq + nk) - nq - nk, p1 - nq - nk);
     }
+    if (!ok && lane == 0) {   // a wait ran out: the copies in flight are waited for before the memory goes
+        const long long from = clock64();
+        for (uint32_t u = used; u < ahead; ++u)
+            while (!mbar_try_wait(&sh.full[u % kRopeStages], (u / kRopeStages) & 1) && clock64() - from < kWaitCycles)
+                ;
+    }
+    __syncwarp();
 }
 
 // seqlens_out from seqlens, in place or not, behind the rows' kernel.
@@ -269,19 +346,34 @@ __global__ void advance_kernel(const RopeArgs a)
         a.seqlens_out[b] = advanced(a, b);
 }
 
+static const void *rope_kernel_for(bool inter, int to)
+{
+    return to == TO_ROWS ? (inter ? (const void *)rope_kernel<true, TO_ROWS> : (const void *)rope_kernel<false, TO_ROWS>)
+         : to == TO_MX8  ? (inter ? (const void *)rope_kernel<true, TO_MX8> : (const void *)rope_kernel<false, TO_MX8>)
+                         : (inter ? (const void *)rope_kernel<true, TO_BF16> : (const void *)rope_kernel<false, TO_BF16>);
+}
+
+constexpr size_t kRopeSmem = kRopeWarps * sizeof(RopeWarp);
+
 cudaError_t launch_rope(const RopeArgs &a, cudaStream_t st)
 {
-    const int all = (a.Hq + 1) / 2 + (a.Hkv + 1) / 2 * (a.v ? 2 : 1);
-    // a warp a token once that fills the GPU; with fewer tokens, up to one warp for two heads
-    const int fill = sm_count() * 32, groups = std::max(1, std::min(all, (fill + a.T - 1) / std::max(1, a.T)));
-    const int tokens = std::max(1, std::min(8, a.T / (2 * fill)));
-    const long long units = (long long)((a.T + tokens - 1) / tokens) * groups;
-    const bool i = a.rope.interleaved != 0;
-    auto kernel = !a.v ? (i ? rope_kernel<true, TO_ROWS> : rope_kernel<false, TO_ROWS>)
-                  : a.cache.format == RETOPK_CACHE_MX8 ? (i ? rope_kernel<true, TO_MX8> : rope_kernel<false, TO_MX8>)
-                                                       : (i ? rope_kernel<true, TO_BF16> : rope_kernel<false, TO_BF16>);
-    return launch_pdl(kernel, dim3((unsigned)((units + kRopeWarps - 1) / kRopeWarps)), dim3(kRopeWarps * 32), 0, st, 1, a,
-                      groups, tokens);
+    auto batches = [](int heads) { return (heads + kRopeHeads - 1) / kRopeHeads; };
+    const long long total = (long long)a.T * (batches(a.Hq) + batches(a.Hkv) * (a.v ? 2 : 1));
+    const int most = sm_count() * kRopeBlocks * kRopeWarps, each = (int)((total + most - 1) / most);
+    const int blocks = (int)((total + (long long)each * kRopeWarps - 1) / ((long long)each * kRopeWarps));
+    const void *kernel = rope_kernel_for(a.rope.interleaved != 0, !a.v ? TO_ROWS : a.cache.format == RETOPK_CACHE_MX8 ? TO_MX8 : TO_BF16);
+    return launch_pdl(reinterpret_cast<void (*)(RopeArgs, int)>(const_cast<void *>(kernel)), dim3(blocks),
+                      dim3(kRopeWarps * 32), kRopeSmem, st, 1, a, each);
+}
+
+cudaError_t configure_rope()
+{
+    cudaError_t e = cudaSuccess;
+    for (int to : {TO_ROWS, TO_BF16, TO_MX8})
+        for (bool inter : {false, true})
+            if (e == cudaSuccess)
+                e = cudaFuncSetAttribute(rope_kernel_for(inter, to), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRopeSmem);
+    return e;
 }
 
 cudaError_t launch_advance(const RopeArgs &a, cudaStream_t st)

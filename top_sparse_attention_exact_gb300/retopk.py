@@ -287,16 +287,19 @@ def profile_reset():
 
 def _call_stream(stream, tensors):
     """The raw stream of a call; every tensor (None passes) has to be on the current device, and so has the stream."""
-    s = stream if stream is not None else torch.cuda.current_stream()
-    dev = s.device_index if stream is None else torch.cuda.current_device()
+    dev = torch.cuda.current_device()
     for t in tensors:
         if t is not None and t.get_device() != dev:
             raise RetopkError(f"expected CUDA tensors on the current device (cuda:{dev}), got one on {t.device}")
     if stream is None:
-        return s.cuda_stream
+        return _raw_stream(dev)
     if stream.device_index != dev:
         raise RetopkError(f"stream of device {stream.device_index} while cuda:{dev} is current")
     return stream.cuda_stream
+
+
+# the current stream's handle, without a Stream object for it (which costs more than the rest of a call's checks)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 def _empty(shape, dtype, device, stream):
@@ -309,19 +312,19 @@ def _empty(shape, dtype, device, stream):
 
 def _tokens(t: torch.Tensor, what: str) -> int:
     """The token stride of a bf16 [T, heads, 128] tensor whose heads lie side by side."""
-    if t.dtype not in _BF16_TYPES or t.dim() != 3 or t.shape[2] != 128:
-        raise RetopkError(f"{what}: a bf16 [T, heads, 128] tensor expected, got {t.dtype} {tuple(t.shape)}")
-    T, h, _ = t.shape
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != 128 or t.dtype not in _BF16_TYPES:
+        raise RetopkError(f"{what}: a bf16 [T, heads, 128] tensor expected, got {t.dtype} {tuple(shape)}")
     st, sh, sd = t.stride()
-    if sd != 1 or (h > 1 and sh != 128):
+    if sd != 1 or (sh != 128 and shape[1] > 1):
         raise RetopkError(f"{what}: a token's heads have to lie side by side, got strides {t.stride()}")
-    return st if T > 1 else max(st, h * 128)
+    return st if shape[0] > 1 else max(st, shape[1] * 128)
 
 
 def _lens(t: torch.Tensor | None, n: int, what: str):
     if t is None:
         return None
-    if t.dtype != torch.int32 or t.dim() != 1 or t.numel() != n or not t.is_contiguous():
+    if t.dtype != torch.int32 or t.shape != (n,) or not t.is_contiguous():
         raise RetopkError(f"{what}: a contiguous int32 [{n}] tensor expected, got {t.dtype} {tuple(t.shape)}")
     return t.data_ptr()
 
@@ -335,7 +338,7 @@ def _status(t: torch.Tensor | None):
 
 
 def _same(t: torch.Tensor, shape, what: str):
-    if t.dtype not in _BF16_TYPES or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.dtype not in _BF16_TYPES or t.shape != shape or not t.is_contiguous():
         raise RetopkError(f"{what}: a contiguous bf16 {tuple(shape)} tensor expected, got {t.dtype} {tuple(t.shape)}")
     return t.data_ptr()
 
@@ -408,7 +411,7 @@ def qk_rope(rope: QKRope, q, k, seqlens, q_out=None, k_out=None, cu_tokens=None,
     st = _call_stream(stream, (q, k, seqlens, q_out, k_out, cu_tokens, *rope.tensors))
     if k.shape[0] != T:
         raise RetopkError(f"q has {T} tokens, k {k.shape[0]}")
-    rc = load().retopk_qk_rope(rope._ref, q.data_ptr(), _tokens(q, "q"), k.data_ptr(), _tokens(k, "k"),
+    rc = (_lib or load()).retopk_qk_rope(rope._ref, q.data_ptr(), _tokens(q, "q"), k.data_ptr(), _tokens(k, "k"),
                                _lens(cu_tokens, B + 1, "cu_tokens"), T, B, Hq, Hkv, _lens(seqlens, B, "seqlens"),
                                _same(q_out, (T, Hq, 128), "q_out"), _same(k_out, (T, Hkv, 128), "k_out"), st)
     _check(rc, "retopk_qk_rope")
@@ -419,14 +422,14 @@ def qkv_append(rope: QKRope, q, k, v, cache: KVCache, seqlens, seqlens_out=None,
                status=None, stream=None):
     """qk_rope with the keys and values written to rows seqlens[b] + i of the cache; returns q_out.  The lengths go to
     seqlens_out (None: seqlens itself advances).  q, k, v may be slices of one fused projection."""
-    T, Hq, Hkv = q.shape[0], q.shape[1], cache.Hkv
-    B = seqlens.numel()
+    T, Hq = q.shape[:2]
+    Hkv, B = cache.Hkv, seqlens.numel()
     q_out = _empty((T, Hq, 128), q.dtype, q.device, stream) if q_out is None else q_out
     seqlens_out = seqlens if seqlens_out is None else seqlens_out
     st = _call_stream(stream, (q, k, v, cache.k, seqlens, seqlens_out, q_out, cu_tokens, status, *rope.tensors))
-    if tuple(k.shape) != (T, Hkv, 128) or k.shape != v.shape:
+    if k.shape != (T, Hkv, 128) or k.shape != v.shape:
         raise RetopkError(f"k and v: [{T}, {Hkv}, 128] expected, got {tuple(k.shape)} and {tuple(v.shape)}")
-    rc = load().retopk_qkv_append(
+    rc = (_lib or load()).retopk_qkv_append(
         rope._ref, q.data_ptr(), _tokens(q, "q"), k.data_ptr(), _tokens(k, "k"), v.data_ptr(), _tokens(v, "v"),
         _lens(cu_tokens, B + 1, "cu_tokens"), T, B, Hq, cache._holds(B, "qkv_append"), _lens(seqlens, B, "seqlens"),
         _lens(seqlens_out, B, "seqlens_out"), _same(q_out, (T, Hq, 128), "q_out"), _status(status), st)
@@ -439,7 +442,7 @@ def cache_copy(src: KVCache, dst: KVCache, first, last, max_rows: int | None = N
     max_rows bounds last - first (None: the smaller capacity)."""
     B = first.numel()
     st = _call_stream(stream, (src.k, dst.k, first, last, status))
-    rc = load().retopk_cache_copy(src._holds(B, "cache_copy"), dst._holds(B, "cache_copy"), _lens(first, B, "first"),
+    rc = (_lib or load()).retopk_cache_copy(src._holds(B, "cache_copy"), dst._holds(B, "cache_copy"), _lens(first, B, "first"),
                                   _lens(last, B, "last"), B, min(src.rows, dst.rows) if max_rows is None else max_rows,
                                   _status(status), st)
     _check(rc, "retopk_cache_copy")
@@ -457,11 +460,11 @@ def chunk_attention(q, cache: KVCache, seqlens, out=None, cu_tokens=None, scale=
     """Causal attention of q [T, Hq, 128] over a bf16 cache that holds the tokens' own rows (seqlens: rows in all);
     returns out.  cu_tokens: offsets of each sequence's tokens (None: one token each, dense decoding).  lse: optional
     fp32 [T, Hq].  workspace: uint8, chunk_attention_workspace_bytes(...) + 256 (None: allocated for the call)."""
-    T, Hq, Hkv = q.shape[0], q.shape[1], cache.Hkv
-    B = seqlens.numel()
+    T, Hq = q.shape[:2]
+    Hkv, B = cache.Hkv, seqlens.numel()
     out = _empty((T, Hq, 128), q.dtype, q.device, stream) if out is None else out
     st = _call_stream(stream, (q, cache.k, seqlens, out, cu_tokens, lse, workspace, status))
-    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (T, Hq) or not lse.is_contiguous()):
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (T, Hq) or not lse.is_contiguous()):
         raise RetopkError(f"lse: a contiguous fp32 [{T}, {Hq}] tensor expected")
     if out.shape != q.shape:
         raise RetopkError(f"out: {tuple(q.shape)} expected, got {tuple(out.shape)}")
@@ -469,7 +472,7 @@ def chunk_attention(q, cache: KVCache, seqlens, out=None, cu_tokens=None, scale=
         workspace = _empty(chunk_attention_workspace_bytes(T, B, Hq, Hkv) + 256, torch.uint8, q.device, stream)
     wp = workspace.data_ptr()
     up = -wp % 256
-    rc = load().retopk_chunk_attention(
+    rc = (_lib or load()).retopk_chunk_attention(
         q.data_ptr(), _tokens(q, "q"), cache._holds(B, "chunk_attention"), _lens(cu_tokens, B + 1, "cu_tokens"), T, B,
         Hq, _lens(seqlens, B, "seqlens"), 0.0 if scale is None else scale, softcap, window, out.data_ptr(),
         _tokens(out, "out"), None if lse is None else lse.data_ptr(), wp + up,
