@@ -43,6 +43,7 @@ constexpr int kAttnStageBytes = kTile * kD * 2;  // 32 KiB: [half of d][key][64]
 constexpr int kHalfBytes = kAttnStageBytes / 2;
 constexpr int kAttnThreads = 12 * 32;
 constexpr int kMmaWarp = 8, kLoadWarp = 9;
+constexpr int kHalf = kTile / 2;                 // keys of half a tile
 // registers of a thread after the split: 2 x 128 x 208 + 128 x 88 = 384 x 168, what the block is launched with
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
 constexpr float kLazy = 8.f;                     // growth of m, in powers of two, that is left to the accumulators
@@ -530,7 +531,7 @@ __device__ __forceinline__ void matrices(const AttnLaunch &c, AttnShared &sh, Wa
     // S_i of the segment's tile t
     auto scores = [&](int i, int t) {
         const uint32_t u = used + ring_k<TWO>(t), st = u % kAttnStages;
-        if (!warp_wait(sh, &sh.kv_full[st], (u / kAttnStages) & 1, a.status))
+        if ((!TWO || i == 0) && !warp_wait(sh, &sh.kv_full[st], (u / kAttnStages) & 1, a.status))
             return false;
         tc_fence_after();
         if (elected()) {
@@ -564,7 +565,8 @@ __device__ __forceinline__ void matrices(const AttnLaunch &c, AttnShared &sh, Wa
                 if (t >= (i ? m1 : m0) || !ok)
                     continue;
                 const uint32_t u = used + ring_v<TWO>(tile(i, t), nt), st = u % kAttnStages;
-                ok = warp_wait(sh, &sh.kv_full[st], (u / kAttnStages) & 1, a.status);
+                if (!TWO || i == 0)   // (both groups' product takes the tile)
+                    ok = warp_wait(sh, &sh.kv_full[st], (u / kAttnStages) & 1, a.status);
                 // P comes in halves, so that the product begins while the second is made
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
@@ -664,113 +666,171 @@ __device__ __forceinline__ void softmax(const AttnLaunch &c, AttnShared &sh, War
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 }
                 if (work) {
+                    const bool part = j * kTile + kTile - 1 > all_hi || j * kTile < all_lo;
+                    // first half of P to its place; handed over once the second is well under way
+                    auto hand_over = [&] {
+                        tc_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive(p_bar);
+                    };
+                    constexpr int kLead = 4, kPairs = kTile / 2;
                     uint32_t x[kTile];
                     float *f = reinterpret_cast<float *>(x);
-                    // the maximum of the first half is taken while the second is on its way (of the raw scores:
-                    // neither scale nor cap changes their order)
-                    const bool part = j * kTile + kTile - 1 > all_hi || j * kTile < all_lo;
-                    const int last = pos - j * kTile, first = low - j * kTile;
-                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                    tc_ld32(s_addr, x);
-                    tc_ld32(s_addr + 32, x + 32);
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        tc_wait_ld32(x + 64 * q);
-                        tc_wait_ld32(x + 64 * q + 32);
-                        if (q == 0) {
-                            tc_ld32(s_addr + 64, x + 64);
-                            tc_ld32(s_addr + 96, x + 96);
-                        }
-                        if (part) {
-#pragma unroll
-                            for (int e = 64 * q; e < 64 * q + 64; ++e)
-                                f[e] = e <= last && e >= first ? f[e] : -INFINITY;
-                        }
-#pragma unroll
-                        for (int e = 64 * q; e < 64 * q + 64; e += 8) {
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                mx[k] = max3(mx[k], f[e + k], f[e + 4 + k]);
-                        }
-                    }
-                    float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
-                    if (CAP) {
-                        top = top == -INFINITY ? top : capped(top, cap_in, cap2);
-                        // cap tanh(s / cap) of all scores, two reciprocals from one (beyond 2^60 the cap is reached)
-#pragma unroll
-                        for (int e = 0; e < kTile; e += 2) {
-                            const float d0 = 1.f + ex2(fminf(f[e] * cap_in, 60.f)), d1 = 1.f + ex2(fminf(f[e + 1] * cap_in, 60.f));
-                            const float both = rcp(d0 * d1);
-                            f[e] = fmaf(-2.f * cap2, both * d1, cap2);
-                            f[e + 1] = fmaf(-2.f * cap2, both * d0, cap2);
-                        }
-                        if (part) {
-#pragma unroll
-                            for (int e = 0; e < kTile; ++e)
-                                f[e] = e <= last && e >= first ? f[e] : -INFINITY;
-                        }
-                    } else {
-                        top *= scale2;
-                    }
-                    // The maximum that the weights are taken against follows the true one only
-                    // when it has grown by more than 2^8: until then the weights are at most 256, and
-                    // the accumulators need no pass over them.
-                    const bool grow = m != -INFINITY && top > m + kLazy;
-                    if (__any_sync(0xffffffffu, grow)) {
-                        ok = warp_wait(sh, &sh.o_full[i], (done + t - 1) & 1, a.status);
-                        if (!ok)
-                            break;
-                        tc_fence_after();
-                        const float f2 = grow ? ex2(m - top) : 1.f;
-                        l *= f2;
-#pragma unroll 1
-                        for (int q = 0; q < 8; ++q) {
-                            uint32_t o[16];
-                            tc_ld16(o_addr + 16 * q, o);
-                            tc_wait_ld16(o);
-#pragma unroll
-                            for (int e = 0; e < 16; ++e)
-                                o[e] = __float_as_uint(__uint_as_float(o[e]) * f2);
-                            tc_st16(o_addr + 16 * q, o);
-                        }
-                    }
-                    if (grow || m == -INFINITY)
-                        m = top;
-                    const float base = m == -INFINITY ? 0.f : m;
-                    // The weights, two keys at a time, in three steps that overlap: the exponents of
-                    // pair n + kLead, the exponentials of pair n, the sum and the rounding of pair n - kLead.
                     float2 sum[2] = {};
-                    const float2 mul = make_float2(scale2, scale2), add = make_float2(-base, -base);
-                    constexpr int kLead = 4, kPairs = kTile / 2;
+                    float base;
+                    // Two keys at a time, in three steps that overlap: the exponents of pair n + kLead, the
+                    // exponentials of pair n, the sum and the rounding of pair n - kLead.
+                    auto exponents = [&](int n) {
+                        const float2 y = make_float2(f[2 * n], f[2 * n + 1]), less = make_float2(-base, -base);
+                        const float2 z = CAP ? add2(y, less) : fma2(y, make_float2(scale2, scale2), less);
+                        f[2 * n] = z.x, f[2 * n + 1] = z.y;
+                    };
+                    auto exponentials = [&](int n) {
+                        f[2 * n] = ex2(f[2 * n]);
+                        f[2 * n + 1] = ex2(f[2 * n + 1]);
+                    };
+                    auto rounding = [&](int n) {
+                        sum[n & 1] = add2(sum[n & 1], make_float2(f[2 * n], f[2 * n + 1]));
+                        x[n] = bf16x2(f[2 * n], f[2 * n + 1]);
+                    };
+                    // The maximum m that the weights are taken against follows the true one only when
+                    // that has grown by more than 2^8: until then the weights are at most 256, and the
+                    // accumulators need no pass over them.  So a tile that is neither the first nor cut by the
+                    // mask begins with its weights and finds its maximum beside them; if it has grown too
+                    // far after all, nothing has been stored and the tile is begun again.
+                    bool made = false;
+                    if (!CAP && t > 0 && !part) {
+                        base = m == -INFINITY ? 0.f : m;
+                        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                        tc_ld32(s_addr, x);
+                        tc_ld32(s_addr + 32, x + 32);
+                        tc_wait_ld32(x);
+                        tc_wait_ld32(x + 32);
+                        tc_ld32(s_addr + 64, x + 64);
+                        tc_ld32(s_addr + 96, x + 96);
 #pragma unroll
-                    for (int n = -kLead; n < kPairs + kLead; ++n) {
-                        if (n + kLead < kPairs) {
-                            const int e = 2 * (n + kLead);
-                            const float2 y = CAP ? add2(make_float2(f[e], f[e + 1]), add) : fma2(make_float2(f[e], f[e + 1]), mul, add);
-                            f[e] = y.x, f[e + 1] = y.y;
+                        for (int n = -kLead; n < kPairs / 2 - kLead; ++n) {
+                            mx[n & 3] = max3(mx[n & 3], f[2 * (n + kLead)], f[2 * (n + kLead) + 1]);
+                            exponents(n + kLead);
+                            if (n >= 0)
+                                exponentials(n);
+                            if (n >= kLead)
+                                rounding(n - kLead);
+                            if (n == 4) {
+                                tc_wait_ld32(x + 64);
+                                tc_wait_ld32(x + 96);
+                            }
+                            if (n >= 4 && n < 20) {   // the second half's maximum
+                                const int e = kHalf + 4 * (n - 4);
+                                mx[n & 3] = max3(mx[n & 3], f[e], f[e + 1]);
+                                mx[n + 1 & 3] = max3(mx[n + 1 & 3], f[e + 2], f[e + 3]);
+                            }
                         }
-                        if (n >= 0 && n < kPairs) {
-                            f[2 * n] = ex2(f[2 * n]);
-                            f[2 * n + 1] = ex2(f[2 * n + 1]);
-                        }
-                        if (n >= kLead) {
-                            const int e = 2 * (n - kLead);
-                            sum[n & 1] = add2(sum[n & 1], make_float2(f[e], f[e + 1]));
-                            x[e >> 1] = bf16x2(f[e], f[e + 1]);
-                        }
-                        // P takes the columns of scores that are in registers; the first half is handed
-                        // over while the second is made
-                        if (n == kPairs / 2 + kLead - 1)
-                            tc_st32(p_addr, x);
-                        if (n == kPairs * 3 / 4) {
-                            tc_wait_st();
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0)
-                                mbar_arrive(p_bar);
+                        made = !__any_sync(0xffffffffu, max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * scale2 > m + kLazy);
+                        if (made) {
+#pragma unroll
+                            for (int n = kPairs / 2 - kLead; n < kPairs + kLead; ++n) {
+                                if (n + kLead < kPairs)
+                                    exponents(n + kLead);
+                                if (n < kPairs)
+                                    exponentials(n);
+                                rounding(n - kLead);
+                                if (n == kPairs / 2 + kLead - 1)
+                                    tc_st32(p_addr, x);
+                                if (n == kPairs * 3 / 4)
+                                    hand_over();
+                            }
+                            tc_st32(p_addr + 32, x + 32);
+                        } else {
+                            sum[0] = sum[1] = make_float2(0.f, 0.f);
                         }
                     }
-                    tc_st32(p_addr + 32, x + 32);
+                    if (!made) {
+                        // the maximum of the first half is taken while the second is on its way (of the raw
+                        // scores: neither scale nor cap changes their order)
+                        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                        const int last = pos - j * kTile, first = low - j * kTile;
+                        tc_ld32(s_addr, x);
+                        tc_ld32(s_addr + 32, x + 32);
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            tc_wait_ld32(x + 64 * q);
+                            tc_wait_ld32(x + 64 * q + 32);
+                            if (q == 0) {
+                                tc_ld32(s_addr + 64, x + 64);
+                                tc_ld32(s_addr + 96, x + 96);
+                            }
+                            if (part) {
+#pragma unroll
+                                for (int e = 64 * q; e < 64 * q + 64; ++e)
+                                    f[e] = e <= last && e >= first ? f[e] : -INFINITY;
+                            }
+#pragma unroll
+                            for (int e = 64 * q; e < 64 * q + 64; e += 8) {
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    mx[k] = max3(mx[k], f[e + k], f[e + 4 + k]);
+                            }
+                        }
+                        float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
+                        if (CAP) {
+                            top = top == -INFINITY ? top : capped(top, cap_in, cap2);
+                            // cap tanh(s / cap) of all scores, two reciprocals from one (beyond 2^60 the cap is reached)
+#pragma unroll
+                            for (int e = 0; e < kTile; e += 2) {
+                                const float d0 = 1.f + ex2(fminf(f[e] * cap_in, 60.f)), d1 = 1.f + ex2(fminf(f[e + 1] * cap_in, 60.f));
+                                const float both = rcp(d0 * d1);
+                                f[e] = fmaf(-2.f * cap2, both * d1, cap2);
+                                f[e + 1] = fmaf(-2.f * cap2, both * d0, cap2);
+                            }
+                            if (part) {
+#pragma unroll
+                                for (int e = 0; e < kTile; ++e)
+                                    f[e] = e <= last && e >= first ? f[e] : -INFINITY;
+                            }
+                        } else {
+                            top *= scale2;
+                        }
+                        const bool grow = m != -INFINITY && top > m + kLazy;
+                        if (__any_sync(0xffffffffu, grow)) {
+                            ok = warp_wait(sh, &sh.o_full[i], (done + t - 1) & 1, a.status);
+                            if (!ok)
+                                break;
+                            tc_fence_after();
+                            const float f2 = grow ? ex2(m - top) : 1.f;
+                            l *= f2;
+#pragma unroll 1
+                            for (int q = 0; q < 8; ++q) {
+                                uint32_t o[16];
+                                tc_ld16(o_addr + 16 * q, o);
+                                tc_wait_ld16(o);
+#pragma unroll
+                                for (int e = 0; e < 16; ++e)
+                                    o[e] = __float_as_uint(__uint_as_float(o[e]) * f2);
+                                tc_st16(o_addr + 16 * q, o);
+                            }
+                        }
+                        if (grow || m == -INFINITY)
+                            m = top;
+                        base = m == -INFINITY ? 0.f : m;
+#pragma unroll
+                        for (int n = -kLead; n < kPairs + kLead; ++n) {
+                            if (n + kLead < kPairs)
+                                exponents(n + kLead);
+                            if (n >= 0 && n < kPairs)
+                                exponentials(n);
+                            if (n >= kLead)
+                                rounding(n - kLead);
+                            // P takes the columns of scores that are in registers
+                            if (n == kPairs / 2 + kLead - 1)
+                                tc_st32(p_addr, x);
+                            if (n == kPairs * 3 / 4)
+                                hand_over();
+                        }
+                        tc_st32(p_addr + 32, x + 32);
+                    }
                     const float2 both = add2(sum[0], sum[1]);
                     l = live ? l + both.x + both.y : 0.f;
                     m = live ? m : -INFINITY;
