@@ -11,12 +11,13 @@
 // one KV head (the row of token t, head g is t G + g), so every head of the group uses
 // the K / V rows that were loaded once.
 //
-// Roles (12 warps, one CTA per SM; two of them idle): two groups of four softmax
+// Roles (12 warps, one CTA per SM; one of them idle): two groups of four softmax
 // warps, each thread one row of its tile, whose 128 scores stay in registers; one
 // thread that issues the matrix instructions (S = Q K^T from shared memory, O += P V
-// with P in tensor memory); one warp that issues the copies.  Shared memory leaves
-// the L1 no room, so a spilled register costs a trip to the L2: what a warp keeps
-// between tiles is small, and its place in the share lies in shared memory.  Tensor memory: S_0, S_1 (P_i takes the first half of
+// with P in tensor memory); one warp that issues the copies; one that walks the
+// CTA's share and tells the others, ahead of time, the segments of items in it.  Shared
+// memory leaves the L1 no room, so a spilled register costs a trip to the L2: what a
+// warp keeps between tiles is small.  Tensor memory: S_0, S_1 (P_i takes the first half of
 // S_i's columns), O_0, O_1, 128 columns each.
 //   two tiles    (TWO):  the groups hold neighbouring tiles of tokens and share
 //                every K / V tile.  For prompts.
@@ -42,7 +43,8 @@ constexpr int kAttnStages = 5;                   // K / V tiles in flight
 constexpr int kAttnStageBytes = kTile * kD * 2;  // 32 KiB: [half of d][key][64]
 constexpr int kHalfBytes = kAttnStageBytes / 2;
 constexpr int kAttnThreads = 12 * 32;
-constexpr int kMmaWarp = 8, kLoadWarp = 9;
+constexpr int kMmaWarp = 8, kLoadWarp = 9, kWalkWarp = 10;
+constexpr int kSegments = 4;                     // known ahead
 constexpr int kHalf = kTile / 2;                 // keys of half a tile
 // registers of a thread after the split: 2 x 128 x 208 + 128 x 88 = 384 x 168, what the block is launched with
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
@@ -110,7 +112,7 @@ __device__ __forceinline__ long long weight(const AttnArgs &a, const Plan &p, co
 }
 
 // The place u units behind the beginning of sequence b.
-__device__ Place place_in(const AttnArgs &a, const Plan &p, const Seq &s, int b, long long u)
+__device__ __forceinline__ Place place_in(const AttnArgs &a, const Plan &p, const Seq &s, int b, long long u)
 {
     const int nb = blocks_of(p, s);
     const long long each = weight(a, p, s, nb);
@@ -201,23 +203,6 @@ __device__ __forceinline__ bool next_segment(const AttnArgs &a, const Plan &p, W
     }
 }
 
-// A warp's place in its share, in shared memory.
-struct WarpWalk {
-    Walk w;
-    Segment s;
-};
-
-// The next segment, found by one lane for its warp (all lanes call).
-__device__ __forceinline__ bool next_of_warp(const AttnArgs &a, const Plan &p, WarpWalk &x)
-{
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0)
-        x.s.more = next_segment(a, p, x.w, x.s);
-    __syncwarp();
-    return x.s.more != 0;
-}
-
-
 struct AttnShared {
     uint64_t kv_full[kAttnStages], kv_empty[kAttnStages];
     uint64_t q_full, q_empty;
@@ -227,7 +212,8 @@ struct AttnShared {
     Place bound[2];
     Seq first;                 // the sequence that bound[0] was found in
     int first_b;
-    WarpWalk walk[kLoadWarp + 1];
+    Segment segments[kSegments];
+    uint64_t seg_full[kSegments], seg_empty[kSegments];
     long long sums[kAttnThreads / 32 + 1];
     uint32_t tmem;
     int failed;
@@ -260,6 +246,37 @@ __device__ __forceinline__ bool wait(AttnShared &sh, uint64_t *bar, uint32_t par
 __device__ __forceinline__ bool warp_wait(AttnShared &sh, uint64_t *bar, uint32_t parity, uint32_t *status)
 {
     return __all_sync(0xffffffffu, wait(sh, bar, parity, status));
+}
+
+// Segment number n of the share; false when there is none (or a wait ran out).
+__device__ __forceinline__ bool segment(AttnShared &sh, uint32_t n, uint32_t *status)
+{
+    const uint32_t k = n % kSegments;
+    return warp_wait(sh, &sh.seg_full[k], (n / kSegments) & 1, status) && sh.segments[k].more;
+}
+
+// This warp is done with it.
+__device__ __forceinline__ void segment_done(AttnShared &sh, uint32_t n)
+{
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0)
+        mbar_arrive(&sh.seg_empty[n % kSegments]);
+}
+
+// ---- the walk: one lane ------------------------------------------------------------
+__device__ __forceinline__ void walk_share(const AttnArgs &a, const Plan &plan, AttnShared &sh)
+{
+    Walk w{sh.bound[0], sh.bound[1], sh.first, sh.first_b};
+    for (uint32_t n = 0;; ++n) {
+        const uint32_t k = n % kSegments;
+        if (n >= kSegments && !wait(sh, &sh.seg_empty[k], (n / kSegments - 1) & 1, a.status))
+            return;
+        const int more = next_segment(a, plan, w, sh.segments[k]);
+        sh.segments[k].more = more;
+        mbar_arrive(&sh.seg_full[k]);
+        if (!more)
+            return;
+    }
 }
 
 // ---- tensor memory and matrix instructions (inline PTX) -------------------------
@@ -416,6 +433,8 @@ __device__ __forceinline__ int ring_v(int t, int nt)
     return TWO || nt == 1 ? 2 * t + 1 : 2 + t + min(t, nt - 2);
 }
 
+constexpr int kMaxShares = 1024;   // CTAs of a launch, one for each SM
+
 // ---- workspace ----------------------------------------------------------------------
 // Places of the n + 1 bounds, then for each CTA two parts (0: of an item that began in an
 // earlier share, 1: of an item that goes on in the next) of `rows` rows: (m, l) pairs, and
@@ -431,22 +450,23 @@ struct AttnLaunch {
     AttnArgs a;
     Plan plan;
     Parts parts;
-    int chunk;   // rows of one K / V copy (a page's, 128 at most)
+    int chunk;    // rows of one K / V copy (a page's, 128 at most)
+    int shares;   // CTAs
 };
 
 // ---- the copies --------------------------------------------------------------------
 template <bool TWO>
-__device__ __forceinline__ void copies(const AttnLaunch &c, AttnShared &sh, WarpWalk &walk, const CUtensorMap &qmap,
+__device__ __forceinline__ void copies(const AttnLaunch &c, AttnShared &sh, const CUtensorMap &qmap,
                                        const CUtensorMap &kmap, const CUtensorMap &vmap, uint32_t qbuf, uint32_t ring,
                                        int lane)
 {
     const AttnArgs &a = c.a;
-    const Segment &s = walk.s;
     const int Hkv = a.cache.n_kv_heads, tile_tokens = kTile / a.G;
     const int half = lane & 1, piece = lane >> 1, pieces = kTile / c.chunk;   // this lane's copy
     bool ok = true;
-    uint32_t used = 0, issued = 0, segs = 0;   // ring slots before this segment, copied so far; Q copies
-    while (ok && next_of_warp(a, c.plan, walk)) {
+    uint32_t used = 0, issued = 0, segs = 0, q_copies = 0;   // ring slots before this segment, copied so far
+    while (ok && segment(sh, segs, a.status)) {
+        const Segment &s = sh.segments[segs % kSegments];
         const int nt = s.j1 - s.j0, L = s.seq.L, j0 = s.j0, hk = s.hk, b = s.b;
         if (lane == 0) {
             ok = segs == 0 || wait(sh, &sh.q_empty, (segs - 1) & 1, a.status);
@@ -457,11 +477,10 @@ __device__ __forceinline__ void copies(const AttnLaunch &c, AttnShared &sh, Warp
                     for (int h = 0; h < 2; ++h)
                         load_3d(qbuf + i * kAttnStageBytes + h * kHalfBytes, &qmap, h * 64, hk * a.G, t0 + i * tile_tokens,
                                 &sh.q_full);
-                ++segs;
+                ++q_copies;
             }
         }
         ok = __shfl_sync(0xffffffffu, (int)ok, 0);
-        segs = __shfl_sync(0xffffffffu, segs, 0);
         // the ring's order: K ahead of V by one tile (or two, one for each stream)
         const int ahead = TWO ? 1 : 2;
         for (int x = -ahead; x < nt && ok; ++x) {
@@ -503,6 +522,7 @@ __device__ __forceinline__ void copies(const AttnLaunch &c, AttnShared &sh, Warp
             }
         }
         used += 2 * nt;
+        segment_done(sh, segs++);
     }
     // a wait ran out: the copies in flight are waited for before the memory goes
     if (*reinterpret_cast<volatile int *>(&sh.failed) && lane == 0) {
@@ -510,7 +530,7 @@ __device__ __forceinline__ void copies(const AttnLaunch &c, AttnShared &sh, Warp
         for (uint32_t u = issued > kAttnStages ? issued - kAttnStages : 0; u < issued; ++u)
             while (!mbar_try_wait(&sh.kv_full[u % kAttnStages], (u / kAttnStages) & 1) && clock64() - t0 < kWaitCycles)
                 ;
-        while (segs && !mbar_try_wait(&sh.q_full, (segs - 1) & 1) && clock64() - t0 < kWaitCycles)
+        while (q_copies && !mbar_try_wait(&sh.q_full, (q_copies - 1) & 1) && clock64() - t0 < kWaitCycles)
             ;
     }
     __syncwarp();
@@ -521,7 +541,7 @@ __device__ __forceinline__ void copies(const AttnLaunch &c, AttnShared &sh, Warp
 // stays the same for all lanes, so that it can live in uniform registers (an
 // instruction issued from a divergent branch cost 110 cycles in place of 64).
 template <bool TWO>
-__device__ __forceinline__ void matrices(const AttnLaunch &c, AttnShared &sh, WarpWalk &walk, uint32_t qbuf, uint32_t ring,
+__device__ __forceinline__ void matrices(const AttnLaunch &c, AttnShared &sh, uint32_t qbuf, uint32_t ring,
                                          uint32_t tmem_any)
 {
     const AttnArgs &a = c.a;
@@ -548,8 +568,8 @@ __device__ __forceinline__ void matrices(const AttnLaunch &c, AttnShared &sh, Wa
         __syncwarp();
         return true;
     };
-    while (ok && next_of_warp(a, c.plan, walk)) {
-        const int nt = __shfl_sync(0xffffffffu, walk.s.j1 - walk.s.j0, 0);
+    while (ok && segment(sh, segs, a.status)) {
+        const int nt = __shfl_sync(0xffffffffu, sh.segments[segs % kSegments].j1 - sh.segments[segs % kSegments].j0, 0);
         const int m0 = TWO ? nt : (nt + 1) / 2, m1 = TWO ? nt : nt / 2;
         auto tile = [&](int i, int t) { return TWO ? t : 2 * t + i; };
         ok = warp_wait(sh, &sh.q_full, segs & 1, a.status);
@@ -597,7 +617,7 @@ __device__ __forceinline__ void matrices(const AttnLaunch &c, AttnShared &sh, Wa
         used += 2 * nt;
         done0 += m0;
         done1 += m1;
-        ++segs;
+        segment_done(sh, segs++);
     }
     if (!ok && elected()) {   // a wait ran out: the instructions in flight end before the tensor memory goes
         tc_commit(&sh.drained);
@@ -610,11 +630,10 @@ __device__ __forceinline__ void matrices(const AttnLaunch &c, AttnShared &sh, Wa
 
 // ---- softmax: group i, row r --------------------------------------------------------------
 template <bool TWO, bool CAP>
-__device__ __forceinline__ void softmax(const AttnLaunch &c, AttnShared &sh, WarpWalk &walk, float *other, uint32_t ring,
+__device__ __forceinline__ void softmax(const AttnLaunch &c, AttnShared &sh, float *other, uint32_t ring,
                                         uint32_t tmem, int warp, int lane)
 {
     const AttnArgs &a = c.a;
-    const Segment &s = walk.s;
     const int i = warp >> 2, r = (warp & 3) * 32 + lane, G = a.G;
     const uint32_t s_addr = tmem + i * kTile + ((uint32_t)(warp & 3) << 21), o_addr = s_addr + 2 * kTile;
     const float scale2 = a.scale * 1.4426950408889634f;     // scores in powers of two
@@ -622,7 +641,8 @@ __device__ __forceinline__ void softmax(const AttnLaunch &c, AttnShared &sh, War
     const float cap_in = CAP ? 2.f * scale2 / a.softcap : 0.f;   // e^2y = 2^(cap_in s)
     bool ok = true;
     uint32_t used = 0, done = 0, segs = 0;
-    while (ok && next_of_warp(a, c.plan, walk)) {
+    while (ok && segment(sh, segs, a.status)) {
+        const Segment &s = sh.segments[segs % kSegments];
         const int nt = s.j1 - s.j0, m_tiles = TWO ? nt : (nt + 1 - i) / 2;
         const int tok = s.k * c.plan.tokens + (TWO ? i * (kTile / G) : 0) + r / G;   // in the sequence
         const bool valid = r < kTile / G * G && tok < s.seq.n;
@@ -930,7 +950,7 @@ __device__ __forceinline__ void softmax(const AttnLaunch &c, AttnShared &sh, War
                 a.lse[t * a.Hq + head] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
         }
         used += 2 * nt;
-        ++segs;
+        segment_done(sh, segs++);
         tc_fence_before();
     }
 }
@@ -961,6 +981,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             mbar_init(&sh.p_full[i][0], 4);
             mbar_init(&sh.p_full[i][1], 4);
             mbar_init(&sh.o_full[i], 1);
+        }
+        for (int s = 0; s < kSegments; ++s) {
+            mbar_init(&sh.seg_full[s], 1);
+            mbar_init(&sh.seg_empty[s], kLoadWarp + 1);
         }
         mbar_init(&sh.x_full, 4);
         mbar_init(&sh.x_empty, 4);
@@ -1031,13 +1055,17 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const long long share = (long long)__umul64hi((unsigned long long)total, plan.inverse) + 1;
     const long long u0 = min(share * blockIdx.x, total), u1 = min(share * (blockIdx.x + 1), total);
     auto find = [&](int b, const Seq &q, long long from, long long weight_of) {
-        if (weight_of > 0 && u0 >= from && u0 < from + weight_of) {
-            sh.bound[0] = place_in(a, plan, q, b, u0 - from);
-            sh.first = q;
-            sh.first_b = b;
+#pragma unroll 1
+        for (int k = 0; k < 2; ++k) {
+            const long long u = k ? u1 : u0;
+            if (weight_of > 0 && u >= from && u < from + weight_of) {
+                sh.bound[k] = place_in(a, plan, q, b, u - from);
+                if (k == 0) {
+                    sh.first = q;
+                    sh.first_b = b;
+                }
+            }
         }
-        if (weight_of > 0 && u1 >= from && u1 < from + weight_of)
-            sh.bound[1] = place_in(a, plan, q, b, u1 - from);
     };
     find(tid, mine, off + up - my_weight, my_weight);
     for (int base = kAttnThreads; base < a.B; base += kAttnThreads) {
@@ -1071,17 +1099,17 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         if (blockIdx.x == gridDim.x - 1)
             c.parts.bound[gridDim.x] = sh.bound[1];
     }
-    if (lane == 0 && warp <= kLoadWarp)
-        sh.walk[warp].w = Walk{sh.bound[0], sh.bound[1], sh.first, sh.first_b};
     if (warp < kMmaWarp) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-        softmax<TWO, CAP>(c, sh, sh.walk[warp], reinterpret_cast<float *>(attn_smem + kAttnStageBytes), ring, tmem, warp, lane);
+        softmax<TWO, CAP>(c, sh, reinterpret_cast<float *>(attn_smem + kAttnStageBytes), ring, tmem, warp, lane);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         if (warp == kLoadWarp)
-            copies<TWO>(c, sh, sh.walk[warp], qmap, kmap, vmap, qbuf, ring, lane);
+            copies<TWO>(c, sh, qmap, kmap, vmap, qbuf, ring, lane);
         else if (warp == kMmaWarp)
-            matrices<TWO>(c, sh, sh.walk[warp], qbuf, ring, tmem);
+            matrices<TWO>(c, sh, qbuf, ring, tmem);
+        else if (warp == kWalkWarp && lane == 0)
+            walk_share(a, plan, sh);
     }
     tc_fence_before();
     __syncthreads();
@@ -1097,6 +1125,7 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnLaunch c, int share
 {
     __shared__ float4 sum[8][32];
     __shared__ float2 ml_of[8];
+    __shared__ uint8_t there[kMaxShares];   // a share between two equal cuts has no part
     pdl_wait();
     pdl_trigger();
     const AttnArgs &a = c.a;
@@ -1106,13 +1135,18 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnLaunch c, int share
         return;
     // parts: share x - 1's part 1, then part 0 of shares x, x + 1, ... while they begin in the item
     const Seq s = sequence(a, at.b);
-    int end = x + 1, more;
+    int n = 1, more;
     do {
-        const int y = end + (int)threadIdx.x;
-        more = __syncthreads_count(y < shares && same_item(c.parts.bound[y], at));
-        end += more;
+        const int i = n + (int)threadIdx.x, y = x - 1 + i;   // part i is of share y
+        bool in = false;
+        if (y < shares) {
+            const Place p0 = c.parts.bound[y], p1 = c.parts.bound[y + 1];
+            in = same_item(p0, at);
+            there[i] = !same_item(p1, at) || p1.cut > p0.cut;
+        }
+        more = __syncthreads_count(in);
+        n += more;
     } while (more == 256);
-    const int n = end - x + 1;
     const bool together = n > 8;
     const int tile_tokens = kTile / a.G, per_tile = tile_tokens * a.G, first = at.k * c.plan.tokens;
     const int rows = min(TWO ? 2 * per_tile : per_tile, (s.n - first) * a.G);
@@ -1134,15 +1168,12 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnLaunch c, int share
             acc.w = fmaf(acc.w, f1, f2 != 0.f ? o.w * f2 : 0.f);
             m = mm;
         };
-#pragma unroll 4
+#pragma unroll 5
         for (int i = together ? warp : 0; i < n; i += together ? 8 : 1) {
-            // a share between two equal cuts has no part
-            const int y = x - 1 + i;
-            const Place p0 = c.parts.bound[y], p1 = c.parts.bound[y + 1];
-            const bool there = i == 0 || !same_item(p1, at) || p1.cut > p0.cut;
+            const bool has = i == 0 || there[i];
             const float2 ml = c.parts.ml[part(i) * c.parts.rows + r];
             const float4 o = c.parts.o[(part(i) * (kD / 4) + lane) * c.parts.rows + r];
-            add(there ? ml.x : -INFINITY, there ? ml.y : 0.f, o);
+            add(has ? ml.x : -INFINITY, has ? ml.y : 0.f, o);
         }
         if (together) {
             sum[warp][lane] = acc;
@@ -1181,7 +1212,7 @@ static int part_rows(int T, int G, bool two)
 
 static size_t carve(int T, int B, int Hq, int Hkv, char *ws, Parts *p)
 {
-    const int G = Hq / Hkv, n = sm_count();
+    const int G = Hq / Hkv, n = std::min(sm_count(), kMaxShares);
     const size_t rows = part_rows(T, G, two_tiles(T, B, G));
     const size_t o_ml = ((n + 1) * sizeof(Place) + 255) / 256 * 256;
     const size_t o_o = o_ml + (2 * n * rows * sizeof(float2) + 255) / 256 * 256;
@@ -1211,10 +1242,13 @@ template <bool TWO>
 static cudaError_t launch_mode(const CUtensorMap &qm, const CUtensorMap &km, const CUtensorMap &vm, const AttnLaunch &c,
                                cudaStream_t st)
 {
-    const int n = sm_count();
+    // no item of four tiles or fewer is cut, so a cache that holds no more needs no join
+    // (and no more CTAs than there may be items)
+    const bool cuts = c.a.capacity > 4 * kTile;
+    const int n = c.shares;
     auto kernel = c.a.softcap > 0.f ? chunk_attention_kernel<TWO, true> : chunk_attention_kernel<TWO, false>;
     cudaError_t e = launch_pdl(kernel, dim3(n), dim3(kAttnThreads), kAttnSmem, st, 1, qm, km, vm, c);
-    if (e != cudaSuccess || n < 2)
+    if (e != cudaSuccess || n < 2 || !cuts)
         return e;
     return launch_pdl(join_kernel<TWO>, dim3(n - 1, TWO ? 16 : 8), dim3(256), 0, st, 1, c, n);
 }
@@ -1227,7 +1261,10 @@ cudaError_t launch_chunk_attention(const AttnArgs &a, cudaStream_t st)
     const bool two = two_tiles(a.T, a.B, a.G);
     c.plan.tokens = two ? 2 * tokens : tokens;
     c.plan.overhead = two ? 128 : 256;
-    c.plan.inverse = ~0ull / (unsigned long long)sm_count();
+    c.shares = std::min(sm_count(), kMaxShares);
+    if (a.capacity <= 4 * kTile)
+        c.shares = (int)std::min<long long>(c.shares, std::min<long long>(a.T, a.T / c.plan.tokens + a.B) * Hkv);
+    c.plan.inverse = ~0ull / (unsigned long long)c.shares;
     carve(a.T, a.B, a.Hq, Hkv, static_cast<char *>(a.ws), &c.parts);
     c.chunk = kTile;
     if (a.cache.table)
