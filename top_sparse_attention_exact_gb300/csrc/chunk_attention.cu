@@ -31,6 +31,8 @@
 // and end inside an item.  A CTA then leaves its unnormalised rows in the
 // workspace, and the join kernel adds them up.  Shares, and with them the order of
 // every sum, depend on the lengths alone.
+#include <math.h>
+
 #include <algorithm>
 
 #include "prompt.cuh"
@@ -48,6 +50,10 @@ constexpr int kSegments = 4;                     // known ahead
 constexpr int kHalf = kTile / 2;                 // keys of half a tile
 // registers of a thread after the split: 2 x 128 x 208 + 128 x 88 = 384 x 168, what the block is launched with
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
+// Weight of an item beside its keys: what beginning and ending it costs, in keys.  (A prompt
+// of 8192 tokens: 494 us with 128, 386 with 512, 399 with 1024; 128 sequences of 1500 keys: 135 us with
+// 256, 126 with 512, 128 with 1024.)
+constexpr int kItemWeight = 512;
 constexpr float kLazy = 8.f;                     // growth of m, in powers of two, that is left to the accumulators
 
 // Where a share begins: an item and the number of its K / V tiles that belong
@@ -63,7 +69,6 @@ __device__ __forceinline__ bool same_item(const Place &x, const Place &y)
 
 struct Plan {
     int tokens;                    // tokens of a block (two tiles', or one tile's)
-    int overhead;                  // weight of an item beside its keys
     unsigned long long inverse;    // 2^64 / shares
 };
 
@@ -100,11 +105,11 @@ __device__ __forceinline__ int blocks_of(const Plan &p, const Seq &s) { return (
 // last key's position, bounded by the window.
 __device__ __forceinline__ long long weight(const AttnArgs &a, const Plan &p, const Seq &s, int k)
 {
-    const int first = max(0, s.L - s.n) + min(p.tokens, s.n) + p.overhead;
+    const int first = max(0, s.L - s.n) + min(p.tokens, s.n) + kItemWeight;
     int grow = k;
     long long flat = 0;
     if (a.window > 0 && a.window < kMaxLen) {
-        const int most = a.window + p.tokens + kTile + p.overhead;
+        const int most = a.window + p.tokens + kTile + kItemWeight;
         grow = most <= first ? 0 : min(k, (most - first) / p.tokens + 1);
         flat = (long long)(k - grow) * most;
     }
@@ -452,6 +457,10 @@ struct AttnLaunch {
     Parts parts;
     int chunk;    // rows of one K / V copy (a page's, 128 at most)
     int shares;   // CTAs
+    // tanh(y) = y (1 + t (b_0 + b_1 t + b_2 t^2 + b_3 t^3)), t = y^2, for |y| <= 1/2: b fitted at Chebyshev
+    // nodes for the smallest largest error (2e-8, and 1e-7 in fp32).  Here for raw scores: y = s scale / softcap,
+    // so cap_poly[i] = b_i (scale / softcap)^(2 i + 2); cap_near: the largest |s|.
+    float cap_poly[4], cap_near;
 };
 
 // ---- the copies --------------------------------------------------------------------
@@ -771,6 +780,7 @@ __device__ __forceinline__ void softmax(const AttnLaunch &c, AttnShared &sh, flo
                         // the maximum of the first half is taken while the second is on its way (of the raw
                         // scores: neither scale nor cap changes their order)
                         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                        float size = 0.f, size2 = 0.f;   // largest |score|
                         const int last = pos - j * kTile, first = low - j * kTile;
                         tc_ld32(s_addr, x);
                         tc_ld32(s_addr + 32, x + 32);
@@ -792,11 +802,30 @@ __device__ __forceinline__ void softmax(const AttnLaunch &c, AttnShared &sh, flo
 #pragma unroll
                                 for (int k = 0; k < 4; ++k)
                                     mx[k] = max3(mx[k], f[e + k], f[e + 4 + k]);
+                                if (CAP) {
+                                    size = max3(size, fabsf(f[e]), fabsf(f[e + 1]));
+                                    size2 = max3(size2, fabsf(f[e + 2]), fabsf(f[e + 3]));
+                                    size = max3(size, fabsf(f[e + 4]), fabsf(f[e + 5]));
+                                    size2 = max3(size2, fabsf(f[e + 6]), fabsf(f[e + 7]));
+                                }
                             }
                         }
+                        size = fmaxf(size, size2);
                         float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
                         if (CAP) {
                             top = top == -INFINITY ? top : capped(top, cap_in, cap2);
+                            if (!__any_sync(0xffffffffu, valid && size > c.cap_near)) {
+                                // |s / cap| <= 1/2 throughout: an odd polynomial
+                                const float2 one = make_float2(1.f, 1.f), c0 = make_float2(c.cap_poly[0], c.cap_poly[0]),
+                                             c1 = make_float2(c.cap_poly[1], c.cap_poly[1]), c2 = make_float2(c.cap_poly[2], c.cap_poly[2]),
+                                             c3 = make_float2(c.cap_poly[3], c.cap_poly[3]), by = make_float2(scale2, scale2);
+#pragma unroll
+                                for (int e = 0; e < kTile; e += 2) {
+                                    const float2 y = make_float2(f[e], f[e + 1]), t2 = mul2(y, y);
+                                    const float2 z = mul2(mul2(y, by), fma2(fma2(fma2(fma2(c3, t2, c2), t2, c1), t2, c0), t2, one));
+                                    f[e] = z.x, f[e + 1] = z.y;
+                                }
+                            } else
                             // cap tanh(s / cap) of all scores, two reciprocals from one (beyond 2^60 the cap is reached)
 #pragma unroll
                             for (int e = 0; e < kTile; e += 2) {
@@ -1260,12 +1289,18 @@ cudaError_t launch_chunk_attention(const AttnArgs &a, cudaStream_t st)
     const int Hkv = a.cache.n_kv_heads, tokens = kTile / a.G;
     const bool two = two_tiles(a.T, a.B, a.G);
     c.plan.tokens = two ? 2 * tokens : tokens;
-    c.plan.overhead = two ? 128 : 256;
     c.shares = std::min(sm_count(), kMaxShares);
     if (a.capacity <= 4 * kTile)
         c.shares = (int)std::min<long long>(c.shares, std::min<long long>(a.T, a.T / c.plan.tokens + a.B) * Hkv);
     c.plan.inverse = ~0ull / (unsigned long long)c.shares;
     carve(a.T, a.B, a.Hq, Hkv, static_cast<char *>(a.ws), &c.parts);
+    if (a.softcap > 0.f) {
+        const double b[4] = {-0.333331435918808, 0.13325878977775574, -0.05304549261927605, 0.01724149100482464};
+        const double y = (double)a.scale / a.softcap;
+        for (int i = 0; i < 4; ++i)
+            c.cap_poly[i] = (float)(b[i] * pow(y, 2 * i + 2));
+        c.cap_near = (float)(0.5 / y);
+    }
     c.chunk = kTile;
     if (a.cache.table)
         while (a.cache.page_rows % c.chunk)
