@@ -457,10 +457,10 @@ struct AttnLaunch {
     Parts parts;
     int chunk;    // rows of one K / V copy (a page's, 128 at most)
     int shares;   // CTAs
-    // tanh(y) = y (1 + t (b_0 + b_1 t + b_2 t^2 + b_3 t^3)), t = y^2, for |y| <= 1/2: b fitted at Chebyshev
-    // nodes for the smallest largest error (2e-8, and 1e-7 in fp32).  Here for raw scores: y = s scale / softcap,
+    // tanh(y) = y (1 + t (b_0 + b_1 t + b_2 t^2)), t = y^2, for |y| <= 1/2: b fitted at Chebyshev nodes for
+    // the smallest largest error (6.4e-7 of the value).  Here for raw scores: y = s scale / softcap,
     // so cap_poly[i] = b_i (scale / softcap)^(2 i + 2); cap_near: the largest |s|.
-    float cap_poly[4], cap_near;
+    float cap_poly[3], cap_near;
 };
 
 // ---- the copies --------------------------------------------------------------------
@@ -490,9 +490,30 @@ __device__ __forceinline__ void copies(const AttnLaunch &c, AttnShared &sh, cons
             }
         }
         ok = __shfl_sync(0xffffffffu, (int)ok, 0);
-        // the ring's order: K ahead of V by one tile (or two, one for each stream)
-        const int ahead = TWO ? 1 : 2;
+        // where this lane's rows of tile t lie: the copy's coordinates in a page and among pages
+        auto look = [&](int t) {
+            int2 at = make_int2(0, a.cache.n_pages * Hkv);   // outside: read as zeros
+            const int pos = (j0 + t) * kTile + piece * c.chunk;
+            if (t < nt && piece < pieces && pos < L) {
+                int page = b;
+                at.x = pos;
+                if (a.cache.table) {
+                    page = a.cache.table[(long long)b * a.cache.table_width + pos / a.cache.page_rows];
+                    at.x = pos % a.cache.page_rows;
+                }
+                if ((uint32_t)page < (uint32_t)a.cache.n_pages)
+                    at.y = page * Hkv + hk;
+                else if (a.status)
+                    atomicOr(a.status, RETOPK_STATUS_BAD_PAGE);
+            }
+            return at;
+        };
+        // The ring's order: K ahead of V by one tile (or two, one for each stream).  A tile is looked up
+        // one step before its K, and once for both.
+        constexpr int ahead = TWO ? 1 : 2;
+        int2 at[3] = {look(0), look(0), look(0)};   // of tiles x, x + 1, x + 2
         for (int x = -ahead; x < nt && ok; ++x) {
+            const int2 next = look(x + ahead + 1);
 #pragma unroll
             for (int isk = 0; isk < 2; ++isk) {
                 const int t = isk ? x + ahead : x;
@@ -500,20 +521,6 @@ __device__ __forceinline__ void copies(const AttnLaunch &c, AttnShared &sh, cons
                     continue;
                 const uint32_t u = used + (isk ? ring_k<TWO>(t) : ring_v<TWO>(t, nt));
                 const int st = u % kAttnStages;
-                const int pos = (j0 + t) * kTile + piece * c.chunk;
-                int z = a.cache.n_pages * Hkv, y = 0;   // outside: read as zeros
-                if (piece < pieces && pos < L) {
-                    int page = b;
-                    y = pos;
-                    if (a.cache.table) {
-                        page = a.cache.table[(long long)b * a.cache.table_width + pos / a.cache.page_rows];
-                        y = pos % a.cache.page_rows;
-                    }
-                    if ((uint32_t)page < (uint32_t)a.cache.n_pages)
-                        z = page * Hkv + hk;
-                    else if (a.status)
-                        atomicOr(a.status, RETOPK_STATUS_BAD_PAGE);
-                }
                 int good = 1;
                 if (lane == 0) {
                     if (u >= kAttnStages)
@@ -526,9 +533,13 @@ __device__ __forceinline__ void copies(const AttnLaunch &c, AttnShared &sh, cons
                     issued = u + 1;
                     if (piece < pieces)
                         load_3d(ring + st * kAttnStageBytes + half * kHalfBytes + piece * c.chunk * 128,
-                                isk ? &kmap : &vmap, half * 64, y, z, &sh.kv_full[st]);
+                                isk ? &kmap : &vmap, half * 64, at[isk ? ahead : 0].x, at[isk ? ahead : 0].y,
+                                &sh.kv_full[st]);
                 }
             }
+            at[0] = at[1];
+            at[1] = TWO ? next : at[2];
+            at[2] = next;
         }
         used += 2 * nt;
         segment_done(sh, segs++);
@@ -713,7 +724,7 @@ __device__ __forceinline__ void softmax(const AttnLaunch &c, AttnShared &sh, flo
                     // exponentials of pair n, the sum and the rounding of pair n - kLead.
                     auto exponents = [&](int n) {
                         const float2 y = make_float2(f[2 * n], f[2 * n + 1]), less = make_float2(-base, -base);
-                        const float2 z = CAP ? add2(y, less) : fma2(y, make_float2(scale2, scale2), less);
+                        const float2 z = fma2(y, make_float2(scale2, scale2), less);
                         f[2 * n] = z.x, f[2 * n + 1] = z.y;
                     };
                     auto exponentials = [&](int n) {
@@ -729,6 +740,31 @@ __device__ __forceinline__ void softmax(const AttnLaunch &c, AttnShared &sh, flo
                     // accumulators need no pass over them.  So a tile that is neither the first nor cut by the
                     // mask begins with its weights and finds its maximum beside them; if it has grown too
                     // far after all, nothing has been stored and the tile is begun again.
+                    // m up to the tile's maximum where that has grown too far, and the accumulators with it;
+                    // false when a wait ran out
+                    auto raise = [&](float top) {
+                        const bool grow = m != -INFINITY && top > m + kLazy;
+                        if (__any_sync(0xffffffffu, grow)) {
+                            if (!warp_wait(sh, &sh.o_full[i], (done + t - 1) & 1, a.status))
+                                return ok = false;
+                            tc_fence_after();
+                            const float f2 = grow ? ex2(m - top) : 1.f;
+                            l *= f2;
+#pragma unroll 1
+                            for (int q = 0; q < 8; ++q) {
+                                uint32_t o[16];
+                                tc_ld16(o_addr + 16 * q, o);
+                                tc_wait_ld16(o);
+#pragma unroll
+                                for (int e = 0; e < 16; ++e)
+                                    o[e] = __float_as_uint(__uint_as_float(o[e]) * f2);
+                                tc_st16(o_addr + 16 * q, o);
+                            }
+                        }
+                        if (grow || m == -INFINITY)
+                            m = top;
+                        return true;
+                    };
                     bool made = false;
                     if (!CAP && t > 0 && !part) {
                         base = m == -INFINITY ? 0.f : m;
@@ -776,11 +812,84 @@ __device__ __forceinline__ void softmax(const AttnLaunch &c, AttnShared &sh, flo
                             sum[0] = sum[1] = make_float2(0.f, 0.f);
                         }
                     }
-                    if (!made) {
-                        // the maximum of the first half is taken while the second is on its way (of the raw
-                        // scores: neither scale nor cap changes their order)
+                    if constexpr (CAP) {
+                        // Capped scores: half a row at a time, read once for the maximum (of the raw scores: the cap
+                        // does not change their order) and once for the weights.  (All 128 at once are
+                        // twice the instructions, more than the caches near the warps hold: 82 us against 76 for 1000
+                        // tokens in windows of 4096 keys.)
+                        float top = -INFINITY, size = 0.f;
+                        const int last = pos - j * kTile, first = low - j * kTile;
+#pragma unroll 1
+                        for (int h = 0; h < 2; ++h) {
+                            tc_ld32(s_addr + kHalf * h, x);
+                            tc_ld32(s_addr + kHalf * h + 32, x + 32);
+                            tc_wait_ld32(x);
+                            tc_wait_ld32(x + 32);
+                            float mx[2] = {-INFINITY, -INFINITY}, big[2] = {};
+                            if (part) {
+#pragma unroll
+                                for (int e = 0; e < kHalf; ++e)
+                                    f[e] = kHalf * h + e <= last && kHalf * h + e >= first ? f[e] : -INFINITY;
+                            }
+#pragma unroll
+                            for (int e = 0; e < kHalf; e += 2) {
+                                mx[e >> 1 & 1] = max3(mx[e >> 1 & 1], f[e], f[e + 1]);
+                                big[e >> 1 & 1] = max3(big[e >> 1 & 1], fabsf(f[e]), fabsf(f[e + 1]));
+                            }
+                            top = max3(top, mx[0], mx[1]);
+                            size = max3(size, big[0], big[1]);
+                        }
+                        // far below the cap throughout: tanh as a polynomial
+                        const bool near = !__any_sync(0xffffffffu, valid && size > c.cap_near);
+                        if (!raise(top == -INFINITY ? top : capped(top, cap_in, cap2)))
+                            break;
+                        base = m == -INFINITY ? 0.f : m;
+#pragma unroll 1
+                        for (int h = 0; h < 2; ++h) {
+                            tc_ld32(s_addr + kHalf * h, x);
+                            tc_ld32(s_addr + kHalf * h + 32, x + 32);
+                            tc_wait_ld32(x);
+                            tc_wait_ld32(x + 32);
+                            if (near) {
+                                auto two = [](float y) { return make_float2(y, y); };
+#pragma unroll
+                                for (int e = 0; e < kHalf; e += 2) {
+                                    const float2 y = make_float2(f[e], f[e + 1]), t2 = mul2(y, y);
+                                    const float2 p = fma2(fma2(two(c.cap_poly[2]), t2, two(c.cap_poly[1])), t2, two(c.cap_poly[0]));
+                                    const float2 z = fma2(mul2(y, two(scale2)), fma2(p, t2, two(1.f)), two(-base));
+                                    f[e] = z.x, f[e + 1] = z.y;
+                                }
+                            } else {
+                                // two reciprocals from one (beyond 2^60 the cap is reached)
+#pragma unroll
+                                for (int e = 0; e < kHalf; e += 2) {
+                                    const float d0 = 1.f + ex2(fminf(f[e] * cap_in, 60.f)), d1 = 1.f + ex2(fminf(f[e + 1] * cap_in, 60.f));
+                                    const float r = rcp(d0 * d1);
+                                    f[e] = fmaf(-2.f * cap2, r * d1, cap2 - base);
+                                    f[e + 1] = fmaf(-2.f * cap2, r * d0, cap2 - base);
+                                }
+                                if (part) {
+#pragma unroll
+                                    for (int e = 0; e < kHalf; ++e)
+                                        f[e] = kHalf * h + e <= last && kHalf * h + e >= first ? f[e] : -INFINITY;
+                                }
+                            }
+#pragma unroll
+                            for (int n = 0; n < kHalf / 2 + kLead; ++n) {
+                                if (n < kHalf / 2)
+                                    exponentials(n);
+                                if (n >= kLead)
+                                    rounding(n - kLead);
+                            }
+                            // P takes the columns of scores that are done with
+                            tc_st32(p_addr + 32 * h, x);
+                            if (h == 0)
+                                hand_over();
+                        }
+                    }
+                    if (!CAP && !made) {
+                        // the maximum of the first half is taken while the second is on its way
                         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                        float size = 0.f, size2 = 0.f;   // largest |score|
                         const int last = pos - j * kTile, first = low - j * kTile;
                         tc_ld32(s_addr, x);
                         tc_ld32(s_addr + 32, x + 32);
@@ -802,67 +911,11 @@ __device__ __forceinline__ void softmax(const AttnLaunch &c, AttnShared &sh, flo
 #pragma unroll
                                 for (int k = 0; k < 4; ++k)
                                     mx[k] = max3(mx[k], f[e + k], f[e + 4 + k]);
-                                if (CAP) {
-                                    size = max3(size, fabsf(f[e]), fabsf(f[e + 1]));
-                                    size2 = max3(size2, fabsf(f[e + 2]), fabsf(f[e + 3]));
-                                    size = max3(size, fabsf(f[e + 4]), fabsf(f[e + 5]));
-                                    size2 = max3(size2, fabsf(f[e + 6]), fabsf(f[e + 7]));
-                                }
                             }
                         }
-                        size = fmaxf(size, size2);
-                        float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
-                        if (CAP) {
-                            top = top == -INFINITY ? top : capped(top, cap_in, cap2);
-                            if (!__any_sync(0xffffffffu, valid && size > c.cap_near)) {
-                                // |s / cap| <= 1/2 throughout: an odd polynomial
-                                const float2 one = make_float2(1.f, 1.f), c0 = make_float2(c.cap_poly[0], c.cap_poly[0]),
-                                             c1 = make_float2(c.cap_poly[1], c.cap_poly[1]), c2 = make_float2(c.cap_poly[2], c.cap_poly[2]),
-                                             c3 = make_float2(c.cap_poly[3], c.cap_poly[3]), by = make_float2(scale2, scale2);
-#pragma unroll
-                                for (int e = 0; e < kTile; e += 2) {
-                                    const float2 y = make_float2(f[e], f[e + 1]), t2 = mul2(y, y);
-                                    const float2 z = mul2(mul2(y, by), fma2(fma2(fma2(fma2(c3, t2, c2), t2, c1), t2, c0), t2, one));
-                                    f[e] = z.x, f[e + 1] = z.y;
-                                }
-                            } else
-                            // cap tanh(s / cap) of all scores, two reciprocals from one (beyond 2^60 the cap is reached)
-#pragma unroll
-                            for (int e = 0; e < kTile; e += 2) {
-                                const float d0 = 1.f + ex2(fminf(f[e] * cap_in, 60.f)), d1 = 1.f + ex2(fminf(f[e + 1] * cap_in, 60.f));
-                                const float both = rcp(d0 * d1);
-                                f[e] = fmaf(-2.f * cap2, both * d1, cap2);
-                                f[e + 1] = fmaf(-2.f * cap2, both * d0, cap2);
-                            }
-                            if (part) {
-#pragma unroll
-                                for (int e = 0; e < kTile; ++e)
-                                    f[e] = e <= last && e >= first ? f[e] : -INFINITY;
-                            }
-                        } else {
-                            top *= scale2;
-                        }
-                        const bool grow = m != -INFINITY && top > m + kLazy;
-                        if (__any_sync(0xffffffffu, grow)) {
-                            ok = warp_wait(sh, &sh.o_full[i], (done + t - 1) & 1, a.status);
-                            if (!ok)
-                                break;
-                            tc_fence_after();
-                            const float f2 = grow ? ex2(m - top) : 1.f;
-                            l *= f2;
-#pragma unroll 1
-                            for (int q = 0; q < 8; ++q) {
-                                uint32_t o[16];
-                                tc_ld16(o_addr + 16 * q, o);
-                                tc_wait_ld16(o);
-#pragma unroll
-                                for (int e = 0; e < 16; ++e)
-                                    o[e] = __float_as_uint(__uint_as_float(o[e]) * f2);
-                                tc_st16(o_addr + 16 * q, o);
-                            }
-                        }
-                        if (grow || m == -INFINITY)
-                            m = top;
+                        const float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * scale2;
+                        if (!raise(top))
+                            break;
                         base = m == -INFINITY ? 0.f : m;
 #pragma unroll
                         for (int n = -kLead; n < kPairs + kLead; ++n) {
@@ -1295,9 +1348,9 @@ cudaError_t launch_chunk_attention(const AttnArgs &a, cudaStream_t st)
     c.plan.inverse = ~0ull / (unsigned long long)c.shares;
     carve(a.T, a.B, a.Hq, Hkv, static_cast<char *>(a.ws), &c.parts);
     if (a.softcap > 0.f) {
-        const double b[4] = {-0.333331435918808, 0.13325878977775574, -0.05304549261927605, 0.01724149100482464};
+        const double b[3] = {-0.3332815934197915, 0.132053598066859, -0.04475064703577332};
         const double y = (double)a.scale / a.softcap;
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 3; ++i)
             c.cap_poly[i] = (float)(b[i] * pow(y, 2 * i + 2));
         c.cap_near = (float)(0.5 / y);
     }
