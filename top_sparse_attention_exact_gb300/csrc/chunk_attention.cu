@@ -438,14 +438,18 @@ __device__ __forceinline__ int ring_v(int t, int nt)
     return TWO || nt == 1 ? 2 * t + 1 : 2 + t + min(t, nt - 2);
 }
 
-constexpr int kMaxShares = 1024;   // CTAs of a launch, one for each SM
+constexpr int kMaxShares = 255;   // CTAs of a launch, one for each SM
 
 // ---- workspace ----------------------------------------------------------------------
 // Places of the n + 1 bounds, then for each CTA two parts (0: of an item that began in an
 // earlier share, 1: of an item that goes on in the next) of `rows` rows: (m, l) pairs, and
 // the accumulators as [column / 4][row][4], so that a warp's rows lie side by side.
+struct Bound {
+    Place at;
+    int n, t0;   // of the place's sequence, where it is inside an item
+};
 struct Parts {
-    Place *bound;
+    Bound *bound;
     float2 *ml;
     float4 *o;
     int rows;
@@ -1177,9 +1181,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     tc_fence_after();
     const uint32_t tmem = sh.tmem;
     if (tid == 0) {
-        c.parts.bound[blockIdx.x] = sh.bound[0];
+        c.parts.bound[blockIdx.x] = Bound{sh.bound[0], sh.first.n, sh.first.t0};
         if (blockIdx.x == gridDim.x - 1)
-            c.parts.bound[gridDim.x] = sh.bound[1];
+            c.parts.bound[gridDim.x] = Bound{sh.bound[1], 0, 0};
     }
     if (warp < kMmaWarp) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
@@ -1207,28 +1211,30 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnLaunch c, int share
 {
     __shared__ float4 sum[8][32];
     __shared__ float2 ml_of[8];
-    __shared__ uint8_t there[kMaxShares];   // a share between two equal cuts has no part
+    __shared__ Place places[kMaxShares + 1];
+    __shared__ uint8_t there[kMaxShares + 1];   // a share between two equal cuts has no part
     pdl_wait();
     pdl_trigger();
     const AttnArgs &a = c.a;
     const int x = blockIdx.x + 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const Place at = c.parts.bound[x], prev = c.parts.bound[x - 1];
+    // bounds x - 1, x, ...; with bound x the sequence, which must not cost another trip to memory
+    const int y = x - 1 + (int)threadIdx.x;
+    if (y <= shares)
+        places[threadIdx.x] = c.parts.bound[y].at;
+    const Bound here = c.parts.bound[x];
+    __syncthreads();
+    const Place at = here.at, prev = places[0];
     if (at.cut == 0 || (same_item(at, prev) && prev.cut > 0))
         return;
     // parts: share x - 1's part 1, then part 0 of shares x, x + 1, ... while they begin in the item
-    const Seq s = sequence(a, at.b);
-    int n = 1, more;
-    do {
-        const int i = n + (int)threadIdx.x, y = x - 1 + i;   // part i is of share y
-        bool in = false;
-        if (y < shares) {
-            const Place p0 = c.parts.bound[y], p1 = c.parts.bound[y + 1];
-            in = same_item(p0, at);
-            there[i] = !same_item(p1, at) || p1.cut > p0.cut;
-        }
-        more = __syncthreads_count(in);
-        n += more;
-    } while (more == 256);
+    bool in = false;
+    if (threadIdx.x > 0 && y < shares) {   // part i = threadIdx.x is of share y
+        const Place p0 = places[threadIdx.x], p1 = places[threadIdx.x + 1];
+        in = same_item(p0, at);
+        there[threadIdx.x] = !same_item(p1, at) || p1.cut > p0.cut;
+    }
+    const int n = 1 + __syncthreads_count(in);
+    const struct { int n, t0; } s{here.n, here.t0};
     const bool together = n > 8;
     const int tile_tokens = kTile / a.G, per_tile = tile_tokens * a.G, first = at.k * c.plan.tokens;
     const int rows = min(TWO ? 2 * per_tile : per_tile, (s.n - first) * a.G);
@@ -1296,10 +1302,10 @@ static size_t carve(int T, int B, int Hq, int Hkv, char *ws, Parts *p)
 {
     const int G = Hq / Hkv, n = std::min(sm_count(), kMaxShares);
     const size_t rows = part_rows(T, G, two_tiles(T, B, G));
-    const size_t o_ml = ((n + 1) * sizeof(Place) + 255) / 256 * 256;
+    const size_t o_ml = ((n + 1) * sizeof(Bound) + 255) / 256 * 256;
     const size_t o_o = o_ml + (2 * n * rows * sizeof(float2) + 255) / 256 * 256;
     if (p) {
-        p->bound = reinterpret_cast<Place *>(ws);
+        p->bound = reinterpret_cast<Bound *>(ws);
         p->ml = reinterpret_cast<float2 *>(ws + o_ml);
         p->o = reinterpret_cast<float4 *>(ws + o_o);
         p->rows = (int)rows;
