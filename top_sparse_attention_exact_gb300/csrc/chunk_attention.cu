@@ -399,6 +399,15 @@ __device__ __forceinline__ void load_3d(uint32_t dst, const CUtensorMap *map, in
         : "memory");
 }
 
+__device__ __forceinline__ void load_3d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar, uint64_t policy)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, %3, %4}], "
+        "[%5], %6;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar)), "l"(policy)
+        : "memory");
+}
+
 __device__ __forceinline__ float ex2(float x)
 {
     float y;
@@ -476,6 +485,10 @@ __device__ __forceinline__ void copies(const AttnLaunch &c, AttnShared &sh, cons
     const AttnArgs &a = c.a;
     const int Hkv = a.cache.n_kv_heads, tile_tokens = kTile / a.G;
     const int half = lane & 1, piece = lane >> 1, pieces = kTile / c.chunk;   // this lane's copy
+    // a few tokens' keys and values pass through the L2 once: they are to leave it the rest, the
+    // kernels' instructions among it
+    uint64_t once;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(once));
     bool ok = true;
     uint32_t used = 0, issued = 0, segs = 0, q_copies = 0;   // ring slots before this segment, copied so far
     while (ok && segment(sh, segs, a.status)) {
@@ -535,10 +548,14 @@ __device__ __forceinline__ void copies(const AttnLaunch &c, AttnShared &sh, cons
                 ok = __shfl_sync(0xffffffffu, good, 0);
                 if (ok) {
                     issued = u + 1;
-                    if (piece < pieces)
-                        load_3d(ring + st * kAttnStageBytes + half * kHalfBytes + piece * c.chunk * 128,
-                                isk ? &kmap : &vmap, half * 64, at[isk ? ahead : 0].x, at[isk ? ahead : 0].y,
-                                &sh.kv_full[st]);
+                    const uint32_t dst = ring + st * kAttnStageBytes + half * kHalfBytes + piece * c.chunk * 128;
+                    const int2 from = at[isk ? ahead : 0];
+                    if (piece < pieces) {
+                        if (TWO)
+                            load_3d(dst, isk ? &kmap : &vmap, half * 64, from.x, from.y, &sh.kv_full[st]);
+                        else
+                            load_3d(dst, isk ? &kmap : &vmap, half * 64, from.x, from.y, &sh.kv_full[st], once);
+                    }
                 }
             }
             at[0] = at[1];
