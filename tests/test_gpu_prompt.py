@@ -228,6 +228,45 @@ def test_append_of_blocks_that_are_not_finite_or_zero():
     assert y[3, 5] == 2.0 ** -133 and (y[3, :5] == 0).all()
 
 
+@pytest.mark.parametrize("inter", [False, True])
+def test_an_infinity_stays_in_its_pair(inter):
+    # without a norm an element reaches its partner of the rotation and no other
+    k = torch.ones((2, 1, D), dtype=torch.bfloat16, device="cuda")
+    k[0, 0, 100], k[1, 0, 3] = float("inf"), float("nan")
+    c = Cache(2, 1, 8, fill=0.0)
+    retopk.qkv_append(retopk.QKRope(freqs(64), interleaved=inter), k, k, k, c.h, i32([1, 1]))
+    bad = lambda b: (~c.k[b, 0, 1].isfinite()).nonzero().flatten().tolist()  # noqa: E731
+    assert bad(0) == [100] and bad(1) == ([2, 3] if inter else [3, 35])
+
+
+def test_append_odd_offsets_and_lengths_stay_inside():
+    for cu, start in (([0, 5, 3, 9], [3, 4, 5]), ([2, 4, 6, 40], [0, 1, 2]), ([-3, 2, 2, 8], [7, -2, 30]), ([9, 9, 9, 9], [1, 2, 3])):
+        q = normal(gen(3), 9, 2, D)
+        c = Cache(3, 2, 32, 16, fill=1.0)
+        out = torch.full((11, 2, D), 9.0, dtype=torch.bfloat16, device="cuda")
+        sl = i32([0, 0, 0, 77])
+        retopk.qkv_append(retopk.QKRope(freqs(128)), q, q, q, c.h, i32(start), sl[:3], out[1:10], cu_tokens=i32(cu))
+        assert (out[0] == 9).all() and (out[10] == 9).all() and sl[3] == 77
+
+
+def test_append_captured_and_replayed_advances_each_time():
+    g = gen(31)
+    B = 3
+    q, k, v = normal(g, B, 4, D), normal(g, B, 2, D), normal(g, B, 2, D)
+    c, sl, qo = Cache(B, 2, 40, fill=0.0), i32([0, 5, 38]), torch.empty((B, 4, D), dtype=torch.bfloat16, device="cuda")
+    rope, st = retopk.QKRope(freqs(128)), torch.zeros(1, dtype=torch.int32, device="cuda")
+    retopk.qkv_append(rope, q, k, v, c.h, sl, q_out=qo, status=st)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        retopk.qkv_append(rope, q, k, v, c.h, sl, q_out=qo, status=st)
+    for _ in range(3):
+        graph.replay()
+    assert sl.tolist() == [4, 9, 40] and st.item() == retopk.STATUS_KV_FULL
+    for b, rows in enumerate((range(4), range(5, 9), range(38, 40))):
+        for r in rows:
+            assert torch.equal(c.v[b, :, r], v[b])
+
+
 @pytest.mark.parametrize("rot,inter", [(128, False), (64, True)])
 def test_qk_rope_is_appends_rows_and_works_in_place(rot, inter):
     g = gen(8)
@@ -303,6 +342,14 @@ def test_copy(src8, dst8, Hkv, sp, dp, first, last):
         assert torch.equal(new.view(torch.uint8), was.view(torch.uint8))
 
 
+def test_copy_stops_at_max_rows():
+    src, dst = filled(gen(4), 2, 2, 300, 16, True, 1), Cache(2, 2, 300, fill=2.0)
+    retopk.cache_copy(src.h, dst.h, i32([0, 100]), i32([300, 300]), 77)
+    for b, f in enumerate((0, 100)):
+        new, old = dst.rows(b, 300)[0], src.rows(b, 300)[0].to(torch.bfloat16).double()
+        assert torch.equal(new[f:f + 77], old[f:f + 77]) and (new[:f] == 2).all() and (new[f + 77:] == 2).all()
+
+
 def test_copy_reports_rows_out_of_range_and_bad_pages():
     src, dst = filled(gen(3), 2, 1, 64, 16, True, 1), Cache(2, 1, 40, fill=2.0)
     st = torch.zeros(1, dtype=torch.int32, device="cuda")
@@ -374,6 +421,17 @@ ATTEND = [  # tokens of each sequence, rows in all, Hq, Hkv, page, window, cap
     ([260], [100], 2, 1, 0, 0, 0.0),                                # tokens 0..159 see no key
     ([700], [5000], 15, 5, 112, 1, 0.0),                            # each token sees itself only
     ([513], [2050], 13, 1, 0, 0, 5.0),
+    ([1] * 700, [(37 * i) % 600 for i in range(700)], 4, 2, 0, 0, 0.0),     # more sequences than a block has threads
+    ([i % 3 for i in range(900)], [(53 * i) % 300 for i in range(900)], 2, 1, 16, 0, 0.0),
+    ([40] * 400, [40 + i % 90 for i in range(400)], 8, 8, 0, 0, 0.0),
+    ([3, 70], [600, 1500], 40, 40, 0, 0, 0.0),                      # many KV heads
+    ([1], [512], 6, 2, 0, 0, 0.0),                                  # a cache of a few tiles, with rows past the length
+    ([130], [515], 3, 3, 64, 0, 0.0),
+    ([2, 90], [800, 700], 8, 2, 0, 0, 1e6),                         # a cap far above all scores
+    ([2, 90], [800, 700], 8, 2, 0, 0, 1e-3),                        # and far below
+    ([2, 90], [800, 700], 8, 2, 0, 200, 1e-30),
+    ([2, 90], [800, 700], 8, 2, 0, (1 << 31) - 1, 0.0),             # a window wider than any history
+    ([2, 90], [800, 700], 8, 2, 0, 1 << 23, 12.0),
 ]
 
 
@@ -437,6 +495,29 @@ def test_attention_lengths_beyond_the_capacity_are_clamped():
     c.put(0, normal(gen(1), 71, 1, D), normal(gen(2), 71, 1, D))
     out = retopk.chunk_attention(q, c.h, i32([5000]))
     check(q, 0, [1], [71], c, out, None, 1 / math.sqrt(D), 0.0, 0)
+
+
+def test_attention_zero_scores_under_a_tiny_cap():
+    q, c = setup([1, 40], [300, 600], 8, 2, 0, 25)
+    q.zero_()
+    for cap in (1e-30, 1e-8, 3.0, 1e30):
+        out = retopk.chunk_attention(q, c.h, i32([300, 600]), cu_tokens=offsets([1, 40]), softcap=cap)
+        check(q, 0, [1, 40], [300, 600], c, out, None, 1 / math.sqrt(D), 0.0, 0)     # all weights equal
+
+
+@pytest.mark.parametrize("cu,lens", [([0, 5, 3, 9], [50, 60, 70]), ([2, 4, 6, 40], [10, 20, 30]), ([0, 0, 0, 0], [9, 9, 9]), ([-4, 2, 7, 7], [9, -9, 3])])
+def test_attention_odd_offsets_and_lengths_stay_inside(cu, lens):
+    # offsets that decrease, leave tokens out or pass the last token; a negative length: no row outside is written
+    q, c = setup([9], [90], 8, 2, 16, 26, pad=0, strided=False)
+    c = Cache(3, 2, 100, 16, fill=0.5)
+    out = torch.full((11, 8, D), 9.0, dtype=torch.bfloat16, device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    retopk.chunk_attention(q, c.h, i32(lens), out[1:10], cu_tokens=i32(cu), status=st)
+    assert st.item() == 0 and (out[0] == 9).all() and (out[10] == 9).all() and not out.isnan().any()
+    flat = sorted({t for b in range(3) for t in range(max(cu[b], 0), min(cu[b + 1], 9))})
+    for t in range(9):
+        if t not in flat:
+            assert (out[1 + t] == 9).all()
 
 
 def test_attention_reports_bad_pages():

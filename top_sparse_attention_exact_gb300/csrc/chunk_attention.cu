@@ -679,7 +679,7 @@ __device__ __forceinline__ void softmax(const AttnLaunch &c, AttnShared &sh, flo
     const uint32_t s_addr = tmem + i * kTile + ((uint32_t)(warp & 3) << 21), o_addr = s_addr + 2 * kTile;
     const float scale2 = a.scale * 1.4426950408889634f;     // scores in powers of two
     const float cap2 = a.softcap * 1.4426950408889634f;
-    const float cap_in = CAP ? 2.f * scale2 / a.softcap : 0.f;   // e^2y = 2^(cap_in s)
+    const float cap_in = CAP ? fminf(2.f * scale2 / a.softcap, 3e38f) : 0.f;   // e^2y = 2^(cap_in s)
     bool ok = true;
     uint32_t used = 0, done = 0, segs = 0;
     while (ok && segment(sh, segs, a.status)) {
@@ -849,20 +849,29 @@ __device__ __forceinline__ void softmax(const AttnLaunch &c, AttnShared &sh, flo
                             float mx[2] = {-INFINITY, -INFINITY}, big[2] = {};
                             if (part) {
 #pragma unroll
-                                for (int e = 0; e < kHalf; ++e)
-                                    f[e] = kHalf * h + e <= last && kHalf * h + e >= first ? f[e] : -INFINITY;
-                            }
+                                for (int e = 0; e < kHalf; ++e) {
+                                    const bool seen = kHalf * h + e <= last && kHalf * h + e >= first;
+                                    mx[e & 1] = fmaxf(mx[e & 1], seen ? f[e] : -INFINITY);
+                                    big[e & 1] = fmaxf(big[e & 1], seen ? fabsf(f[e]) : 0.f);
+                                }
+                            } else {
 #pragma unroll
-                            for (int e = 0; e < kHalf; e += 2) {
-                                mx[e >> 1 & 1] = max3(mx[e >> 1 & 1], f[e], f[e + 1]);
-                                big[e >> 1 & 1] = max3(big[e >> 1 & 1], fabsf(f[e]), fabsf(f[e + 1]));
+                                for (int e = 0; e < kHalf; e += 2) {
+                                    mx[e >> 1 & 1] = max3(mx[e >> 1 & 1], f[e], f[e + 1]);
+                                    big[e >> 1 & 1] = max3(big[e >> 1 & 1], fabsf(f[e]), fabsf(f[e + 1]));
+                                }
                             }
                             top = max3(top, mx[0], mx[1]);
                             size = max3(size, big[0], big[1]);
                         }
                         // far below the cap throughout: tanh as a polynomial
+                        auto near_capped = [&](float y) {
+                            const float t2 = y * y;
+                            return y * scale2 * fmaf(fmaf(fmaf(c.cap_poly[2], t2, c.cap_poly[1]), t2, c.cap_poly[0]), t2, 1.f);
+                        };
                         const bool near = !__any_sync(0xffffffffu, valid && size > c.cap_near);
-                        if (!raise(top == -INFINITY ? top : capped(top, cap_in, cap2)))
+                        // (their capped maximum by the form that the others take)
+                        if (!raise(top == -INFINITY ? top : near ? near_capped(top) : capped(top, cap_in, cap2)))
                             break;
                         base = m == -INFINITY ? 0.f : m;
 #pragma unroll 1
@@ -889,11 +898,11 @@ __device__ __forceinline__ void softmax(const AttnLaunch &c, AttnShared &sh, flo
                                     f[e] = fmaf(-2.f * cap2, r * d1, cap2 - base);
                                     f[e + 1] = fmaf(-2.f * cap2, r * d0, cap2 - base);
                                 }
-                                if (part) {
+                            }
+                            if (part) {
 #pragma unroll
-                                    for (int e = 0; e < kHalf; ++e)
-                                        f[e] = kHalf * h + e <= last && kHalf * h + e >= first ? f[e] : -INFINITY;
-                                }
+                                for (int e = 0; e < kHalf; ++e)
+                                    f[e] = kHalf * h + e <= last && kHalf * h + e >= first ? f[e] : -INFINITY;
                             }
 #pragma unroll
                             for (int n = 0; n < kHalf / 2 + kLead; ++n) {
@@ -1375,7 +1384,8 @@ cudaError_t launch_chunk_attention(const AttnArgs &a, cudaStream_t st)
         const double y = (double)a.scale / a.softcap;
         for (int i = 0; i < 3; ++i)
             c.cap_poly[i] = (float)(b[i] * pow(y, 2 * i + 2));
-        c.cap_near = (float)(0.5 / y);
+        // (a cap so small that the powers overflow: the other form for all but no scores)
+        c.cap_near = isfinite(c.cap_poly[2]) ? (float)(0.5 / y) : -1.f;
     }
     c.chunk = kTile;
     if (a.cache.table)

@@ -225,7 +225,7 @@ int retopk_chunk_attention(const retopk_bf16 *q, int64_t q_stride, const retopk_
     a.B = B;
     a.Hq = Hq;
     a.G = Hq / cache->n_kv_heads;
-    a.window = window;
+    a.window = window < kMaxLen ? window : 0;   // (a wider one hides nothing)
     a.scale = scale > 0.f ? scale : 1.0f / sqrtf((float)kD);
     a.softcap = softcap;
     a.ws = d_workspace;
