@@ -1230,8 +1230,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
-// Joins the parts of the item that bound blockIdx.x + 1 cuts first.  A warp takes a
-// row, or, where a row has many parts, the block takes it and shares them out.
+// Joins the parts of the item that bound blockIdx.x + 1 cuts first.  One, two, four
+// or eight warps of a block take a row and share out its parts: as many as leave the
+// grid's blocks about one pass over the rows.
 template <bool TWO>
 __global__ void __launch_bounds__(256) join_kernel(const AttnLaunch c, int shares)
 {
@@ -1254,26 +1255,28 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnLaunch c, int share
         return;
     // parts: share x - 1's part 1, then part 0 of shares x, x + 1, ... while they begin in the item
     bool in = false;
-    if (threadIdx.x > 0 && y < shares) {   // part i = threadIdx.x is of share y
+    if (y < shares) {   // part i = threadIdx.x is of share y
         const Place p0 = places[threadIdx.x], p1 = places[threadIdx.x + 1];
-        in = same_item(p0, at);
-        there[threadIdx.x] = !same_item(p1, at) || p1.cut > p0.cut;
+        in = threadIdx.x > 0 && same_item(p0, at);
+        there[threadIdx.x] = threadIdx.x == 0 || !same_item(p1, at) || p1.cut > p0.cut;
     }
     const int n = 1 + __syncthreads_count(in);
-    const struct { int n, t0; } s{here.n, here.t0};
-    const bool together = n > 8;
     const int tile_tokens = kTile / a.G, per_tile = tile_tokens * a.G, first = at.k * c.plan.tokens;
-    const int rows = min(TWO ? 2 * per_tile : per_tile, (s.n - first) * a.G);
-    const int step = together ? 1 : 8;   // parts and rows of a warp
-    for (int r0 = blockIdx.y * step + (together ? 0 : warp); r0 < rows; r0 += gridDim.y * step) {
-        const int second = r0 >= per_tile, in = r0 - second * per_tile;
-        const int r = second * kTile + in, tok = first + second * tile_tokens + in / a.G;
-        auto part = [&](int i) { return (size_t)(2 * (x - 1 + i) + (i == 0)); };
+    const int rows = min(TWO ? 2 * per_tile : per_tile, (here.n - first) * a.G);
+    int crew = 1;   // warps of a row
+    while (crew < 8 && 4 * crew < n && 2 * crew * rows <= 8 * (int)gridDim.y)
+        crew *= 2;
+    const int mate = warp % crew, step = 8 / crew;   // rows of the block at a time
+    for (int base = blockIdx.y * step; base < rows; base += gridDim.y * step) {
+        const int r0 = base + warp / crew;
+        const bool real = r0 < rows;
+        const int second = r0 >= per_tile, in_tile = r0 - second * per_tile;
+        const int r = second * kTile + in_tile;
         float m = -INFINITY, l = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         auto add = [&](float m2, float l2, float4 o) {
-            const float mm = fmaxf(m, m2), base = mm == -INFINITY ? 0.f : mm;
-            const float f1 = ex2(m - base), f2 = m2 == -INFINITY ? 0.f : ex2(m2 - base);
+            const float mm = fmaxf(m, m2), zero = mm == -INFINITY ? 0.f : mm;
+            const float f1 = ex2(m - zero), f2 = m2 == -INFINITY ? 0.f : ex2(m2 - zero);
             l = l * f1 + l2 * f2;
             // (a part without a row's keys may hold anything)
             acc.x = fmaf(acc.x, f1, f2 != 0.f ? o.x * f2 : 0.f);
@@ -1282,30 +1285,42 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnLaunch c, int share
             acc.w = fmaf(acc.w, f1, f2 != 0.f ? o.w * f2 : 0.f);
             m = mm;
         };
-#pragma unroll 5
-        for (int i = together ? warp : 0; i < n; i += together ? 8 : 1) {
-            const bool has = i == 0 || there[i];
-            const float2 ml = c.parts.ml[part(i) * c.parts.rows + r];
-            const float4 o = c.parts.o[(part(i) * (kD / 4) + lane) * c.parts.rows + r];
-            add(has ? ml.x : -INFINITY, has ? ml.y : 0.f, o);
+#pragma unroll 1
+        for (int i0 = mate; i0 < n && real; i0 += 4 * crew) {   // four parts on their way at once
+            float2 ml[4];
+            float4 o[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int i = i0 + k * crew;
+                ml[k] = make_float2(-INFINITY, 0.f);
+                o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (i < n && there[i]) {
+                    const size_t part = 2 * (x - 1 + i) + (i == 0);
+                    ml[k] = c.parts.ml[part * c.parts.rows + r];
+                    o[k] = c.parts.o[(part * (kD / 4) + lane) * c.parts.rows + r];
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                add(ml[k].x, ml[k].y, o[k]);
         }
-        if (together) {
+        if (crew > 1) {
             sum[warp][lane] = acc;
             if (lane == 0)
                 ml_of[warp] = make_float2(m, l);
             __syncthreads();
-            if (warp == 0) {
-                m = -INFINITY, l = 0.f, acc = make_float4(0.f, 0.f, 0.f, 0.f);
-                for (int i = 0; i < 8; ++i)
-                    add(ml_of[i].x, ml_of[i].y, sum[i][lane]);
-            }
+            if (mate == 0)
+#pragma unroll 1
+                for (int i = 1; i < crew; ++i)
+                    add(ml_of[warp + i].x, ml_of[warp + i].y, sum[warp + i][lane]);
             __syncthreads();
-            if (warp != 0)
-                continue;
         }
+        if (mate != 0 || !real)
+            continue;
+        const int tok = first + second * tile_tokens + in_tile / a.G;
         const float inv = l > 0.f ? 1.f / l : 0.f;
-        const size_t t = s.t0 + tok;
-        const int h = at.hk * a.G + in % a.G;
+        const size_t t = here.t0 + tok;
+        const int h = at.hk * a.G + in_tile % a.G;
         *reinterpret_cast<uint2 *>(a.out + t * a.out_stride + h * kD + lane * 4) =
             make_uint2(bf16x2(acc.x * inv, acc.y * inv), bf16x2(acc.z * inv, acc.w * inv));
         if (a.lse && lane == 0)
