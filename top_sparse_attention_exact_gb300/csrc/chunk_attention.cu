@@ -470,6 +470,7 @@ struct AttnLaunch {
     Parts parts;
     int chunk;    // rows of one K / V copy (a page's, 128 at most)
     int shares;   // CTAs
+    long long items;   // at most
     // tanh(y) = y (1 + t (b_0 + b_1 t + b_2 t^2)), t = y^2, for |y| <= 1/2: b fitted at Chebyshev nodes for
     // the smallest largest error (6.4e-7 of the value).  Here for raw scores: y = s scale / softcap,
     // so cap_poly[i] = b_i (scale / softcap)^(2 i + 2); cap_near: the largest |s|.
@@ -1230,37 +1231,73 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
-// Joins the parts of the item that bound blockIdx.x + 1 cuts first.  One, two, four
-// or eight warps of a block take a row and share out its parts: as many as leave the
-// grid's blocks about one pass over the rows.
+// Joins the parts of an item.  With two tiles the grid's columns are the cut items (few
+// items of many rows then have many blocks each: 36 tokens over 17663 keys 48 -> 38 us);
+// with one, where that search costs more than it gives, they are the bounds, and the first
+// that cuts an item has it.  One, two, four or eight warps of a block take a row and share
+// out its parts: as many as leave the item's blocks about one pass over the rows.
 template <bool TWO>
 __global__ void __launch_bounds__(256) join_kernel(const AttnLaunch c, int shares)
 {
     __shared__ float4 sum[8][32];
     __shared__ float2 ml_of[8];
-    __shared__ Place places[kMaxShares + 1];
-    __shared__ uint8_t there[kMaxShares + 1];   // a share between two equal cuts has no part
+    __shared__ Bound bounds[kMaxShares + 1];
+    __shared__ uint16_t list[kMaxShares + 1];   // the item's parts
+    __shared__ int counts[8], first_cut;
     pdl_wait();
     pdl_trigger();
     const AttnArgs &a = c.a;
-    const int x = blockIdx.x + 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    // bounds x - 1, x, ...; with bound x the sequence, which must not cost another trip to memory
-    const int y = x - 1 + (int)threadIdx.x;
-    if (y <= shares)
-        places[threadIdx.x] = c.parts.bound[y].at;
-    const Bound here = c.parts.bound[x];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid <= shares)
+        bounds[tid] = c.parts.bound[tid];
+    if (tid == 0)
+        first_cut = 0;
     __syncthreads();
-    const Place at = here.at, prev = places[0];
-    if (at.cut == 0 || (same_item(at, prev) && prev.cut > 0))
-        return;
-    // parts: share x - 1's part 1, then part 0 of shares x, x + 1, ... while they begin in the item
-    bool in = false;
-    if (y < shares) {   // part i = threadIdx.x is of share y
-        const Place p0 = places[threadIdx.x], p1 = places[threadIdx.x + 1];
-        in = threadIdx.x > 0 && same_item(p0, at);
-        there[threadIdx.x] = threadIdx.x == 0 || !same_item(p1, at) || p1.cut > p0.cut;
+    // the bounds that are the first to cut their item, counted up to this thread's
+    const Place mine = tid <= shares ? bounds[tid].at : Place{0, 0, 0, 0};
+    const Place prev = tid > 0 && tid <= shares ? bounds[tid - 1].at : Place{0, 0, 0, 0};
+    const bool cuts = tid > 0 && tid < shares && mine.cut > 0 && !(same_item(mine, prev) && prev.cut > 0);
+    auto rank = [&](bool flag, int &total) {
+        const uint32_t votes = __ballot_sync(0xffffffffu, flag);
+        if (lane == 0)
+            counts[warp] = __popc(votes);
+        __syncthreads();
+        int before = __popc(votes & ((1u << lane) - 1));
+        total = 0;
+        for (int w = 0; w < 8; ++w) {
+            before += w < warp ? counts[w] : 0;
+            total += counts[w];
+        }
+        __syncthreads();
+        return before;
+    };
+    int n, x;
+    if constexpr (TWO) {
+        if (rank(cuts, n) == (int)blockIdx.x && cuts)
+            first_cut = tid;
+        __syncthreads();
+        x = first_cut;
+        if (x == 0)
+            return;
+    } else {
+        x = blockIdx.x + 1;
+        const Place p = bounds[x].at, q = bounds[x - 1].at;
+        if (p.cut == 0 || (same_item(p, q) && q.cut > 0))
+            return;
     }
-    const int n = 1 + __syncthreads_count(in);
+    const Bound here = bounds[x];
+    const Place at = here.at;
+    // parts: share x - 1's part 1, then part 0 of shares x, x + 1, ... while they begin in the item (a
+    // share between two equal cuts has none)
+    bool in = tid == x - 1;
+    if (tid >= x && tid < shares) {
+        const Place next = bounds[tid + 1].at;
+        in = same_item(mine, at) && (!same_item(next, at) || next.cut > mine.cut);
+    }
+    const int slot = rank(in, n);
+    if (in)
+        list[slot] = (uint16_t)(2 * tid + (tid == x - 1));
+    __syncthreads();
     const int tile_tokens = kTile / a.G, per_tile = tile_tokens * a.G, first = at.k * c.plan.tokens;
     const int rows = min(TWO ? 2 * per_tile : per_tile, (here.n - first) * a.G);
     int crew = 1;   // warps of a row
@@ -1294,8 +1331,8 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnLaunch c, int share
                 const int i = i0 + k * crew;
                 ml[k] = make_float2(-INFINITY, 0.f);
                 o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (i < n && there[i]) {
-                    const size_t part = 2 * (x - 1 + i) + (i == 0);
+                if (i < n) {
+                    const size_t part = list[i];
                     ml[k] = c.parts.ml[part * c.parts.rows + r];
                     o[k] = c.parts.o[(part * (kD / 4) + lane) * c.parts.rows + r];
                 }
@@ -1379,7 +1416,10 @@ static cudaError_t launch_mode(const CUtensorMap &qm, const CUtensorMap &km, con
     cudaError_t e = launch_pdl(kernel, dim3(n), dim3(kAttnThreads), kAttnSmem, st, 1, qm, km, vm, c);
     if (e != cudaSuccess || n < 2 || !cuts)
         return e;
-    return launch_pdl(join_kernel<TWO>, dim3(n - 1, TWO ? 16 : 8), dim3(256), 0, st, 1, c, n);
+    // the items that may be cut, and blocks for each: few items have many parts
+    const int cut = TWO ? (int)std::min<long long>(n - 1, c.items) : n - 1;
+    const int each = TWO ? std::max(8, std::min(64, 1216 / cut)) : 8;
+    return launch_pdl(join_kernel<TWO>, dim3(cut, each), dim3(256), 0, st, 1, c, n);
 }
 
 cudaError_t launch_chunk_attention(const AttnArgs &a, cudaStream_t st)
@@ -1390,8 +1430,9 @@ cudaError_t launch_chunk_attention(const AttnArgs &a, cudaStream_t st)
     const bool two = two_tiles(a.T, a.B, a.G);
     c.plan.tokens = two ? 2 * tokens : tokens;
     c.shares = std::min(sm_count(), kMaxShares);
+    c.items = std::min<long long>(a.T, a.T / c.plan.tokens + a.B) * Hkv;
     if (a.capacity <= 4 * kTile)
-        c.shares = (int)std::min<long long>(c.shares, std::min<long long>(a.T, a.T / c.plan.tokens + a.B) * Hkv);
+        c.shares = (int)std::min<long long>(c.shares, c.items);
     c.plan.inverse = ~0ull / (unsigned long long)c.shares;
     carve(a.T, a.B, a.Hq, Hkv, static_cast<char *>(a.ws), &c.parts);
     if (a.softcap > 0.f) {
