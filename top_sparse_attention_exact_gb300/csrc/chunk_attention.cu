@@ -682,7 +682,7 @@ __device__ __forceinline__ void softmax(const AttnLaunch &c, AttnShared &sh, flo
     const float cap2 = a.softcap * 1.4426950408889634f;
     const float cap_in = CAP ? fminf(2.f * scale2 / a.softcap, 3e38f) : 0.f;   // e^2y = 2^(cap_in s)
     bool ok = true;
-    uint32_t used = 0, done = 0, segs = 0;
+    uint32_t used = 0, done = 0, segs = 0, pairs = 0;   // pairs: joins of the two streams
     while (ok && segment(sh, segs, a.status)) {
         const Segment &s = sh.segments[segs % kSegments];
         const int nt = s.j1 - s.j0, m_tiles = TWO ? nt : (nt + 1 - i) / 2;
@@ -989,12 +989,13 @@ __device__ __forceinline__ void softmax(const AttnLaunch &c, AttnShared &sh, flo
         const int head = s.hk * G + r % G;
         // stream 1's rows join stream 0's through shared memory, 32 columns at a time
         float *const ml = other + 32 * kTile;
+        const bool pair = !TWO && nt > 1;   // stream 1 had a tile
         float f0 = 1.f, f1 = 0.f;
 #pragma unroll 1
-        for (int h = 0; h < 4; ++h) {
+        for (int h = 0; h < 4 && (TWO || i == 0 || pair); ++h) {
             if (!TWO && i == 1) {
-                // (four phases a segment, so the parities stay)
-                if (ok && (h > 0 || segs > 0))
+                // (four phases each time, so the parities stay)
+                if (ok && (h > 0 || pairs > 0))
                     ok = warp_wait(sh, &sh.x_empty, (h & 1) ^ 1, a.status);
                 if (h == 0) {
                     ml[r] = m;
@@ -1008,7 +1009,7 @@ __device__ __forceinline__ void softmax(const AttnLaunch &c, AttnShared &sh, flo
                 tc_wait_ld32(x);
             }
             if (!TWO && i == 1) {
-                if (work && nt > 1) {
+                if (work) {
 #pragma unroll
                     for (int e = 0; e < 32; ++e)
                         other[e * kTile + r] = y[e];
@@ -1018,22 +1019,20 @@ __device__ __forceinline__ void softmax(const AttnLaunch &c, AttnShared &sh, flo
                     mbar_arrive(&sh.x_full);
                 continue;
             }
-            if (!TWO) {
+            if (pair) {
                 if (ok)
                     ok = warp_wait(sh, &sh.x_full, h & 1, a.status);
-                if (nt > 1) {
-                    if (h == 0) {
-                        const float m1 = ml[r], mm = fmaxf(m, m1), b0 = mm == -INFINITY ? 0.f : mm;
-                        f0 = ex2(m - b0);
-                        f1 = ex2(m1 - b0);
-                        l = l * f0 + ml[kTile + r] * f1;
-                        m = mm;
-                    }
-                    if (work) {
+                if (h == 0) {
+                    const float m1 = ml[r], mm = fmaxf(m, m1), b0 = mm == -INFINITY ? 0.f : mm;
+                    f0 = ex2(m - b0);
+                    f1 = ex2(m1 - b0);
+                    l = l * f0 + ml[kTile + r] * f1;
+                    m = mm;
+                }
+                if (work) {
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            y[e] = fmaf(other[e * kTile + r], f1, y[e] * f0);
-                    }
+                    for (int e = 0; e < 32; ++e)
+                        y[e] = fmaf(other[e * kTile + r], f1, y[e] * f0);
                 }
                 __syncwarp();
                 if (lane == 0)
@@ -1063,6 +1062,7 @@ __device__ __forceinline__ void softmax(const AttnLaunch &c, AttnShared &sh, flo
                 a.lse[t * a.Hq + head] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
         }
         used += 2 * nt;
+        pairs += pair;
         segment_done(sh, segs++);
         tc_fence_before();
     }
