@@ -22,7 +22,7 @@
 //   two tiles    (TWO):  the groups hold neighbouring tiles of tokens and share
 //                every K / V tile.  For prompts.
 //   two streams  (!TWO): both groups hold the same tile; group i takes the K / V
-//                tiles of its parity, joined through shared memory at the end.
+//                tiles of its parity, joined at the end.
 //                For a few tokens over a long history.
 // Either way the matrix unit works on one group while the other is in its softmax.
 //
@@ -223,7 +223,7 @@ struct AttnShared {
     uint32_t tmem;
     int failed;
 };
-// two Q tiles, the ring, AttnShared; with one Q tile the second's place serves the streams' join
+// two Q tiles, the ring, AttnShared; with one Q tile the second's place serves the streams' join (1 KB)
 constexpr size_t kAttnSmem = (2 + kAttnStages) * (size_t)kAttnStageBytes + sizeof(AttnShared);
 static_assert(kAttnSmem <= kMaxDynSmem, "one CTA's shared memory");
 
@@ -672,7 +672,7 @@ __device__ __forceinline__ void matrices(const AttnLaunch &c, AttnShared &sh, ui
 
 // ---- softmax: group i, row r --------------------------------------------------------------
 template <bool TWO, bool CAP>
-__device__ __forceinline__ void softmax(const AttnLaunch &c, AttnShared &sh, float *other, uint32_t ring,
+__device__ __forceinline__ void softmax(const AttnLaunch &c, AttnShared &sh, float *ml, uint32_t ring,
                                         uint32_t tmem, int warp, int lane)
 {
     const AttnArgs &a = c.a;
@@ -682,7 +682,8 @@ __device__ __forceinline__ void softmax(const AttnLaunch &c, AttnShared &sh, flo
     const float cap2 = a.softcap * 1.4426950408889634f;
     const float cap_in = CAP ? fminf(2.f * scale2 / a.softcap, 3e38f) : 0.f;   // e^2y = 2^(cap_in s)
     bool ok = true;
-    uint32_t used = 0, done = 0, segs = 0, pairs = 0;   // pairs: joins of the two streams
+    uint32_t used = 0, done = 0, segs = 0, joins = 0;   // joins: of the two streams
+    uint32_t done1 = 0;                               // tiles of stream 1
     while (ok && segment(sh, segs, a.status)) {
         const Segment &s = sh.segments[segs % kSegments];
         const int nt = s.j1 - s.j0, m_tiles = TWO ? nt : (nt + 1 - i) / 2;
@@ -704,6 +705,8 @@ __device__ __forceinline__ void softmax(const AttnLaunch &c, AttnShared &sh, flo
                 const bool live = t >= 0;
                 if (live)
                     ok = warp_wait(sh, &sh.s_full[i], (done + t) & 1, a.status);
+                if (!TWO && i == 1 && t == 0 && joins > 0 && ok)   // stream 0 has read the last accumulators
+                    ok = warp_wait(sh, &sh.x_empty, (joins - 1) & 1, a.status);
                 if (!ok)
                     break;
                 tc_fence_after();
@@ -978,7 +981,8 @@ __device__ __forceinline__ void softmax(const AttnLaunch &c, AttnShared &sh, flo
             }
         }
         done += m_tiles;
-        if (ok && m_tiles > 0)
+        done1 += nt / 2;
+        if (ok && m_tiles > 0 && (TWO || i == 0))
             ok = warp_wait(sh, &sh.o_full[i], (done - 1) & 1, a.status);
         tc_fence_after();
         // ---- the rows' end: a share's part, or the output
@@ -987,56 +991,41 @@ __device__ __forceinline__ void softmax(const AttnLaunch &c, AttnShared &sh, flo
         const int row = (TWO ? i * kTile : 0) + r;
         const size_t t = s.seq.t0 + tok;
         const int head = s.hk * G + r % G;
-        // stream 1's rows join stream 0's through shared memory, 32 columns at a time
-        float *const ml = other + 32 * kTile;
+        // Stream 1's rows join stream 0's: its maxima and sums through shared memory, its accumulators straight
+        // from the tensor memory, whose lanes are the same rows.
         const bool pair = !TWO && nt > 1;   // stream 1 had a tile
         float f0 = 1.f, f1 = 0.f;
+        if (pair && i == 1) {
+            ml[r] = m;
+            ml[kTile + r] = l;
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&sh.x_full);
+        } else if (pair) {
+            if (ok)
+                ok = warp_wait(sh, &sh.x_full, joins & 1, a.status) && warp_wait(sh, &sh.o_full[1], (done1 - 1) & 1, a.status);
+            tc_fence_after();
+            const float m1 = ml[r], mm = fmaxf(m, m1), b0 = mm == -INFINITY ? 0.f : mm;
+            f0 = ex2(m - b0);
+            f1 = ex2(m1 - b0);
+            l = l * f0 + ml[kTile + r] * f1;
+            m = mm;
+        }
 #pragma unroll 1
-        for (int h = 0; h < 4 && (TWO || i == 0 || pair); ++h) {
-            if (!TWO && i == 1) {
-                // (four phases each time, so the parities stay)
-                if (ok && (h > 0 || pairs > 0))
-                    ok = warp_wait(sh, &sh.x_empty, (h & 1) ^ 1, a.status);
-                if (h == 0) {
-                    ml[r] = m;
-                    ml[kTile + r] = l;
-                }
-            }
+        for (int h = 0; h < 4 && (TWO || i == 0); ++h) {   // 32 columns
             uint32_t x[32];
             float *y = reinterpret_cast<float *>(x);
             if (work) {
                 tc_ld32(o_addr + 32 * h, x);
                 tc_wait_ld32(x);
             }
-            if (!TWO && i == 1) {
-                if (work) {
+            if (pair && work) {
+                uint32_t z[32];
+                tc_ld32(o_addr + kTile + 32 * h, z);
+                tc_wait_ld32(z);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        other[e * kTile + r] = y[e];
-                }
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(&sh.x_full);
-                continue;
-            }
-            if (pair) {
-                if (ok)
-                    ok = warp_wait(sh, &sh.x_full, h & 1, a.status);
-                if (h == 0) {
-                    const float m1 = ml[r], mm = fmaxf(m, m1), b0 = mm == -INFINITY ? 0.f : mm;
-                    f0 = ex2(m - b0);
-                    f1 = ex2(m1 - b0);
-                    l = l * f0 + ml[kTile + r] * f1;
-                    m = mm;
-                }
-                if (work) {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        y[e] = fmaf(other[e * kTile + r], f1, y[e] * f0);
-                }
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(&sh.x_empty);
+                for (int e = 0; e < 32; ++e)
+                    y[e] = fmaf(__uint_as_float(z[e]), f1, y[e] * f0);
             }
             if (valid && ok) {
                 if (whole) {
@@ -1062,7 +1051,13 @@ __device__ __forceinline__ void softmax(const AttnLaunch &c, AttnShared &sh, flo
                 a.lse[t * a.Hq + head] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
         }
         used += 2 * nt;
-        pairs += pair;
+        if (pair && i == 0) {   // stream 1 may accumulate again
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&sh.x_empty);
+        }
+        joins += pair;
         segment_done(sh, segs++);
         tc_fence_before();
     }
