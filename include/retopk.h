@@ -68,7 +68,8 @@ enum {
 #define RETOPK_STATUS_TIMEOUT     0x8u  /* a bounded pipeline wait expired (the step's
                                            results are not valid)                  */
 #define RETOPK_STATUS_BAD_PAGE    0x20u /* a page-table entry outside [0, n_pages): its
-                                           rows are neither read nor written        */
+                                           rows are neither read nor written
+                                           (attention takes them as zeros)          */
 #define RETOPK_STATUS_GATHER      0x10u /* a gathered K/V row index outside [0, L) was
                                           skipped: checked by builds with
                                           RETOPK_CHECKED defined, and always by
@@ -465,10 +466,10 @@ int retopk_cache_copy(const retopk_cache *src, const retopk_cache *dst, const in
  *   s_j = scale q.k_j, with softcap > 0: softcap tanh(s_j / softcap)
  *   out = sum_j softmax(s)_j v_j,   lse = log sum_j exp(s_j)
  * q, out [T, Hq, 128] bf16, tokens q_stride / out_stride elements apart; lse
- * [T, Hq] fp32 or NULL.  A token that sees no key (L_b < n_b, L_b = 0) gets
+ * [T, Hq] fp32 or NULL; out may be q where the strides are the same.  A token that sees no key (L_b < n_b, L_b = 0) gets
  * zeros and lse = -inf.  The cache must be RETOPK_CACHE_BF16; rows at or past
  * L_b are never used, whatever they hold.  A row below L_b that is not finite
- * may reach every token of its sequence.  Lengths beyond the cache's capacity
+ * may reach every token of its sequence; a query that is not stays in its row.  Lengths beyond the cache's capacity
  * are clamped to it.  scale 0 means 1/sqrt(128).
  * d_workspace: >= retopk_chunk_attention_workspace_bytes, 256-byte aligned;
  * concurrent calls need one each.  Long histories of few tokens are split over the GPU

@@ -579,6 +579,34 @@ def test_attention_repeats_bit_for_bit():
         assert torch.equal(retopk.chunk_attention(q, c.h, sl, cu_tokens=cu)[:95], first)
 
 
+@pytest.mark.parametrize("n,L", [([1, 1, 1], [300, 70000, 5]), ([200, 1, 40], [900, 20000, 700])])
+@pytest.mark.parametrize("cap", [0.0, 20.0])
+def test_attention_of_queries_that_are_not_finite_stays_in_their_rows(n, L, cap):
+    q, c = setup(n, L, 14, 2, 64, 31, pad=0, strided=False)
+    T, at, lens = sum(n), offsets(n), i32(L)
+    lse, lse2 = (torch.empty((T, 14), device="cuda") for _ in range(2))
+    good = retopk.chunk_attention(q, c.h, lens, cu_tokens=at, lse=lse, softcap=cap)
+    bad = q.clone()
+    rows = [(0, 3), (n[0], 0), (T - 1, 13)]     # one in each sequence: whole, cut and short histories
+    for t, h in rows:
+        bad[t, h] = float("nan")
+    out = retopk.chunk_attention(bad, c.h, lens, cu_tokens=at, lse=lse2, softcap=cap)
+    hit = torch.zeros((T, 14), dtype=torch.bool, device="cuda")
+    for t, h in rows:
+        hit[t, h] = True
+    assert out[hit].isnan().all() and lse2[hit].isnan().all()
+    # the rows beside them may take another way to the same sums, so they are held to the formula
+    check(q, 0, n, L, c, torch.where(hit[..., None], good, out), torch.where(hit, lse, lse2), 1 / math.sqrt(D), cap, 0)
+
+
+@pytest.mark.parametrize("n,L", [([1, 1], [300, 70000]), ([300, 40], [3000, 4000])])
+def test_attention_into_its_queries(n, L):
+    q, c = setup(n, L, 28, 4, 0, 32, pad=0)
+    at, lens = offsets(n), i32(L)
+    want = retopk.chunk_attention(q, c.h, lens, cu_tokens=at)
+    assert torch.equal(retopk.chunk_attention(q, c.h, lens, q, cu_tokens=at), want)
+
+
 def test_calls_refuse_tensors_elsewhere():
     q, c = setup([1], [10], 4, 1, 0, 19, pad=0)
     with pytest.raises(retopk.RetopkError):
@@ -587,6 +615,8 @@ def test_calls_refuse_tensors_elsewhere():
         retopk.chunk_attention(q, c.h, i32([10]).cpu())
     with pytest.raises(retopk.RetopkError):
         retopk.chunk_attention(q, c.h, i32([10]), lse=torch.empty((2, 4), device="cuda"))
+    with pytest.raises(retopk.RetopkError):
+        retopk.chunk_attention(q, c.h, i32([10]), workspace=torch.empty(1, dtype=torch.uint8, device="cuda").expand(1 << 24))
 
 
 # ---- together --------------------------------------------------------------------------------------------------------

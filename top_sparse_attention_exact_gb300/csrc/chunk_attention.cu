@@ -429,6 +429,14 @@ __device__ __forceinline__ float max3(float a, float b, float c)
     return d;
 }
 
+// The smaller one, NaN where either is.
+__device__ __forceinline__ float min_nan(float a, float b)
+{
+    float d;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+
 // softcap tanh(s / softcap) in powers of two, with tanh(y) = 1 - 2 / (1 + e^2y).
 __device__ __forceinline__ float capped(float s, float in, float cap2)
 {
@@ -897,7 +905,7 @@ __device__ __forceinline__ void softmax(const AttnLaunch &c, AttnShared &sh, flo
                                 // two reciprocals from one (beyond 2^60 the cap is reached)
 #pragma unroll
                                 for (int e = 0; e < kHalf; e += 2) {
-                                    const float d0 = 1.f + ex2(fminf(f[e] * cap_in, 60.f)), d1 = 1.f + ex2(fminf(f[e + 1] * cap_in, 60.f));
+                                    const float d0 = 1.f + ex2(min_nan(f[e] * cap_in, 60.f)), d1 = 1.f + ex2(min_nan(f[e + 1] * cap_in, 60.f));
                                     const float r = rcp(d0 * d1);
                                     f[e] = fmaf(-2.f * cap2, r * d1, cap2 - base);
                                     f[e + 1] = fmaf(-2.f * cap2, r * d0, cap2 - base);
@@ -1029,7 +1037,7 @@ __device__ __forceinline__ void softmax(const AttnLaunch &c, AttnShared &sh, flo
             }
             if (valid && ok) {
                 if (whole) {
-                    const float inv = l > 0.f ? 1.f / l : 0.f;
+                    const float inv = l == 0.f ? 0.f : 1.f / l;
                     uint16_t *const dst = a.out + t * a.out_stride + head * kD + h * 32;
 #pragma unroll
                     for (int e = 0; e < 32; e += 8)
@@ -1048,7 +1056,7 @@ __device__ __forceinline__ void softmax(const AttnLaunch &c, AttnShared &sh, flo
             if (!whole)
                 c.parts.ml[part * c.parts.rows + row] = make_float2(m, l);
             else if (a.lse)
-                a.lse[t * a.Hq + head] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+                a.lse[t * a.Hq + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
         }
         used += 2 * nt;
         if (pair && i == 0) {   // stream 1 may accumulate again
@@ -1350,13 +1358,13 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnLaunch c, int share
         if (mate != 0 || !real)
             continue;
         const int tok = first + second * tile_tokens + in_tile / a.G;
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
         const size_t t = here.t0 + tok;
         const int h = at.hk * a.G + in_tile % a.G;
         *reinterpret_cast<uint2 *>(a.out + t * a.out_stride + h * kD + lane * 4) =
             make_uint2(bf16x2(acc.x * inv, acc.y * inv), bf16x2(acc.z * inv, acc.w * inv));
         if (a.lse && lane == 0)
-            a.lse[t * a.Hq + h] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+            a.lse[t * a.Hq + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
     }
 }
 

@@ -458,7 +458,7 @@ def chunk_attention_workspace_bytes(T, B, Hq, Hkv) -> int:
 def chunk_attention(q, cache: KVCache, seqlens, out=None, cu_tokens=None, scale=None, softcap=0.0, window=0, lse=None,
                     workspace=None, status=None, stream=None):
     """Causal attention of q [T, Hq, 128] over a bf16 cache that holds the tokens' own rows (seqlens: rows in all);
-    returns out.  cu_tokens: offsets of each sequence's tokens (None: one token each, dense decoding).  lse: optional
+    returns out (which may be q).  cu_tokens: offsets of each sequence's tokens (None: one token each, dense decoding).  lse: optional
     fp32 [T, Hq].  workspace: uint8, chunk_attention_workspace_bytes(...) + 256 (None: allocated for the call)."""
     T, Hq = q.shape[:2]
     Hkv, B = cache.Hkv, seqlens.numel()
@@ -470,6 +470,8 @@ def chunk_attention(q, cache: KVCache, seqlens, out=None, cu_tokens=None, scale=
         raise RetopkError(f"out: {tuple(q.shape)} expected, got {tuple(out.shape)}")
     if workspace is None:
         workspace = _empty(chunk_attention_workspace_bytes(T, B, Hq, Hkv) + 256, torch.uint8, q.device, stream)
+    if not workspace.is_contiguous():
+        raise RetopkError("workspace: a contiguous tensor expected")
     wp = workspace.data_ptr()
     up = -wp % 256
     rc = (_lib or load()).retopk_chunk_attention(
