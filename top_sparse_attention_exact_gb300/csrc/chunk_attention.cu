@@ -481,7 +481,7 @@ struct AttnLaunch {
     long long items;   // at most
     // tanh(y) = y (1 + t (b_0 + b_1 t + b_2 t^2)), t = y^2, for |y| <= 1/2: b fitted at Chebyshev nodes for
     // the smallest largest error (6.4e-7 of the value).  Here for raw scores: y = s scale / softcap,
-    // so cap_poly[i] = b_i (scale / softcap)^(2 i + 2); cap_near: the largest |s|.
+    // in powers of two, so cap_poly[i] = b_i (scale / softcap)^(2 i + 2) scale log2(e); cap_near: the largest |s|.
     float cap_poly[3], cap_near;
 };
 
@@ -692,6 +692,7 @@ __device__ __forceinline__ void softmax(const AttnLaunch &c, AttnShared &sh, flo
     bool ok = true;
     uint32_t used = 0, done = 0, segs = 0, joins = 0;   // joins: of the two streams
     uint32_t done1 = 0;                               // tiles of stream 1
+    bool near = !CAP;                                 // the last tile's scores were all far below the cap
     while (ok && segment(sh, segs, a.status)) {
         const Segment &s = sh.segments[segs % kSegments];
         const int nt = s.j1 - s.j0, m_tiles = TWO ? nt : (nt + 1 - i) / 2;
@@ -755,10 +756,21 @@ __device__ __forceinline__ void softmax(const AttnLaunch &c, AttnShared &sh, flo
                     float base;
                     // Two keys at a time, in three steps that overlap: the exponents of pair n + kLead, the
                     // exponentials of pair n, the sum and the rounding of pair n - kLead.
+                    // (capped scores: by the polynomial, where all are far below the cap)
+                    auto two = [](float y) { return make_float2(y, y); };
                     auto exponents = [&](int n) {
-                        const float2 y = make_float2(f[2 * n], f[2 * n + 1]), less = make_float2(-base, -base);
-                        const float2 z = fma2(y, make_float2(scale2, scale2), less);
+                        const float2 y = make_float2(f[2 * n], f[2 * n + 1]);
+                        float2 factor = two(scale2);
+                        if (CAP) {
+                            const float2 t2 = mul2(y, y);
+                            factor = fma2(fma2(fma2(two(c.cap_poly[2]), t2, two(c.cap_poly[1])), t2, two(c.cap_poly[0])), t2, factor);
+                        }
+                        const float2 z = fma2(y, factor, two(-base));
                         f[2 * n] = z.x, f[2 * n + 1] = z.y;
+                    };
+                    auto near_capped = [&](float y) {
+                        const float t2 = y * y;
+                        return y * fmaf(fmaf(fmaf(c.cap_poly[2], t2, c.cap_poly[1]), t2, c.cap_poly[0]), t2, scale2);
                     };
                     auto exponentials = [&](int n) {
                         f[2 * n] = ex2(f[2 * n]);
@@ -776,12 +788,14 @@ __device__ __forceinline__ void softmax(const AttnLaunch &c, AttnShared &sh, flo
                     // m up to the tile's maximum where that has grown too far, and the accumulators with it;
                     // false when a wait ran out
                     auto raise = [&](float top) {
-                        const bool grow = m != -INFINITY && top > m + kLazy;
+                        const bool grow = valid && m != -INFINITY && top > m + kLazy;
                         if (__any_sync(0xffffffffu, grow)) {
                             if (!warp_wait(sh, &sh.o_full[i], (done + t - 1) & 1, a.status))
                                 return ok = false;
                             tc_fence_after();
-                            const float f2 = grow ? ex2(m - top) : 1.f;
+                            // every row goes up: the next tiles then find none just below the limit
+                            const float up = fmaxf(m, top), f2 = m == -INFINITY ? 1.f : ex2(m - up);
+                            m = up;
                             l *= f2;
 #pragma unroll 1
                             for (int q = 0; q < 8; ++q) {
@@ -794,14 +808,19 @@ __device__ __forceinline__ void softmax(const AttnLaunch &c, AttnShared &sh, flo
                                 tc_st16(o_addr + 16 * q, o);
                             }
                         }
-                        if (grow || m == -INFINITY)
+                        if (m == -INFINITY)
                             m = top;
                         return true;
                     };
                     bool made = false;
-                    if (!CAP && t > 0 && !part) {
+                    if (near && t > 0 && !part) {
                         base = m == -INFINITY ? 0.f : m;
-                        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, big[2] = {};
+                        auto seen = [&](int k, int e) {
+                            mx[k & 3] = max3(mx[k & 3], f[e], f[e + 1]);
+                            if (CAP)
+                                big[k & 1] = max3(big[k & 1], fabsf(f[e]), fabsf(f[e + 1]));
+                        };
                         tc_ld32(s_addr, x);
                         tc_ld32(s_addr + 32, x + 32);
                         tc_wait_ld32(x);
@@ -810,7 +829,7 @@ __device__ __forceinline__ void softmax(const AttnLaunch &c, AttnShared &sh, flo
                         tc_ld32(s_addr + 96, x + 96);
 #pragma unroll
                         for (int n = -kLead; n < kPairs / 2 - kLead; ++n) {
-                            mx[n & 3] = max3(mx[n & 3], f[2 * (n + kLead)], f[2 * (n + kLead) + 1]);
+                            seen(n, 2 * (n + kLead));
                             exponents(n + kLead);
                             if (n >= 0)
                                 exponentials(n);
@@ -822,11 +841,13 @@ __device__ __forceinline__ void softmax(const AttnLaunch &c, AttnShared &sh, flo
                             }
                             if (n >= 4 && n < 20) {   // the second half's maximum
                                 const int e = kHalf + 4 * (n - 4);
-                                mx[n & 3] = max3(mx[n & 3], f[e], f[e + 1]);
-                                mx[n + 1 & 3] = max3(mx[n + 1 & 3], f[e + 2], f[e + 3]);
+                                seen(n, e);
+                                seen(n + 1, e + 2);
                             }
                         }
-                        made = !__any_sync(0xffffffffu, max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * scale2 > m + kLazy);
+                        const float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
+                        made = !__any_sync(0xffffffffu, valid && (CAP ? fmaxf(big[0], big[1]) > c.cap_near || near_capped(top) > m + kLazy
+                                                                   : top * scale2 > m + kLazy));
                         if (made) {
 #pragma unroll
                             for (int n = kPairs / 2 - kLead; n < kPairs + kLead; ++n) {
@@ -845,7 +866,7 @@ __device__ __forceinline__ void softmax(const AttnLaunch &c, AttnShared &sh, flo
                             sum[0] = sum[1] = make_float2(0.f, 0.f);
                         }
                     }
-                    if constexpr (CAP) {
+                    if (CAP && !made) {
                         // Capped scores: half a row at a time, read once for the maximum (of the raw scores: the cap
                         // does not change their order) and once for the weights.  (All 128 at once are
                         // twice the instructions, more than the caches near the warps hold: 82 us against 76 for 1000
@@ -877,11 +898,7 @@ __device__ __forceinline__ void softmax(const AttnLaunch &c, AttnShared &sh, flo
                             size = max3(size, big[0], big[1]);
                         }
                         // far below the cap throughout: tanh as a polynomial
-                        auto near_capped = [&](float y) {
-                            const float t2 = y * y;
-                            return y * scale2 * fmaf(fmaf(fmaf(c.cap_poly[2], t2, c.cap_poly[1]), t2, c.cap_poly[0]), t2, 1.f);
-                        };
-                        const bool near = !__any_sync(0xffffffffu, valid && size > c.cap_near);
+                        near = !__any_sync(0xffffffffu, valid && size > c.cap_near);
                         // (their capped maximum by the form that the others take)
                         if (!raise(top == -INFINITY ? top : near ? near_capped(top) : capped(top, cap_in, cap2)))
                             break;
@@ -893,14 +910,9 @@ __device__ __forceinline__ void softmax(const AttnLaunch &c, AttnShared &sh, flo
                             tc_wait_ld32(x);
                             tc_wait_ld32(x + 32);
                             if (near) {
-                                auto two = [](float y) { return make_float2(y, y); };
 #pragma unroll
-                                for (int e = 0; e < kHalf; e += 2) {
-                                    const float2 y = make_float2(f[e], f[e + 1]), t2 = mul2(y, y);
-                                    const float2 p = fma2(fma2(two(c.cap_poly[2]), t2, two(c.cap_poly[1])), t2, two(c.cap_poly[0]));
-                                    const float2 z = fma2(mul2(y, two(scale2)), fma2(p, t2, two(1.f)), two(-base));
-                                    f[e] = z.x, f[e + 1] = z.y;
-                                }
+                                for (int n = 0; n < kHalf / 2; ++n)
+                                    exponents(n);
                             } else {
                                 // two reciprocals from one (beyond 2^60 the cap is reached)
 #pragma unroll
@@ -1442,7 +1454,7 @@ cudaError_t launch_chunk_attention(const AttnArgs &a, cudaStream_t st)
         const double b[3] = {-0.3332815934197915, 0.132053598066859, -0.04475064703577332};
         const double y = (double)a.scale / a.softcap;
         for (int i = 0; i < 3; ++i)
-            c.cap_poly[i] = (float)(b[i] * pow(y, 2 * i + 2));
+            c.cap_poly[i] = (float)(b[i] * pow(y, 2 * i + 2) * a.scale * 1.4426950408889634);
         // (a cap so small that the powers overflow: the other form for all but no scores)
         c.cap_near = isfinite(c.cap_poly[2]) ? (float)(0.5 / y) : -1.f;
     }
