@@ -142,7 +142,9 @@ __device__ __forceinline__ Place place_in(const AttnArgs &a, const Plan &p, cons
     const long long begin = weight(a, p, s, r.k);
     // short items are cut into no small parts: joining costs more than it gives
     const int nt = hi - lo, grain = nt >= 64 ? 1 : nt >= 16 ? 2 : 4;
-    const int x = (int)(__fdividef((float)(int)(u - begin), (float)(int)(weight(a, p, s, r.k + 1) - begin)) * nt);
+    // (half the item's own weight lies before its first tile, half behind its last)
+    const int in = (int)(u - begin) - kItemWeight / 2, keys = (int)(weight(a, p, s, r.k + 1) - begin) - kItemWeight;
+    const int x = (int)(__fdividef((float)max(in, 0), (float)keys) * nt);
     r.cut = (x + grain / 2) / grain * grain;
     if (r.cut >= nt) {   // the beginning of the next item
         r.cut = 0;
