@@ -869,29 +869,30 @@ __device__ __forceinline__ void softmax(const AttnLaunch &c, AttnShared &sh, flo
                         }
                     }
                     if (CAP && !made) {
-                        // Capped scores: half a row at a time, read once for the maximum (of the raw scores: the cap
-                        // does not change their order) and once for the weights.  (All 128 at once are
-                        // twice the instructions, more than the caches near the warps hold: 82 us against 76 for 1000
-                        // tokens in windows of 4096 keys.)
+                        // Capped scores that the one pass above does not take (an item's first tile, one that the mask
+                        // cuts, scores near the cap): a quarter of a row at a time, read once for the maximum (of the
+                        // raw scores: the cap does not change their order) and once for the weights.  Small code
+                        // matters here, as it is run now and then only: 16 tokens of 16 sequences over 5000 keys
+                        // take 35 us, by half rows 38; whole rows were slower again (1000 tokens in windows of
+                        // 4096 keys 82 us, by half rows 76).
+                        constexpr int kPiece = 32;
                         float top = -INFINITY, size = 0.f;
                         const int last = pos - j * kTile, first = low - j * kTile;
 #pragma unroll 1
-                        for (int h = 0; h < 2; ++h) {
-                            tc_ld32(s_addr + kHalf * h, x);
-                            tc_ld32(s_addr + kHalf * h + 32, x + 32);
+                        for (int h = 0; h < kTile / kPiece; ++h) {
+                            tc_ld32(s_addr + kPiece * h, x);
                             tc_wait_ld32(x);
-                            tc_wait_ld32(x + 32);
                             float mx[2] = {-INFINITY, -INFINITY}, big[2] = {};
                             if (part) {
 #pragma unroll
-                                for (int e = 0; e < kHalf; ++e) {
-                                    const bool seen = kHalf * h + e <= last && kHalf * h + e >= first;
+                                for (int e = 0; e < kPiece; ++e) {
+                                    const bool seen = kPiece * h + e <= last && kPiece * h + e >= first;
                                     mx[e & 1] = fmaxf(mx[e & 1], seen ? f[e] : -INFINITY);
                                     big[e & 1] = fmaxf(big[e & 1], seen ? fabsf(f[e]) : 0.f);
                                 }
                             } else {
 #pragma unroll
-                                for (int e = 0; e < kHalf; e += 2) {
+                                for (int e = 0; e < kPiece; e += 2) {
                                     mx[e >> 1 & 1] = max3(mx[e >> 1 & 1], f[e], f[e + 1]);
                                     big[e >> 1 & 1] = max3(big[e >> 1 & 1], fabsf(f[e]), fabsf(f[e + 1]));
                                 }
@@ -906,19 +907,17 @@ __device__ __forceinline__ void softmax(const AttnLaunch &c, AttnShared &sh, flo
                             break;
                         base = m == -INFINITY ? 0.f : m;
 #pragma unroll 1
-                        for (int h = 0; h < 2; ++h) {
-                            tc_ld32(s_addr + kHalf * h, x);
-                            tc_ld32(s_addr + kHalf * h + 32, x + 32);
+                        for (int h = 0; h < kTile / kPiece; ++h) {
+                            tc_ld32(s_addr + kPiece * h, x);
                             tc_wait_ld32(x);
-                            tc_wait_ld32(x + 32);
                             if (near) {
 #pragma unroll
-                                for (int n = 0; n < kHalf / 2; ++n)
+                                for (int n = 0; n < kPiece / 2; ++n)
                                     exponents(n);
                             } else {
                                 // two reciprocals from one (beyond 2^60 the cap is reached)
 #pragma unroll
-                                for (int e = 0; e < kHalf; e += 2) {
+                                for (int e = 0; e < kPiece; e += 2) {
                                     const float d0 = 1.f + ex2(min_nan(f[e] * cap_in, 60.f)), d1 = 1.f + ex2(min_nan(f[e + 1] * cap_in, 60.f));
                                     const float r = rcp(d0 * d1);
                                     f[e] = fmaf(-2.f * cap2, r * d1, cap2 - base);
@@ -927,19 +926,19 @@ __device__ __forceinline__ void softmax(const AttnLaunch &c, AttnShared &sh, flo
                             }
                             if (part) {
 #pragma unroll
-                                for (int e = 0; e < kHalf; ++e)
-                                    f[e] = kHalf * h + e <= last && kHalf * h + e >= first ? f[e] : -INFINITY;
+                                for (int e = 0; e < kPiece; ++e)
+                                    f[e] = kPiece * h + e <= last && kPiece * h + e >= first ? f[e] : -INFINITY;
                             }
 #pragma unroll
-                            for (int n = 0; n < kHalf / 2 + kLead; ++n) {
-                                if (n < kHalf / 2)
+                            for (int n = 0; n < kPiece / 2 + kLead; ++n) {
+                                if (n < kPiece / 2)
                                     exponentials(n);
                                 if (n >= kLead)
                                     rounding(n - kLead);
                             }
                             // P takes the columns of scores that are done with
-                            tc_st32(p_addr + 32 * h, x);
-                            if (h == 0)
+                            tc_st16(p_addr + kPiece / 2 * h, x);
+                            if (h == kTile / kPiece / 2 - 1)
                                 hand_over();
                         }
                     }
