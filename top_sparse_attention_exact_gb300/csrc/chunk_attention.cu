@@ -737,11 +737,13 @@ __device__ __forceinline__ void softmax(const AttnLaunch &c, AttnShared &sh, flo
                     ok = warp_wait(sh, &sh.kv_full[st], (u / kAttnStages) & 1, a.status);
                     if (!ok)
                         break;
-                    if (j * kTile + r >= s.seq.L) {
-#pragma unroll 1
-                        for (int q = 0; q < 16; ++q)
+                    // (the warp's 32 rows, four halves of rows at a time: 8 lanes side by side in each)
+#pragma unroll(TWO ? 2 : 1)
+                    for (int q = 0; q < 16; ++q) {
+                        const int row = (r & ~31) + (q & 7) * 4 + lane / 8;
+                        if (j * kTile + row >= s.seq.L)
                             asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
-                                             ring + st * kAttnStageBytes + (q >> 3) * kHalfBytes + r * 128 + (q & 7) * 16),
+                                             ring + st * kAttnStageBytes + (q >> 3) * kHalfBytes + row * 128 + (lane & 7) * 16),
                                          "r"(0)
                                          : "memory");
                     }
