@@ -32,9 +32,9 @@
 // workspace, and the join kernel adds them up.  Shares, and with them the order of
 // every sum, depend on the lengths alone.
 //
-// Measured (28 query heads over 4 KV heads but where said).  4096 tokens over 32768 keys: 1260 us,
-// 1.43 PFLOP/s, held by the GPU's power limit (1200 us in short bursts), the matrix unit busy 59 % of the
-// cycles between its waits for the softmax.  One token over 131072 keys: 51 us, 5.3 TB/s, of which the stream
+// Measured (28 query heads over 4 KV heads but where said).  4096 tokens over 32768 keys: 1228 us,
+// 1.47 PFLOP/s, held by the GPU's power limit (1133 us in short bursts, held by the chain softmax -> P V ->
+// Q K of each group).  One token over 131072 keys: 51 us, 5.3 TB/s, of which the stream
 // takes 40.  61 ragged sequences of 9000 keys, 32 over 8 heads: 216 us, 6.8 TB/s, the memory's rate.  3 x 333
 // tokens in windows of 4096 keys, capped, 16 over 2 heads: 64 us, 0.52 PFLOP/s, held by the softmax's instructions.
 #include <math.h>
@@ -55,6 +55,7 @@ constexpr int kMmaWarp = 8, kLoadWarp = 9, kWalkWarp = 10;
 constexpr int kSegments = 4;                     // known ahead
 constexpr int kHalf = kTile / 2;                 // keys of half a tile
 // registers of a thread after the split: 2 x 128 x 208 + 128 x 88 = 384 x 168, what the block is launched with
+// (4096 tokens over 32768 keys in short bursts: 1133 us; with 216 and 72 or 224 and 56, 1190)
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
 // Weight of an item beside its keys: what beginning and ending it costs, in keys.  (A prompt
 // of 8192 tokens: 494 us with 128, 386 with 512, 399 with 1024; 128 sequences of 1500 keys: 135 us with
@@ -759,7 +760,7 @@ __device__ __forceinline__ void softmax(const AttnLaunch &c, AttnShared &sh, flo
                         if (lane == 0)
                             mbar_arrive(p_bar);
                     };
-                    constexpr int kLead = 4, kPairs = kTile / 2;
+                    constexpr int kLead = 4, kPairs = kTile / 2;   // (1133 us as above; with 2, 3, 6: 1166, 1146, 1184)
                     uint32_t x[kTile];
                     float *f = reinterpret_cast<float *>(x);
                     float2 sum[2] = {};
