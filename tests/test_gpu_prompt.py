@@ -490,6 +490,19 @@ def test_attention_scores_that_grow_along_the_history():
     check(q, 0, n, L, c, out, None, 1 / math.sqrt(D), 0.0, 0)
 
 
+@pytest.mark.parametrize("n,L,window", [([200], [3000], 0), ([1], [9000], 0), ([90, 3], [2500, 6000], 700)])
+@pytest.mark.parametrize("cap", [0.0, 4.0, 30.0, 1000.0])
+def test_attention_scores_whose_size_comes_and_goes(n, L, window, cap):
+    # stretches of small and of large scores: far below the cap and at it by turns, maxima that jump and stay
+    q, c = setup(n, L, 7, 1, 0, 33, qscale=1.0)
+    for b, rows in enumerate(L):
+        wave = torch.exp2(6 * torch.sin(torch.arange(rows, device="cuda") / 211.0) - 3)[:, None, None]
+        c.put(b, (normal(gen(34 + b), rows, 1, D) * wave).to(torch.bfloat16), normal(gen(36 + b), rows, 1, D))
+    lse = torch.empty((sum(n) + 2, 7), device="cuda")
+    out = retopk.chunk_attention(q, c.h, i32(L), cu_tokens=offsets(n), softcap=cap, window=window, lse=lse)
+    check(q, 0, n, L, c, out, lse, 1 / math.sqrt(D), cap, window)
+
+
 def test_attention_lengths_beyond_the_capacity_are_clamped():
     q, c = setup([1], [64], 4, 1, 0, 12, pad=0)
     c.put(0, normal(gen(1), 71, 1, D), normal(gen(2), 71, 1, D))
