@@ -32,10 +32,10 @@
 // workspace, and the join kernel adds them up.  Shares, and with them the order of
 // every sum, depend on the lengths alone.
 //
-// Measured (28 query heads over 4 KV heads but where said).  4096 tokens over 32768 keys: 1228 us,
-// 1.47 PFLOP/s, held by the GPU's power limit (1133 us in short bursts, held by the chain softmax -> P V ->
-// Q K of each group).  One token over 131072 keys: 51 us, 5.3 TB/s, of which the stream
-// takes 40.  61 ragged sequences of 9000 keys, 32 over 8 heads: 216 us, 6.8 TB/s, the memory's rate.  3 x 333
+// Measured (28 query heads over 4 KV heads but where said).  4096 tokens over 32768 keys: 1224 us,
+// 1.48 PFLOP/s, held by the GPU's power limit (1133 us in short bursts, held by the chain softmax -> P V ->
+// Q K of each group).  One token over 131072 keys: 51 us, 5.2 TB/s, of which the stream
+// takes 40.  61 ragged sequences of 9000 keys, 32 over 8 heads: 219 us, 6.7 TB/s, 98 % of a plain copy's rate.  3 x 333
 // tokens in windows of 4096 keys, capped, 16 over 2 heads: 64 us, 0.52 PFLOP/s, held by the softmax's instructions.
 #include <math.h>
 
@@ -147,7 +147,8 @@ __device__ __forceinline__ Place place_in(const AttnArgs &a, const Plan &p, cons
     int lo, hi;
     tiles_of(a, p, s, r.k, lo, hi);
     const long long begin = weight(a, p, s, r.k);
-    // short items are cut into no small parts: joining costs more than it gives
+    // short items are cut into no small parts: joining costs more than it gives (8 sequences of 50 tokens over 1000
+    // keys 29 us, cut anywhere 32); long ones anywhere (4 of 19 over 9000 keys 32 us, by fours 34)
     const int nt = hi - lo, grain = nt >= 64 ? 1 : nt >= 16 ? 2 : 4;
     // (half the item's own weight lies before its first tile, half behind its last)
     const int in = (int)(u - begin) - kItemWeight / 2, keys = (int)(weight(a, p, s, r.k + 1) - begin) - kItemWeight;
@@ -1402,9 +1403,11 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnLaunch c, int share
 }
 
 // ---- host side ----------------------------------------------------------------
-// Two tiles of tokens a block where the sequences have more tokens than a tile
-// on average; else one tile and two streams of keys.
-static bool two_tiles(int T, int B, int G) { return T / B > kTile / G; }
+// Two tiles of tokens a block where the sequences have more tokens than one and a half tiles
+// on average; else one tile and two streams of keys.  (18 tokens a tile.  40 sequences over 1500 keys, streams against
+// two tiles: of 12 tokens 39 us against 45, of 24 51 against 54, of 36 63 against 59, of 72 100 against 79;
+// 4 over 9000: of 24 30 against 32, of 36 35 against 38, of 72 47 against 48.)
+static bool two_tiles(int T, int B, int G) { return T / B > kTile / G * 3 / 2; }
 
 // Rows of a part.
 static int part_rows(int T, int G, bool two)
