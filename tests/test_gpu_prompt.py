@@ -551,6 +551,21 @@ def test_attention_shared_pages():
     check(q, 0, [1, 1], [200, 150], c, out, None, 1 / math.sqrt(D), 0.0, 0)
 
 
+@pytest.mark.parametrize("Hq,Hkv", [(7, 1), (28, 4), (3, 1), (16, 1)])
+@pytest.mark.parametrize("n,page", [(1, 0), (1, 16), (2, 48), (30, 0)])
+@pytest.mark.parametrize("tail", [float("nan"), float("inf")])
+def test_attention_past_the_length_in_tiles_that_some_warps_have_no_token_for(Hq, Hkv, n, page, tail):
+    # The last tile ends among keys 32..63: values past the length there are cleared by lanes whose warp may have no
+    # row of its own (few heads, few tokens), and reach the product's first half.
+    lens = [33, 44, 47, 63, 128 + 34, 256 + 44, 384 + 61, 1280 + 50]
+    q, c = setup([n] * len(lens), lens, Hq, Hkv, page, 41 + n + Hq)
+    for x in (c.k, c.v):
+        x.copy_(torch.where(x.isnan(), torch.full_like(x, tail), x))
+    lse = torch.empty((len(lens) * n + 2, Hq), device="cuda")
+    out = retopk.chunk_attention(q, c.h, i32(lens), cu_tokens=offsets([n] * len(lens)), lse=lse)
+    check(q, 0, [n] * len(lens), lens, c, out, lse, 1 / math.sqrt(D), 0.0, 0)
+
+
 def test_attention_captured_and_replayed_with_new_lengths():
     lens, n = [900, 333], [1, 1]
     q, c = setup(n, lens, 28, 4, 64, 15, pad=0, strided=False)

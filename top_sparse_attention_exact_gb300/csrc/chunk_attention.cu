@@ -761,6 +761,7 @@ __device__ __forceinline__ void softmax(const AttnLaunch &c, AttnShared &sh, flo
                                          : "memory");
                     }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();   // every lane's rows are clear before one lane hands over P, rows to it or not
                 }
                 if (work) {
                     const bool part = j * kTile + kTile - 1 > all_hi || j * kTile < all_lo;
