@@ -566,6 +566,46 @@ def test_attention_past_the_length_in_tiles_that_some_warps_have_no_token_for(Hq
     check(q, 0, [n] * len(lens), lens, c, out, lse, 1 / math.sqrt(D), 0.0, 0)
 
 
+@pytest.mark.parametrize("Hq,Hkv", [(7, 1), (28, 4), (16, 1)])
+@pytest.mark.parametrize("n,page,window", [(1, 0, 0), (1, 16, 100), (3, 48, 0), (40, 0, 0), (64, 16, 57)])
+@pytest.mark.parametrize("cap", [5.0, 1e-3])
+def test_attention_capped_scores_beside_keys_past_the_length(Hq, Hkv, n, page, window, cap):
+    # Scores past half the cap, and lengths that end between two neighbouring keys: the last key, and each token's own,
+    # have a hidden one beside them, whose score is NaN or infinite where it lies past the length.
+    lens = [n, 129, 301, 128 + 33, 256 + 63, 2051]
+    q, c = setup([n] * len(lens), lens, Hq, Hkv, page, 43 + n + Hq, qscale=6.0)
+    lse = torch.empty((len(lens) * n + 2, Hq), device="cuda")
+    for tail in (float("nan"), float("inf"), -float("inf")):
+        for x in (c.k, c.v):
+            x.copy_(torch.where(x.isfinite(), x, torch.full_like(x, tail)))
+        out = retopk.chunk_attention(q, c.h, i32(lens), cu_tokens=offsets([n] * len(lens)), softcap=cap, window=window, lse=lse)
+        check(q, 0, [n] * len(lens), lens, c, out, lse, 1 / math.sqrt(D), cap, window)
+
+
+@pytest.mark.parametrize("n,L", [([1, 1], [301, 7001]), ([200, 3], [901, 2051])])
+def test_attention_capped_queries_that_are_not_finite_stay_in_their_rows(n, L):
+    # the same of scores past half the cap, with odd lengths and NaN behind them: rows of such a query are NaN, no others
+    q, c = setup(n, L, 14, 2, 64, 47, pad=0, qscale=6.0, strided=False)
+    T, at, lens = sum(n), offsets(n), i32(L)
+    hit = torch.zeros((T, 14), dtype=torch.bool, device="cuda")
+    hit[0, 3] = hit[n[0], 0] = hit[T - 1, 13] = True
+    clean = q.clone()
+    q[hit] = float("nan")
+    lse = torch.empty((T, 14), device="cuda")
+    for cap in (5.0, 1e-3):
+        out = retopk.chunk_attention(q, c.h, lens, cu_tokens=at, lse=lse, softcap=cap)
+        assert out[hit].isnan().all() and lse[hit].isnan().all()
+        t = 0
+        for b in range(len(n)):
+            sel, rows = slice(t, t + n[b]), c.rows(b, L[b])
+            t += n[b]
+            ref, rl, mass, d = reference(clean[sel], *rows, L[b] - n[b], 1 / math.sqrt(D), cap, 0)
+            bad = (out[sel].double() - ref).abs() > 2.0 ** -8 * ref.abs() + (2.0 ** -8 + 2 * d + 2.0 ** -14) * mass
+            off = (lse[sel].double() - rl).abs() > d + 2.0 ** -20 * (1 + rl.abs())
+            assert not out[sel][~hit[sel]].isnan().any() and not lse[sel][~hit[sel]].isnan().any()
+            assert not bad[~hit[sel]].any() and not off[~hit[sel]].any()
+
+
 def test_attention_captured_and_replayed_with_new_lengths():
     lens, n = [900, 333], [1, 1]
     q, c = setup(n, lens, 28, 4, 64, 15, pad=0, strided=False)

@@ -439,11 +439,11 @@ __device__ __forceinline__ float max3(float a, float b, float c)
     return d;
 }
 
-// The smaller one, NaN where either is.
-__device__ __forceinline__ float min_nan(float a, float b)
+// The largest one, NaN where one is.
+__device__ __forceinline__ float max3_nan(float a, float b, float c)
 {
     float d;
-    asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
 
@@ -910,18 +910,21 @@ __device__ __forceinline__ void softmax(const AttnLaunch &c, AttnShared &sh, flo
                                 for (int e = 0; e < kPiece; ++e) {
                                     const bool seen = kPiece * h + e <= last && kPiece * h + e >= first;
                                     mx[e & 1] = fmaxf(mx[e & 1], seen ? f[e] : -INFINITY);
-                                    big[e & 1] = fmaxf(big[e & 1], seen ? fabsf(f[e]) : 0.f);
+                                    big[e & 1] = max3_nan(big[e & 1], big[e & 1], seen ? fabsf(f[e]) : 0.f);
                                 }
                             } else {
 #pragma unroll
                                 for (int e = 0; e < kPiece; e += 2) {
                                     mx[e >> 1 & 1] = max3(mx[e >> 1 & 1], f[e], f[e + 1]);
-                                    big[e >> 1 & 1] = max3(big[e >> 1 & 1], fabsf(f[e]), fabsf(f[e + 1]));
+                                    big[e >> 1 & 1] = max3_nan(big[e >> 1 & 1], fabsf(f[e]), fabsf(f[e + 1]));
                                 }
                             }
                             top = max3(top, mx[0], mx[1]);
-                            size = max3(size, big[0], big[1]);
+                            size = max3_nan(size, big[0], big[1]);
                         }
+                        // (a seen score that is NaN makes the row's sum NaN: by size, as the weights lose it)
+                        if (size != size)
+                            l = size;
                         // far below the cap throughout: tanh as a polynomial
                         near = !__any_sync(0xffffffffu, valid && size > c.cap_near);
                         // (their capped maximum by the form that the others take)
@@ -937,10 +940,11 @@ __device__ __forceinline__ void softmax(const AttnLaunch &c, AttnShared &sh, flo
                                 for (int n = 0; n < kPiece / 2; ++n)
                                     exponents(n);
                             } else {
-                                // two reciprocals from one (beyond 2^60 the cap is reached)
+                                // two reciprocals from one (beyond 2^60 the cap is reached).  A hidden score may be
+                                // NaN and is the partner of one that is seen, so NaN takes the bound here
 #pragma unroll
                                 for (int e = 0; e < kPiece; e += 2) {
-                                    const float d0 = 1.f + ex2(min_nan(f[e] * cap_in, 60.f)), d1 = 1.f + ex2(min_nan(f[e + 1] * cap_in, 60.f));
+                                    const float d0 = 1.f + ex2(fminf(f[e] * cap_in, 60.f)), d1 = 1.f + ex2(fminf(f[e + 1] * cap_in, 60.f));
                                     const float r = rcp(d0 * d1);
                                     f[e] = fmaf(-2.f * cap2, r * d1, cap2 - base);
                                     f[e + 1] = fmaf(-2.f * cap2, r * d0, cap2 - base);
