@@ -249,6 +249,24 @@ def test_append_odd_offsets_and_lengths_stay_inside():
         assert (out[0] == 9).all() and (out[10] == 9).all() and sl[3] == 77
 
 
+def test_append_offsets_and_lengths_at_the_ends_of_their_type():
+    # differences of these pass 32 bits: no sequence whose tokens do not fit is written or advances
+    low, high = -(1 << 31), (1 << 31) - 1
+    for cu, start in (([low, 2, 4, 9], [3, 4, 5]), ([0, 2, 4, high], [3, high, 5]), ([low, high, high, high], [0, low, 2])):
+        q = normal(gen(3), 9, 2, D)
+        c = Cache(3, 2, 32, 16, fill=1.0)
+        before, st = c.snapshot(), torch.zeros(1, dtype=torch.int32, device="cuda")
+        out, sl = torch.full((11, 2, D), 9.0, dtype=torch.bfloat16, device="cuda"), i32([0, 0, 0, 77])
+        retopk.qkv_append(retopk.QKRope(freqs(128)), q, q, q, c.h, i32(start), sl[:3], out[1:10], cu_tokens=i32(cu), status=st)
+        fits = [s >= 0 and 0 <= b - a and s + b - a <= 32 for a, b, s in zip(cu, cu[1:], start)]
+        assert sl.tolist() == [s + b - a if f else s for a, b, s, f in zip(cu, cu[1:], start, fits)] + [77]
+        assert (out[0] == 9).all() and (out[10] == 9).all() and st.item() in (0, retopk.STATUS_KV_FULL)
+        for b in range(3):      # pages of sequences that do not fit are as they were
+            if not fits[b]:
+                pages = c.table[b].long()
+                assert all(torch.equal(x[pages], y[pages]) for x, y in zip(c.snapshot(), before))
+
+
 def test_append_captured_and_replayed_advances_each_time():
     g = gen(31)
     B = 3

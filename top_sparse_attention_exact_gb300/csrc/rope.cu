@@ -51,8 +51,8 @@ __device__ __forceinline__ int sequence_of(const int32_t *cu, int B, int t, int 
 
 __device__ __forceinline__ int advanced(const RopeArgs &a, int b)
 {
-    const int n = a.cu ? a.cu[b + 1] - a.cu[b] : 1, L = a.seqlens[b];
-    return L >= 0 && n >= 0 && (long long)L + n <= a.capacity ? L + n : L;
+    const long long n = a.cu ? (long long)a.cu[b + 1] - a.cu[b] : 1, L = a.seqlens[b];
+    return (int)(L >= 0 && n >= 0 && L + n <= a.capacity ? L + n : L);
 }
 
 // Where the keys and values go.
@@ -184,13 +184,13 @@ __global__ void __launch_bounds__(kRopeWarps * 32, kRopeBlocks) rope_kernel(cons
             }
             if (begin <= t && t < end) {
                 L = a.seqlens[b];
-                fits = L >= 0 && (long long)L + (end - begin) <= a.capacity;
+                fits = L >= 0 && (long long)L + end - begin <= a.capacity;   // (whatever the offsets: no row outside is written)
             }
             in_page = 0;
         }
         const bool in = begin <= t && t < end;
         if (in) {
-            const int pos = L + (t - begin);
+            const int pos = (int)((uint32_t)L + (uint32_t)t - (uint32_t)begin);   // (of a sequence that fits: within the capacity)
             if (TO && !fits && t == begin && p0 == 0 && lane == 0 && a.status)
                 atomicOr(a.status, RETOPK_STATUS_KV_FULL);
             if (p0 < nq + nk) {
