@@ -471,8 +471,9 @@ int retopk_cache_copy(const retopk_cache *src, const retopk_cache *dst, const in
  * L_b are never used, whatever they hold.  A row below L_b that is not finite
  * may reach every token of its sequence; a query that is not stays in its row.  Lengths beyond the cache's capacity
  * are clamped to it.  scale 0 means 1/sqrt(128).
- * d_workspace: >= retopk_chunk_attention_workspace_bytes, 256-byte aligned;
- * concurrent calls need one each.  Long histories of few tokens are split over the GPU
+ * d_workspace: >= retopk_chunk_attention_workspace_bytes, 256-byte aligned; what
+ * it gives for T tokens is enough for fewer of the same heads, whatever their sequences
+ * (on the device that was current: it counts the SMs); concurrent calls need one each.  Long histories of few tokens are split over the GPU
  * and joined from it.  Results do not depend on the other sequences of the call beyond
  * rounding.  Graph-capturable. */
 size_t retopk_chunk_attention_workspace_bytes(int T, int B, int Hq, int Hkv);

@@ -101,6 +101,15 @@ def test_attention_workspace_sizes(lib):
         assert n(*bad) == 0
 
 
+@pytest.mark.parametrize("Hq,Hkv", [(28, 4), (32, 8), (16, 1), (8, 8), (7, 1)])
+def test_a_workspace_of_the_largest_call_is_enough_for_smaller_ones(lib, Hq, Hkv):
+    n = lib.retopk_chunk_attention_workspace_bytes
+    sizes = [1, 2, 7, 17, 18, 27, 28, 36, 128, 192, 193, 512, 4096, 1 << 20]
+    at = {(T, B): n(T, B, Hq, Hkv) for T in sizes for B in sizes[:-1]}
+    for (T, B), most in at.items():
+        assert most > 0 and all(size <= most for (T2, _), size in at.items() if T2 <= T)
+
+
 def test_copy_refuses(lib):
     a, b, other = cache(), cache(k=P + 65536, v=P + 65536), cache(k=P + 65536, v=P + 65536, n_kv_heads=2)
     call = lambda x, y, first=P, last=P, B=2, rows=10, st=None: lib.retopk_cache_copy(  # noqa: E731

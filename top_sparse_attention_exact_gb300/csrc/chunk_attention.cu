@@ -1420,22 +1420,27 @@ static int part_rows(int T, int G, bool two)
     return two ? 2 * kTile : (int)std::min<long long>(kTile, ((long long)T * G + 7) / 8 * 8);
 }
 
-static size_t carve(int T, int B, int Hq, int Hkv, char *ws, Parts *p)
+static size_t carve(int rows, char *ws, Parts *p)
 {
-    const int G = Hq / Hkv, n = std::min(sm_count(), kMaxShares);
-    const size_t rows = part_rows(T, G, two_tiles(T, B, G));
+    const int n = std::min(sm_count(), kMaxShares);
     const size_t o_ml = ((n + 1) * sizeof(Bound) + 255) / 256 * 256;
-    const size_t o_o = o_ml + (2 * n * rows * sizeof(float2) + 255) / 256 * 256;
+    const size_t o_o = o_ml + (2 * n * (size_t)rows * sizeof(float2) + 255) / 256 * 256;
     if (p) {
         p->bound = reinterpret_cast<Bound *>(ws);
         p->ml = reinterpret_cast<float2 *>(ws + o_ml);
         p->o = reinterpret_cast<float4 *>(ws + o_o);
-        p->rows = (int)rows;
+        p->rows = rows;
     }
-    return o_o + 2 * n * rows * kD * sizeof(float);
+    return o_o + 2 * n * (size_t)rows * kD * sizeof(float);
 }
 
-size_t chunk_attention_ws(int T, int B, int Hq, int Hkv) { return carve(T, B, Hq, Hkv, nullptr, nullptr); }
+// Enough for fewer tokens and any number of sequences as well: of all batches of T tokens, the one of a single sequence
+// has the most rows a part.
+size_t chunk_attention_ws(int T, int Hq, int Hkv)
+{
+    const int G = Hq / Hkv;
+    return carve(part_rows(T, G, two_tiles(T, 1, G)), nullptr, nullptr);
+}
 
 static bool make_map(CUtensorMap *map, const void *p, cuuint64_t d1, cuuint64_t d2, cuuint64_t s1, cuuint64_t s2, int b1,
                      int b2)
@@ -1478,7 +1483,7 @@ cudaError_t launch_chunk_attention(const AttnArgs &a, cudaStream_t st)
     if (a.capacity <= 4 * kTile)
         c.shares = (int)std::min<long long>(c.shares, c.items);
     c.plan.inverse = ~0ull / (unsigned long long)c.shares;
-    carve(a.T, a.B, a.Hq, Hkv, static_cast<char *>(a.ws), &c.parts);
+    carve(part_rows(a.T, a.G, two), static_cast<char *>(a.ws), &c.parts);
     if (a.softcap > 0.f) {
         const double b[3] = {-0.3332815934197915, 0.132053598066859, -0.04475064703577332};
         const double y = (double)a.scale / a.softcap;

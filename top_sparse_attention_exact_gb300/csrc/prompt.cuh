@@ -170,7 +170,7 @@ struct AttnArgs {
     float scale, softcap;
     void *ws;
 };
-size_t chunk_attention_ws(int T, int B, int Hq, int Hkv);
+size_t chunk_attention_ws(int T, int Hq, int Hkv);
 cudaError_t launch_chunk_attention(const AttnArgs &a, cudaStream_t st);
 
 }  // namespace retopk

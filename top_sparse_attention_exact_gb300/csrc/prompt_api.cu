@@ -184,7 +184,7 @@ size_t retopk_chunk_attention_workspace_bytes(int T, int B, int Hq, int Hkv)
     if (T < 0 || B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || T > kMaxTokens || B > kMaxBatch ||
         Hq > kMaxHeads || Hq / Hkv > kMaxGroup)
         return 0;
-    return chunk_attention_ws(T, B, Hq, Hkv);
+    return chunk_attention_ws(T, Hq, Hkv);
 }
 
 int retopk_chunk_attention(const retopk_bf16 *q, int64_t q_stride, const retopk_cache *cache,
