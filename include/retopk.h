@@ -433,12 +433,13 @@ typedef struct retopk_rope {
  * positions seqlens[b], seqlens[b] + 1, ... (seqlens: rows before these
  * tokens), into q_out [T, Hq, 128] and k_out [T, Hkv, 128].  With one token for
  * each sequence its outputs are the q and k_new of retopk_decode_step_kv.
- * q_out may be q and k_out may be k where the strides are the outputs'.
+ * q_out may be q and k_out may be k where the strides are the outputs'; outputs that
+ * share memory with the inputs, or with each other, in any other way are refused.
  *
  * retopk_qkv_append: the same, with the keys and the values written to rows
  * seqlens[b] + i of the cache (bf16 or MX8), and seqlens_out[b] = seqlens[b] +
  * the sequence's tokens.  seqlens_out may be seqlens (advanced in place, as
- * retopk_append_kv does, by a second launch) or a separate buffer.  A sequence
+ * retopk_append_kv does, by a second launch) or a separate buffer (one that overlaps it is refused).  A sequence
  * whose tokens do not fit sets RETOPK_STATUS_KV_FULL and keeps its rows and
  * its length; its queries are still written. */
 int retopk_qk_rope(const retopk_rope *rope, const retopk_bf16 *q, int64_t q_stride, const retopk_bf16 *k,
@@ -455,7 +456,7 @@ int retopk_qkv_append(const retopk_rope *rope, const retopk_bf16 *q, int64_t q_s
  * that decoding reads, bf16 rows are parked in MX8 form, pages are gathered
  * into contiguous rows.  Equal formats copy bits.  max_rows bounds last[b] -
  * first[b] (it sizes the launch; rows beyond it are not copied); rows outside either cache's
- * capacity are not copied and set RETOPK_STATUS_GATHER.  src and dst must not overlap. */
+ * capacity are not copied and set RETOPK_STATUS_GATHER.  src and dst must not overlap (refused). */
 int retopk_cache_copy(const retopk_cache *src, const retopk_cache *dst, const int32_t *first, const int32_t *last,
                       int B, int max_rows, uint32_t *d_status, void *stream);
 
@@ -466,7 +467,7 @@ int retopk_cache_copy(const retopk_cache *src, const retopk_cache *dst, const in
  *   s_j = scale q.k_j, with softcap > 0: softcap tanh(s_j / softcap)
  *   out = sum_j softmax(s)_j v_j,   lse = log sum_j exp(s_j)
  * q, out [T, Hq, 128] bf16, tokens q_stride / out_stride elements apart; lse
- * [T, Hq] fp32 or NULL; out may be q where the strides are the same.  A token that sees no key (L_b < n_b, L_b = 0) gets
+ * [T, Hq] fp32 or NULL; out may be q where the strides are the same (another overlap is refused).  A token that sees no key (L_b < n_b, L_b = 0) gets
  * zeros and lse = -inf.  The cache must be RETOPK_CACHE_BF16; rows at or past
  * L_b are never used, whatever they hold.  A row below L_b that is not finite
  * may reach every token of its sequence; a query that is not stays in its row.  Lengths beyond the cache's capacity

@@ -693,6 +693,19 @@ def test_attention_into_its_queries(n, L):
     assert torch.equal(retopk.chunk_attention(q, c.h, lens, q, cu_tokens=at), want)
 
 
+@pytest.mark.parametrize("n,L", [([1, 1], [300, 7000]), ([300, 40], [900, 400])])
+def test_attention_between_its_queries(n, L):
+    # queries and outputs by turns in the rows of one buffer
+    q, c = setup(n, L, 28, 4, 0, 33, pad=0)
+    T, at, lens = sum(n), offsets(n), i32(L)
+    want = retopk.chunk_attention(q, c.h, lens, cu_tokens=at)
+    for first, second in ((0, 28), (28, 0)):
+        both = torch.zeros((T, 56, D), dtype=torch.bfloat16, device="cuda")
+        x, y = both[:, first:first + 28], both[:, second:second + 28]
+        x.copy_(q)
+        assert torch.equal(retopk.chunk_attention(x, c.h, lens, y, cu_tokens=at), want) and torch.equal(x, q)
+
+
 def test_calls_refuse_tensors_elsewhere():
     q, c = setup([1], [10], 4, 1, 0, 19, pad=0)
     with pytest.raises(retopk.RetopkError):

@@ -110,6 +110,27 @@ def test_a_workspace_of_the_largest_call_is_enough_for_smaller_ones(lib, Hq, Hkv
         assert most > 0 and all(size <= most for (T2, _), size in at.items() if T2 <= T)
 
 
+def test_outputs_that_overlap_what_is_read_are_refused(lib):
+    far, c = P + (1 << 20), cache(k=P + (1 << 24), v=P + (1 << 25))
+    ok = dict(c=c, q=P, k=P + 65536, v=P + 131072, qo=far, sl=P + 262144, so=P + 262144)
+    for kw in (dict(qo=P + 2048), dict(qo=P + 65536 + 1024), dict(qo=P + 131072 - 1024), dict(q=P + 1024, qo=P), dict(so=P + 262144 + 4),
+               dict(so=P + 262144 - 4)):
+        assert append(lib, **{**ok, **kw}) == -1
+    r = rope()
+    turn = lambda qo, ko, k=P + 65536: lib.retopk_qk_rope(  # noqa: E731
+        ctypes.addressof(r), P, 1024, k, 512, None, 2, 2, 8, 4, P + 262144, qo, ko, None)
+    for qo, ko in ((P + 16, far), (far, P + 2048), (P + 65536, far), (far, far + 2048), (far + 1024, far), (P, P)):
+        assert turn(qo, ko) == -1
+    # rows of 1024 elements in the same or another stride
+    for q, qs, out, os in ((P, 2048, P, 1024), (P, 1024, P, 2048), (P, 2048, P + 1024, 2048), (P, 2048, P + 3072, 2048),
+                           (P + 1024, 2048, P, 2048), (P, 1024, P + 2048, 1024), (P, 2048, P + 2048, 1024)):
+        assert attend(lib, c=c, q=q, qs=qs, out=out, os=os, sl=P + 65536, ws=P + 131072) == -1
+    a = cache()     # 2 pages of 102400 bytes
+    for b in (cache(k=P + 65536, v=far), cache(k=far, v=P + 204784), cache(k=far, v=P), cache(k=P - 204784, v=far)):
+        for x, y in ((a, b), (b, a)):
+            assert lib.retopk_cache_copy(ctypes.addressof(x), ctypes.addressof(y), P, P, 2, 10, None, None) == -1
+
+
 def test_copy_refuses(lib):
     a, b, other = cache(), cache(k=P + 65536, v=P + 65536), cache(k=P + 65536, v=P + 65536, n_kv_heads=2)
     call = lambda x, y, first=P, last=P, B=2, rows=10, st=None: lib.retopk_cache_copy(  # noqa: E731

@@ -46,12 +46,44 @@ int check_tokens(int T, int B, int Hq, int Hkv, const int32_t *cu, const int32_t
     return RETOPK_OK;
 }
 
+// Bytes of a cache's keys (or values).
+size_t pool_bytes(const retopk_cache &c)
+{
+    return (size_t)c.n_pages * c.n_kv_heads * c.page_rows * kD * (c.format == RETOPK_CACHE_MX8 ? 1 : 2);
+}
+
 // A strided [T, heads, 128] tensor.
 int check_rows(const void *p, int64_t stride, int heads)
 {
     if (!p || stride < (int64_t)heads * kD || stride > INT32_MAX)
         return RETOPK_ERR_INVALID;
     return aligned(p, 16) && stride % 8 == 0 ? RETOPK_OK : RETOPK_ERR_ALIGN;
+}
+
+// Bytes [p, p + n) and [q, q + m).
+bool meet(const void *p, size_t n, const void *q, size_t m)
+{
+    return (uintptr_t)p < (uintptr_t)q + m && (uintptr_t)q < (uintptr_t)p + n;
+}
+
+// Whether two strided [T, heads, 128] tensors share an element; of two whose rows lie between each other's, those of one
+// stride are told apart, others count as sharing.
+bool rows_meet(const void *p, int64_t ps, int pheads, const void *q, int64_t qs, int qheads, int T)
+{
+    const int64_t pw = (int64_t)pheads * kD * 2, qw = (int64_t)qheads * kD * 2;   // bytes
+    if (!meet(p, (T - 1) * ps * 2 + pw, q, (T - 1) * qs * 2 + qw))
+        return false;
+    if (ps != qs || T == 1)
+        return true;
+    const int64_t s = ps * 2, d = (((int64_t)((uintptr_t)q - (uintptr_t)p)) % s + s) % s;
+    return d < pw || d + qw > s;
+}
+
+// An output of rows that are one of the inputs', row for row, or share nothing with it.
+bool may_write(const void *out, int64_t out_stride, const void *in, int64_t in_stride, int heads, int T)
+{
+    return (out == in && (out_stride == in_stride || T == 1)) ||
+           !rows_meet(out, out_stride, heads, in, in_stride, heads, T);
 }
 
 int check_rope(const retopk_rope *r)
@@ -84,6 +116,11 @@ int retopk_qk_rope(const retopk_rope *rope, const retopk_bf16 *q, int64_t q_stri
         return RETOPK_ERR_INVALID;
     if (!aligned(q_out, 16) || !aligned(k_out, 16))
         return RETOPK_ERR_ALIGN;
+    const int64_t qw = (int64_t)Hq * kD, kw = (int64_t)Hkv * kD;
+    if (!may_write(q_out, qw, q, q_stride, Hq, T) || !may_write(k_out, kw, k, k_stride, Hkv, T) ||
+        rows_meet(q_out, qw, Hq, k, k_stride, Hkv, T) || rows_meet(k_out, kw, Hkv, q, q_stride, Hq, T) ||
+        rows_meet(q_out, qw, Hq, k_out, kw, Hkv, T))
+        return RETOPK_ERR_INVALID;
     if ((e = ensure_configured()))
         return e;
     RopeArgs a{};
@@ -125,7 +162,13 @@ int retopk_qkv_append(const retopk_rope *rope, const retopk_bf16 *q, int64_t q_s
             return RETOPK_ERR_INVALID;
         if (!aligned(q_out, 16))
             return RETOPK_ERR_ALIGN;
+        const int64_t qw = (int64_t)Hq * kD;
+        if (!may_write(q_out, qw, q, q_stride, Hq, T) || rows_meet(q_out, qw, Hq, k, k_stride, Hkv, T) ||
+            rows_meet(q_out, qw, Hq, v, v_stride, Hkv, T))
+            return RETOPK_ERR_INVALID;
     }
+    if (seqlens_out != seqlens && meet(seqlens_out, B * sizeof(int32_t), seqlens, B * sizeof(int32_t)))
+        return RETOPK_ERR_INVALID;
     if ((e = ensure_configured()))
         return e;
     RopeArgs a{};
@@ -176,6 +219,10 @@ int retopk_cache_copy(const retopk_cache *src, const retopk_cache *dst, const in
         return RETOPK_ERR_ALIGN;
     if (max_rows == 0)
         return RETOPK_OK;
+    for (const void *x : {src->k, src->v})
+        for (const void *y : {dst->k, dst->v})
+            if (meet(x, pool_bytes(*src), y, pool_bytes(*dst)))
+                return RETOPK_ERR_INVALID;
     return cuda_rc(launch_cache_copy(*src, *dst, first, last, B, max_rows, d_status, (cudaStream_t)stream));
 }
 
@@ -208,6 +255,8 @@ int retopk_chunk_attention(const retopk_bf16 *q, int64_t q_stride, const retopk_
     if (!d_workspace || !aligned(d_workspace, 256) ||
         bytes < retopk_chunk_attention_workspace_bytes(T, B, Hq, cache->n_kv_heads))
         return RETOPK_ERR_WORKSPACE;
+    if (!may_write(out, out_stride, q, q_stride, Hq, T))
+        return RETOPK_ERR_INVALID;
     if ((e = ensure_configured()))
         return e;
     AttnArgs a{};
