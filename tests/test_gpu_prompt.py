@@ -706,6 +706,19 @@ def test_attention_between_its_queries(n, L):
         assert torch.equal(retopk.chunk_attention(x, c.h, lens, y, cu_tokens=at), want) and torch.equal(x, q)
 
 
+def test_numbers_beyond_32_bits_are_not_taken_for_others():
+    q, c = setup([1], [600], 4, 1, 0, 20, pad=0)
+    lens, flat = i32([600]), Cache(1, 1, 600, fill=0.0)
+    want = retopk.chunk_attention(q, c.h, lens)
+    assert torch.equal(retopk.chunk_attention(q, c.h, lens, window=(1 << 32) + 5), want)
+    for kw in (dict(window=-(1 << 32)), dict(softcap=1e-50), dict(scale=1e-50), dict(softcap=1e39), dict(scale=-1.0)):
+        with pytest.raises(retopk.RetopkError):
+            retopk.chunk_attention(q, c.h, lens, **kw)
+    for rows in ((1 << 32) + 5, -(1 << 32) + 5):
+        with pytest.raises(retopk.RetopkError):
+            retopk.cache_copy(c.h, flat.h, i32([0]), lens, rows)
+
+
 def test_calls_refuse_tensors_elsewhere():
     q, c = setup([1], [10], 4, 1, 0, 19, pad=0)
     with pytest.raises(retopk.RetopkError):

@@ -164,3 +164,14 @@ def test_python_handles_check_their_tensors():
                 lambda: retopk.KVCache(k, k)._holds(3, "call")):
         with pytest.raises(retopk.RetopkError):
             bad()
+
+
+def test_python_numbers_do_not_wrap_into_others():
+    for n in ((1 << 32) + 4, 1 << 31, -(1 << 32) + 1, -1):
+        with pytest.raises(retopk.RetopkError):
+            retopk.chunk_attention_workspace_bytes(n, 1, 28, 4)
+    assert retopk._bound((1 << 32) + 5) == (1 << 31) - 1 and retopk._bound(-(1 << 32)) == -1 and retopk._bound(7) == 7
+    assert retopk._real(0.0, "x") == 0.0 and retopk._real(1e-30, "x") == 1e-30
+    for bad in (lambda: retopk.QKRope(eps=1e-50), lambda: retopk._real(-1e-50, "x")):
+        with pytest.raises(retopk.RetopkError):
+            bad()

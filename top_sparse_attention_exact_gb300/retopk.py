@@ -337,6 +337,18 @@ def _status(t: torch.Tensor | None):
     return t.data_ptr()
 
 
+def _bound(n: int) -> int:
+    """A bound that C takes in 32 bits: one above them bounds as little as their largest, one below zero is refused there."""
+    return max(-1, min(n, (1 << 31) - 1))
+
+
+def _real(x: float, what: str) -> float:
+    """A number that C takes in 32 bits, where a zero has a meaning of its own."""
+    if x != 0 and ctypes.c_float(x).value == 0:
+        raise RetopkError(f"{what}: {x} is zero in 32 bits")
+    return x
+
+
 def _same(t: torch.Tensor, shape, what: str):
     if t.dtype not in _BF16_TYPES or t.shape != shape or not t.is_contiguous():
         raise RetopkError(f"{what}: a contiguous bf16 {tuple(shape)} tensor expected, got {t.dtype} {tuple(t.shape)}")
@@ -396,7 +408,7 @@ class QKRope:
             raise RetopkError("inv_freq: a contiguous fp32 [rot_dim / 2] tensor expected")
         self.tensors = (inv_freq, q_weight, k_weight)
         p = lambda t: None if t is None else t.data_ptr()  # noqa: E731
-        self.struct = retopk_rope(p(q_weight), p(k_weight), p(inv_freq), eps,
+        self.struct = retopk_rope(p(q_weight), p(k_weight), p(inv_freq), _real(eps, "eps"),
                                   0 if inv_freq is None else 2 * inv_freq.numel(), 1 if interleaved else 0)
         self._ref = ctypes.addressof(self.struct)
 
@@ -443,13 +455,14 @@ def cache_copy(src: KVCache, dst: KVCache, first, last, max_rows: int | None = N
     B = first.numel()
     st = _call_stream(stream, (src.k, dst.k, first, last, status))
     rc = (_lib or load()).retopk_cache_copy(src._holds(B, "cache_copy"), dst._holds(B, "cache_copy"), _lens(first, B, "first"),
-                                  _lens(last, B, "last"), B, min(src.rows, dst.rows) if max_rows is None else max_rows,
+                                  _lens(last, B, "last"), B,
+                                  min(src.rows, dst.rows) if max_rows is None else _bound(max_rows),
                                   _status(status), st)
     _check(rc, "retopk_cache_copy")
 
 
 def chunk_attention_workspace_bytes(T, B, Hq, Hkv) -> int:
-    n = load().retopk_chunk_attention_workspace_bytes(T, B, Hq, Hkv)
+    n = load().retopk_chunk_attention_workspace_bytes(_bound(T), _bound(B), _bound(Hq), _bound(Hkv))
     if n == 0:
         raise RetopkError("chunk_attention_workspace_bytes: invalid sizes")
     return int(n)
@@ -458,8 +471,8 @@ def chunk_attention_workspace_bytes(T, B, Hq, Hkv) -> int:
 def chunk_attention(q, cache: KVCache, seqlens, out=None, cu_tokens=None, scale=None, softcap=0.0, window=0, lse=None,
                     workspace=None, status=None, stream=None):
     """Causal attention of q [T, Hq, 128] over a bf16 cache that holds the tokens' own rows (seqlens: rows in all);
-    returns out (which may be q).  cu_tokens: offsets of each sequence's tokens (None: one token each, dense decoding).  lse: optional
-    fp32 [T, Hq].  workspace: uint8, chunk_attention_workspace_bytes(...) + 256 (None: allocated for the call)."""
+    returns out (which may be q).  cu_tokens: offsets of each sequence's tokens (None: one token each, dense decoding).  scale: 1/sqrt(128)
+    where None or 0.  lse: optional fp32 [T, Hq].  workspace: uint8, chunk_attention_workspace_bytes(...) + 256 (None: allocated for the call)."""
     T, Hq = q.shape[:2]
     Hkv, B = cache.Hkv, seqlens.numel()
     out = _empty((T, Hq, 128), q.dtype, q.device, stream) if out is None else out
@@ -476,7 +489,8 @@ def chunk_attention(q, cache: KVCache, seqlens, out=None, cu_tokens=None, scale=
     up = -wp % 256
     rc = (_lib or load()).retopk_chunk_attention(
         q.data_ptr(), _tokens(q, "q"), cache._holds(B, "chunk_attention"), _lens(cu_tokens, B + 1, "cu_tokens"), T, B,
-        Hq, _lens(seqlens, B, "seqlens"), 0.0 if scale is None else scale, softcap, window, out.data_ptr(),
+        Hq, _lens(seqlens, B, "seqlens"), 0.0 if scale is None else _real(scale, "scale"),
+        _real(softcap, "softcap"), _bound(window), out.data_ptr(),
         _tokens(out, "out"), None if lse is None else lse.data_ptr(), wp + up,
         max(0, workspace.numel() * workspace.element_size() - up), _status(status), st)
     _check(rc, "retopk_chunk_attention")
