@@ -303,6 +303,28 @@ def test_qk_rope_is_appends_rows_and_works_in_place(rot, inter):
     assert torch.equal(q, q2) and torch.equal(k, k2)
 
 
+@pytest.mark.parametrize("rot,inter,norm", [(128, False, True), (64, True, False), (32, False, True), (0, False, True)])
+def test_qk_rope_of_ragged_tokens(rot, inter, norm):
+    g = gen(11 + rot)
+    n, start, Hq, Hkv = [7, 0, 1, 130, 33], [0, 3, 16, 500, 1 << 20], 28, 4
+    T = sum(n)
+    proj = normal(g, T + 3, (Hq + Hkv) * D, scale=2.0)
+    q, k = (x.view(T + 3, -1, D) for x in proj.split([Hq * D, Hkv * D], dim=1))
+    qw, kw = (normal(g, D) for _ in range(2)) if norm else (None, None)
+    inv = freqs(rot) if rot else None
+    qo, ko = (torch.full((T + 3, H, D), 7.0, dtype=torch.bfloat16, device="cuda") for H in (Hq, Hkv))
+    sl = i32(start)
+    retopk.qk_rope(retopk.QKRope(inv, qw, kw, interleaved=inter), q, k, sl, qo, ko, cu_tokens=offsets(n))
+    assert sl.tolist() == start and (qo[T:] == 7).all() and (ko[T:] == 7).all()
+    t = 0
+    for b in range(len(n)):
+        sel, pos = slice(t, t + n[b]), start[b] + torch.arange(n[b], device="cuda")
+        t += n[b]
+        for x, w, out in ((q, qw, qo), (k, kw, ko)):
+            ref, tol = rotated(x[sel], w, inv, pos, inter, 1e-6)
+            assert ((out[sel].double() - ref).abs() <= 2.0 ** -8 * ref.abs() + tol).all()
+
+
 def test_append_nothing_moves_lengths_over():
     c = Cache(2, 2, 32)
     e = torch.empty((0, 4, D), dtype=torch.bfloat16, device="cuda")
@@ -719,6 +741,54 @@ def test_numbers_beyond_32_bits_are_not_taken_for_others():
             retopk.cache_copy(c.h, flat.h, i32([0]), lens, rows)
 
 
+@pytest.mark.parametrize("n,L,Hq,Hkv,page", [([1], [70001], 28, 4, 0), ([1, 1], [40000, 30001], 16, 1, 16), ([40], [20011], 7, 1, 48),
+                                             ([3, 9], [9000, 25003], 8, 8, 0), ([300], [8300], 28, 4, 64)])
+def test_attention_counts_every_tile_of_a_long_history_once(n, L, Hq, Hkv, page):
+    # Column d of V is 1 in one tile of 128 keys and 0 elsewhere, other tiles each time: an output is that tile's share of
+    # the weights, and its bound is relative to it.
+    q, c = setup(n, L, Hq, Hkv, page, 50, pad=0, qscale=0.5)
+    at, lens = offsets(n), i32(L)
+    for first in range(0, -(-max(L) // 128), D):
+        for b, rows in enumerate(L):
+            tile = torch.arange(rows, device="cuda") // 128 - first
+            p, r = c.at(b, rows)
+            c.v[p, :, r] = (tile[:, None] == torch.arange(D, device="cuda")).to(torch.bfloat16)[:, None]
+        out = retopk.chunk_attention(q, c.h, lens, cu_tokens=at)
+        check(q, 0, n, L, c, out, None, 1 / math.sqrt(D), 0.0, 0)
+
+
+@pytest.mark.parametrize("n,L", [([600] + [1] * 40, [700] + [50 * i for i in range(1, 41)]), ([1] * 20 + [1500], [900] * 20 + [1700]),
+                                 ([2049], [2049]), ([1] * 30 + [64, 257], [100 * i for i in range(30)] + [64, 3001])])
+@pytest.mark.parametrize("cap", [0.0, 5.0])
+def test_attention_of_prompts_among_single_tokens(n, L, cap):
+    q, c = setup(n, L, 14, 2, 48, 51)
+    lse = torch.empty((sum(n) + 2, 14), device="cuda")
+    out = retopk.chunk_attention(q, c.h, i32(L), cu_tokens=offsets(n), softcap=cap, lse=lse)
+    check(q, 0, n, L, c, out, lse, 1 / math.sqrt(D), cap, 0)
+
+
+def test_attention_of_several_batches_in_one_workspace():
+    # the largest call's workspace serves smaller ones, with more and with fewer sequences
+    ws = torch.empty(retopk.chunk_attention_workspace_bytes(900, 512, 28, 4) + 256, dtype=torch.uint8, device="cuda")
+    calls = []
+    for i, (n, L) in enumerate((([3] * 300, [60 + i for i in range(300)]), ([900], [2000]), ([1], [30000]), ([20, 5], [4000, 900]))):
+        q, c = setup(n, L, 28, 4, 16, 60 + i, pad=0)
+        calls.append((q, c, i32(L), offsets(n), retopk.chunk_attention(q, c.h, i32(L), cu_tokens=offsets(n))))
+    graphs = []
+    for q, c, lens, at, want in calls:
+        out = torch.empty_like(want)
+        assert torch.equal(retopk.chunk_attention(q, c.h, lens, out, cu_tokens=at, workspace=ws), want)
+        graphs.append((torch.cuda.CUDAGraph(), out))
+        with torch.cuda.graph(graphs[-1][0]):
+            retopk.chunk_attention(q, c.h, lens, out, cu_tokens=at, workspace=ws)
+    for _ in range(2):      # captured calls that share it, one behind the other
+        for g, out in graphs:
+            out.zero_()
+            g.replay()
+        for (g, out), call in zip(graphs, calls):
+            assert torch.equal(out, call[4])
+
+
 def test_calls_refuse_tensors_elsewhere():
     q, c = setup([1], [10], 4, 1, 0, 19, pad=0)
     with pytest.raises(retopk.RetopkError):
@@ -729,6 +799,67 @@ def test_calls_refuse_tensors_elsewhere():
         retopk.chunk_attention(q, c.h, i32([10]), lse=torch.empty((2, 4), device="cuda"))
     with pytest.raises(retopk.RetopkError):
         retopk.chunk_attention(q, c.h, i32([10]), workspace=torch.empty(1, dtype=torch.uint8, device="cuda").expand(1 << 24))
+
+
+# ---- far offsets -------------------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("contiguous", [False, True])
+def test_rows_past_two_to_the_31_elements(contiguous):
+    """Appended, attended, parked and read back in pools of more than 2^31 elements, in their last pages."""
+    g = gen(70)
+    Hq, n = 8, [40, 3]
+    if contiguous:      # sequences 0 and 2 lie below, 1 (and the last rows of 2) beyond
+        B, Hkv, page, rows, start = 3, 1, 0, 1 << 23, [5, 7, (1 << 23) - 40]
+        n, pages, table = [3, 40, 40], 3, None
+    else:
+        B, Hkv, page, rows, start = 2, 4, 256, 1024, [500, 250]
+        pages = (1 << 31) // (Hkv * page * D) + 9
+        table = i32([[pages - 1 - 2 * i, pages - 2 - 2 * i][b] for b in range(2) for i in range(4)]).view(2, 4)
+    T, last = sum(n), [a + b for a, b in zip(start, n)]
+    shape = (pages, Hkv, page or rows, D)
+    assert pages * Hkv * (page or rows) * D > 1 << 31
+    kv = [torch.zeros(shape, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    c = Cache.__new__(Cache)
+    c.page, c.mx8, c.table, c.k, c.v, c.ks, c.vs = page, False, table, kv[0], kv[1], None, None
+    c.h = retopk.KVCache(*kv, table=table)
+    q, k, v = normal(g, T, Hq, D), normal(g, T, Hkv, D), normal(g, T, Hkv, D)
+    sl, at, st = i32(start), offsets(n), torch.zeros(1, dtype=torch.int32, device="cuda")
+    rope = retopk.QKRope()      # (rows as they are)
+    retopk.qkv_append(rope, q, k, v, c.h, sl, cu_tokens=at, status=st)
+    assert sl.tolist() == last and st.item() == 0
+    new = [slice(a - b, a) for a, b in zip(np.cumsum(n).tolist(), n)]
+
+    def place(b):
+        pos = torch.arange(start[b], last[b], device="cuda")
+        return (table[b, pos // page].long(), pos % page) if page else (torch.full_like(pos, b), pos)
+
+    for b in range(B):
+        p, r = place(b)
+        assert torch.equal(c.k[p, :, r], k[new[b]]) and torch.equal(c.v[p, :, r], v[new[b]])
+    out = retopk.chunk_attention(q, c.h, sl, cu_tokens=at, window=30)
+    for b in range(B):      # rows before the new ones are zeros: 29 of them, where there are as many
+        zeros = torch.zeros((min(start[b], 29), Hkv, D), dtype=torch.bfloat16, device="cuda")
+        ref, _, mass, d = reference(q[new[b]], torch.cat([zeros, k[new[b]]]), torch.cat([zeros, v[new[b]]]), len(zeros), 1 / math.sqrt(D), 0.0, 30)
+        assert ((out[new[b]].double() - ref).abs() <= 2.0 ** -8 * ref.abs() + (2.0 ** -8 + 2 * d + 2.0 ** -14) * mass).all()
+    codes = [torch.zeros(shape, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    scales = [torch.zeros(shape[:3] + (4,), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    parked = retopk.KVCache(*codes, table=table, k_scale=scales[0], v_scale=scales[1])
+    retopk.cache_copy(c.h, parked, i32(start), sl, 64, status=st)
+    for x in kv:
+        x.zero_()
+    retopk.cache_copy(parked, c.h, i32(start), sl, 64, status=st)
+    again = [[x[p, :, r].clone() for x in kv] for p, r in map(place, range(B))]
+    for b in range(B):
+        for x, y in zip(again[b], (k[new[b]], v[new[b]])):
+            top = y.double().unflatten(-1, (4, 32)).abs().amax(-1, keepdim=True).expand(-1, -1, 4, 32).flatten(-2)
+            assert ((x.double() - y.double()).abs() <= torch.maximum(2.0 ** -4 * y.double().abs(), top * 2.0 ** -17)).all()
+    # the same rows from the 8-bit append
+    for x in codes + scales + kv:
+        x.zero_()
+    retopk.qkv_append(rope, q, k, v, parked, i32(start), cu_tokens=at, status=st)
+    retopk.cache_copy(parked, c.h, i32(start), sl, 64, status=st)
+    assert st.item() == 0
+    for b in range(B):
+        assert all(torch.equal(x[place(b)[0], :, place(b)[1]], y) for x, y in zip(kv, again[b]))
 
 
 # ---- together --------------------------------------------------------------------------------------------------------
