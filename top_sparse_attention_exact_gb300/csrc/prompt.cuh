@@ -134,11 +134,6 @@ __device__ __forceinline__ void unpack8(const uint4 &u, float (&x)[8])
     x[4] = bf16lo(u.z), x[5] = bf16hi(u.z), x[6] = bf16lo(u.w), x[7] = bf16hi(u.w);
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&x)[8])
-{
-    return make_uint4(bf16x2(x[0], x[1]), bf16x2(x[2], x[3]), bf16x2(x[4], x[5]), bf16x2(x[6], x[7]));
-}
-
 // ---- launchers ----------------------------------------------------------------
 struct RopeArgs {
     const uint16_t *q, *k, *v;                 // v == NULL: no cache
