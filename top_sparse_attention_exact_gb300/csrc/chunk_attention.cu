@@ -761,7 +761,6 @@ __device__ __forceinline__ void softmax(const AttnLaunch &c, AttnShared &sh, flo
                                          : "memory");
                     }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    __syncwarp();   // every lane's rows are clear before one lane hands over P, rows to it or not
                 }
                 if (work) {
                     const bool part = j * kTile + kTile - 1 > all_hi || j * kTile < all_lo;
@@ -1018,8 +1017,10 @@ __device__ __forceinline__ void softmax(const AttnLaunch &c, AttnShared &sh, flo
                     l = live ? l + both.x + both.y : 0.f;
                     m = live ? m : -INFINITY;
                     tc_wait_st();
-                } else if (lane == 0) {
-                    mbar_arrive(p_bar);
+                } else {
+                    __syncwarp();   // every lane's rows past the length are clear (hand_over has its own)
+                    if (lane == 0)
+                        mbar_arrive(p_bar);
                 }
                 tc_fence_before();
                 __syncwarp();
