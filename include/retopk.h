@@ -387,7 +387,10 @@ int retopk_support_overlap(const int32_t *S, const int32_t *others, int rows, in
                                  with the smallest scale that keeps the 32 values
                                  within 448, codes rounded to nearest even once.  A
                                  block with a NaN or an infinity gets scale 255 and
-                                 reads back as NaN; an all-zero block scale 0.       */
+                                 reads back as NaN; an all-zero block scale 0.
+                                 retopk_qkv_append and retopk_cache_copy write such
+                                 rows, retopk_cache_copy alone reads them: before it is
+                                 attended or decoded a sequence is read back to bf16. */
 
 /* The keys and values of B sequences: k and v are [n_pages, n_kv_heads,
  * page_rows, 128] (bf16, or e4m3 bytes with k_scale / v_scale [n_pages,
@@ -476,7 +479,9 @@ int retopk_cache_copy(const retopk_cache *src, const retopk_cache *dst, const in
  * it gives for T tokens is enough for fewer of the same heads, whatever their sequences
  * (on the device that was current: it counts the SMs); concurrent calls need one each.  Long histories of few tokens are split over the GPU
  * and joined from it.  Results do not depend on the other sequences of the call beyond
- * rounding.  Graph-capturable. */
+ * rounding; the weights are rounded to bf16 once, which out carries (2^-8 sum_j p_j |v_j|), all else is fp32.
+ * A call is shaped by its mean of tokens a sequence: a prompt of thousands of tokens beside a hundred and
+ * more single tokens is sooner done in a call of its own.  Graph-capturable. */
 size_t retopk_chunk_attention_workspace_bytes(int T, int B, int Hq, int Hkv);
 int retopk_chunk_attention(const retopk_bf16 *q, int64_t q_stride, const retopk_cache *cache,
                            const int32_t *cu_tokens, int T, int B, int Hq, const int32_t *seqlens, float scale,

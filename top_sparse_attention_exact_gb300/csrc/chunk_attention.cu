@@ -32,11 +32,18 @@
 // workspace, and the join kernel adds them up.  Shares, and with them the order of
 // every sum, depend on the lengths alone.
 //
-// Measured (28 query heads over 4 KV heads but where said).  4096 tokens over 32768 keys: 1224 us,
-// 1.48 PFLOP/s, held by the GPU's power limit (1133 us in short bursts, held by the chain softmax -> P V ->
+// Rounding.  Scores, maxima, sums, parts and accumulators have 32 bits.  P is rounded to bf16, as the matrix
+// instruction takes both operands in one type and V is bf16: an output is off by up to 2^-8 sum_j p_j |v_j| for it
+// (against 64 bits 0.0019 to 0.0023 of the outputs' size, where 32-bit weights give 0.0017, the output's own rounding).
+//
+// Measured (28 query heads over 4 KV heads but where said).  4096 tokens over 32768 keys: 1233 us,
+// 1.47 PFLOP/s, held by the GPU's power limit (1133 us in short bursts, held by the chain softmax -> P V ->
 // Q K of each group).  One token over 131072 keys: 51 us, 5.2 TB/s, of which the stream
 // takes 40.  61 ragged sequences of 9000 keys, 32 over 8 heads: 219 us, 6.7 TB/s, 98 % of a plain copy's rate.  3 x 333
-// tokens in windows of 4096 keys, capped, 16 over 2 heads: 64 us, 0.52 PFLOP/s, held by the softmax's instructions.
+// tokens in windows of 4096 keys, 16 over 2 heads: 53 us; capped, 65 us, and 80 with scores past half the cap.
+// What an item costs beside its tiles shows where items are short or shares small: a prompt of 2048 tokens 60 us and
+// of 8192 388 (0.50 and 1.24 PFLOP/s), 128 sequences of 1500 keys, 32 over 8 heads, 130 us (3.9 TB/s), 36 tokens over
+// 17663 keys, 16 over 2 heads, 39 us (0.13 PFLOP/s), one token over 300 keys 11.7 us.
 #include <math.h>
 
 #include <algorithm>
@@ -58,8 +65,8 @@ constexpr int kHalf = kTile / 2;                 // keys of half a tile
 // (4096 tokens over 32768 keys in short bursts: 1133 us; with 216 and 72 or 224 and 56, 1190)
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
 // Weight of an item beside its keys: what beginning and ending it costs, in keys.  (A prompt
-// of 8192 tokens: 494 us with 128, 386 with 512, 399 with 1024; 128 sequences of 1500 keys: 135 us with
-// 256, 126 with 512, 128 with 1024.)
+// of 8192 tokens: 494 us with 128, 386 with 512, 399 with 1024; 128 sequences of 1500 keys, 32 over 8 heads: 135 us
+// with 256, 126 with 512, 128 with 1024.)
 constexpr int kItemWeight = 512;
 constexpr float kLazy = 8.f;                     // growth of m, in powers of two, that is left to the accumulators
 
@@ -893,9 +900,9 @@ __device__ __forceinline__ void softmax(const AttnLaunch &c, AttnShared &sh, flo
                         // Capped scores that the one pass above does not take (an item's first tile, one that the mask
                         // cuts, scores near the cap): a quarter of a row at a time, read once for the maximum (of the
                         // raw scores: the cap does not change their order) and once for the weights.  Small code
-                        // matters here, as it is run now and then only: 16 tokens of 16 sequences over 5000 keys
-                        // take 35 us, by half rows 38; whole rows were slower again (1000 tokens in windows of
-                        // 4096 keys 82 us, by half rows 76).
+                        // matters here, as it is run now and then only: one token of each of 16 sequences over
+                        // 5000 keys takes 35 us, by half rows 38; whole rows were slower again (3 x 333 tokens in
+                        // windows of 4096 keys, 16 over 2 heads, 82 us, by half rows 76).
                         constexpr int kPiece = 32;
                         float top = -INFINITY, size = 0.f;
                         const int last = pos - j * kTile, first = low - j * kTile;
@@ -1275,7 +1282,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 }
 
 // Joins the parts of an item.  With two tiles the grid's columns are the cut items (few
-// items of many rows then have many blocks each: 36 tokens over 17663 keys 48 -> 38 us);
+// items of many rows then have many blocks each: 36 tokens over 17663 keys, 16 over 2 heads, 48 -> 38 us);
 // with one, where that search costs more than it gives, they are the bounds, and the first
 // that cuts an item has it.  One, two, four or eight warps of a block take a row and share
 // out its parts: as many as leave the item's blocks about one pass over the rows.
@@ -1412,7 +1419,11 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnLaunch c, int share
 // Two tiles of tokens a block where the sequences have more tokens than one and a half tiles
 // on average; else one tile and two streams of keys.  (18 tokens a tile.  40 sequences over 1500 keys, streams against
 // two tiles: of 12 tokens 39 us against 45, of 24 51 against 54, of 36 63 against 59, of 72 100 against 79;
-// 4 over 9000: of 24 30 against 32, of 36 35 against 38, of 72 47 against 48.)
+// 4 over 9000: of 24 30 against 32, of 36 35 against 38, of 72 47 against 48.)  The mean stands for all sequences, as
+// the lengths are the device's: a prompt among many single tokens takes the streams.  Against two calls, the prompt
+// in one and the tokens in the other, 4096 tokens over 32768 keys beside 200 single tokens over 9000 take 2064 us
+// (two calls 1729), 4096 over 4096 beside 200 over 1500 274 (259); with fewer tokens beside it one call is the faster:
+// 512 over 9000 beside 63 over 9000 221 (254), 4096 over 32768 beside 63 over 9000 1350 (1382, in two tiles).
 static bool two_tiles(int T, int B, int G) { return T / B > kTile / G * 3 / 2; }
 
 // Rows of a part.
