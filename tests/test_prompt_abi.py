@@ -122,7 +122,7 @@ def test_outputs_that_overlap_what_is_read_are_refused(lib):
     for qo, ko in ((P + 16, far), (far, P + 2048), (P + 65536, far), (far, far + 2048), (far + 1024, far), (P, P)):
         assert turn(qo, ko) == -1
     # rows of 1024 elements in the same or another stride
-    for q, qs, out, os in ((P, 2048, P, 1024), (P, 1024, P, 2048), (P, 2048, P + 1024, 2048), (P, 2048, P + 3072, 2048),
+    for q, qs, out, os in ((P, 2048, P, 1024), (P, 1024, P, 2048), (P, 2048, P + 1024, 2048), (P, 2048, P + 2064, 2048),
                            (P + 1024, 2048, P, 2048), (P, 1024, P + 2048, 1024), (P, 2048, P + 2048, 1024)):
         assert attend(lib, c=c, q=q, qs=qs, out=out, os=os, sl=P + 65536, ws=P + 131072) == -1
     a = cache()     # 2 pages of 102400 bytes
