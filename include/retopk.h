@@ -391,18 +391,28 @@ int retopk_support_overlap(const int32_t *S, const int32_t *others, int rows, in
                                  retopk_qkv_append and retopk_cache_copy write such
                                  rows, retopk_cache_copy alone reads them: before it is
                                  attended or decoded a sequence is read back to bf16. */
+#define RETOPK_CACHE_FP4  2   /* a row is 128 e2m1 codes, two a byte (element 2 i in the low
+                                 half of byte i), and 8 scale bytes: value = code * scale for
+                                 each 16 elements.  A code is a sign (bit 3) and one of 0, 0.5,
+                                 1, 1.5, 2, 3, 4, 6; a scale byte is the upper bits of a positive
+                                 fp16: 5 of exponent, 3 of mantissa.  Written with
+                                 the largest size over 6 rounded to nearest, at most 10240 (so
+                                 values beyond 61440 saturate), codes rounded to nearest even
+                                 once.  A block with a NaN or an infinity gets scale 255 and
+                                 reads back as NaN.  retopk_qkv_append and retopk_cache_copy
+                                 write such rows, retopk_cache_copy reads them. */
 
 /* The keys and values of B sequences: k and v are [n_pages, n_kv_heads,
  * page_rows, 128] (bf16, or e4m3 bytes with k_scale / v_scale [n_pages,
- * n_kv_heads, page_rows, 4]).  Row i of sequence b is row i % page_rows of page
+ * n_kv_heads, page_rows, 4], or 64 bytes a row with scales [..., 8] for FP4).  Row i of sequence b is row i % page_rows of page
  * table[b * table_width + i / page_rows].  table == NULL: page b holds sequence
  * b whole (n_pages >= B, page_rows = max_len) -- the contiguous layout of the
  * calls above.  With a table, page_rows is a multiple of 16.  Sequences may share
  * pages that no call writes.  The struct is host memory, read during the call; all its pointers
- * are device memory, 16-byte aligned (table: 4-byte, scales: 4-byte). */
+ * are device memory, 16-byte aligned (table: 4-byte, scales: as many bytes as a row has). */
 typedef struct retopk_cache {
     void *k, *v;
-    uint8_t *k_scale, *v_scale;   /* RETOPK_CACHE_MX8 only                        */
+    uint8_t *k_scale, *v_scale;   /* RETOPK_CACHE_MX8 and RETOPK_CACHE_FP4 only   */
     const int32_t *table;         /* [B, table_width], or NULL                    */
     int32_t format;               /* RETOPK_CACHE_*                               */
     int32_t n_pages, n_kv_heads, page_rows, table_width;
@@ -440,7 +450,7 @@ typedef struct retopk_rope {
  * share memory with the inputs, or with each other, in any other way are refused.
  *
  * retopk_qkv_append: the same, with the keys and the values written to rows
- * seqlens[b] + i of the cache (bf16 or MX8), and seqlens_out[b] = seqlens[b] +
+ * seqlens[b] + i of the cache (of any format), and seqlens_out[b] = seqlens[b] +
  * the sequence's tokens.  seqlens_out may be seqlens (advanced in place, as
  * retopk_append_kv does, by a second launch) or a separate buffer (one that overlaps it is refused).  A sequence
  * whose tokens do not fit sets RETOPK_STATUS_KV_FULL and keeps its rows and
@@ -456,7 +466,7 @@ int retopk_qkv_append(const retopk_rope *rope, const retopk_bf16 *q, int64_t q_s
 /* Rows [first[b], last[b]) of every sequence of `src` into the same rows of
  * `dst` (device int32 [B]); both caches have the same n_kv_heads and may differ in
  * format, paging and row capacity: quantised rows are read back into the cache
- * that decoding reads, bf16 rows are parked in MX8 form, pages are gathered
+ * that decoding reads, bf16 rows are parked in MX8 or FP4 form, pages are gathered
  * into contiguous rows.  Equal formats copy bits.  max_rows bounds last[b] -
  * first[b] (it sizes the launch; rows beyond it are not copied); rows outside either cache's
  * capacity are not copied and set RETOPK_STATUS_GATHER.  src and dst must not overlap (refused). */

@@ -1,7 +1,7 @@
-// cache_copy.cu -- rows of one cache into another: 8-bit rows read back,
+// cache_copy.cu -- rows of one cache into another: 8-bit and 4-bit rows read back,
 // bf16 rows quantised, pages gathered or scattered.  Memory bound: each row is
-// read and written once.  4 heads: 1048576 rows read back 476 us, 6.8 TB/s; 8 heads:
-// 7 x 40000 rows quantised 202 us, 6.6 TB/s; a plain copy reaches 6.8.
+// read and written once.  4 heads: 1048576 8-bit rows read back 476 us, 6.8 TB/s; 8 heads:
+// 7 x 40000 rows quantised to 8 bits 202 us, 6.6 TB/s; a plain copy reaches 6.8.
 #include <algorithm>
 
 #include "prompt.cuh"
@@ -9,17 +9,80 @@
 namespace retopk {
 
 constexpr int kCopyThreads = 128;
-// rows in flight per 8 lanes (7 x 40000 rows quantised: 201 us with 3, 210 with 2, 206 with 4; 1048576 rows read
-// back: 474, with 3 488, with 4 489; small blocks also start sooner: 3 x 4099 rows 7.5 us, 10.1 in blocks of 128 rows)
-__host__ __device__ constexpr int copy_rows(bool src8, bool dst8) { return !src8 && dst8 ? 3 : 2; }
+// rows in flight per 8 lanes (7 x 40000 rows quantised to 8 bits: 201 us with 3, 210 with 2, 206 with 4; 1048576 8-bit rows
+// read back: 474, with 3 488, with 4 489; small blocks also start sooner: 3 x 4099 rows 7.5 us, 10.1 in blocks of 128 rows)
+__host__ __device__ constexpr int copy_rows(int src, int dst)
+{
+    return src == RETOPK_CACHE_BF16 && dst != RETOPK_CACHE_BF16 ? 3 : 2;
+}
+
+// Sixteen elements of a row as they are read: bf16, 8-bit or 4-bit codes.
+template <int FORMAT>
+struct Piece {
+    uint32_t w[FORMAT == RETOPK_CACHE_BF16 ? 8 : FORMAT == RETOPK_CACHE_MX8 ? 4 : 2];
+
+    __device__ __forceinline__ void load(const char *row, int lane)
+    {
+        if constexpr (FORMAT == RETOPK_CACHE_FP4) {
+            const uint2 x = reinterpret_cast<const uint2 *>(row)[lane];
+            w[0] = x.x, w[1] = x.y;
+        } else {
+#pragma unroll
+            for (int i = 0; i < (int)sizeof(w) / 16; ++i) {
+                const uint4 x = reinterpret_cast<const uint4 *>(row)[lane * ((int)sizeof(w) / 16) + i];
+                w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
+            }
+        }
+    }
+    __device__ __forceinline__ void store(char *row, int lane) const
+    {
+        if constexpr (FORMAT == RETOPK_CACHE_FP4) {
+            reinterpret_cast<uint2 *>(row)[lane] = make_uint2(w[0], w[1]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < (int)sizeof(w) / 16; ++i)
+                reinterpret_cast<uint4 *>(row)[lane * ((int)sizeof(w) / 16) + i] =
+                    make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        }
+    }
+    // the elements, with the scale byte that they share
+    __device__ __forceinline__ void values(uint32_t scale, float (&x)[16]) const
+    {
+        if constexpr (FORMAT == RETOPK_CACHE_BF16) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                x[2 * i] = bf16lo(w[i]), x[2 * i + 1] = bf16hi(w[i]);
+        } else if constexpr (FORMAT == RETOPK_CACHE_MX8) {
+            const float s = mx_value(scale);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float2 v = e4m3x2_value(w[i / 2] >> (i & 1) * 16 & 0xffffu);
+                x[2 * i] = v.x * s, x[2 * i + 1] = v.y * s;
+            }
+        } else {
+            const float s = fp4_value(scale);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                uint32_t h[4];
+                e2m1x8_halves(w[i], h);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float2 v = __half22float2(reinterpret_cast<const __half2 &>(h[k]));
+                    x[8 * i + 2 * k] = v.x * s, x[8 * i + 2 * k + 1] = v.y * s;
+                }
+            }
+        }
+    }
+};
 
 // 8 lanes a row, 16 elements a lane.
-template <bool SRC8, bool DST8>
+template <int SRC, int DST>
 __global__ void __launch_bounds__(kCopyThreads)
     cache_copy_kernel(const retopk_cache src, const retopk_cache dst, const int32_t *first, const int32_t *last,
                       long long capacity, int max_rows, uint32_t *status)
 {
-    constexpr int kCopyRows = copy_rows(SRC8, DST8), kCopyTile = kCopyThreads / 8 * kCopyRows;   // rows of a block
+    constexpr int kCopyRows = copy_rows(SRC, DST), kCopyTile = kCopyThreads / 8 * kCopyRows;   // rows of a block
+    constexpr int kSrcScales = row_scales(SRC), kDstScales = row_scales(DST);
     pdl_wait();
     pdl_trigger();
     const int hk = blockIdx.y >> 1, isv = blockIdx.y & 1, b = blockIdx.z;
@@ -37,7 +100,7 @@ __global__ void __launch_bounds__(kCopyThreads)
     uint8_t *ds = isv ? dst.v_scale : dst.k_scale;
     // all rows of the block are on their way before the first is written
     long long rd[kCopyRows];
-    uint4 in[kCopyRows][SRC8 ? 1 : 2];
+    Piece<SRC> in[kCopyRows];
     uint32_t sc[kCopyRows];
 #pragma unroll
     for (int u = 0; u < kCopyRows; ++u) {
@@ -52,77 +115,75 @@ __global__ void __launch_bounds__(kCopyThreads)
             rd[u] = -1;
             rs = 0;   // (read for nothing: the pool's first row)
         }
-        if (SRC8) {
-            in[u][0] = reinterpret_cast<const uint4 *>(sk + rs * kD)[lane];
-            sc[u] = ss[rs * kMxScales + (DST8 ? lane & 3 : lane / 2)];
-        } else {
-            in[u][0] = (reinterpret_cast<const uint4 *>(sk + rs * 2 * kD) + 2 * lane)[0];
-            in[u][SRC8 ? 0 : 1] = (reinterpret_cast<const uint4 *>(sk + rs * 2 * kD) + 2 * lane)[1];
-        }
+        in[u].load(sk + rs * row_bytes(SRC), lane);
+        // (bits are copied a scale a lane, values take the lane's own)
+        if constexpr (kSrcScales > 0)
+            sc[u] = ss[rs * kSrcScales + (SRC == DST ? lane % kSrcScales : lane * kSrcScales / 8)];
     }
 #pragma unroll
     for (int u = 0; u < kCopyRows; ++u) {
         const bool ok = rd[u] >= 0;
-        const uint4 v0 = in[u][0], v1 = in[u][SRC8 ? 0 : 1];
-        if (SRC8 && DST8) {
+        char *to = dk + rd[u] * row_bytes(DST);
+        if constexpr (SRC == DST) {
             if (ok) {
-                reinterpret_cast<uint4 *>(dk + rd[u] * kD)[lane] = v0;
-                if (lane < kMxScales)
-                    ds[rd[u] * kMxScales + lane] = (uint8_t)sc[u];
+                in[u].store(to, lane);
+                if constexpr (kSrcScales > 0)
+                    if (lane < kSrcScales)
+                        ds[rd[u] * kDstScales + lane] = (uint8_t)sc[u];
             }
-        } else if (!DST8) {
-            uint4 o0 = v0, o1 = v1;
-            if (SRC8) {
-                const float s = mx_value(sc[u]);
-                const uint32_t w[4] = {v0.x, v0.y, v0.z, v0.w};
-                uint32_t o[8];
+            continue;
+        }
+        float x[16];
+        in[u].values(kSrcScales > 0 ? sc[u] : 0u, x);
+        Piece<DST> out;
+        if constexpr (DST == RETOPK_CACHE_BF16) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float2 v = e4m3x2_value(w[i / 2] >> (i & 1) * 16 & 0xffffu);
-                    o[i] = bf16x2(v.x * s, v.y * s);
-                }
-                o0 = make_uint4(o[0], o[1], o[2], o[3]);
-                o1 = make_uint4(o[4], o[5], o[6], o[7]);
-            }
-            if (ok) {
-                uint4 *d = reinterpret_cast<uint4 *>(dk + rd[u] * 2 * kD) + 2 * lane;
-                d[0] = o0;
-                d[1] = o1;
-            }
+            for (int i = 0; i < 8; ++i)
+                out.w[i] = bf16x2(x[2 * i], x[2 * i + 1]);
         } else {
-            float x[8], y[8];
-            unpack8(v0, x);
-            unpack8(v1, y);
             uint32_t m = 0;
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                m = max(m, max(__float_as_uint(x[e]) & 0x7fffffffu, __float_as_uint(y[e]) & 0x7fffffffu));
-            m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-            if (ok) {
-                const uint32_t s = mx_scale(m);
+            for (int e = 0; e < 16; ++e)
+                m = max(m, __float_as_uint(x[e]) & 0x7fffffffu);
+            uint32_t s;
+            if constexpr (DST == RETOPK_CACHE_MX8) {
+                m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+                s = mx_scale(m);
                 const float q = mx_inverse(s);
-                uint4 c;
-                c.x = e4m3x2(x[0] * q, x[1] * q) | e4m3x2(x[2] * q, x[3] * q) << 16;
-                c.y = e4m3x2(x[4] * q, x[5] * q) | e4m3x2(x[6] * q, x[7] * q) << 16;
-                c.z = e4m3x2(y[0] * q, y[1] * q) | e4m3x2(y[2] * q, y[3] * q) << 16;
-                c.w = e4m3x2(y[4] * q, y[5] * q) | e4m3x2(y[6] * q, y[7] * q) << 16;
-                reinterpret_cast<uint4 *>(dk + rd[u] * kD)[lane] = c;
-                if ((lane & 1) == 0)
-                    ds[rd[u] * kMxScales + lane / 2] = (uint8_t)s;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    out.w[i] = e4m3x2(x[4 * i] * q, x[4 * i + 1] * q) | e4m3x2(x[4 * i + 2] * q, x[4 * i + 3] * q) << 16;
+            } else {
+                s = fp4_scale(m);
+                const float f = fp4_value(s);
+                out.w[0] = e2m1x8(x, f);
+                out.w[1] = e2m1x8(x + 8, f);
             }
+            if (ok && lane % (8 / kDstScales) == 0)
+                ds[rd[u] * kDstScales + lane / (8 / kDstScales)] = (uint8_t)s;
         }
+        if (ok)
+            out.store(to, lane);
     }
+}
+
+template <int SRC>
+static auto copy_kernel_to(int dst)
+{
+    return dst == RETOPK_CACHE_BF16 ? cache_copy_kernel<SRC, RETOPK_CACHE_BF16>
+           : dst == RETOPK_CACHE_MX8 ? cache_copy_kernel<SRC, RETOPK_CACHE_MX8>
+                                     : cache_copy_kernel<SRC, RETOPK_CACHE_FP4>;
 }
 
 cudaError_t launch_cache_copy(const retopk_cache &src, const retopk_cache &dst, const int32_t *first,
                               const int32_t *last, int B, int max_rows, uint32_t *status, cudaStream_t st)
 {
     const long long capacity = std::min(cache_capacity(src), cache_capacity(dst));
-    const bool s8 = src.format == RETOPK_CACHE_MX8, d8 = dst.format == RETOPK_CACHE_MX8;
-    const int tile = kCopyThreads / 8 * copy_rows(s8, d8);
+    const int tile = kCopyThreads / 8 * copy_rows(src.format, dst.format);
     const dim3 grid((max_rows + tile - 1) / tile, 2 * src.n_kv_heads, B), block(kCopyThreads);
-    auto kernel = s8 ? (d8 ? cache_copy_kernel<true, true> : cache_copy_kernel<true, false>)
-                     : (d8 ? cache_copy_kernel<false, true> : cache_copy_kernel<false, false>);
+    auto kernel = src.format == RETOPK_CACHE_BF16  ? copy_kernel_to<RETOPK_CACHE_BF16>(dst.format)
+                  : src.format == RETOPK_CACHE_MX8 ? copy_kernel_to<RETOPK_CACHE_MX8>(dst.format)
+                                                   : copy_kernel_to<RETOPK_CACHE_FP4>(dst.format);
     return launch_pdl(kernel, grid, block, 0, st, 1, src, dst, first, last, capacity, max_rows, status);
 }
 

@@ -1,6 +1,6 @@
 // prompt.cuh -- what the prompt-side kernels share (rotated append, cache
-// copy, chunk attention): addressing of contiguous and paged caches, the
-// 8-bit block format, and the lookup of a token's sequence.
+// copy, chunk attention): addressing of contiguous and paged caches, the 8-bit
+// and 4-bit block formats, and the lookup of a token's sequence.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -11,6 +11,18 @@ namespace retopk {
 
 constexpr int kMxBlock = 32;                    // elements that share a scale byte
 constexpr int kMxScales = kD / kMxBlock;        // scale bytes of a row
+constexpr int kFp4Block = 16;                   // the same of 4-bit rows
+constexpr int kFp4Scales = kD / kFp4Block;
+
+// Bytes of a row's elements, and of its scales.
+__host__ __device__ constexpr int row_bytes(int format)
+{
+    return format == RETOPK_CACHE_FP4 ? kD / 2 : format == RETOPK_CACHE_MX8 ? kD : 2 * kD;
+}
+__host__ __device__ constexpr int row_scales(int format)
+{
+    return format == RETOPK_CACHE_FP4 ? kFp4Scales : format == RETOPK_CACHE_MX8 ? kMxScales : 0;
+}
 
 // Capacity of a sequence in rows.
 inline long long cache_capacity(const retopk_cache &c)
@@ -97,6 +109,69 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi)
 {
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// ---- 4-bit rows: e2m1 codes with one scale for 16 elements --------------------
+// A scale byte is the upper bits of an fp16 (5 of exponent, 3 of mantissa, no sign).
+// With 3 mantissa bits a block's largest element lies within 2^-4 of the code 6 (a
+// power of two would leave it anywhere in (3, 6]), and 16 elements of any size down
+// to 2^-19 find a scale without a second one for the tensor.  Code times scale has at
+// most 6 significant bits and is exact in fp16 and in bf16.
+constexpr uint32_t kFp4Top = 226;   // the largest that is written, 10240: six times it is an fp16
+
+// Scale byte of a block from the largest |x| (its fp32 bits): a sixth of it, rounded to nearest even.
+__device__ __forceinline__ uint32_t fp4_scale(uint32_t amax_bits)
+{
+    if (amax_bits >= 0x7f800000u)
+        return 255u;
+    const float s = __uint_as_float(amax_bits) / 6.f;
+    const uint32_t u = __float_as_uint(s);
+    const uint32_t byte = s < 0x1p-14f ? (uint32_t)rintf(s * 0x1p17f) : ((u + 0x7ffffu + (u >> 20 & 1u)) >> 20) - (112u << 3);
+    return min(byte, kFp4Top);
+}
+
+__device__ __forceinline__ float fp4_value(uint32_t byte)
+{
+    return __half2float(__ushort_as_half((unsigned short)(byte << 7)));
+}
+
+// Eight elements as codes, the first in the low bits: x / s rounded once to the nearest
+// code, ties to the even one.  s has 4 significant bits and a border between two codes at most 3,
+// so bf16 elements do lie on borders, where a product with 1 / s would fall to either side.  What
+// the product leaves, x - q s, is exact, and adding its quotient brings q to the border itself.
+__device__ __forceinline__ uint32_t e2m1x8(const float *x, float s)
+{
+    const float r = s > 0.f ? 1.f / s : 0.f;
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float q[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            q[k] = x[2 * i + k] * r;
+            q[k] = fmaf(fmaf(-q[k], s, x[2 * i + k]), r, q[k]);
+        }
+        uint32_t c;
+        asm("{\n .reg .b8 b;\n cvt.rn.satfinite.e2m1x2.f32 b, %1, %2;\n cvt.u32.u8 %0, b;\n}\n" : "=r"(c) : "f"(q[1]), "f"(q[0]));
+        w |= c << 8 * i;
+    }
+    return w;
+}
+
+// Eight codes as fp16, two a register.
+__device__ __forceinline__ void e2m1x8_halves(uint32_t codes, uint32_t (&h)[4])
+{
+    asm("{\n .reg .b8 a, b, c, d;\n mov.b32 {a, b, c, d}, %4;\n cvt.rn.f16x2.e2m1x2 %0, a;\n cvt.rn.f16x2.e2m1x2 %1, b;\n"
+        " cvt.rn.f16x2.e2m1x2 %2, c;\n cvt.rn.f16x2.e2m1x2 %3, d;\n}\n"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(codes));
+}
+
+__device__ __forceinline__ uint32_t f16x2(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
 

@@ -19,9 +19,10 @@ int check_cache(const retopk_cache *c, int B)
 {
     if (!c || !c->k || !c->v || c->n_pages < 1 || c->n_kv_heads < 1 || c->page_rows < 1)
         return RETOPK_ERR_INVALID;
-    if (c->format != RETOPK_CACHE_BF16 && c->format != RETOPK_CACHE_MX8)
+    if (c->format != RETOPK_CACHE_BF16 && c->format != RETOPK_CACHE_MX8 && c->format != RETOPK_CACHE_FP4)
         return RETOPK_ERR_INVALID;
-    if (c->format == RETOPK_CACHE_MX8 && (!c->k_scale || !c->v_scale))
+    const int scales = row_scales(c->format);   // bytes of a row
+    if (scales && (!c->k_scale || !c->v_scale))
         return RETOPK_ERR_INVALID;
     if (c->table ? c->table_width < 1 || c->page_rows % 16 != 0 : c->n_pages < B)
         return RETOPK_ERR_INVALID;
@@ -29,7 +30,7 @@ int check_cache(const retopk_cache *c, int B)
         (long long)c->n_pages * c->n_kv_heads >= INT32_MAX)
         return RETOPK_ERR_UNSUPPORTED;
     if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->table, 4) ||
-        (c->format == RETOPK_CACHE_MX8 && (!aligned(c->k_scale, 4) || !aligned(c->v_scale, 4))))
+        (scales && (!aligned(c->k_scale, scales) || !aligned(c->v_scale, scales))))
         return RETOPK_ERR_ALIGN;
     return RETOPK_OK;
 }
@@ -49,7 +50,7 @@ int check_tokens(int T, int B, int Hq, int Hkv, const int32_t *cu, const int32_t
 // Bytes of a cache's keys (or values).
 size_t pool_bytes(const retopk_cache &c)
 {
-    return (size_t)c.n_pages * c.n_kv_heads * c.page_rows * kD * (c.format == RETOPK_CACHE_MX8 ? 1 : 2);
+    return (size_t)c.n_pages * c.n_kv_heads * c.page_rows * row_bytes(c.format);
 }
 
 // A strided [T, heads, 128] tensor.

@@ -56,7 +56,7 @@ __device__ __forceinline__ int advanced(const RopeArgs &a, int b)
 }
 
 // Where the keys and values go.
-enum { TO_ROWS = 0, TO_BF16 = 1, TO_MX8 = 2 };   // k_out (no values), a bf16 cache, an 8-bit cache
+enum { TO_ROWS = 0, TO_BF16 = 1, TO_MX8 = 2, TO_FP4 = 3 };   // k_out (no values), a cache of bf16, 8-bit or 4-bit rows
 
 // A lane's part of the norm and the rotation, with the weights in it: partners a, b
 // become f (a ac - b bs) and f (b bc + a as), f the norm's factor.
@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, kRopeBlocks) rope_kernel(cons
         // batches lo .. hi of the queries (0), keys (1) or values (2)
         auto heads = [&](auto kind_, int lo, int hi) {
             constexpr int kind = decltype(kind_)::value;
-            constexpr bool cached = TO && kind > 0, mx8 = TO == TO_MX8 && kind > 0;
+            constexpr bool cached = TO && kind > 0, mx8 = TO == TO_MX8 && kind > 0, fp4 = TO == TO_FP4 && kind > 0;
             const int H = kind ? a.Hkv : a.Hq;
             const bool there = in && (!cached || at >= 0);
             const bool norm = kind < 2 && (kind == 0 ? a.rope.q_weight : a.rope.k_weight) != nullptr;
@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, kRopeBlocks) rope_kernel(cons
             // four heads of a batch, one for each quarter of the warp
             auto four = [&](const uint8_t *from, uint8_t *to, uint8_t *sc, bool real) {
                 const uint4 u = *reinterpret_cast<const uint4 *>(from), v = *reinterpret_cast<const uint4 *>(from + 16 * (c1 - c0));
-                if (kind == 2 && !mx8) {
+                if (kind == 2 && !mx8 && !fp4) {
                     if (real) {
                         *reinterpret_cast<uint4 *>(to) = u;
                         *reinterpret_cast<uint4 *>(to + 16 * (c1 - c0)) = v;
@@ -272,8 +272,8 @@ __global__ void __launch_bounds__(kRopeWarps * 32, kRopeBlocks) rope_kernel(cons
                         y[second_of<INTER>(e)] = fmaf(xb, tn.bc[e], pa * tn.as[e]) * f;
                     }
                 }
-                if (mx8) {
-                    // the largest of each 32 elements: four runs of eight
+                if (mx8 || fp4) {
+                    // the largest of each block: four runs of eight, or two
                     uint32_t m0 = 0, m1 = 0;
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
@@ -285,12 +285,23 @@ __global__ void __launch_bounds__(kRopeWarps * 32, kRopeBlocks) rope_kernel(cons
                     sh.tops[which][c1] = m1;
                     __syncwarp();
                     auto scale = [&](int c) {
+                        if constexpr (fp4) {
+                            const uint2 m = *reinterpret_cast<const uint2 *>(&sh.tops[which][c & 14]);
+                            return fp4_scale(max(m.x, m.y));
+                        }
                         const uint4 m = *reinterpret_cast<const uint4 *>(&sh.tops[which][c & 12]);
                         return mx_scale(max(max(m.x, m.y), max(m.z, m.w)));
                     };
                     const uint32_t s0 = scale(c0), s1 = scale(c1);
-                    const float f0 = mx_inverse(s0), f1 = mx_inverse(s1);
-                    if (real) {
+                    const float f0 = fp4 ? fp4_value(s0) : mx_inverse(s0), f1 = fp4 ? fp4_value(s1) : mx_inverse(s1);
+                    if (real && fp4) {
+                        *reinterpret_cast<uint32_t *>(to) = e2m1x8(y, f0);
+                        *reinterpret_cast<uint32_t *>(to + 4 * (c1 - c0)) = e2m1x8(y + 8, f1);
+                        if ((c0 & 1) == 0)
+                            sc[c0 / 2] = (uint8_t)s0;
+                        if ((c1 & 1) == 0)
+                            sc[c1 / 2] = (uint8_t)s1;
+                    } else if (real) {
                         *reinterpret_cast<uint2 *>(to) =
                             make_uint2(e4m3x2(y[0] * f0, y[1] * f0) | e4m3x2(y[2] * f0, y[3] * f0) << 16,
                                        e4m3x2(y[4] * f0, y[5] * f0) | e4m3x2(y[6] * f0, y[7] * f0) << 16);
@@ -309,13 +320,14 @@ __global__ void __launch_bounds__(kRopeWarps * 32, kRopeBlocks) rope_kernel(cons
                 }
             };
             // where this lane's elements of the first four heads go, and the step to the next four
-            constexpr int size = mx8 ? 1 : 2;
+            constexpr int format = fp4 ? RETOPK_CACHE_FP4 : mx8 ? RETOPK_CACHE_MX8 : RETOPK_CACHE_BF16;
+            constexpr int bytes = row_bytes(format), scales = row_scales(format);   // of a row
             const long long first_row = cached ? at + (long long)(lo * kRopeHeads + which) * a.cache.page_rows
                                                : (long long)t * H + lo * kRopeHeads + which;
             uint8_t *to = static_cast<uint8_t *>(kind == 0 ? a.q_out : kind == 2 ? a.cache.v : TO ? a.cache.k : a.k_out) +
-                          first_row * (kD * size) + 8 * size * c0;
-            uint8_t *sc = mx8 ? (kind == 2 ? a.cache.v_scale : a.cache.k_scale) + first_row * kMxScales : nullptr;
-            const long long step = (cached ? a.cache.page_rows : 1) * 4ll * kD * size;
+                          first_row * bytes + bytes / 16 * c0;
+            uint8_t *sc = scales ? (kind == 2 ? a.cache.v_scale : a.cache.k_scale) + first_row * scales : nullptr;
+            const long long step_rows = (cached ? a.cache.page_rows : 1) * 4ll, step = step_rows * bytes;
             for (int p = lo; p < hi; ++p) {
                 const int stage = used % kRopeStages;
                 ok = __all_sync(0xffffffffu, wait_full(&sh.full[stage], (used / kRopeStages) & 1, a.status));
@@ -328,13 +340,13 @@ __global__ void __launch_bounds__(kRopeWarps * 32, kRopeBlocks) rope_kernel(cons
                     if (left == kRopeHeads) {
 #pragma unroll
                         for (int i = 0; i < kRopeHeads / 4; ++i)
-                            four(from + i * 8 * kD, to + i * step, sc + i * (step / (kD / kMxScales)), true);
+                            four(from + i * 8 * kD, to + i * step, sc + i * step_rows * scales, true);
                     } else {
                         for (int i = 0; 4 * i < left; ++i)
-                            four(from + i * 8 * kD, to + i * step, sc + i * (step / (kD / kMxScales)), 4 * i + which < left);
+                            four(from + i * 8 * kD, to + i * step, sc + i * step_rows * scales, 4 * i + which < left);
                     }
                     to += kRopeHeads / 4 * step;
-                    sc += kRopeHeads / 4 * (step / (kD / kMxScales));
+                    sc += kRopeHeads / 4 * step_rows * scales;
                 }
                 __syncwarp();   // all lanes have read the batch
                 if (lane == 0)
@@ -371,6 +383,7 @@ static const void *rope_kernel_to(int to)
 {
     return to == TO_ROWS ? (const void *)rope_kernel<INTER, FULL, TO_ROWS>
          : to == TO_MX8  ? (const void *)rope_kernel<INTER, FULL, TO_MX8>
+         : to == TO_FP4  ? (const void *)rope_kernel<INTER, FULL, TO_FP4>
                          : (const void *)rope_kernel<INTER, FULL, TO_BF16>;
 }
 
@@ -388,7 +401,8 @@ cudaError_t launch_rope(const RopeArgs &a, cudaStream_t st)
     const long long total = (long long)a.T * (batches(a.Hq) + batches(a.Hkv) * (a.v ? 2 : 1));
     const int most = sm_count() * kRopeBlocks * kRopeWarps, each = (int)((total + most - 1) / most);
     const int blocks = (int)((total + (long long)each * kRopeWarps - 1) / ((long long)each * kRopeWarps));
-    const void *kernel = rope_kernel_for(a.rope.interleaved != 0, a.rope.rot_dim == kD, !a.v ? TO_ROWS : a.cache.format == RETOPK_CACHE_MX8 ? TO_MX8 : TO_BF16);
+    const int to = !a.v ? TO_ROWS : a.cache.format == RETOPK_CACHE_FP4 ? TO_FP4 : a.cache.format == RETOPK_CACHE_MX8 ? TO_MX8 : TO_BF16;
+    const void *kernel = rope_kernel_for(a.rope.interleaved != 0, a.rope.rot_dim == kD, to);
     return launch_pdl(reinterpret_cast<void (*)(RopeArgs, int)>(const_cast<void *>(kernel)), dim3(blocks),
                       dim3(kRopeWarps * 32), kRopeSmem, st, 1, a, each);
 }
@@ -396,7 +410,7 @@ cudaError_t launch_rope(const RopeArgs &a, cudaStream_t st)
 cudaError_t configure_rope()
 {
     cudaError_t e = cudaSuccess;
-    for (int to : {TO_ROWS, TO_BF16, TO_MX8})
+    for (int to : {TO_ROWS, TO_BF16, TO_MX8, TO_FP4})
         for (int x = 0; x < 4; ++x)
             if (e == cudaSuccess)
                 e = cudaFuncSetAttribute(rope_kernel_for(x & 1, x & 2, to), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRopeSmem);

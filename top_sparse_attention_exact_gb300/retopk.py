@@ -21,7 +21,7 @@ _lib = None
 RETOPK_PATH_REUSE, RETOPK_PATH_FALLBACK, RETOPK_PATH_REFRESH = 0, 1, 2
 STATUS_BAD_INDEX, STATUS_KV_FULL, STATUS_NONFINITE, STATUS_TIMEOUT, STATUS_GATHER = 0x1, 0x2, 0x4, 0x8, 0x10
 STATUS_BAD_PAGE = 0x20
-CACHE_BF16, CACHE_MX8 = 0, 1
+CACHE_BF16, CACHE_MX8, CACHE_FP4 = 0, 1, 2
 
 EXPORTED = ("retopk_workspace_bytes", "retopk_create", "retopk_destroy", "retopk_init_cache",
             "retopk_append_kv", "retopk_decode_step", "retopk_decode_step_kv", "retopk_get_diagnostics",
@@ -358,23 +358,25 @@ def _same(t: torch.Tensor, shape, what: str):
 class KVCache:
     """The keys and values of some sequences, as the prompt-side calls see them (struct retopk_cache).
 
-    k, v: [pages, Hkv, rows, 128], bf16, or uint8 e4m3 codes with k_scale, v_scale uint8 [pages, Hkv, rows, 4].
+    k, v: [pages, Hkv, rows, 128], bf16, or uint8 e4m3 codes with k_scale, v_scale uint8 [pages, Hkv, rows, 4]; or
+    4-bit codes, uint8 [pages, Hkv, rows, 64] with k_scale, v_scale uint8 [pages, Hkv, rows, 8].
     table: int32 [B, width], the pages of each sequence in order (rows a multiple of 16); None: page b holds
     sequence b whole, the [B, Hkv, max_len, 128] layout of the decode calls.  Keeps the tensors alive."""
 
     def __init__(self, k, v, table=None, k_scale=None, v_scale=None):
-        mx8 = k.dtype == torch.uint8
+        coded = k.dtype == torch.uint8
+        fp4 = coded and k.dim() == 4 and k.shape[3] == 64
         for what, t in (("k", k), ("v", v)):
-            if t.dim() != 4 or t.shape != k.shape or t.shape[3] != 128 or t.dtype != k.dtype or not t.is_contiguous():
-                raise RetopkError(f"{what}: contiguous k and v of one type, [pages, Hkv, rows, 128], expected")
-        if not mx8:
+            if t.dim() != 4 or t.shape != k.shape or t.shape[3] != (64 if fp4 else 128) or t.dtype != k.dtype or not t.is_contiguous():
+                raise RetopkError(f"{what}: contiguous k and v of one type, [pages, Hkv, rows, 128], or 64 bytes a row of 4-bit codes, expected")
+        if not coded:
             _bf16(k)
         scales = (k_scale, v_scale)
-        if mx8 != all(t is not None for t in scales) or (not mx8 and any(t is not None for t in scales)):
+        if coded != all(t is not None for t in scales) or (not coded and any(t is not None for t in scales)):
             raise RetopkError("k_scale and v_scale belong to uint8 caches, and only to those")
         for t in scales:
-            if t is not None and (t.dtype != torch.uint8 or tuple(t.shape) != (*k.shape[:3], 4) or not t.is_contiguous()):
-                raise RetopkError("scales: contiguous uint8 [pages, Hkv, rows, 4] tensors expected")
+            if t is not None and (t.dtype != torch.uint8 or tuple(t.shape) != (*k.shape[:3], 8 if fp4 else 4) or not t.is_contiguous()):
+                raise RetopkError(f"scales: contiguous uint8 [pages, Hkv, rows, {8 if fp4 else 4}] tensors expected")
         if table is not None and (table.dtype != torch.int32 or table.dim() != 2 or not table.is_contiguous()):
             raise RetopkError("table: a contiguous int32 [B, width] tensor expected")
         self.tensors = (k, v, table, k_scale, v_scale)
@@ -386,7 +388,7 @@ class KVCache:
         pages, Hkv, rows, _ = k.shape
         self.Hkv, self.B = Hkv, pages if table is None else table.shape[0]
         self.rows = rows if table is None else rows * table.shape[1]
-        self.struct = retopk_cache(p(k), p(v), p(k_scale), p(v_scale), p(table), CACHE_MX8 if mx8 else CACHE_BF16,
+        self.struct = retopk_cache(p(k), p(v), p(k_scale), p(v_scale), p(table), CACHE_FP4 if fp4 else CACHE_MX8 if coded else CACHE_BF16,
                                    pages, Hkv, rows, 0 if table is None else table.shape[1])
         self._ref = ctypes.addressof(self.struct)
 
