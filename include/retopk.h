@@ -400,7 +400,8 @@ int retopk_support_overlap(const int32_t *S, const int32_t *others, int rows, in
                                  values beyond 61440 saturate), codes rounded to nearest even
                                  once.  A block with a NaN or an infinity gets scale 255 and
                                  reads back as NaN.  retopk_qkv_append and retopk_cache_copy
-                                 write such rows, retopk_cache_copy reads them. */
+                                 write such rows, retopk_cache_copy and
+                                 retopk_chunk_attention read them. */
 
 /* The keys and values of B sequences: k and v are [n_pages, n_kv_heads,
  * page_rows, 128] (bf16, or e4m3 bytes with k_scale / v_scale [n_pages,
@@ -481,7 +482,8 @@ int retopk_cache_copy(const retopk_cache *src, const retopk_cache *dst, const in
  *   out = sum_j softmax(s)_j v_j,   lse = log sum_j exp(s_j)
  * q, out [T, Hq, 128] bf16, tokens q_stride / out_stride elements apart; lse
  * [T, Hq] fp32 or NULL; out may be q where the strides are the same (another overlap is refused).  A token that sees no key (L_b < n_b, L_b = 0) gets
- * zeros and lse = -inf.  The cache must be RETOPK_CACHE_BF16; rows at or past
+ * zeros and lse = -inf.  The cache is RETOPK_CACHE_BF16 or
+ * RETOPK_CACHE_FP4 (whose values are exact in the products; MX8 is refused); rows at or past
  * L_b are never used, whatever they hold.  A row below L_b that is not finite
  * may reach every token of its sequence; a query that is not stays in its row.  Lengths beyond the cache's capacity
  * are clamped to it.  scale 0 means 1/sqrt(128).
@@ -489,7 +491,8 @@ int retopk_cache_copy(const retopk_cache *src, const retopk_cache *dst, const in
  * it gives for T tokens is enough for fewer of the same heads, whatever their sequences
  * (on the device that was current: it counts the SMs); concurrent calls need one each.  Long histories of few tokens are split over the GPU
  * and joined from it.  Results do not depend on the other sequences of the call beyond
- * rounding; the weights are rounded to bf16 once, which out carries (2^-8 sum_j p_j |v_j|), all else is fp32.
+ * rounding; the weights are rounded to bf16 once, which out carries (2^-8 sum_j p_j |v_j|), over 4-bit rows to
+ * fp16 (2^-11 sum_j p_j |v_j| + 2^-32 sum_j |v_j|); all else is fp32.
  * A call is shaped by its mean of tokens a sequence: a prompt of thousands of tokens beside a hundred and
  * more single tokens is sooner done in a call of its own.  Graph-capturable. */
 size_t retopk_chunk_attention_workspace_bytes(int T, int B, int Hq, int Hkv);

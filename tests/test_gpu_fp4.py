@@ -1,11 +1,18 @@
-"""The 4-bit cache (RETOPK_CACHE_FP4): rotated append into it and copies from and to it, against plain 64-bit
-formulas (GPU).
+"""The 4-bit cache (RETOPK_CACHE_FP4): rotated append into it, copies from and to it, attention over it, against plain
+64-bit formulas (GPU).
 
 Tolerances.  u = 2^-24 is half a step of fp32, half a step of bf16 is 2^-8 relative to the value.
   codes      of values that are exact (values, bf16 rows) scale and codes have one right answer: ties go to even.
              A rotated key is off by at most 2^-18 of the head's largest element (see the prompt-side tests): its
              scale may be a neighbour of the right one only where a sixth of the largest lies that near the border, its
              code is off by at most half the codes' gap and that error.
+  attention  a 4-bit value is exact in fp16 and bf16, so keys and values add no rounding of their own.  A score is a sum of 128
+             products, off by at most 128 u sum|q k| scale <= 2^-17 times that sum, and the exponential's argument and
+             result by 2^-20 more: d; a capped score is off by no more.  The weights are rounded to fp16 once: by 2^-11 of
+             each, or by half of fp16's smallest step, 2^-25, where that is more.  They are taken so that the row's
+             largest is at least 2^7, so that is 2^-32 of p at most.  The output is rounded to bf16:
+             |out - exact| <= 2^-8 |exact| + (2^-11 + 2 d + 2^-14) sum_j p_j |v_j| + 2^-32 sum_j |v_j|.
+             lse is off by d + 2^-20 (1 + |lse|).
 """
 import math
 
@@ -369,3 +376,324 @@ def test_append_captured_and_replayed_advances_each_time():
         p, r = c.at(b, 42)
         for i in rows:
             assert torch.equal(c.vs[p[i], :, r[i]].long(), byte[b])
+
+
+# ---- attention -------------------------------------------------------------------------------------------------------
+def check(q, n, lens, c, out, lse, scale, cap, window):
+    """Against 64-bit attention over the values that the rows stand for."""
+    t, Hkv = 0, c.k.shape[1]
+    for b, (m, L) in enumerate(zip(n, lens)):
+        sel = slice(t, t + m)
+        t += m
+        if m == 0:
+            continue
+        G = q.shape[1] // Hkv
+        k, v = (x.repeat_interleave(G, 1) for x in c.rows(b, L))
+        x = q[sel].double()
+        pos = torch.arange(L - m, L, device="cuda")[:, None]
+        j = torch.arange(L, device="cuda")
+        seen = (j <= pos) & ((j > pos - window) if window else True)
+        s = torch.einsum("thd,jhd->htj", x, k) * scale
+        d = 2.0 ** -17 * scale * torch.einsum("thd,jhd->htj", x.abs(), k.abs())
+        if cap:
+            s = cap * torch.tanh(s / cap)
+        s = s.masked_fill(~seen, -math.inf)
+        d = d.masked_fill(~seen, 0.0).amax(-1).T[..., None] if L else torch.zeros((m, q.shape[1], 1), device="cuda", dtype=torch.float64)
+        d = d + 2.0 ** -20
+        p = torch.softmax(s, -1).nan_to_num(0.0)
+        ref, size = torch.einsum("htj,jhd->thd", p, v), torch.einsum("htj,jhd->thd", p, v.abs())
+        tol = 2.0 ** -8 * ref.abs() + (2.0 ** -11 + 2 * d + 2.0 ** -14) * size + 2.0 ** -32 * v.abs().sum(0)
+        err = (out[sel].double() - ref).abs()
+        assert (err <= tol).all().item(), (b, float((err - tol).max()), float((err / (size + 1e-30)).max()))
+        if lse is not None:
+            rl = torch.logsumexp(s, -1).T
+            none = rl == -math.inf
+            assert torch.equal(lse[sel] == -math.inf, none)
+            assert ((lse[sel].double() - rl).abs() <= d[..., 0] + 2.0 ** -20 * (1 + rl.abs()))[~none].all()
+
+
+ATTEND = [  # tokens of each sequence, rows in all, Hq, Hkv, page, window, cap
+    ([1], [1], 1, 1, 0, 0, 0.0),                                    # a single key
+    ([1], [300], 28, 4, 0, 0, 0.0),
+    ([1], [129], 7, 1, 16, 0, 0.0),
+    ([1] * 9, [1, 2, 15, 16, 17, 31, 32, 33, 1000], 16, 1, 48, 0, 0.0),
+    ([1] * 9, [63, 64, 65, 127, 128, 129, 255, 256, 257], 8, 1, 0, 0, 0.0),
+    ([1] * 5, [0, 5, 400, 17, 16], 32, 8, 64, 0, 50.0),             # a sequence without rows
+    ([3] * 4, [3, 64, 500, 2], 8, 8, 0, 0, 0.0),                    # the last: fewer rows than tokens
+    ([1, 1], [70001, 333], 28, 4, 256, 0, 0.0),                     # a long history beside a short one
+    ([1] * 3, [30011, 30000, 5], 5, 1, 0, 0, 0.0),
+    ([5], [40000], 16, 2, 0, 0, 30.0),
+    ([2, 4], [9000, 700], 7, 1, 16, 0, 0.0),
+    ([1, 2], [9000, 9000], 12, 4, 0, 100, 0.0),
+    ([1], [20000], 28, 4, 64, 5000, 0.0),                           # a window of a long history
+    ([1, 1], [2000, 50], 9, 1, 0, 1, 2.0),
+    ([77], [77], 4, 2, 0, 0, 0.0),
+    ([300], [300], 28, 4, 128, 0, 0.0),
+    ([129], [1300], 16, 1, 16, 0, 0.0),
+    ([64, 0, 1, 200], [64, 50, 700, 900], 10, 2, 48, 0, 0.0),
+    ([200, 37], [1000, 37], 6, 6, 0, 33, 0.0),                      # a window inside one tile
+    ([150], [900], 14, 2, 64, 257, 20.0),
+    ([260], [100], 2, 1, 0, 0, 0.0),                                # tokens 0..159 see no key
+    ([700], [5000], 15, 5, 112, 1, 0.0),                            # each token sees itself only
+    ([513], [2050], 13, 1, 0, 0, 5.0),
+    ([1] * 700, [(37 * i) % 600 for i in range(700)], 4, 2, 0, 0, 0.0),     # more sequences than a block has threads
+    ([i % 3 for i in range(900)], [(53 * i) % 300 for i in range(900)], 2, 1, 16, 0, 0.0),
+    ([40] * 400, [40 + i % 90 for i in range(400)], 8, 8, 0, 0, 0.0),
+    ([1] * 63 + [900], [700 + 9 * i for i in range(63)] + [900], 28, 4, 64, 0, 0.0),     # a prompt among single tokens
+    ([3, 70], [600, 1500], 40, 40, 0, 0, 0.0),                      # many KV heads
+    ([1], [512], 6, 2, 0, 0, 0.0),                                  # a cache of a few tiles, with rows past the length
+    ([130], [515], 3, 3, 64, 0, 0.0),
+    ([2, 90], [800, 700], 8, 2, 0, 0, 1e6),                         # a cap far above all scores
+    ([2, 90], [800, 700], 8, 2, 0, 0, 1e-3),                        # and far below
+    ([1, 1], [800, 700], 8, 2, 0, 0, 1e6),
+    ([1, 1], [800, 700], 8, 2, 0, 0, 1e-3),
+    ([2, 90], [800, 700], 8, 2, 0, (1 << 31) - 1, 0.0),             # a window wider than any history
+    ([1, 1], [800, 700], 8, 2, 0, 1 << 23, 12.0),
+]
+
+
+def setup(n, lens, Hq, Hkv, page, seed, pad=2, qscale=2.0, strided=True, sizes=(0.05, 0.4)):
+    g = gen(seed)
+    T = sum(n)
+    wide = normal(g, T + pad, Hq + 3, D, scale=qscale)
+    q = wide[:, :Hq] if strided else wide[:, :Hq].contiguous()
+    c = Cache(len(n), Hkv, max(max(lens), 1) + 7, page, seed=seed)  # rows past the lengths are NaN
+    for b, L in enumerate(lens):
+        c.put(b, packed(g, L, Hkv, sizes=sizes), packed(g, L, Hkv, sizes=sizes))
+    return q, c
+
+
+@pytest.mark.parametrize("n,lens,Hq,Hkv,page,window,cap", ATTEND)
+def test_attention(n, lens, Hq, Hkv, page, window, cap):
+    q, c = setup(n, lens, Hq, Hkv, page, sum(lens) + Hq)
+    T = sum(n)
+    wide = torch.full((T + 2, Hq + 1, D), 9.0, dtype=torch.bfloat16, device="cuda")
+    out, lse = wide[:, :Hq], torch.full((T + 2, Hq), 9.0, device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    retopk.chunk_attention(q, c.h, i32(lens), out, cu_tokens=offsets(n), softcap=cap, window=window, lse=lse, status=st)
+    assert st.item() == 0
+    check(q, n, lens, c, out, lse, 1 / math.sqrt(D), cap, window)
+    # rows behind the last sequence and columns beside the heads are as they were
+    assert (wide[T:] == 9).all() and (lse[T:] == 9).all() and (wide[:, Hq:] == 9).all()
+
+
+@pytest.mark.parametrize("B,L", [(1, 260), (6, 1000)])
+def test_attention_one_token_each_without_offsets(B, L):
+    q, c = setup([1] * B, [L] * B, 8, 2, 0, B, pad=0, strided=False)
+    out = retopk.chunk_attention(q, c.h, i32([L] * B), scale=0.3)
+    check(q, [1] * B, [L] * B, c, out, None, 0.3, 0.0, 0)
+    same = q.clone()
+    assert retopk.chunk_attention(same, c.h, i32([L] * B), same, scale=0.3) is same      # out may be q
+    assert torch.equal(same, out)
+
+
+@pytest.mark.parametrize("n", [[1, 1], [3, 2], [1, 40]])
+@pytest.mark.parametrize("sizes", [(2.0 ** -15, 2.0 ** -11), (2.0 ** -12, 6000.0), (0.1, 0.1), (1.0, 60.0)])
+def test_attention_scales_of_all_sizes(n, sizes):
+    # small ones (among fp16's subnormals, code by scale), ones that differ by 2^24 within a row, large scores
+    L = [600, 3100]
+    q, c = setup(n, L, 14, 2, 0, 3, sizes=sizes)
+    q.mul_(0.05 / sizes[1])
+    lse = torch.empty((sum(n) + 2, 14), device="cuda")
+    for scale in (None, 20.0):
+        out = retopk.chunk_attention(q, c.h, i32(L), cu_tokens=offsets(n), lse=lse, scale=scale)
+        check(q, n, L, c, out, lse, scale or 1 / math.sqrt(D), 0.0, 0)
+
+
+@pytest.mark.parametrize("n", [[1, 1], [1, 40]])
+def test_attention_queries_of_all_sizes(n):
+    # elements and rows that differ by far more than fp16 holds
+    L = [500, 900]
+    q, c = setup(n, L, 8, 2, 16, 5)
+    size = torch.exp2(torch.randint(-60, 3, q.shape[:2] + (1,), generator=gen(6), device="cuda").float())
+    q.mul_(size.to(torch.bfloat16))
+    q[:, :, ::2] *= 2.0 ** -30
+    out = retopk.chunk_attention(q, c.h, i32(L), cu_tokens=offsets(n))
+    check(q, n, L, c, out, None, 1 / math.sqrt(D), 0.0, 0)
+    up = (q.float() * 2.0 ** 62).to(torch.bfloat16)       # the same scores from far larger queries
+    out = retopk.chunk_attention(up, c.h, i32(L), cu_tokens=offsets(n), scale=2.0 ** -62 / math.sqrt(D))
+    check(q, n, L, c, out, None, 1 / math.sqrt(D), 0.0, 0)
+
+
+@pytest.mark.parametrize("n,L,window", [([200], [3000], 0), ([1], [9000], 0), ([90, 3], [2500, 6000], 700), ([1, 2], [9000, 2000], 1500)])
+@pytest.mark.parametrize("cap", [0.0, 4.0, 30.0, 1000.0])
+def test_attention_scores_whose_size_comes_and_goes(n, L, window, cap):
+    # stretches of small and of large scores: maxima that jump and stay, capped ones far below the cap and at it by turns
+    q, c = setup(n, L, 7, 1, 0, 33, qscale=1.0)
+    for b, rows in enumerate(L):
+        wave = torch.exp2(6 * torch.sin(torch.arange(rows, device="cuda") / 211.0) - 3)[:, None, None]
+        codes, scales = packed(gen(34 + b), rows, 1, sizes=(0.3, 0.31))
+        s = (scale_of(scales) * wave).half().view(torch.int16) >> 7
+        c.put(b, (codes, s.to(torch.uint8)), packed(gen(36 + b), rows, 1))
+    lse = torch.empty((sum(n) + 2, 7), device="cuda")
+    out = retopk.chunk_attention(q, c.h, i32(L), cu_tokens=offsets(n), softcap=cap, window=window, lse=lse)
+    check(q, n, L, c, out, lse, 1 / math.sqrt(D), cap, window)
+
+
+@pytest.mark.parametrize("n,L", [([1], [20000]), ([3], [20000]), ([200], [6000])])
+def test_attention_scores_that_grow_along_the_history(n, L):
+    q, c = setup(n, L, 8, 1, 0, 4, qscale=1.0)
+    q.copy_(q.abs())
+    ramp = torch.linspace(0.02, 0.6, L[0], device="cuda")[:, None, None]
+    codes = torch.randint(0, 256, (L[0], 1, 64), generator=gen(9), device="cuda", dtype=torch.uint8) & 0x77      # no signs
+    c.put(0, (codes, (ramp.expand(-1, 1, 8).half().view(torch.int16) >> 7).to(torch.uint8)), packed(gen(10), L[0], 1))
+    out = retopk.chunk_attention(q, c.h, i32(L), cu_tokens=offsets(n))
+    check(q, n, L, c, out, None, 1 / math.sqrt(D), 0.0, 0)
+
+
+@pytest.mark.parametrize("n", [1, 3, 30])
+def test_attention_a_wide_tail_beside_a_peak(n):
+    # one key of weight 1 and 60000 of 2^-21 .. 2^-18 with values of one sign: their sum is far from lost
+    L = 60000
+    q, c = setup([n], [L], 8, 1, 0, 7)
+    q.fill_(0.125)
+    codes = torch.full((L, 1, 64), 0x22, dtype=torch.uint8, device="cuda")      # ones
+    scales = torch.full((L, 1, 8), 0, dtype=torch.uint8, device="cuda")
+    scales[77] = 0x3c << 1                                                       # 1: a score of 16, times the scale
+    c.put(0, (codes, scales), (codes, torch.full_like(scales, 0x3c << 1)))
+    c.vs[0, 0, 77] = 0                                                           # the peak's own value: 0
+    for scale in (14.0 / 16, 12.5 / 16):
+        out = retopk.chunk_attention(q, c.h, i32([L]), cu_tokens=offsets([n]), scale=scale)
+        check(q, [n], [L], c, out, None, scale, 0.0, 0)
+        assert out[:n].float().mean() > 0.01
+
+
+def test_attention_lengths_beyond_the_capacity_are_clamped():
+    for n in ([1], [40]):
+        q, c = setup(n, [64], 4, 1, 0, 12, pad=0)
+        c.put(0, packed(gen(1), 71, 1), packed(gen(2), 71, 1))
+        out = retopk.chunk_attention(q, c.h, i32([5000]), cu_tokens=offsets(n))
+        check(q, n, [71], c, out, None, 1 / math.sqrt(D), 0.0, 0)
+
+
+@pytest.mark.parametrize("cu,lens", [([0, 5, 3, 9], [50, 60, 70]), ([2, 4, 6, 40], [10, 20, 30]), ([0, 0, 0, 0], [9, 9, 9]), ([-4, 2, 7, 7], [9, -9, 3]),
+                                     ([-(1 << 31), 2, (1 << 31) - 1, 9], [9, (1 << 31) - 1, -(1 << 31)]), ([0, 1, 2, 3], [90, 50, 100])])
+@pytest.mark.parametrize("T", [9, 3])
+def test_attention_odd_offsets_and_lengths_stay_inside(cu, lens, T):
+    # offsets that decrease, leave tokens out or pass the last token; a negative length: no row outside is written
+    q, _ = setup([T], [90], 8, 2, 16, 26, pad=0, strided=False)
+    c = Cache(3, 2, 100, 16)
+    for b in range(3):
+        c.put(b, packed(gen(b), 112, 2), packed(gen(b + 9), 112, 2))
+    out = torch.full((T + 2, 8, D), 9.0, dtype=torch.bfloat16, device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    retopk.chunk_attention(q, c.h, i32(lens), out[1:T + 1], cu_tokens=i32(cu), status=st)
+    assert st.item() == 0 and (out[0] == 9).all() and (out[T + 1] == 9).all() and not out.isnan().any()
+    flat = {t for b in range(3) for t in range(max(cu[b], 0), min(cu[b + 1], T))}
+    for t in range(T):
+        if t not in flat:
+            assert (out[1 + t] == 9).all()
+
+
+@pytest.mark.parametrize("n", [[1, 1], [30, 40]])
+def test_attention_reports_bad_pages(n):
+    q, c = setup(n, [100, 100], 4, 1, 16, 13, pad=0)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    call = lambda: retopk.chunk_attention(q, c.h, i32([100, 100]), cu_tokens=offsets(n), status=st)  # noqa: E731
+    good = call().clone()
+    c.table[0, 2], c.table[0, 3] = c.k.shape[0], -7
+    out = call()
+    assert st.item() == retopk.STATUS_BAD_PAGE
+    assert torch.equal(out[n[0]:], good[n[0]:]) and not out.isnan().any()
+
+
+@pytest.mark.parametrize("n", [[1, 1], [20, 90]])
+def test_attention_shared_pages(n):
+    q, c = setup(n, [200, 150], 4, 2, 16, 14, pad=0)
+    c.table[1, :9] = c.table[0, :9]
+    out = retopk.chunk_attention(q, c.h, i32([200, 150]), cu_tokens=offsets(n))
+    check(q, n, [200, 150], c, out, None, 1 / math.sqrt(D), 0.0, 0)
+
+
+@pytest.mark.parametrize("n,L", [([1, 1], [301, 7001]), ([200, 3], [901, 2051])])
+@pytest.mark.parametrize("cap", [0.0, 5.0])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_attention_queries_that_are_not_finite_stay_in_their_rows(n, L, cap, bad):
+    q, c = setup(n, L, 14, 2, 64, 47, pad=0, qscale=6.0, strided=False)
+    T = sum(n)
+    hit = torch.zeros((T, 14), dtype=torch.bool, device="cuda")
+    hit[0, 3] = hit[n[0], 0] = hit[T - 1, 13] = True
+    clean = q.clone()
+    q[..., 5][hit] = bad
+    lse = torch.empty((T, 14), device="cuda")
+    out = retopk.chunk_attention(q, c.h, i32(L), cu_tokens=offsets(n), lse=lse, softcap=cap)
+    if math.isnan(bad):
+        assert out[hit].isnan().all() and lse[hit].isnan().all()
+    want = retopk.chunk_attention(clean, c.h, i32(L), cu_tokens=offsets(n), softcap=cap)
+    assert ((out.float() - want.float()).abs()[~hit] <= 2.0 ** -7 * want.float().abs()[~hit] + 0.01).all() and lse[~hit].isfinite().all()
+
+
+@pytest.mark.parametrize("n", [[1], [40]])
+def test_attention_a_pool_past_2_31_elements(n):
+    pages = 70000                                          # 64 bytes x 512 rows a page: 2.3e9
+    k, v = (torch.zeros((pages, 1, 512, 64), dtype=torch.uint8, device="cuda") for _ in range(2))
+    ks, vs = (torch.zeros((pages, 1, 512, 8), dtype=torch.uint8, device="cuda") for _ in range(2))
+    q, c = setup(n, [600], 4, 1, 0, 15, pad=0)
+    for far, near in ((k, c.k), (v, c.v), (ks, c.ks), (vs, c.vs)):
+        far[pages - 1, 0], far[3, 0, :88] = near[0, 0, :512], near[0, 0, 512:600]
+    h = retopk.KVCache(k, v, table=i32([[pages - 1, 3]]), k_scale=ks, v_scale=vs)
+    out = retopk.chunk_attention(q, h, i32([600]), cu_tokens=offsets(n))
+    check(q, n, [600], c, out, None, 1 / math.sqrt(D), 0.0, 0)
+
+
+@pytest.mark.parametrize("n", [[1, 1, 1], [3, 3, 3], [100, 1, 30]])
+def test_attention_captured_follows_lengths_and_two_graphs_share_a_workspace(n):
+    L = [700, 5000, 40]
+    q, c = setup(n, L, 28, 4, 64, 21, pad=0, strided=False)
+    T, lens, at = sum(n), i32(L), offsets(n)
+    ws = torch.empty(retopk.chunk_attention_workspace_bytes(T, 3, 28, 4) + 256, dtype=torch.uint8, device="cuda")
+    outs = [torch.empty_like(q) for _ in range(2)]
+    call = lambda o: retopk.chunk_attention(q, c.h, lens, o, cu_tokens=at, workspace=ws)  # noqa: E731
+    call(outs[0])
+    graphs = []
+    for o in outs:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            call(o)
+    for new in ([700, 5000, 40], [100, 4000, 30], [512, 64, 35]):
+        lens.copy_(i32(new))
+        for o in outs:
+            o.fill_(7)
+        for x in (0, 1, 0, 1):
+            graphs[x].replay()
+        for o in outs:
+            check(q, n, new, c, o, None, 1 / math.sqrt(D), 0.0, 0)
+    assert torch.equal(*outs)
+
+
+@pytest.mark.parametrize("n", [[1] * 4, [2] * 4, [90] * 4])
+def test_attention_on_another_stream_and_two_calls_at_once(n):
+    L = [3000, 100, 2047, 901]
+    q, c = setup(n, L, 8, 2, 0, 22, pad=0, strided=False)
+    want = retopk.chunk_attention(q, c.h, i32(L), cu_tokens=offsets(n)).clone()
+    lens, at = i32(L), offsets(n)
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], []
+    for _ in range(3):
+        for s in streams:
+            got.append(retopk.chunk_attention(q, c.h, lens, cu_tokens=at, stream=s))
+    torch.cuda.synchronize()
+    for x in got:
+        assert torch.equal(x, want)      # the order of every sum follows from the lengths alone
+
+
+def test_a_sequence_from_prompt_to_sparse_decoding():
+    # a prompt and single tokens are appended in 4 bits and attended, then read back for the decode steps
+    g, Hq, Hkv, n0, steps = gen(40), 8, 2, 200, 5
+    c, flat = Cache(1, Hkv, 256, 16), Cache(1, Hkv, 256, 0, "bf16")
+    sl, rope = i32([0]), retopk.QKRope(freqs(128), normal(g, D), normal(g, D))
+    for n in [n0] + [1] * steps:
+        x = normal(g, n, Hq + 2 * Hkv, D)
+        q = retopk.qkv_append(rope, x[:, :Hq], x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:], c.h, sl, cu_tokens=i32([0, n]))
+        out = retopk.chunk_attention(q, c.h, sl, cu_tokens=i32([0, n]))
+        check(q, [n], [sl.item()], c, out, None, 1 / math.sqrt(D), 0.0, 0)
+    L = sl.item()
+    assert L == n0 + steps
+    retopk.cache_copy(c.h, flat.h, i32([0]), sl)
+    for x, y in zip(flat.rows(0, L), c.rows(0, L)):
+        assert torch.equal(x, y)
+    again = retopk.chunk_attention(q, flat.h, sl)
+    assert ((again.float() - out.float()).abs() <= 2.0 ** -6 * out.float().abs() + 2.0 ** -8).all()
+    full = torch.empty((1, Hq, D), dtype=torch.bfloat16, device="cuda")
+    retopk.exact_topk_attention_step(q, flat.k, flat.v, sl, 256, full)      # every key is among the best 256
+    assert ((full.float() - out.float()).abs() <= 2.0 ** -6 * out.float().abs() + 2.0 ** -8).all()

@@ -55,20 +55,29 @@ namespace retopk {
 
 constexpr int kTile = 128;                       // rows and keys of a tile
 constexpr int kAttnStages = 5;                   // K / V tiles in flight
+constexpr int kFp4Stages = 4;                    // the same over 4-bit rows
 constexpr int kAttnStageBytes = kTile * kD * 2;  // 32 KiB: [half of d][key][64]
 constexpr int kHalfBytes = kAttnStageBytes / 2;
-constexpr int kAttnThreads = 12 * 32;
-constexpr int kMmaWarp = 8, kLoadWarp = 9, kWalkWarp = 10;
+constexpr int kAttnThreads = 12 * 32, kFp4Threads = 16 * 32;
+constexpr int kMmaWarp = 8, kLoadWarp = 9, kWalkWarp = 10, kExpandWarp = 12, kExpandWarps = 4;
+template <bool FP4>
+constexpr int kStagesOf = FP4 ? kFp4Stages : kAttnStages;
 constexpr int kSegments = 4;                     // known ahead
 constexpr int kHalf = kTile / 2;                 // keys of half a tile
 // registers of a thread after the split: 2 x 128 x 208 + 128 x 88 = 384 x 168, what the block is launched with
 // (4096 tokens over 32768 keys in short bursts: 1133 us; with 216 and 72 or 224 and 56, 1190)
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
+// over 4-bit rows: 2 x 128 x 200 + 2 x 128 x 56 = 512 x 128
+constexpr int kFp4SoftmaxRegs = 200, kFp4OtherRegs = 56;
 // Weight of an item beside its keys: what beginning and ending it costs, in keys.  (A prompt
 // of 8192 tokens: 494 us with 128, 386 with 512, 399 with 1024; 128 sequences of 1500 keys, 32 over 8 heads: 135 us
 // with 256, 126 with 512, 128 with 1024.)
 constexpr int kItemWeight = 512;
 constexpr float kLazy = 8.f;                     // growth of m, in powers of two, that is left to the accumulators
+// Over 4-bit rows V is fp16 and so is P: m lies 2^7 below the maximum, so that weights reach from 2^15 down to fp16's 2^-24
+// and a long row's small ones are not lost.
+template <bool FP4>
+constexpr float kLift = FP4 ? 7.f : 0.f;
 
 // Where a share begins: an item and the number of its K / V tiles that belong
 // to earlier shares.
@@ -236,7 +245,7 @@ struct AttnShared {
     int first_b;
     Segment segments[kSegments];
     uint64_t seg_full[kSegments], seg_empty[kSegments];
-    long long sums[kAttnThreads / 32 + 1];
+    long long sums[kFp4Threads / 32 + 1];
     uint32_t tmem;
     int failed;
 };
@@ -380,6 +389,7 @@ constexpr uint32_t kDescLead = (uint32_t)(kHalfBytes >> 4) << 16;   // V's block
 // fp32 accumulators, bf16 operands, M = N = 128.
 constexpr uint32_t kIdescS = 1u << 4 | 1u << 7 | 1u << 10 | (kTile / 8) << 17 | (kTile / 16) << 24;
 constexpr uint32_t kIdescO = kIdescS | 1u << 16;   // B (V) is MN-major
+constexpr uint32_t kIdescO16 = kIdescO & ~(1u << 7 | 1u << 10);   // the same of fp16 operands
 
 __device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t accumulate)
 {
@@ -390,12 +400,12 @@ __device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint3
         : "memory");
 }
 
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t accumulate)
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate)
 {
     asm volatile(
         "{\n .reg .pred p;\n .reg .b64 y;\n setp.ne.u32 p, %5, 0;\n mov.b64 y, {%2, %3};\n"
         " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n}\n" ::"r"(d),
-        "r"(a), "r"(b), "r"(kDescHigh), "r"(kIdescO), "r"(accumulate)
+        "r"(a), "r"(b), "r"(kDescHigh), "r"(idesc), "r"(accumulate)
         : "memory");
 }
 
@@ -502,8 +512,8 @@ struct AttnLaunch {
     float cap_poly[3], cap_near;
 };
 
-// ---- the copies --------------------------------------------------------------------
-template <bool TWO>
+// ---- the copies (over 4-bit rows: of Q alone) ----------------------------------------
+template <bool TWO, bool FP4>
 __device__ __forceinline__ void copies(const AttnLaunch &c, AttnShared &sh, const CUtensorMap &qmap,
                                        const CUtensorMap &kmap, const CUtensorMap &vmap, uint32_t qbuf, uint32_t ring,
                                        int lane)
@@ -533,6 +543,10 @@ __device__ __forceinline__ void copies(const AttnLaunch &c, AttnShared &sh, cons
             }
         }
         ok = __shfl_sync(0xffffffffu, (int)ok, 0);
+        if constexpr (FP4) {
+            segment_done(sh, segs++);
+            continue;
+        }
         // where this lane's rows of tile t lie: the copy's coordinates in a page and among pages
         auto look = [&](int t) {
             int2 at = make_int2(0, a.cache.n_pages * Hkv);   // outside: read as zeros
@@ -603,22 +617,183 @@ __device__ __forceinline__ void copies(const AttnLaunch &c, AttnShared &sh, cons
     __syncwarp();
 }
 
+// ---- 4-bit rows into the ring: four warps, 32 keys of a tile each -----------------------
+// Copies bring codes and scales (72 bytes a row) three tiles ahead into a place of each warp's own.  Four lanes a row, 32
+// codes a lane, become bf16 keys (as Q is) or fp16 values in the layout that a tensor copy would have left.  Both hold
+// code times scale exactly.  A row past the length, or in a bad page, gets scales of zero.
+constexpr int kRawTiles = 3, kRawRow = kD / 2 + kFp4Scales, kRawBytes = kTile / kExpandWarps * kRawRow;   // of a warp's part
+static_assert(kRawTiles * kExpandWarps * kRawBytes <= (kAttnStages - kFp4Stages) * kAttnStageBytes, "the ring's last place");
+
+template <bool TWO>
+__device__ __forceinline__ void expand(const AttnLaunch &c, AttnShared &sh, uint32_t raw, uint32_t ring, int warp, int lane)
+{
+    const AttnArgs &a = c.a;
+    const int Hkv = a.cache.n_kv_heads, chunk = lane & 3, quad = lane >> 2;
+    raw += warp * kRawTiles * kRawBytes;
+    bool ok = true;
+    uint32_t used = 0, segs = 0;
+    uint32_t queue[kRawTiles] = {}, waiting = 0;   // tiles on their way, the oldest first: twice the ring's slot, plus one for keys
+    uint32_t to = 0, from = 0;                // places of the next copy, and of the oldest
+    auto next_place = [](uint32_t x) { return x + kRawBytes == kRawTiles * kRawBytes ? 0 : x + kRawBytes; };
+    auto group = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
+    // the oldest tile into the ring; one group of copies a tile, empty ones at the end
+    auto oldest = [&] {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kRawTiles - 1) : "memory");
+        __syncwarp();
+        const uint32_t u = queue[0] >> 1, st = u % kFp4Stages;
+        const bool keys = queue[0] & 1;
+#pragma unroll
+        for (int i = 0; i + 1 < kRawTiles; ++i)
+            queue[i] = queue[i + 1];
+        --waiting;
+        if (u >= kFp4Stages && !warp_wait(sh, &sh.kv_empty[st], (u / kFp4Stages - 1) & 1, a.status))
+            return false;
+        const uint32_t half = chunk >> 1, dst = ring + st * kAttnStageBytes + half * kHalfBytes;
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            const uint32_t in_part = p * 8 + quad, row = warp * 32 + in_part;
+            uint32_t w[4], s;
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                         : "r"(raw + from + in_part * (kD / 2) + chunk * 16));
+            asm volatile("{\n .reg .u16 x;\n ld.shared.u16 x, [%1];\n cvt.u32.u16 %0, x;\n}\n"
+                         : "=r"(s)
+                         : "r"(raw + from + 32 * (kD / 2) + in_part * kFp4Scales + chunk * 2));
+            // the lanes of the row's second half begin with their third word: then 8 lanes meet no bank twice
+            const uint32_t turn = half * 2;
+            uint32_t lo = (s & 255u) * 0x00800080u, hi = (s >> 8) * 0x00800080u;   // fp16, twice
+            if (half) {
+                uint32_t x = w[0];
+                w[0] = w[2], w[2] = x;
+                x = w[1];
+                w[1] = w[3], w[3] = x;
+                x = lo;
+                lo = hi, hi = x;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t h[4];
+                e2m1x8_halves(w[i], h);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const __half2 y = __hmul2(reinterpret_cast<const __half2 &>(h[e]), reinterpret_cast<const __half2 &>(i < 2 ? lo : hi));
+                    h[e] = reinterpret_cast<const uint32_t &>(y);
+                    if (keys) {
+                        const float2 f = __half22float2(y);
+                        h[e] = bf16x2(f.x, f.y);
+                    }
+                }
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + row * 128 + ((((chunk & 1) * 4 + (i ^ turn)) ^ (row & 7)) << 4)),
+                             "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3])
+                             : "memory");
+            }
+        }
+        from = next_place(from);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();   // (also: all lanes have read the place that the next copy takes)
+        if (lane == 0)
+            mbar_arrive(&sh.kv_full[st]);
+        return true;
+    };
+    while (ok && segment(sh, segs, a.status)) {
+        const Segment &s = sh.segments[segs % kSegments];
+        const int nt = s.j1 - s.j0, L = s.seq.L, j0 = s.j0, hk = s.hk, b = s.b;
+        // where this warp's rows of tile t lie, for each 16 of them: the head's rows of a page (-1: none), and the row there
+        struct Rows {
+            int page[2], row[2];
+        };
+        auto look = [&](int t) {
+            Rows at;
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                const int pos = (j0 + t) * kTile + warp * 32 + g * 16;
+                at.page[g] = -1;
+                at.row[g] = pos;
+                if (t < nt && pos < L) {
+                    int page = b;
+                    if (a.cache.table) {
+                        page = a.cache.table[(long long)b * a.cache.table_width + pos / a.cache.page_rows];
+                        at.row[g] = pos % a.cache.page_rows;
+                    }
+                    if ((uint32_t)page < (uint32_t)a.cache.n_pages)
+                        at.page[g] = page * Hkv + hk;
+                    else if (a.status)
+                        atomicOr(a.status, RETOPK_STATUS_BAD_PAGE);
+                }
+            }
+            return at;
+        };
+        constexpr int ahead = TWO ? 1 : 2;   // the ring's order, as in copies()
+        Rows at[3] = {look(0), look(0), look(0)};
+        for (int x = -ahead; x < nt && ok; ++x) {
+            const Rows next = look(x + ahead + 1);
+#pragma unroll
+            for (int isk = 0; isk < 2; ++isk) {
+                const int t = isk ? x + ahead : x;
+                if (t < 0 || t >= nt || !ok)
+                    continue;
+                const Rows &r = at[isk ? ahead : 0];
+                const uint8_t *codes = static_cast<const uint8_t *>(isk ? a.cache.k : a.cache.v), *scales = isk ? a.cache.k_scale : a.cache.v_scale;
+                const int pos = (j0 + t) * kTile + warp * 32;
+                long long first[2];
+#pragma unroll
+                for (int g = 0; g < 2; ++g)
+                    first[g] = (long long)r.page[g] * a.cache.page_rows + r.row[g];
+#pragma unroll
+                for (int p = 0; p < 4; ++p) {
+                    const int in_part = p * 8 + quad;
+                    if (r.page[p / 2] >= 0 && pos + in_part < L)
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(raw + to + in_part * (kD / 2) + chunk * 16),
+                                     "l"(codes + (first[p / 2] + (in_part & 15)) * (kD / 2) + chunk * 16)
+                                     : "memory");
+                }
+                const bool there = r.page[lane >> 4 ? 1 : 0] >= 0 && pos + lane < L;
+                const long long row = (lane >> 4 ? first[1] : first[0]) + (lane & 15);
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(raw + to + 32 * (kD / 2) + lane * kFp4Scales),
+                             "l"(scales + (there ? row * kFp4Scales : 0)), "r"(there ? 8 : 0)
+                             : "memory");
+                group();
+                to = next_place(to);
+                queue[0] = waiting == 0 ? 2 * (used + (isk ? ring_k<TWO>(t) : ring_v<TWO>(t, nt))) + isk : queue[0];
+                queue[1] = waiting == 1 ? 2 * (used + (isk ? ring_k<TWO>(t) : ring_v<TWO>(t, nt))) + isk : queue[1];
+                queue[2] = waiting == 2 ? 2 * (used + (isk ? ring_k<TWO>(t) : ring_v<TWO>(t, nt))) + isk : queue[2];
+                if (++waiting == kRawTiles)
+                    ok = oldest();
+            }
+            at[0] = at[1];
+            at[1] = TWO ? next : at[2];
+            at[2] = next;
+        }
+        used += 2 * nt;
+        segment_done(sh, segs++);
+    }
+    while (ok && waiting > 0) {
+        // (as if kRawTiles were on their way)
+        for (uint32_t i = waiting; i < kRawTiles; ++i)
+            group();
+        ok = oldest();
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncwarp();
+}
+
 // ---- the matrix instructions ------------------------------------------------------------
 // The whole warp walks and waits, one lane issues: what addresses the operands
 // stays the same for all lanes, so that it can live in uniform registers (an
 // instruction issued from a divergent branch cost 110 cycles in place of 64).
-template <bool TWO>
+template <bool TWO, bool FP4>
 __device__ __forceinline__ void matrices(const AttnLaunch &c, AttnShared &sh, uint32_t qbuf, uint32_t ring,
                                          uint32_t tmem_any)
 {
+    constexpr int kStages = kStagesOf<FP4>;
     const AttnArgs &a = c.a;
     const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_any, 0);
     bool ok = true;
     uint32_t used = 0, segs = 0, done0 = 0, done1 = 0;   // done: tiles of each group before this segment
     // S_i of the segment's tile t
     auto scores = [&](int i, int t) {
-        const uint32_t u = used + ring_k<TWO>(t), st = u % kAttnStages;
-        if ((!TWO || i == 0) && !warp_wait(sh, &sh.kv_full[st], (u / kAttnStages) & 1, a.status))
+        const uint32_t u = used + ring_k<TWO>(t), st = u % kStages;
+        if ((!TWO || i == 0) && !warp_wait(sh, &sh.kv_full[st], (u / kStages) & 1, a.status))
             return false;
         tc_fence_after();
         if (elected()) {
@@ -651,9 +826,9 @@ __device__ __forceinline__ void matrices(const AttnLaunch &c, AttnShared &sh, ui
             for (int i = 0; i < 2; ++i) {
                 if (t >= (i ? m1 : m0) || !ok)
                     continue;
-                const uint32_t u = used + ring_v<TWO>(tile(i, t), nt), st = u % kAttnStages;
+                const uint32_t u = used + ring_v<TWO>(tile(i, t), nt), st = u % kStages;
                 if (!TWO || i == 0)   // (both groups' product takes the tile)
-                    ok = warp_wait(sh, &sh.kv_full[st], (u / kAttnStages) & 1, a.status);
+                    ok = warp_wait(sh, &sh.kv_full[st], (u / kStages) & 1, a.status);
                 // P comes in halves, so that the product begins while the second is made
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
@@ -665,7 +840,7 @@ __device__ __forceinline__ void matrices(const AttnLaunch &c, AttnShared &sh, ui
                         const uint32_t v = (ring + st * kAttnStageBytes) >> 4 | kDescLead;
 #pragma unroll
                         for (int x = 4 * h; x < 4 * h + 4; ++x)
-                            mma_ts(tmem + (2 + i) * kTile, tmem + i * kTile + x * 8, v + (x * 2048 >> 4), t > 0 || x > 0);
+                            mma_ts(tmem + (2 + i) * kTile, tmem + i * kTile + x * 8, v + (x * 2048 >> 4), FP4 ? kIdescO16 : kIdescO, t > 0 || x > 0);
                         if (h == 1) {
                             tc_commit(&sh.o_full[i]);
                             if (!TWO || i == 1)
@@ -696,7 +871,7 @@ __device__ __forceinline__ void matrices(const AttnLaunch &c, AttnShared &sh, ui
 }
 
 // ---- softmax: group i, row r --------------------------------------------------------------
-template <bool TWO, bool CAP>
+template <bool TWO, bool CAP, bool FP4>
 __device__ __forceinline__ void softmax(const AttnLaunch &c, AttnShared &sh, float *ml, uint32_t ring,
                                         uint32_t tmem, int warp, int lane)
 {
@@ -739,8 +914,8 @@ __device__ __forceinline__ void softmax(const AttnLaunch &c, AttnShared &sh, flo
                 const uint32_t p_addr = live ? s_addr : o_addr;
                 uint64_t *const p_bar = live ? sh.p_full[i] : sh.nobody;
                 // V rows past the length may hold anything, and 0 times that is not 0: they are
-                // cleared where the tile is used first
-                if (live && (!TWO || i == 0) && (j + 1) * kTile > s.seq.L) {
+                // cleared where the tile is used first (4-bit ones are expanded to zeros)
+                if (!FP4 && live && (!TWO || i == 0) && (j + 1) * kTile > s.seq.L) {
                     const uint32_t u = used + ring_v<TWO>(j - s.j0, nt);
                     const int st = u % kAttnStages;
                     ok = warp_wait(sh, &sh.kv_full[st], (u / kAttnStages) & 1, a.status);
@@ -808,7 +983,7 @@ __device__ __forceinline__ void softmax(const AttnLaunch &c, AttnShared &sh, flo
                     };
                     auto rounding = [&](int n) {
                         sum[n & 1] = add2(sum[n & 1], make_float2(f[2 * n], f[2 * n + 1]));
-                        x[n] = bf16x2(f[2 * n], f[2 * n + 1]);
+                        x[n] = FP4 ? f16x2(f[2 * n], f[2 * n + 1]) : bf16x2(f[2 * n], f[2 * n + 1]);
                     };
                     // The maximum m that the weights are taken against follows the true one only when
                     // that has grown by more than 2^8: until then the weights are at most 256, and the
@@ -818,6 +993,7 @@ __device__ __forceinline__ void softmax(const AttnLaunch &c, AttnShared &sh, flo
                     // m up to the tile's maximum where that has grown too far, and the accumulators with it;
                     // false when a wait ran out
                     auto raise = [&](float top) {
+                        top -= kLift<FP4>;
                         const bool grow = valid && m != -INFINITY && top > m + kLazy;
                         if (__any_sync(0xffffffffu, grow)) {
                             if (!warp_wait(sh, &sh.o_full[i], (done + t - 1) & 1, a.status))
@@ -876,8 +1052,8 @@ __device__ __forceinline__ void softmax(const AttnLaunch &c, AttnShared &sh, flo
                             }
                         }
                         const float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
-                        made = !__any_sync(0xffffffffu, valid && (CAP ? fmaxf(big[0], big[1]) > c.cap_near || near_capped(top) > m + kLazy
-                                                                   : top * scale2 > m + kLazy));
+                        made = !__any_sync(0xffffffffu, valid && (CAP ? fmaxf(big[0], big[1]) > c.cap_near || near_capped(top) > m + (kLazy + kLift<FP4>)
+                                                                   : top * scale2 > m + (kLazy + kLift<FP4>)));
                         if (made) {
 #pragma unroll
                             for (int n = kPairs / 2 - kLead; n < kPairs + kLead; ++n) {
@@ -1118,11 +1294,12 @@ __device__ __forceinline__ void softmax(const AttnLaunch &c, AttnShared &sh, flo
     }
 }
 
-template <bool TWO, bool CAP>
-__global__ void __launch_bounds__(kAttnThreads, 1)
+template <bool TWO, bool CAP, bool FP4>
+__global__ void __launch_bounds__(FP4 ? kFp4Threads : kAttnThreads, 1)
     chunk_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                            const __grid_constant__ CUtensorMap vmap, const AttnLaunch c)
 {
+    constexpr int kThreads = FP4 ? kFp4Threads : kAttnThreads, kStages = kStagesOf<FP4>;
     extern __shared__ __align__(1024) unsigned char attn_smem[];
     AttnShared &sh = *reinterpret_cast<AttnShared *>(attn_smem + (2 + kAttnStages) * kAttnStageBytes);
     const AttnArgs &a = c.a;
@@ -1133,8 +1310,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const int Hkv = a.cache.n_kv_heads;
 
     if (tid == 0) {
-        for (int s = 0; s < kAttnStages; ++s) {
-            mbar_init(&sh.kv_full[s], 1);
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&sh.kv_full[s], FP4 ? kExpandWarps : 1);
             mbar_init(&sh.kv_empty[s], 1);
         }
         mbar_init(&sh.q_full, 1);
@@ -1147,7 +1324,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
         for (int s = 0; s < kSegments; ++s) {
             mbar_init(&sh.seg_full[s], 1);
-            mbar_init(&sh.seg_empty[s], kLoadWarp + 1);
+            mbar_init(&sh.seg_empty[s], kLoadWarp + 1 + (FP4 ? kExpandWarps : 0));
         }
         mbar_init(&sh.x_full, 4);
         mbar_init(&sh.x_empty, 4);
@@ -1180,7 +1357,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     Seq mine{0, 0, 0};
     const long long my_weight = of_sequence(tid, mine);
     long long total = my_weight;
-    for (int b = tid + kAttnThreads; b < a.B; b += kAttnThreads) {
+    for (int b = tid + kThreads; b < a.B; b += kThreads) {
         Seq q;
         total += of_sequence(b, q);
     }
@@ -1191,7 +1368,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         if (lane >= o)
             up += y;
     }
-    if (a.B > kAttnThreads) {
+    if (a.B > kThreads) {
 #pragma unroll
         for (int o = 16; o; o >>= 1)
             total += __shfl_xor_sync(0xffffffffu, total, o);
@@ -1199,7 +1376,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             sh.sums[warp] = total;
         __syncthreads();
         total = 0;
-        for (int i = 0; i < kAttnThreads / 32; ++i)
+        for (int i = 0; i < kThreads / 32; ++i)
             total += sh.sums[i];
         __syncthreads();
     }
@@ -1208,12 +1385,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     __syncthreads();
     long long off = 0, round = 0;
 #pragma unroll
-    for (int i = 0; i < kAttnThreads / 32; ++i) {
+    for (int i = 0; i < kThreads / 32; ++i) {
         const long long x = sh.sums[i];
         off += i < warp ? x : 0;
         round += x;
     }
-    if (a.B <= kAttnThreads)
+    if (a.B <= kThreads)
         total = round;
     const long long share = (long long)__umul64hi((unsigned long long)total, plan.inverse) + 1;
     const long long u0 = min(share * blockIdx.x, total), u1 = min(share * (blockIdx.x + 1), total);
@@ -1231,7 +1408,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
     };
     find(tid, mine, off + up - my_weight, my_weight);
-    for (int base = kAttnThreads; base < a.B; base += kAttnThreads) {
+    for (int base = kThreads; base < a.B; base += kThreads) {
         const long long before = round;
         Seq q{0, 0, 0};
         const long long x = of_sequence(base + tid, q);
@@ -1247,7 +1424,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             sh.sums[warp] = up;
         __syncthreads();
         off = before;
-        for (int i = 0; i < kAttnThreads / 32; ++i) {
+        for (int i = 0; i < kThreads / 32; ++i) {
             off += i < warp ? sh.sums[i] : 0;
             round += sh.sums[i];
         }
@@ -1263,16 +1440,18 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             c.parts.bound[gridDim.x] = Bound{sh.bound[1], 0, 0};
     }
     if (warp < kMmaWarp) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-        softmax<TWO, CAP>(c, sh, reinterpret_cast<float *>(attn_smem + kAttnStageBytes), ring, tmem, warp, lane);
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(FP4 ? kFp4SoftmaxRegs : kSoftmaxRegs));
+        softmax<TWO, CAP, FP4>(c, sh, reinterpret_cast<float *>(attn_smem + kAttnStageBytes), ring, tmem, warp, lane);
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(FP4 ? kFp4OtherRegs : kOtherRegs));
         if (warp == kLoadWarp)
-            copies<TWO>(c, sh, qmap, kmap, vmap, qbuf, ring, lane);
+            copies<TWO, FP4>(c, sh, qmap, kmap, vmap, qbuf, ring, lane);
         else if (warp == kMmaWarp)
-            matrices<TWO>(c, sh, qbuf, ring, tmem);
+            matrices<TWO, FP4>(c, sh, qbuf, ring, tmem);
         else if (warp == kWalkWarp && lane == 0)
             walk_share(a, plan, sh);
+        else if (FP4 && warp >= kExpandWarp)
+            expand<TWO>(c, sh, ring + kStages * kAttnStageBytes, ring, warp - kExpandWarp, lane);
     }
     tc_fence_before();
     __syncthreads();
@@ -1473,8 +1652,10 @@ static cudaError_t launch_mode(const CUtensorMap &qm, const CUtensorMap &km, con
     // (and no more CTAs than there may be items)
     const bool cuts = c.a.capacity > 4 * kTile;
     const int n = c.shares;
-    auto kernel = c.a.softcap > 0.f ? chunk_attention_kernel<TWO, true> : chunk_attention_kernel<TWO, false>;
-    cudaError_t e = launch_pdl(kernel, dim3(n), dim3(kAttnThreads), kAttnSmem, st, 1, qm, km, vm, c);
+    const bool fp4 = c.a.cache.format == RETOPK_CACHE_FP4, cap = c.a.softcap > 0.f;
+    auto kernel = fp4 ? (cap ? chunk_attention_kernel<TWO, true, true> : chunk_attention_kernel<TWO, false, true>)
+                      : (cap ? chunk_attention_kernel<TWO, true, false> : chunk_attention_kernel<TWO, false, false>);
+    cudaError_t e = launch_pdl(kernel, dim3(n), dim3(fp4 ? kFp4Threads : kAttnThreads), kAttnSmem, st, 1, qm, km, vm, c);
     if (e != cudaSuccess || n < 2 || !cuts)
         return e;
     // the items that may be cut, and blocks for each: few items have many parts
@@ -1510,9 +1691,12 @@ cudaError_t launch_chunk_attention(const AttnArgs &a, cudaStream_t st)
             c.chunk /= 2;
     CUtensorMap qm, km, vm;
     const cuuint64_t page = (cuuint64_t)a.cache.page_rows * kD * 2, pages = (cuuint64_t)a.cache.n_pages * Hkv;
-    if (!make_map(&qm, a.q, a.Hq, a.T, kD * 2, a.q_stride * 2, a.G, tokens) ||
-        !make_map(&km, a.cache.k, a.cache.page_rows, pages, kD * 2, page, c.chunk, 1) ||
-        !make_map(&vm, a.cache.v, a.cache.page_rows, pages, kD * 2, page, c.chunk, 1))
+    if (!make_map(&qm, a.q, a.Hq, a.T, kD * 2, a.q_stride * 2, a.G, tokens))
+        return cudaErrorInvalidValue;
+    km = vm = qm;   // (4-bit rows are not copied by maps)
+    if (a.cache.format == RETOPK_CACHE_BF16 &&
+        (!make_map(&km, a.cache.k, a.cache.page_rows, pages, kD * 2, page, c.chunk, 1) ||
+        !make_map(&vm, a.cache.v, a.cache.page_rows, pages, kD * 2, page, c.chunk, 1)))
         return cudaErrorInvalidValue;
     return two ? launch_mode<true>(qm, km, vm, c, st) : launch_mode<false>(qm, km, vm, c, st);
 }
@@ -1524,10 +1708,14 @@ cudaError_t configure_chunk_attention()
         if (e == cudaSuccess)
             e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kAttnSmem);
     };
-    set((const void *)chunk_attention_kernel<true, true>);
-    set((const void *)chunk_attention_kernel<true, false>);
-    set((const void *)chunk_attention_kernel<false, true>);
-    set((const void *)chunk_attention_kernel<false, false>);
+    set((const void *)chunk_attention_kernel<true, true, false>);
+    set((const void *)chunk_attention_kernel<true, false, false>);
+    set((const void *)chunk_attention_kernel<false, true, false>);
+    set((const void *)chunk_attention_kernel<false, false, false>);
+    set((const void *)chunk_attention_kernel<true, true, true>);
+    set((const void *)chunk_attention_kernel<true, false, true>);
+    set((const void *)chunk_attention_kernel<false, true, true>);
+    set((const void *)chunk_attention_kernel<false, false, true>);
     return e;
 }
 

@@ -243,7 +243,7 @@ int retopk_chunk_attention(const retopk_bf16 *q, int64_t q_stride, const retopk_
     int e;
     if ((e = check_cache(cache, B)) || (e = check_tokens(T, B, Hq, cache->n_kv_heads, cu_tokens, seqlens)))
         return e;
-    if (cache->format != RETOPK_CACHE_BF16)
+    if (cache->format == RETOPK_CACHE_MX8)
         return RETOPK_ERR_UNSUPPORTED;
     if (!(scale >= 0.f) || isinf(scale) || !(softcap >= 0.f) || isinf(softcap) || window < 0)
         return RETOPK_ERR_INVALID;

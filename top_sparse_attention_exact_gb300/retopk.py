@@ -472,7 +472,7 @@ def chunk_attention_workspace_bytes(T, B, Hq, Hkv) -> int:
 
 def chunk_attention(q, cache: KVCache, seqlens, out=None, cu_tokens=None, scale=None, softcap=0.0, window=0, lse=None,
                     workspace=None, status=None, stream=None):
-    """Causal attention of q [T, Hq, 128] over a bf16 cache that holds the tokens' own rows (seqlens: rows in all);
+    """Causal attention of q [T, Hq, 128] over a bf16 or 4-bit cache that holds the tokens' own rows (seqlens: rows in all);
     returns out (which may be q).  cu_tokens: offsets of each sequence's tokens (None: one token each, dense decoding).  scale: 1/sqrt(128)
     where None or 0.  lse: optional fp32 [T, Hq].  workspace: uint8, chunk_attention_workspace_bytes(...) + 256 (None: allocated for the call)."""
     T, Hq = q.shape[:2]
