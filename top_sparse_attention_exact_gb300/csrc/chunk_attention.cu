@@ -48,12 +48,12 @@
 
 #include <algorithm>
 
+#include "attention_plan.cuh"
 #include "prompt.cuh"
 #include "tensor_map.cuh"
 
 namespace retopk {
 
-constexpr int kTile = 128;                       // rows and keys of a tile
 constexpr int kAttnStages = 5;                   // K / V tiles in flight
 constexpr int kFp4Stages = 4;                    // the same over 4-bit rows
 constexpr int kAttnStageBytes = kTile * kD * 2;  // 32 KiB: [half of d][key][64]
@@ -69,170 +69,20 @@ constexpr int kHalf = kTile / 2;                 // keys of half a tile
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
 // over 4-bit rows: 2 x 128 x 200 + 2 x 128 x 56 = 512 x 128
 constexpr int kFp4SoftmaxRegs = 200, kFp4OtherRegs = 56;
-// Weight of an item beside its keys: what beginning and ending it costs, in keys.  (A prompt
-// of 8192 tokens: 494 us with 128, 386 with 512, 399 with 1024; 128 sequences of 1500 keys, 32 over 8 heads: 135 us
-// with 256, 126 with 512, 128 with 1024.)
-constexpr int kItemWeight = 512;
+struct ChunkCost {
+    // Weight of an item beside its keys: what beginning and ending it costs, in keys.  (A prompt
+    // of 8192 tokens: 494 us with 128, 386 with 512, 399 with 1024; 128 sequences of 1500 keys, 32 over 8 heads: 135 us
+    // with 256, 126 with 512, 128 with 1024.)
+    static constexpr int kItem = 512;
+    // short items are cut into no small parts: joining costs more than it gives (8 sequences of 50 tokens over 1000
+    // keys 29 us, cut anywhere 32); long ones anywhere (4 of 19 over 9000 keys 32 us, by fours 34)
+    static __device__ __forceinline__ int grain(int nt) { return nt >= 64 ? 1 : nt >= 16 ? 2 : 4; }
+};
 constexpr float kLazy = 8.f;                     // growth of m, in powers of two, that is left to the accumulators
 // Over 4-bit rows V is fp16 and so is P: m lies 2^7 below the maximum, so that weights reach from 2^15 down to fp16's 2^-24
 // and a long row's small ones are not lost.
 template <bool FP4>
 constexpr float kLift = FP4 ? 7.f : 0.f;
-
-// Where a share begins: an item and the number of its K / V tiles that belong
-// to earlier shares.
-struct Place {
-    int b, hk, k, cut;
-};
-
-__device__ __forceinline__ bool same_item(const Place &x, const Place &y)
-{
-    return x.b == y.b && x.hk == y.hk && x.k == y.k;
-}
-
-struct Plan {
-    int tokens;                    // tokens of a block (two tiles', or one tile's)
-    unsigned long long inverse;    // 2^64 / shares
-};
-
-// Tokens, first token and rows of a sequence.
-struct Seq {
-    int n, t0, L;
-};
-
-__device__ __forceinline__ Seq sequence(const AttnArgs &a, int b)
-{
-    Seq s;
-    s.t0 = b;
-    s.n = 1;
-    if (a.cu) {
-        s.t0 = min(max(a.cu[b], 0), a.T);
-        s.n = min(max(a.cu[b + 1], s.t0), a.T) - s.t0;
-    }
-    s.L = max(0, min(a.seqlens[b], a.capacity));
-    return s;
-}
-
-// K / V tiles [lo, hi) that the tokens of block k see; one (wholly masked) tile
-// where they see none, so that their rows are written.
-__device__ __forceinline__ void tiles_of(const AttnArgs &a, const Plan &p, const Seq &s, int k, int &lo, int &hi)
-{
-    const int first = s.L - s.n + k * p.tokens, last = s.L - s.n + min(s.n, (k + 1) * p.tokens) - 1;
-    hi = last < 0 ? 1 : last / kTile + 1;
-    lo = a.window > 0 ? min(max(0, first - a.window + 1) / kTile, hi - 1) : 0;
-}
-
-__device__ __forceinline__ int blocks_of(const Plan &p, const Seq &s) { return (s.n + p.tokens - 1) / p.tokens; }
-
-// Weight of the first k blocks of a sequence, for one head: block i weighs its
-// last key's position, bounded by the window.
-__device__ __forceinline__ long long weight(const AttnArgs &a, const Plan &p, const Seq &s, int k)
-{
-    const int first = max(0, s.L - s.n) + min(p.tokens, s.n) + kItemWeight;
-    int grow = k;
-    long long flat = 0;
-    if (a.window > 0 && a.window < kMaxLen) {
-        const int most = a.window + p.tokens + kTile + kItemWeight;
-        grow = most <= first ? 0 : min(k, (most - first) / p.tokens + 1);
-        flat = (long long)(k - grow) * most;
-    }
-    return (long long)grow * first + (long long)p.tokens * grow * (grow - 1) / 2 + flat;
-}
-
-// The place u units behind the beginning of sequence b.
-__device__ __forceinline__ Place place_in(const AttnArgs &a, const Plan &p, const Seq &s, int b, long long u)
-{
-    const int nb = blocks_of(p, s);
-    const long long each = weight(a, p, s, nb);
-    Place r{b, 0, 0, 0};
-    if (a.cache.n_kv_heads > 32) {
-        r.hk = (int)(u / each);
-        u -= r.hk * each;
-    } else {
-        for (; u >= each; u -= each)
-            ++r.hk;
-    }
-    int top = nb - 1;
-    while (r.k < top) {   // the last block that begins at or before u
-        const int mid = (r.k + top + 1) / 2;
-        if (weight(a, p, s, mid) <= u)
-            r.k = mid;
-        else
-            top = mid - 1;
-    }
-    int lo, hi;
-    tiles_of(a, p, s, r.k, lo, hi);
-    const long long begin = weight(a, p, s, r.k);
-    // short items are cut into no small parts: joining costs more than it gives (8 sequences of 50 tokens over 1000
-    // keys 29 us, cut anywhere 32); long ones anywhere (4 of 19 over 9000 keys 32 us, by fours 34)
-    const int nt = hi - lo, grain = nt >= 64 ? 1 : nt >= 16 ? 2 : 4;
-    // (half the item's own weight lies before its first tile, half behind its last)
-    const int in = (int)(u - begin) - kItemWeight / 2, keys = (int)(weight(a, p, s, r.k + 1) - begin) - kItemWeight;
-    const int x = (int)(__fdividef((float)max(in, 0), (float)keys) * nt);
-    r.cut = (x + grain / 2) / grain * grain;
-    if (r.cut >= nt) {   // the beginning of the next item
-        r.cut = 0;
-        if (++r.k == nb) {
-            r.k = 0;
-            if (++r.hk == a.cache.n_kv_heads) {
-                r.hk = 0;
-                ++r.b;
-            }
-        }
-    }
-    return r;
-}
-
-// ---- the walk over a share ---------------------------------------------------------
-struct Walk {
-    Place at, end;
-    Seq seq;
-    int loaded;   // sequence that seq describes
-};
-
-struct Segment {
-    int b, hk, k;
-    int lo, j0, j1, hi;   // K / V tiles [j0, j1) of the item's [lo, hi)
-    Seq seq;
-    int more;             // 0: the share is done
-};
-
-__device__ __forceinline__ bool next_segment(const AttnArgs &a, const Plan &p, Walk &w, Segment &s)
-{
-    for (;;) {
-        if (w.at.b > w.end.b || w.at.b >= a.B ||
-            (w.at.b == w.end.b &&
-             (w.at.hk > w.end.hk || (w.at.hk == w.end.hk && (w.at.k > w.end.k || (w.at.k == w.end.k && w.at.cut >= w.end.cut))))))
-            return false;
-        if (w.loaded != w.at.b) {
-            w.seq = sequence(a, w.at.b);
-            w.loaded = w.at.b;
-        }
-        const int nb = blocks_of(p, w.seq);
-        if (nb == 0) {
-            w.at = Place{w.at.b + 1, 0, 0, 0};
-            continue;
-        }
-        s.b = w.at.b;
-        s.hk = w.at.hk;
-        s.k = w.at.k;
-        tiles_of(a, p, w.seq, s.k, s.lo, s.hi);
-        s.j0 = s.lo + w.at.cut;
-        s.j1 = same_item(w.at, w.end) ? s.lo + w.end.cut : s.hi;
-        w.at.cut = 0;
-        if (++w.at.k == nb) {
-            w.at.k = 0;
-            if (++w.at.hk == a.cache.n_kv_heads) {
-                w.at.hk = 0;
-                ++w.at.b;
-            }
-        }
-        if (s.j1 > s.j0) {
-            s.seq = w.seq;
-            return true;
-        }
-    }
-}
 
 struct AttnShared {
     uint64_t kv_full[kAttnStages], kv_empty[kAttnStages];
@@ -240,12 +90,9 @@ struct AttnShared {
     uint64_t s_full[2], p_full[2][2], o_full[2];
     uint64_t x_full, x_empty;   // the streams' join in shared memory
     uint64_t drained, nobody[2];
-    Place bound[2];
-    Seq first;                 // the sequence that bound[0] was found in
-    int first_b;
+    Share share;
     Segment segments[kSegments];
     uint64_t seg_full[kSegments], seg_empty[kSegments];
-    long long sums[kFp4Threads / 32 + 1];
     uint32_t tmem;
     int failed;
 };
@@ -297,7 +144,7 @@ __device__ __forceinline__ void segment_done(AttnShared &sh, uint32_t n)
 // ---- the walk: one lane ------------------------------------------------------------
 __device__ __forceinline__ void walk_share(const AttnArgs &a, const Plan &plan, AttnShared &sh)
 {
-    Walk w{sh.bound[0], sh.bound[1], sh.first, sh.first_b};
+    Walk w{sh.share.bound[0], sh.share.bound[1], sh.share.first, sh.share.first_b};
     for (uint32_t n = 0;; ++n) {
         const uint32_t k = n % kSegments;
         if (n >= kSegments && !wait(sh, &sh.seg_empty[k], (n / kSegments - 1) & 1, a.status))
@@ -485,13 +332,8 @@ __device__ __forceinline__ int ring_v(int t, int nt)
 constexpr int kMaxShares = 255;   // CTAs of a launch, one for each SM
 
 // ---- workspace ----------------------------------------------------------------------
-// Places of the n + 1 bounds, then for each CTA two parts (0: of an item that began in an
-// earlier share, 1: of an item that goes on in the next) of `rows` rows: (m, l) pairs, and
-// the accumulators as [column / 4][row][4], so that a warp's rows lie side by side.
-struct Bound {
-    Place at;
-    int n, t0;   // of the place's sequence, where it is inside an item
-};
+// Of each part `rows` rows: (m, l) pairs, and the accumulators as [column / 4][row][4], so that a warp's rows lie side
+// by side.
 struct Parts {
     Bound *bound;
     float2 *ml;
@@ -1307,7 +1149,6 @@ __global__ void __launch_bounds__(FP4 ? kFp4Threads : kAttnThreads, 1)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t qbuf = smem_u32(attn_smem);   // 1024-byte aligned, as the swizzle wants it
     const uint32_t ring = qbuf + 2 * kAttnStageBytes;
-    const int Hkv = a.cache.n_kv_heads;
 
     if (tid == 0) {
         for (int s = 0; s < kStages; ++s) {
@@ -1333,8 +1174,8 @@ __global__ void __launch_bounds__(FP4 ? kFp4Threads : kAttnThreads, 1)
         mbar_init(&sh.nobody[1], 1 << 16);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         sh.failed = 0;
-        sh.bound[0] = sh.bound[1] = Place{a.B, 0, 0, 0};
-        sh.first_b = -1;
+        sh.share.bound[0] = sh.share.bound[1] = Place{a.B, 0, 0, 0};
+        sh.share.first_b = -1;
         for (const CUtensorMap *map : {&qmap, &kmap, &vmap})
             asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
     }
@@ -1346,98 +1187,15 @@ __global__ void __launch_bounds__(FP4 ? kFp4Threads : kAttnThreads, 1)
     pdl_wait();
     pdl_trigger();
 
-    // ---- this CTA's share: the sum of all weights, then the places of its two
-    //      bounds.  Up to 384 sequences stay in the threads' registers.
-    auto of_sequence = [&](int b, Seq &q) {
-        if (b >= a.B)
-            return 0ll;
-        q = sequence(a, b);
-        return Hkv * weight(a, plan, q, blocks_of(plan, q));
-    };
-    Seq mine{0, 0, 0};
-    const long long my_weight = of_sequence(tid, mine);
-    long long total = my_weight;
-    for (int b = tid + kThreads; b < a.B; b += kThreads) {
-        Seq q;
-        total += of_sequence(b, q);
-    }
-    long long up = my_weight;   // of the first round: the running sum within the warp
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, up, o);
-        if (lane >= o)
-            up += y;
-    }
-    if (a.B > kThreads) {
-#pragma unroll
-        for (int o = 16; o; o >>= 1)
-            total += __shfl_xor_sync(0xffffffffu, total, o);
-        if (lane == 0)
-            sh.sums[warp] = total;
-        __syncthreads();
-        total = 0;
-        for (int i = 0; i < kThreads / 32; ++i)
-            total += sh.sums[i];
-        __syncthreads();
-    }
-    if (lane == 31)
-        sh.sums[warp] = up;
-    __syncthreads();
-    long long off = 0, round = 0;
-#pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) {
-        const long long x = sh.sums[i];
-        off += i < warp ? x : 0;
-        round += x;
-    }
-    if (a.B <= kThreads)
-        total = round;
-    const long long share = (long long)__umul64hi((unsigned long long)total, plan.inverse) + 1;
-    const long long u0 = min(share * blockIdx.x, total), u1 = min(share * (blockIdx.x + 1), total);
-    auto find = [&](int b, const Seq &q, long long from, long long weight_of) {
-#pragma unroll 1
-        for (int k = 0; k < 2; ++k) {
-            const long long u = k ? u1 : u0;
-            if (weight_of > 0 && u >= from && u < from + weight_of) {
-                sh.bound[k] = place_in(a, plan, q, b, u - from);
-                if (k == 0) {
-                    sh.first = q;
-                    sh.first_b = b;
-                }
-            }
-        }
-    };
-    find(tid, mine, off + up - my_weight, my_weight);
-    for (int base = kThreads; base < a.B; base += kThreads) {
-        const long long before = round;
-        Seq q{0, 0, 0};
-        const long long x = of_sequence(base + tid, q);
-        up = x;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long y = __shfl_up_sync(0xffffffffu, up, o);
-            if (lane >= o)
-                up += y;
-        }
-        __syncthreads();
-        if (lane == 31)
-            sh.sums[warp] = up;
-        __syncthreads();
-        off = before;
-        for (int i = 0; i < kThreads / 32; ++i) {
-            off += i < warp ? sh.sums[i] : 0;
-            round += sh.sums[i];
-        }
-        find(base + tid, q, off + up - x, x);
-    }
+    find_share<ChunkCost, kThreads>(a, plan, sh.share);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sh.tmem;
     if (tid == 0) {
-        c.parts.bound[blockIdx.x] = Bound{sh.bound[0], sh.first.n, sh.first.t0};
+        c.parts.bound[blockIdx.x] = Bound{sh.share.bound[0], sh.share.first.n, sh.share.first.t0};
         if (blockIdx.x == gridDim.x - 1)
-            c.parts.bound[gridDim.x] = Bound{sh.bound[1], 0, 0};
+            c.parts.bound[gridDim.x] = Bound{sh.share.bound[1], 0, 0};
     }
     if (warp < kMmaWarp) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(FP4 ? kFp4SoftmaxRegs : kSoftmaxRegs));
