@@ -242,5 +242,9 @@ struct AttnArgs {
 };
 size_t chunk_attention_ws(int T, int Hq, int Hkv);
 cudaError_t launch_chunk_attention(const AttnArgs &a, cudaStream_t st);
+// over 4-bit rows, where sequences have few of them
+bool takes_rows(int T, int B, int G);
+size_t row_attention_ws();
+cudaError_t launch_row_attention(const AttnArgs &a, cudaStream_t st);
 
 }  // namespace retopk

@@ -2,6 +2,8 @@
 // append, cache copy, chunk attention): argument checks and launches.
 #include <math.h>
 
+#include <algorithm>
+
 #include "prompt.cuh"
 
 using namespace retopk;
@@ -232,7 +234,7 @@ size_t retopk_chunk_attention_workspace_bytes(int T, int B, int Hq, int Hkv)
     if (T < 0 || B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || T > kMaxTokens || B > kMaxBatch ||
         Hq > kMaxHeads || Hq / Hkv > kMaxGroup)
         return 0;
-    return chunk_attention_ws(T, Hq, Hkv);
+    return std::max(chunk_attention_ws(T, Hq, Hkv), row_attention_ws());
 }
 
 int retopk_chunk_attention(const retopk_bf16 *q, int64_t q_stride, const retopk_cache *cache,
@@ -279,6 +281,8 @@ int retopk_chunk_attention(const retopk_bf16 *q, int64_t q_stride, const retopk_
     a.scale = scale > 0.f ? scale : 1.0f / sqrtf((float)kD);
     a.softcap = softcap;
     a.ws = d_workspace;
+    if (cache->format == RETOPK_CACHE_FP4 && takes_rows(T, B, a.G))
+        return cuda_rc(launch_row_attention(a, (cudaStream_t)stream));
     return cuda_rc(launch_chunk_attention(a, (cudaStream_t)stream));
 }
 

@@ -1,0 +1,708 @@
+// row_attention.cu -- causal attention of a few query rows a sequence over a
+// 4-bit cache: single tokens of a batch, and a few drafted ones.
+//
+// Mathematics.  As in chunk_attention.cu: s_j = scale q.k_j (capped: softcap tanh(s_j / softcap)), out = sum_j exp(s_j) v_j /
+// sum_j exp(s_j) over the keys that a token sees, in one pass with a running maximum m and sum l of each row, parts
+// joined by their (m, l).
+//
+// What bounds it.  144 bytes a key and head for keys and values, and the work of making 256 codes a key into
+// numbers: each conversion gives two, at 64 lanes a cycle of an SM, so a key takes 2 cycles of that pipe where the
+// memory takes 6.  The matrix work is small (rows: a group's query heads, times the tokens), so it is done
+// by warps (mma.sync), in the transposed form whose rows are the keys: then 8 columns hold 8 query rows, codes become operands
+// in the registers that they were loaded to, and nothing is written to shared memory but what the copies bring.
+//   S^T = K Q^T     a lane's 32 codes of a key, 16 bytes, are its part of 8 steps of the contraction
+//   O^T = V^T P^T   a lane's 16 codes of four keys, one scale block each; codes of two keys are brought side by side
+//                   four bits at a time before they are converted; P^T is a transposed 8 x 8 of half words
+// A warp takes 32 keys of every 128, with a ring of its own: copies bring 32 keys' codes and scales two tiles ahead.  Four
+// warps are a CTA, so that one CTA's end of an item lies beside the others' work.
+//
+// Rounding.  Code times scale is exact in fp16.  A query row is brought to fp16's range by a power of two, so
+// its elements are exact down to 2^-28 of the largest.  P is rounded to fp16 (m lies 2^7 below the maximum when
+// it is taken and is raised when that has grown by 2^8 more, so weights reach from 2^15 down to 2^-24).  All else has 32 bits.
+#include <math.h>
+
+#include <algorithm>
+
+#include "attention_plan.cuh"
+
+namespace retopk {
+
+namespace {
+
+constexpr int kRowWarps = 4, kRowThreads = kRowWarps * 32;
+constexpr int kWarpKeys = kTile / kRowWarps;
+constexpr int kRowStages = 3;                                  // tiles of a warp's ring
+constexpr int kCodeBytes = kWarpKeys * kD / 2, kScaleBytes = kWarpKeys * kFp4Scales;
+constexpr int kStageBytes = 2 * (kCodeBytes + kScaleBytes);    // K's codes, V's codes, K's scales, V's scales
+constexpr int kSumRow = kD + 4;                                // floats of a row where the warps' sums meet
+constexpr float kLift = 7.f, kLazy = 8.f;                      // as in chunk_attention.cu
+constexpr int kMaxRowShares = 1024;
+
+// CTAs of an SM, by the tiles of 8 query rows.
+__host__ __device__ constexpr int row_blocks(int nt) { return nt == 1 ? 4 : 3; }
+
+struct RowCost {
+    static constexpr int kItem = 256;
+    static __device__ __forceinline__ int grain(int nt) { return nt > 8 ? 1 : 8; }
+};
+
+// Parts of items, as in attention_plan.cuh, of `rows` rows: (m, l) pairs, and 128 sums a row.
+struct RowParts {
+    Bound *bound;
+    float2 *ml;
+    float *o;
+    int rows;
+};
+
+struct RowLaunch {
+    AttnArgs a;
+    Plan plan;
+    RowParts parts;
+    int step_pages, step_rows;   // pages and rows that a tile's keys are on from the last one's
+};
+
+template <int NT>
+struct RowShared {
+    Share share;
+    Walk walk;
+    Segment segments[2];
+    float2 ml[kRowWarps][8 * NT];
+};
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float rcp(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t mul_halves(uint32_t a, uint32_t b)
+{
+    uint32_t d;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+__device__ __forceinline__ void mma_f16_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                              uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transposed(uint32_t x)
+{
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+__device__ __forceinline__ void lds128(uint32_t addr, uint32_t (&w)[4])
+{
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(addr));
+}
+__device__ __forceinline__ void lds64(uint32_t addr, uint32_t (&w)[2])
+{
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t addr)
+{
+    uint32_t x;
+    asm volatile("{\n .reg .u16 h;\n ld.shared.u16 h, [%1];\n cvt.u32.u16 %0, h;\n}\n" : "=r"(x) : "r"(addr));
+    return x;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t addr)
+{
+    uint32_t x;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(x) : "r"(addr));
+    return x;
+}
+// Bytes that are there, zeros where they are not.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void *src, bool there)
+{
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(there ? 8 : 0) : "memory");
+}
+
+// tanh(y), |y| < 1/2 by the polynomial of chunk_attention.cu (6.4e-7 of the value).
+__device__ __forceinline__ float tanh_of(float y)
+{
+    const float t = y * y;
+    const float small = y * fmaf(fmaf(fmaf(-0.04475064703577332f, t, 0.132053598066859f), t, -0.3332815934197915f), t, 1.f);
+    const float large = fmaf(-2.f, rcp(1.f + ex2(y * 2.885390081777927f)), 1.f);
+    return fabsf(y) < 0.5f ? small : large;
+}
+
+}  // namespace
+
+template <int NT, bool CAP>
+__global__ void __launch_bounds__(kRowThreads, row_blocks(NT)) row_attention_kernel(const __grid_constant__ RowLaunch c)
+{
+    extern __shared__ __align__(16) unsigned char row_smem[];
+    RowShared<NT> &sh = *reinterpret_cast<RowShared<NT> *>(row_smem + kRowWarps * kRowStages * kStageBytes);
+    const AttnArgs &a = c.a;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3, G = a.G;
+    const uint32_t ring = smem_u32(row_smem) + warp * kRowStages * kStageBytes;
+    if (tid == 0) {
+        sh.share.bound[0] = sh.share.bound[1] = Place{a.B, 0, 0, 0};
+        sh.share.first_b = -1;
+    }
+    pdl_wait();
+    pdl_trigger();
+    find_share<RowCost, kRowThreads>(a, c.plan, sh.share);
+    __syncthreads();
+    if (tid == 0) {
+        c.parts.bound[blockIdx.x] = Bound{sh.share.bound[0], sh.share.first.n, sh.share.first.t0};
+        if (blockIdx.x == gridDim.x - 1)
+            c.parts.bound[gridDim.x] = Bound{sh.share.bound[1], 0, 0};
+        sh.walk = Walk{sh.share.bound[0], sh.share.bound[1], sh.share.first, sh.share.first_b};
+        sh.segments[0].more = next_segment(a, c.plan, sh.walk, sh.segments[0]);
+    }
+    // Keys of a group of 16, by the number of the matrix' row: of rows 2 i and 2 i + 1 the first four and the second, so
+    // that what 8 lanes (keys), or 16 (values), load lies in different banks
+    auto key_of = [](int r) { return (r & 1 ? ((r >> 1 & 3) ^ 1) + 4 : r >> 1 & 3) + (r & 8); };
+    const uint32_t k_at = key_of(g) * (kD / 2) + t4 * 16, ks_at = 2 * kCodeBytes + key_of(g) * kFp4Scales + t4 * 2;
+    // values: the 16-byte pieces of keys 2, 3 of every four change places by two
+    const uint32_t v_at = kCodeBytes + ((g >> 1 ^ (t4 >> 1) << 1) << 4) + (g & 1) * 8;
+    const uint32_t va = key_of(2 * t4) * (kD / 2) + v_at, vb = key_of(2 * t4 + 1) * (kD / 2) + v_at;
+    const uint32_t vs_at = 2 * kCodeBytes + kScaleBytes + g;
+    const uint32_t vsa = key_of(2 * t4) * kFp4Scales + vs_at, vsb = key_of(2 * t4 + 1) * kFp4Scales + vs_at;
+
+    for (int n = 0;; ++n) {
+        __syncthreads();   // the segment is known, and the sums of the one before have been read
+        const Segment &s = sh.segments[n & 1];
+        if (!s.more)
+            break;
+        const int nt = s.j1 - s.j0, L = s.seq.L, tok0 = s.k * c.plan.tokens, tokens = min(c.plan.tokens, s.seq.n - tok0);
+        const int first = L - s.seq.n + tok0, last = first + tokens - 1;   // positions of the tokens
+        const int low = a.window > 0 ? first - a.window + 1 : 0;           // the first key that one sees
+        const int pos0 = s.j0 * kTile + warp * kWarpKeys;
+
+        // ---- the copies: this warp's keys of a tile.  Pages are looked up a tile ahead.
+        int index = 0, row = pos0;       // of tile `look` ahead: its place in the table, the row in that page
+        if (a.cache.table) {
+            index = pos0 / a.cache.page_rows;
+            row = pos0 % a.cache.page_rows;
+        }
+        int page[2], at[2];              // of the next tile, for each 16 keys: page, row in it
+        bool asked[2];                   // it has keys to be read
+        auto look = [&](int t) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int pos = pos0 + t * kTile + 16 * i;
+                int x = index, r = row + 16 * i;
+                if (a.cache.table && r >= a.cache.page_rows) {
+                    r -= a.cache.page_rows;
+                    ++x;
+                }
+                at[i] = r;
+                asked[i] = t < nt && pos < L && pos <= last && pos + 15 >= low;
+                page[i] = s.b;
+                if (asked[i] && a.cache.table)
+                    page[i] = a.cache.table[(long long)s.b * a.cache.table_width + x];
+            }
+            index += c.step_pages;
+            row += c.step_rows;
+            if (a.cache.table && row >= a.cache.page_rows) {
+                row -= a.cache.page_rows;
+                ++index;
+            }
+        };
+        uint32_t to = ring;
+        auto issue = [&](int t) {
+            if (t < nt) {
+                const int left = L - (pos0 + t * kTile);
+                long long from[2];
+                bool there[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    there[i] = asked[i] && (uint32_t)page[i] < (uint32_t)a.cache.n_pages;
+                    if (asked[i] && !there[i] && a.status)
+                        atomicOr(a.status, RETOPK_STATUS_BAD_PAGE);
+                    from[i] = there[i] ? ((long long)page[i] * a.cache.n_kv_heads + s.hk) * a.cache.page_rows + at[i] : 0;
+                }
+                const int piece = lane & 3, swapped = piece ^ (lane >> 3 & 1) << 1;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = 8 * i + g;
+                    const bool ok = there[i / 2] && r < left;
+                    const long long x = ok ? (from[i / 2] + (r & 15)) * (kD / 2) + piece * 16 : 0;
+                    copy_async<16>(to + r * (kD / 2) + piece * 16, static_cast<const char *>(a.cache.k) + x, ok);
+                    copy_async<16>(to + kCodeBytes + r * (kD / 2) + swapped * 16, static_cast<const char *>(a.cache.v) + x, ok);
+                }
+                const bool ok = (lane >> 4 ? there[1] : there[0]) && lane < left;
+                const long long x = ok ? ((lane >> 4 ? from[1] : from[0]) + (lane & 15)) * kFp4Scales : 0;
+                copy_async<8>(to + 2 * kCodeBytes + lane * kFp4Scales, a.cache.k_scale + x, ok);
+                copy_async<8>(to + 2 * kCodeBytes + kScaleBytes + lane * kFp4Scales, a.cache.v_scale + x, ok);
+                look(t + 1);
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            to = to + kStageBytes == ring + kRowStages * kStageBytes ? ring : to + kStageBytes;
+        };
+        look(0);
+#pragma unroll
+        for (int t = 0; t < kRowStages - 1; ++t)
+            issue(t);
+        if (tid == 0)
+            sh.segments[(n + 1) & 1].more = next_segment(a, c.plan, sh.walk, sh.segments[(n + 1) & 1]);
+
+        // ---- the queries: column g of each 8, this lane's 32 elements, as fp16 of at most 2^15
+        uint32_t q[NT][16];
+        float factor[NT][2];             // of a column's scores: in powers of two, or over the cap
+        int hi[NT][2];                   // the last key that a column sees
+#pragma unroll
+        for (int x = 0; x < NT; ++x) {
+            const int r = 8 * x + g, tok = r / G;
+            uint32_t w[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                w[i] = 0;
+            if (tok < tokens) {
+                const uint4 *src = reinterpret_cast<const uint4 *>(a.q + (long long)(s.seq.t0 + tok0 + tok) * a.q_stride +
+                                                                   (s.hk * G + r % G) * kD + t4 * 32);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint4 y = src[i];
+                    w[4 * i] = y.x, w[4 * i + 1] = y.y, w[4 * i + 2] = y.z, w[4 * i + 3] = y.w;
+                }
+            }
+            uint32_t top = 0;
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                top = max(top, max(w[i] << 16 & 0x7fffffffu, w[i] & 0x7fff0000u));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const int e = top == 0 ? 0 : max((int)(top >> 23) - 127 - 14, -100);
+            const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                q[x][i] = f16x2(bf16lo(w[i]) * down, bf16hi(w[i]) * down);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int col = 2 * t4 + k;
+                const float up = __uint_as_float((uint32_t)(127 + __shfl_sync(0xffffffffu, e, col * 4)) << 23);
+                factor[x][k] = CAP ? fminf(a.scale * up / a.softcap, 3e38f) : a.scale * 1.4426950408889634f * up;
+                hi[x][k] = min(first + (8 * x + col) / G, last);
+            }
+        }
+
+        // ---- the tiles
+        float o[NT][8][4], m[NT][2], l[NT][2];
+#pragma unroll
+        for (int x = 0; x < NT; ++x) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                o[x][j][0] = o[x][j][1] = o[x][j][2] = o[x][j][3] = 0.f;
+            m[x][0] = m[x][1] = -INFINITY;
+            l[x][0] = l[x][1] = 0.f;
+        }
+        uint32_t from = ring;
+        for (int t = 0; t < nt; ++t) {
+            issue(t + kRowStages - 1);
+            asm volatile("cp.async.wait_group %0;" ::"n"(kRowStages - 1) : "memory");
+            __syncwarp();
+            const int pos = pos0 + t * kTile;
+            if (pos <= last && pos + kWarpKeys > low) {
+                float sc[2][NT][4];
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+#pragma unroll
+                    for (int x = 0; x < NT; ++x)
+                        sc[half][x][0] = sc[half][x][1] = sc[half][x][2] = sc[half][x][3] = 0.f;
+                    const uint32_t base = from + half * 16 * (kD / 2), sbase = from + half * 16 * kFp4Scales;
+                    uint32_t w0[4], w1[4];
+                    lds128(base + k_at, w0);
+                    lds128(base + k_at + 8 * (kD / 2), w1);
+                    const uint32_t s0 = lds16(sbase + ks_at), s1 = lds16(sbase + ks_at + 8 * kFp4Scales);
+                    const uint32_t s0a = (s0 & 255u) * 0x00800080u, s0b = (s0 >> 8) * 0x00800080u;   // fp16, twice
+                    const uint32_t s1a = (s1 & 255u) * 0x00800080u, s1b = (s1 >> 8) * 0x00800080u;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t h0[4], h1[4];
+                        e2m1x8_halves(w0[i], h0);
+                        e2m1x8_halves(w1[i], h1);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            h0[k] = mul_halves(h0[k], i < 2 ? s0a : s0b);
+                            h1[k] = mul_halves(h1[k], i < 2 ? s1a : s1b);
+                        }
+#pragma unroll
+                        for (int x = 0; x < NT; ++x) {
+                            mma_f16_16816(sc[half][x], h0[0], h1[0], h0[1], h1[1], q[x][4 * i], q[x][4 * i + 1]);
+                            mma_f16_16816(sc[half][x], h0[2], h1[2], h0[3], h1[3], q[x][4 * i + 2], q[x][4 * i + 3]);
+                        }
+                    }
+                }
+                // scores in powers of two; hidden ones -inf
+                const bool part = pos + kWarpKeys - 1 > first || (a.window > 0 && pos < last - a.window + 1);
+                float top[NT][2];
+                bool grow = false;
+#pragma unroll
+                for (int x = 0; x < NT; ++x) {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        top[x][k] = -INFINITY;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            float &z = sc[i >> 1][x][(i & 1) * 2 + k];
+                            z *= factor[x][k];
+                            if (CAP)
+                                z = tanh_of(z) * (a.softcap * 1.4426950408889634f);
+                            if (part) {
+                                const int key = pos + (i >> 1) * 16 + key_of(g) + (i & 1) * 8;
+                                if (key > hi[x][k] || (a.window > 0 && key <= hi[x][k] - a.window))
+                                    z = -INFINITY;
+                            }
+                            top[x][k] = fmaxf(top[x][k], z);
+                        }
+                        grow |= top[x][k] > m[x][k] + (kLift + kLazy);
+                    }
+                }
+                if (__any_sync(0xffffffffu, grow)) {   // every column up to its maximum, and the sums with it
+#pragma unroll
+                    for (int x = 0; x < NT; ++x) {
+                        float down[2];
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            float y = top[x][k];
+#pragma unroll
+                            for (int d = 4; d < 32; d *= 2)
+                                y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, d));
+                            y = fmaxf(m[x][k], y - kLift);
+                            down[k] = m[x][k] == -INFINITY ? 1.f : ex2(m[x][k] - y);
+                            m[x][k] = y;
+                            l[x][k] *= down[k];
+                        }
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                o[x][j][e] *= down[e & 1];
+                    }
+                }
+                uint32_t p[2][NT][2];
+#pragma unroll
+                for (int x = 0; x < NT; ++x) {
+                    const float b0 = m[x][0] == -INFINITY ? 0.f : m[x][0], b1 = m[x][1] == -INFINITY ? 0.f : m[x][1];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float y0 = ex2(sc[i >> 1][x][(i & 1) * 2] - b0), y1 = ex2(sc[i >> 1][x][(i & 1) * 2 + 1] - b1);
+                        l[x][0] += y0;
+                        l[x][1] += y1;
+                        p[i >> 1][x][i & 1] = transposed(f16x2(y0, y1));
+                    }
+                }
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const uint32_t base = from + half * 16 * (kD / 2), sbase = from + half * 16 * kFp4Scales;
+                    uint32_t wa[2], wb[2], wc[2], wd[2];
+                    lds64(base + va, wa);
+                    lds64(base + vb, wb);
+                    lds64(base + va + 8 * (kD / 2), wc);
+                    lds64(base + vb + 8 * (kD / 2), wd);
+                    const uint32_t s0 = lds8(sbase + vsa) << 7 | lds8(sbase + vsb) << 23;
+                    const uint32_t s1 = lds8(sbase + vsa + 8 * kFp4Scales) << 7 | lds8(sbase + vsb + 8 * kFp4Scales) << 23;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        constexpr uint32_t kLow = 0x0f0f0f0fu;
+                        uint32_t h[4][4];   // elements 0, 2, 4, 6 of the word of keys a and b; 1, 3, 5, 7; the same of c and d
+                        e2m1x8_halves((wa[i] & kLow) | (wb[i] << 4 & ~kLow), h[0]);
+                        e2m1x8_halves((wa[i] >> 4 & kLow) | (wb[i] & ~kLow), h[1]);
+                        e2m1x8_halves((wc[i] & kLow) | (wd[i] << 4 & ~kLow), h[2]);
+                        e2m1x8_halves((wc[i] >> 4 & kLow) | (wd[i] & ~kLow), h[3]);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+#pragma unroll
+                            for (int y = 0; y < 4; ++y)
+                                h[y][k] = mul_halves(h[y][k], y < 2 ? s0 : s1);
+#pragma unroll
+                            for (int x = 0; x < NT; ++x)
+                                mma_f16_16816(o[x][4 * i + k], h[0][k], h[1][k], h[2][k], h[3][k], p[half][x][0], p[half][x][1]);
+                        }
+                    }
+                }
+            }
+            __syncwarp();   // all lanes have read the tile
+            from = from + kStageBytes == ring + kRowStages * kStageBytes ? ring : from + kStageBytes;
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncwarp();
+
+        // ---- the warps' sums meet in shared memory: element 16 g + 2 j + e of a row at 16 j + 2 g + e
+        float *sums = reinterpret_cast<float *>(row_smem + warp * kRowStages * kStageBytes);
+        static_assert(8 * NT * kSumRow * 4 <= kRowStages * kStageBytes, "in the warp's ring");
+#pragma unroll
+        for (int x = 0; x < NT; ++x) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                float *dst = sums + (8 * x + 2 * t4 + k) * kSumRow + 2 * g;
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    *reinterpret_cast<float2 *>(dst + 16 * j) = make_float2(o[x][j][k], o[x][j][2 + k]);
+#pragma unroll
+                for (int d = 4; d < 32; d *= 2)
+                    l[x][k] += __shfl_xor_sync(0xffffffffu, l[x][k], d);
+                if (g == 0)
+                    sh.ml[warp][8 * x + 2 * t4 + k] = make_float2(m[x][k], l[x][k]);
+            }
+        }
+        __syncthreads();
+        const bool whole = s.j0 == s.lo && s.j1 == s.hi;
+        const size_t part = 2 * blockIdx.x + (s.j0 == s.lo);
+        for (int i = tid; i < tokens * G * (kD / 2); i += kRowThreads) {
+            const int r = i / (kD / 2), x = i % (kD / 2);
+            float mm = -INFINITY, ll = 0.f;
+#pragma unroll
+            for (int w = 0; w < kRowWarps; ++w)
+                mm = fmaxf(mm, sh.ml[w][r].x);
+            const float zero = mm == -INFINITY ? 0.f : mm;
+            float2 y = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < kRowWarps; ++w) {
+                const float2 ml = sh.ml[w][r];
+                const float f = ex2(ml.x - zero);
+                const float2 v = *reinterpret_cast<const float2 *>(row_smem + w * kRowStages * kStageBytes +
+                                                                   4 * (r * kSumRow + 16 * (x & 7) + 2 * (x >> 3)));
+                ll = fmaf(ml.y, f, ll);
+                y.x = fmaf(v.x, f, y.x);
+                y.y = fmaf(v.y, f, y.y);
+            }
+            if (whole) {
+                const size_t t = s.seq.t0 + tok0 + r / G;
+                const int head = s.hk * G + r % G;
+                const float inv = ll == 0.f ? 0.f : 1.f / ll;
+                *reinterpret_cast<uint32_t *>(a.out + t * a.out_stride + head * kD + 2 * x) = bf16x2(y.x * inv, y.y * inv);
+                if (a.lse && x == 0)
+                    a.lse[t * a.Hq + head] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * 0.6931471805599453f;
+            } else {
+                *reinterpret_cast<float2 *>(c.parts.o + (part * c.parts.rows + r) * kD + 2 * x) = y;
+                if (x == 0)
+                    c.parts.ml[part * c.parts.rows + r] = make_float2(mm, ll);
+            }
+        }
+    }
+}
+
+// Joins the parts of an item.  BY_ITEM, for few items: the grid's columns are the cut items, in order; else they are the
+// bounds, and the first that cuts an item has it.  One, two, four or eight warps take a row and share out its parts.
+template <bool BY_ITEM>
+__global__ void __launch_bounds__(256) row_join_kernel(const __grid_constant__ RowLaunch c, int shares)
+{
+    __shared__ float4 sum[8][32];
+    __shared__ float2 ml_of[8];
+    __shared__ uint16_t list[kMaxRowShares + 1];
+    __shared__ int counts[8], found;
+    pdl_wait();
+    pdl_trigger();
+    const AttnArgs &a = c.a;
+    const Bound *const bound = c.parts.bound;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    // flags before this thread's, and all of them
+    auto rank = [&](bool flag, int &total) {
+        const uint32_t votes = __ballot_sync(0xffffffffu, flag);
+        __syncthreads();
+        if (lane == 0)
+            counts[warp] = __popc(votes);
+        __syncthreads();
+        int before = __popc(votes & ((1u << lane) - 1));
+        total = 0;
+        for (int w = 0; w < 8; ++w) {
+            before += w < warp ? counts[w] : 0;
+            total += counts[w];
+        }
+        return before;
+    };
+    // bound i is the first that cuts its item
+    auto cuts = [&](int i) {
+        if (i < 1 || i >= shares)
+            return false;
+        const Place p = bound[i].at, before = bound[i - 1].at;
+        return p.cut > 0 && !(same_item(p, before) && before.cut > 0);
+    };
+    int x = blockIdx.x + 1;
+    if constexpr (BY_ITEM) {
+        if (tid == 0)
+            found = 0;
+        int done = 0;
+        for (int base = 1; base < shares && done <= (int)blockIdx.x; base += 256) {
+            const bool flag = cuts(base + tid);
+            int here;
+            if (rank(flag, here) + done == (int)blockIdx.x && flag)
+                found = base + tid;
+            done += here;
+        }
+        __syncthreads();
+        x = found;
+        if (x == 0)
+            return;
+    } else if (!cuts(x)) {
+        return;
+    }
+    // parts: share x - 1's part 1, then part 0 of shares x, x + 1, ... while they begin in the item (a
+    // share between two equal cuts has none)
+    const Bound here = bound[x];
+    const Place at = here.at;
+    int n = 1;
+    if (tid == 0)
+        list[0] = (uint16_t)(2 * (x - 1) + 1);
+    for (int base = x; base < shares; base += 256) {
+        const int i = base + tid;
+        bool in = false;
+        if (i < shares) {
+            const Place p = bound[i].at, next = bound[i + 1].at;
+            in = same_item(p, at) && (!same_item(next, at) || next.cut > p.cut);
+        }
+        int more;
+        const int slot = n + rank(in, more);
+        if (in)
+            list[slot] = (uint16_t)(2 * i);
+        n += more;
+        if (!same_item(bound[min(base + 256, shares)].at, at))
+            break;
+    }
+    __syncthreads();
+    const int first = at.k * c.plan.tokens, rows = min(c.plan.tokens, here.n - first) * a.G;
+    int crew = 1;   // warps of a row
+    while (crew < 8 && 4 * crew < n && 2 * crew * rows <= 8 * (int)gridDim.y)
+        crew *= 2;
+    const int mate = warp % crew, step = 8 / crew;   // rows of the block at a time
+    for (int base = blockIdx.y * step; base < rows; base += gridDim.y * step) {
+        const int r = base + warp / crew;
+        const bool real = r < rows;
+        float m = -INFINITY, l = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        auto add = [&](float m2, float l2, float4 o) {
+            const float mm = fmaxf(m, m2), zero = mm == -INFINITY ? 0.f : mm;
+            const float f1 = ex2(m - zero), f2 = ex2(m2 - zero);
+            l = l * f1 + l2 * f2;
+            acc.x = fmaf(acc.x, f1, o.x * f2);
+            acc.y = fmaf(acc.y, f1, o.y * f2);
+            acc.z = fmaf(acc.z, f1, o.z * f2);
+            acc.w = fmaf(acc.w, f1, o.w * f2);
+            m = mm;
+        };
+#pragma unroll 1
+        for (int i0 = mate; i0 < n && real; i0 += 4 * crew) {   // four parts on their way at once
+            float2 ml[4];
+            float4 o[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int i = i0 + k * crew;
+                ml[k] = make_float2(-INFINITY, 0.f);
+                o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (i < n) {
+                    const size_t part = list[i];
+                    ml[k] = c.parts.ml[part * c.parts.rows + r];
+                    o[k] = reinterpret_cast<const float4 *>(c.parts.o + (part * c.parts.rows + r) * kD)[lane];
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                add(ml[k].x, ml[k].y, o[k]);
+        }
+        if (crew > 1) {
+            sum[warp][lane] = acc;
+            if (lane == 0)
+                ml_of[warp] = make_float2(m, l);
+            __syncthreads();
+            if (mate == 0)
+#pragma unroll 1
+                for (int i = 1; i < crew; ++i)
+                    add(ml_of[warp + i].x, ml_of[warp + i].y, sum[warp + i][lane]);
+            __syncthreads();
+        }
+        if (mate != 0 || !real)
+            continue;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const size_t t = here.t0 + first + r / a.G;
+        const int h = at.hk * a.G + r % a.G;
+        *reinterpret_cast<uint2 *>(a.out + t * a.out_stride + h * kD + lane * 4) =
+            make_uint2(bf16x2(acc.x * inv, acc.y * inv), bf16x2(acc.z * inv, acc.w * inv));
+        if (a.lse && lane == 0)
+            a.lse[t * a.Hq + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+    }
+}
+
+// ---- host side ----------------------------------------------------------------
+static size_t carve(int nt, char *ws, RowParts *p)
+{
+    const int n = std::min(sm_count() * row_blocks(nt), kMaxRowShares), rows = 8 * nt;
+    const size_t o_ml = ((n + 1) * sizeof(Bound) + 255) / 256 * 256;
+    const size_t o_o = o_ml + (2 * n * (size_t)rows * sizeof(float2) + 255) / 256 * 256;
+    if (p) {
+        p->bound = reinterpret_cast<Bound *>(ws);
+        p->ml = reinterpret_cast<float2 *>(ws + o_ml);
+        p->o = reinterpret_cast<float *>(ws + o_o);
+        p->rows = rows;
+    }
+    return o_o + 2 * n * (size_t)rows * kD * sizeof(float);
+}
+
+size_t row_attention_ws() { return std::max(carve(1, nullptr, nullptr), carve(2, nullptr, nullptr)); }
+
+// Up to 16 rows a sequence and KV head on average.
+bool takes_rows(int T, int B, int G) { return (long long)T * G <= 16ll * B; }
+
+template <int NT>
+static cudaError_t launch_rows(const AttnArgs &a, cudaStream_t st)
+{
+    RowLaunch c{};
+    c.a = a;
+    const int Hkv = a.cache.n_kv_heads;
+    c.plan.tokens = 8 * NT / a.G;
+    const long long items = std::min<long long>(a.T, a.T / c.plan.tokens + a.B) * Hkv;   // at most
+    int n = std::min(sm_count() * row_blocks(NT), kMaxRowShares);
+    const bool cuts = a.capacity > 8 * kTile;   // shorter items are not cut
+    if (!cuts)
+        n = (int)std::min<long long>(n, items);
+    c.plan.inverse = ~0ull / (unsigned long long)n;
+    carve(NT, static_cast<char *>(a.ws), &c.parts);
+    c.step_rows = kTile;
+    if (a.cache.table) {
+        c.step_pages = kTile / a.cache.page_rows;
+        c.step_rows = kTile % a.cache.page_rows;
+    }
+    const size_t smem = kRowWarps * kRowStages * kStageBytes + sizeof(RowShared<NT>);
+    cudaError_t e = launch_pdl(a.softcap > 0.f ? row_attention_kernel<NT, true> : row_attention_kernel<NT, false>, dim3(n),
+                               dim3(kRowThreads), smem, st, 1, c);
+    if (e != cudaSuccess || n < 2 || !cuts)
+        return e;
+    if (items <= sm_count())
+        return launch_pdl(row_join_kernel<true>, dim3((int)std::min<long long>(n - 1, items), 8 * NT), dim3(256), 0, st, 1, c, n);
+    return launch_pdl(row_join_kernel<false>, dim3(n - 1), dim3(256), 0, st, 1, c, n);
+}
+
+cudaError_t launch_row_attention(const AttnArgs &a, cudaStream_t st)
+{
+    return a.G <= 8 && (long long)a.T * a.G <= 8ll * a.B ? launch_rows<1>(a, st) : launch_rows<2>(a, st);
+}
+
+cudaError_t configure_row_attention()
+{
+    cudaError_t e = cudaSuccess;
+    auto set = [&](const void *f, size_t shared) {
+        const size_t smem = kRowWarps * kRowStages * kStageBytes + shared;
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(f, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    };
+    set((const void *)row_attention_kernel<1, false>, sizeof(RowShared<1>));
+    set((const void *)row_attention_kernel<1, true>, sizeof(RowShared<1>));
+    set((const void *)row_attention_kernel<2, false>, sizeof(RowShared<2>));
+    set((const void *)row_attention_kernel<2, true>, sizeof(RowShared<2>));
+    return e;
+}
+
+}  // namespace retopk
