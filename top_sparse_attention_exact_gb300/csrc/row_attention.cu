@@ -83,6 +83,13 @@ __device__ __forceinline__ float rcp(float x)
     return y;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 __device__ __forceinline__ uint32_t mul_halves(uint32_t a, uint32_t b)
 {
     uint32_t d;
@@ -125,14 +132,15 @@ __device__ __forceinline__ uint32_t lds8(uint32_t addr)
     asm volatile("ld.shared.u8 %0, [%1];" : "=r"(x) : "r"(addr));
     return x;
 }
-// Bytes that are there, zeros where they are not.
-template <int BYTES>
-__device__ __forceinline__ void copy_async(uint32_t dst, const void *src, bool there)
+template <int OFFSET>
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src)
 {
-    if constexpr (BYTES == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(there ? 8 : 0) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0 + %2], [%1 + %2], 16;" ::"r"(dst), "l"(src), "n"(OFFSET) : "memory");
+}
+// Eight bytes, or zeros.
+__device__ __forceinline__ void copy8(uint32_t dst, const void *src, bool there)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(there ? 8 : 0) : "memory");
 }
 
 // tanh(y), |y| < 1/2 by the polynomial of chunk_attention.cu (6.4e-7 of the value).
@@ -176,6 +184,7 @@ __global__ void __launch_bounds__(kRowThreads, row_blocks(NT)) row_attention_ker
     // values: the 16-byte pieces of keys 2, 3 of every four change places by two
     const uint32_t v_at = kCodeBytes + ((g >> 1 ^ (t4 >> 1) << 1) << 4) + (g & 1) * 8;
     const uint32_t va = key_of(2 * t4) * (kD / 2) + v_at, vb = key_of(2 * t4 + 1) * (kD / 2) + v_at;
+    const uint32_t code_from = lane * 16, v_to = kCodeBytes + (g * 4 + (t4 ^ (g >> 1 & 1) << 1)) * 16;   // of the copies
     const uint32_t vs_at = 2 * kCodeBytes + kScaleBytes + g;
     const uint32_t vsa = key_of(2 * t4) * kFp4Scales + vs_at, vsb = key_of(2 * t4 + 1) * kFp4Scales + vs_at;
 
@@ -223,7 +232,7 @@ __global__ void __launch_bounds__(kRowThreads, row_blocks(NT)) row_attention_ker
         auto issue = [&](int t) {
             if (t < nt) {
                 const int left = L - (pos0 + t * kTile);
-                long long from[2];
+                long long from[2];   // rows
                 bool there[2];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
@@ -232,19 +241,32 @@ __global__ void __launch_bounds__(kRowThreads, row_blocks(NT)) row_attention_ker
                         atomicOr(a.status, RETOPK_STATUS_BAD_PAGE);
                     from[i] = there[i] ? ((long long)page[i] * a.cache.n_kv_heads + s.hk) * a.cache.page_rows + at[i] : 0;
                 }
-                const int piece = lane & 3, swapped = piece ^ (lane >> 3 & 1) << 1;
+                // rows that are not there keep what codes the place held, and get scales of zero
+                constexpr int kEight = 8 * (kD / 2);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r = 8 * i + g;
-                    const bool ok = there[i / 2] && r < left;
-                    const long long x = ok ? (from[i / 2] + (r & 15)) * (kD / 2) + piece * 16 : 0;
-                    copy_async<16>(to + r * (kD / 2) + piece * 16, static_cast<const char *>(a.cache.k) + x, ok);
-                    copy_async<16>(to + kCodeBytes + r * (kD / 2) + swapped * 16, static_cast<const char *>(a.cache.v) + x, ok);
+                for (int i = 0; i < 2; ++i) {
+                    const char *k = static_cast<const char *>(a.cache.k) + from[i] * (kD / 2) + code_from;
+                    const char *v = static_cast<const char *>(a.cache.v) + from[i] * (kD / 2) + code_from;
+                    if (there[i] && 16 * i + 16 <= left) {
+                        copy16<0>(to + 2 * i * kEight + code_from, k);
+                        copy16<kEight>(to + 2 * i * kEight + code_from, k);
+                        copy16<0>(to + 2 * i * kEight + v_to, v);
+                        copy16<kEight>(to + 2 * i * kEight + v_to, v);
+                    } else if (there[i]) {
+                        if (16 * i + g < left) {
+                            copy16<0>(to + 2 * i * kEight + code_from, k);
+                            copy16<0>(to + 2 * i * kEight + v_to, v);
+                        }
+                        if (16 * i + 8 + g < left) {
+                            copy16<kEight>(to + 2 * i * kEight + code_from, k);
+                            copy16<kEight>(to + 2 * i * kEight + v_to, v);
+                        }
+                    }
                 }
                 const bool ok = (lane >> 4 ? there[1] : there[0]) && lane < left;
                 const long long x = ok ? ((lane >> 4 ? from[1] : from[0]) + (lane & 15)) * kFp4Scales : 0;
-                copy_async<8>(to + 2 * kCodeBytes + lane * kFp4Scales, a.cache.k_scale + x, ok);
-                copy_async<8>(to + 2 * kCodeBytes + kScaleBytes + lane * kFp4Scales, a.cache.v_scale + x, ok);
+                copy8(to + 2 * kCodeBytes + lane * kFp4Scales, a.cache.k_scale + x, ok);
+                copy8(to + 2 * kCodeBytes + kScaleBytes + lane * kFp4Scales, a.cache.v_scale + x, ok);
                 look(t + 1);
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
@@ -292,10 +314,15 @@ __global__ void __launch_bounds__(kRowThreads, row_blocks(NT)) row_attention_ker
             for (int k = 0; k < 2; ++k) {
                 const int col = 2 * t4 + k;
                 const float up = __uint_as_float((uint32_t)(127 + __shfl_sync(0xffffffffu, e, col * 4)) << 23);
-                factor[x][k] = CAP ? fminf(a.scale * up / a.softcap, 3e38f) : a.scale * 1.4426950408889634f * up;
+                // (never zero, as a hidden score is -inf and has to stay so)
+                factor[x][k] = CAP ? fminf(a.scale * up / a.softcap, 3e38f) : fmaxf(a.scale * 1.4426950408889634f * up, 1e-38f);
                 hi[x][k] = min(first + (8 * x + col) / G, last);
             }
         }
+
+        // what the scores that the softmax sees are multiplied by, to be in powers of two
+        const float cap2 = fmaxf(a.softcap * 1.4426950408889634f, 1e-38f);
+        auto unit = [&](int x, int k) { return CAP ? cap2 : factor[x][k]; };
 
         // ---- the tiles
         float o[NT][8][4], m[NT][2], l[NT][2];
@@ -344,28 +371,32 @@ __global__ void __launch_bounds__(kRowThreads, row_blocks(NT)) row_attention_ker
                         }
                     }
                 }
-                // scores in powers of two; hidden ones -inf
-                const bool part = pos + kWarpKeys - 1 > first || (a.window > 0 && pos < last - a.window + 1);
-                float top[NT][2];
+                // capped scores over the cap; hidden ones -inf
+                if (CAP) {
+#pragma unroll
+                    for (int x = 0; x < NT; ++x)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            sc[i >> 2][x][i & 3] = tanh_of(sc[i >> 2][x][i & 3] * factor[x][i & 1]);
+                }
+                if (pos + kWarpKeys - 1 > first || (a.window > 0 && pos < last - a.window + 1)) {
+#pragma unroll
+                    for (int x = 0; x < NT; ++x)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int key = pos + (i >> 2) * 16 + key_of(g) + (i >> 1 & 1) * 8, h = hi[x][i & 1];
+                            if (key > h || (a.window > 0 && key <= h - a.window))
+                                sc[i >> 2][x][i & 3] = -INFINITY;
+                        }
+                }
+                float top[NT][2];   // in powers of two
                 bool grow = false;
 #pragma unroll
                 for (int x = 0; x < NT; ++x) {
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        top[x][k] = -INFINITY;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            float &z = sc[i >> 1][x][(i & 1) * 2 + k];
-                            z *= factor[x][k];
-                            if (CAP)
-                                z = tanh_of(z) * (a.softcap * 1.4426950408889634f);
-                            if (part) {
-                                const int key = pos + (i >> 1) * 16 + key_of(g) + (i & 1) * 8;
-                                if (key > hi[x][k] || (a.window > 0 && key <= hi[x][k] - a.window))
-                                    z = -INFINITY;
-                            }
-                            top[x][k] = fmaxf(top[x][k], z);
-                        }
+                        const float y = max3(fmaxf(sc[0][x][k], sc[0][x][2 + k]), sc[1][x][k], sc[1][x][2 + k]);
+                        top[x][k] = y * unit(x, k);
                         grow |= top[x][k] > m[x][k] + (kLift + kLazy);
                     }
                 }
@@ -397,7 +428,8 @@ __global__ void __launch_bounds__(kRowThreads, row_blocks(NT)) row_attention_ker
                     const float b0 = m[x][0] == -INFINITY ? 0.f : m[x][0], b1 = m[x][1] == -INFINITY ? 0.f : m[x][1];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const float y0 = ex2(sc[i >> 1][x][(i & 1) * 2] - b0), y1 = ex2(sc[i >> 1][x][(i & 1) * 2 + 1] - b1);
+                        const float y0 = ex2(fmaf(sc[i >> 1][x][(i & 1) * 2], unit(x, 0), -b0));
+                        const float y1 = ex2(fmaf(sc[i >> 1][x][(i & 1) * 2 + 1], unit(x, 1), -b1));
                         l[x][0] += y0;
                         l[x][1] += y1;
                         p[i >> 1][x][i & 1] = transposed(f16x2(y0, y1));
