@@ -47,6 +47,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "attention_plan.cuh"
 #include "prompt.cuh"
@@ -87,6 +88,8 @@ constexpr float kLift = FP4 ? 7.f : 0.f;
 struct AttnShared {
     uint64_t kv_full[kAttnStages], kv_empty[kAttnStages];
     uint64_t q_full, q_empty;
+    uint64_t raw_full[3], raw_empty[3];   // 4-bit tiles on their way to the warps that expand them
+    int raw_what[3];
     uint64_t s_full[2], p_full[2][2], o_full[2];
     uint64_t x_full, x_empty;   // the streams' join in shared memory
     uint64_t drained, nobody[2];
@@ -354,8 +357,8 @@ struct AttnLaunch {
     float cap_poly[3], cap_near;
 };
 
-// ---- the copies (over 4-bit rows: of Q alone) ----------------------------------------
-template <bool TWO, bool FP4>
+// ---- the copies --------------------------------------------------------------------
+template <bool TWO>
 __device__ __forceinline__ void copies(const AttnLaunch &c, AttnShared &sh, const CUtensorMap &qmap,
                                        const CUtensorMap &kmap, const CUtensorMap &vmap, uint32_t qbuf, uint32_t ring,
                                        int lane)
@@ -385,10 +388,6 @@ __device__ __forceinline__ void copies(const AttnLaunch &c, AttnShared &sh, cons
             }
         }
         ok = __shfl_sync(0xffffffffu, (int)ok, 0);
-        if constexpr (FP4) {
-            segment_done(sh, segs++);
-            continue;
-        }
         // where this lane's rows of tile t lie: the copy's coordinates in a page and among pages
         auto look = [&](int t) {
             int2 at = make_int2(0, a.cache.n_pages * Hkv);   // outside: read as zeros
@@ -459,164 +458,195 @@ __device__ __forceinline__ void copies(const AttnLaunch &c, AttnShared &sh, cons
     __syncwarp();
 }
 
-// ---- 4-bit rows into the ring: four warps, 32 keys of a tile each -----------------------
-// Copies bring codes and scales (72 bytes a row) three tiles ahead into a place of each warp's own.  Four lanes a row, 32
-// codes a lane, become bf16 keys (as Q is) or fp16 values in the layout that a tensor copy would have left.  Both hold
-// code times scale exactly.  A row past the length, or in a bad page, gets scales of zero.
-constexpr int kRawTiles = 3, kRawRow = kD / 2 + kFp4Scales, kRawBytes = kTile / kExpandWarps * kRawRow;   // of a warp's part
-static_assert(kRawTiles * kExpandWarps * kRawBytes <= (kAttnStages - kFp4Stages) * kAttnStageBytes, "the ring's last place");
+// ---- 4-bit rows ----------------------------------------------------------------------
+// One warp brings Q, and the codes and scales of tiles (72 bytes a key) three ahead of use.  It knows the order of
+// the ring's places, so the warps that expand them need to be told keys from values only.  Codes come by bulk copies
+// (4096 tokens over 32768 keys: 2812 us with 16 bytes a lane, as one warp cannot ask for more than that brings), scales, which
+// may lie at any multiple of 8 bytes, 8 bytes a lane.  Rows past the length, or in a bad page, get scales of zero.
+constexpr int kRawTiles = 3, kRawCodes = kTile * kD / 2, kRawBytes = kRawCodes + kTile * kFp4Scales;
+static_assert(kRawTiles * kRawBytes <= (kAttnStages - kFp4Stages) * kAttnStageBytes, "the ring's last place");
+enum { RAW_VALUES = 0, RAW_KEYS = 1, RAW_END = 2 };
 
 template <bool TWO>
-__device__ __forceinline__ void expand(const AttnLaunch &c, AttnShared &sh, uint32_t raw, uint32_t ring, int warp, int lane)
+__device__ __forceinline__ void bring(const AttnLaunch &c, AttnShared &sh, const CUtensorMap &qmap, uint32_t qbuf,
+                                      unsigned char *raw, int lane)
 {
     const AttnArgs &a = c.a;
-    const int Hkv = a.cache.n_kv_heads, chunk = lane & 3, quad = lane >> 2;
-    raw += warp * kRawTiles * kRawBytes;
+    const int Hkv = a.cache.n_kv_heads, tile_tokens = kTile / a.G, shift = 31 - __clz(c.chunk);
     bool ok = true;
-    uint32_t used = 0, segs = 0;
-    uint32_t queue[kRawTiles] = {}, waiting = 0;   // tiles on their way, the oldest first: twice the ring's slot, plus one for keys
-    uint32_t to = 0, from = 0;                // places of the next copy, and of the oldest
-    auto next_place = [](uint32_t x) { return x + kRawBytes == kRawTiles * kRawBytes ? 0 : x + kRawBytes; };
-    auto group = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
-    // the oldest tile into the ring; one group of copies a tile, empty ones at the end
-    auto oldest = [&] {
-        asm volatile("cp.async.wait_group %0;" ::"n"(kRawTiles - 1) : "memory");
-        __syncwarp();
-        const uint32_t u = queue[0] >> 1, st = u % kFp4Stages;
-        const bool keys = queue[0] & 1;
-#pragma unroll
-        for (int i = 0; i + 1 < kRawTiles; ++i)
-            queue[i] = queue[i + 1];
-        --waiting;
-        if (u >= kFp4Stages && !warp_wait(sh, &sh.kv_empty[st], (u / kFp4Stages - 1) & 1, a.status))
-            return false;
-        const uint32_t half = chunk >> 1, dst = ring + st * kAttnStageBytes + half * kHalfBytes;
-#pragma unroll
-        for (int p = 0; p < 4; ++p) {
-            const uint32_t in_part = p * 8 + quad, row = warp * 32 + in_part;
-            uint32_t w[4], s;
-            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                         : "r"(raw + from + in_part * (kD / 2) + chunk * 16));
-            asm volatile("{\n .reg .u16 x;\n ld.shared.u16 x, [%1];\n cvt.u32.u16 %0, x;\n}\n"
-                         : "=r"(s)
-                         : "r"(raw + from + 32 * (kD / 2) + in_part * kFp4Scales + chunk * 2));
-            // the lanes of the row's second half begin with their third word: then 8 lanes meet no bank twice
-            const uint32_t turn = half * 2;
-            uint32_t lo = (s & 255u) * 0x00800080u, hi = (s >> 8) * 0x00800080u;   // fp16, twice
-            if (half) {
-                uint32_t x = w[0];
-                w[0] = w[2], w[2] = x;
-                x = w[1];
-                w[1] = w[3], w[3] = x;
-                x = lo;
-                lo = hi, hi = x;
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint32_t h[4];
-                e2m1x8_halves(w[i], h);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const __half2 y = __hmul2(reinterpret_cast<const __half2 &>(h[e]), reinterpret_cast<const __half2 &>(i < 2 ? lo : hi));
-                    h[e] = reinterpret_cast<const uint32_t &>(y);
-                    if (keys) {
-                        const float2 f = __half22float2(y);
-                        h[e] = bf16x2(f.x, f.y);
-                    }
-                }
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + row * 128 + ((((chunk & 1) * 4 + (i ^ turn)) ^ (row & 7)) << 4)),
-                             "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3])
-                             : "memory");
-            }
+    uint32_t segs = 0, used = 0, q_copies = 0;
+    // place `used` is free, and once what was copied to it is there it holds `what`
+    auto begin = [&] {
+        return used < kRawTiles || warp_wait(sh, &sh.raw_empty[used % kRawTiles], (used / kRawTiles - 1) & 1, a.status);
+    };
+    auto end = [&](int what) {
+        uint64_t *bar = &sh.raw_full[used % kRawTiles];
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+        if (lane == 0) {
+            sh.raw_what[used % kRawTiles] = what;
+            mbar_arrive(bar);
         }
-        from = next_place(from);
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();   // (also: all lanes have read the place that the next copy takes)
-        if (lane == 0)
-            mbar_arrive(&sh.kv_full[st]);
-        return true;
+        ++used;
     };
     while (ok && segment(sh, segs, a.status)) {
         const Segment &s = sh.segments[segs % kSegments];
         const int nt = s.j1 - s.j0, L = s.seq.L, j0 = s.j0, hk = s.hk, b = s.b;
-        // where this warp's rows of tile t lie, for each 16 of them: the head's rows of a page (-1: none), and the row there
-        struct Rows {
-            int page[2], row[2];
-        };
+        if (lane == 0) {
+            ok = segs == 0 || wait(sh, &sh.q_empty, (segs - 1) & 1, a.status);
+            if (ok) {
+                const int t0 = s.seq.t0 + s.k * c.plan.tokens;
+                mbar_expect_tx(&sh.q_full, (TWO ? 2 : 1) * tile_tokens * a.G * kD * 2);
+                for (int i = 0; i < (TWO ? 2 : 1); ++i)
+                    for (int h = 0; h < 2; ++h)
+                        load_3d(qbuf + i * kAttnStageBytes + h * kHalfBytes, &qmap, h * 64, hk * a.G, t0 + i * tile_tokens,
+                                &sh.q_full);
+                ++q_copies;
+            }
+        }
+        ok = __shfl_sync(0xffffffffu, (int)ok, 0);
+        // where this lane's rows of tile t lie (a piece of c.chunk), as a row of the pool; -1: nowhere
         auto look = [&](int t) {
-            Rows at;
-#pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                const int pos = (j0 + t) * kTile + warp * 32 + g * 16;
-                at.page[g] = -1;
-                at.row[g] = pos;
-                if (t < nt && pos < L) {
-                    int page = b;
-                    if (a.cache.table) {
-                        page = a.cache.table[(long long)b * a.cache.table_width + pos / a.cache.page_rows];
-                        at.row[g] = pos % a.cache.page_rows;
-                    }
-                    if ((uint32_t)page < (uint32_t)a.cache.n_pages)
-                        at.page[g] = page * Hkv + hk;
-                    else if (a.status)
-                        atomicOr(a.status, RETOPK_STATUS_BAD_PAGE);
+            const int pos = (j0 + t) * kTile + (lane << shift);
+            long long at = -1;
+            if (lane < kTile >> shift && t < nt && pos < L) {
+                int page = b, row = pos;
+                if (a.cache.table) {
+                    page = a.cache.table[(long long)b * a.cache.table_width + pos / a.cache.page_rows];
+                    row = pos % a.cache.page_rows;
                 }
+                if ((uint32_t)page < (uint32_t)a.cache.n_pages)
+                    at = ((long long)page * Hkv + hk) * a.cache.page_rows + row;
+                else if (a.status)
+                    atomicOr(a.status, RETOPK_STATUS_BAD_PAGE);
             }
             return at;
         };
         constexpr int ahead = TWO ? 1 : 2;   // the ring's order, as in copies()
-        Rows at[3] = {look(0), look(0), look(0)};
+        long long at[3] = {look(0), look(0), look(0)};
         for (int x = -ahead; x < nt && ok; ++x) {
-            const Rows next = look(x + ahead + 1);
+            const long long next = look(x + ahead + 1);
 #pragma unroll
             for (int isk = 0; isk < 2; ++isk) {
                 const int t = isk ? x + ahead : x;
                 if (t < 0 || t >= nt || !ok)
                     continue;
-                const Rows &r = at[isk ? ahead : 0];
+                ok = begin();
+                if (!ok)
+                    break;
+                const long long mine = at[isk ? ahead : 0];
                 const uint8_t *codes = static_cast<const uint8_t *>(isk ? a.cache.k : a.cache.v), *scales = isk ? a.cache.k_scale : a.cache.v_scale;
-                const int pos = (j0 + t) * kTile + warp * 32;
-                long long first[2];
-#pragma unroll
-                for (int g = 0; g < 2; ++g)
-                    first[g] = (long long)r.page[g] * a.cache.page_rows + r.row[g];
-#pragma unroll
-                for (int p = 0; p < 4; ++p) {
-                    const int in_part = p * 8 + quad;
-                    if (r.page[p / 2] >= 0 && pos + in_part < L)
-                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(raw + to + in_part * (kD / 2) + chunk * 16),
-                                     "l"(codes + (first[p / 2] + (in_part & 15)) * (kD / 2) + chunk * 16)
-                                     : "memory");
+                const int left = L - (j0 + t) * kTile;
+                unsigned char *place = raw + used % kRawTiles * kRawBytes;
+                const uint32_t to = smem_u32(place);
+                if (mine >= 0) {   // (rows past the length too, where the pool has them)
+                    const int pos = (j0 + t) * kTile + (lane << shift);
+                    const uint32_t bytes = min(c.chunk, a.capacity - pos) * (kD / 2);
+                    uint64_t *bar = &sh.raw_full[used % kRawTiles];
+                    asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
+                    bulk_load(reinterpret_cast<void *>(place + (lane << shift) * (kD / 2)), codes + mine * (kD / 2), bytes, bar);
                 }
-                const bool there = r.page[lane >> 4 ? 1 : 0] >= 0 && pos + lane < L;
-                const long long row = (lane >> 4 ? first[1] : first[0]) + (lane & 15);
-                asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(raw + to + 32 * (kD / 2) + lane * kFp4Scales),
-                             "l"(scales + (there ? row * kFp4Scales : 0)), "r"(there ? 8 : 0)
-                             : "memory");
-                group();
-                to = next_place(to);
-                queue[0] = waiting == 0 ? 2 * (used + (isk ? ring_k<TWO>(t) : ring_v<TWO>(t, nt))) + isk : queue[0];
-                queue[1] = waiting == 1 ? 2 * (used + (isk ? ring_k<TWO>(t) : ring_v<TWO>(t, nt))) + isk : queue[1];
-                queue[2] = waiting == 2 ? 2 * (used + (isk ? ring_k<TWO>(t) : ring_v<TWO>(t, nt))) + isk : queue[2];
-                if (++waiting == kRawTiles)
-                    ok = oldest();
+#pragma unroll
+                for (int i = 0; i < kTile / 32; ++i) {
+                    const int r = 32 * i + lane;
+                    const long long first = __shfl_sync(0xffffffffu, mine, r >> shift);
+                    const bool there = first >= 0 && r < left;
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to + kRawCodes + r * kFp4Scales),
+                                 "l"(scales + (there ? (first + (r & (c.chunk - 1))) * kFp4Scales : 0)), "r"(there ? 8 : 0)
+                                 : "memory");
+                }
+                end(isk ? RAW_KEYS : RAW_VALUES);
             }
             at[0] = at[1];
             at[1] = TWO ? next : at[2];
             at[2] = next;
         }
-        used += 2 * nt;
         segment_done(sh, segs++);
     }
-    while (ok && waiting > 0) {
-        // (as if kRawTiles were on their way)
-        for (uint32_t i = waiting; i < kRawTiles; ++i)
-            group();
-        ok = oldest();
-    }
+    if (ok && begin())
+        end(RAW_END);
     asm volatile("cp.async.wait_all;" ::: "memory");
+    if (*reinterpret_cast<volatile int *>(&sh.failed) && lane == 0) {   // a wait ran out: the copies in flight end before the memory goes
+        const long long t0 = clock64();
+        for (uint32_t u = used > kRawTiles ? used - kRawTiles : 0; u < used; ++u)
+            while (!mbar_try_wait(&sh.raw_full[u % kRawTiles], (u / kRawTiles) & 1) && clock64() - t0 < kWaitCycles)
+                ;
+        while (q_copies && !mbar_try_wait(&sh.q_full, (q_copies - 1) & 1) && clock64() - t0 < kWaitCycles)
+            ;
+    }
     __syncwarp();
+}
+
+// Four warps, 32 keys of a tile each: four lanes a key, 32 codes a lane, which become bf16 keys (as Q is) or fp16 values in
+// the layout that a tensor copy would have left.  Both hold code times scale exactly.
+template <bool TWO>
+__device__ __forceinline__ void expand(const AttnLaunch &c, AttnShared &sh, uint32_t raw, uint32_t ring, int warp, int lane)
+{
+    uint32_t *const status = c.a.status;
+    const uint32_t chunk = lane & 3, half = chunk >> 1, row0 = warp * 32 + (lane >> 2);   // rows row0 + 8 p
+    const uint32_t turn = half * 2;
+    for (uint32_t u = 0;; ++u) {
+        const uint32_t place = u % kRawTiles, st = u % kFp4Stages;
+        if (!warp_wait(sh, &sh.raw_full[place], (u / kRawTiles) & 1, status))
+            return;
+        const int what = sh.raw_what[place];
+        if (what == RAW_END)
+            return;
+        // all loads go before the first store, which nothing tells them apart from
+        const uint32_t from = raw + place * kRawBytes;
+        uint32_t w[4][4], s[4];
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            const uint32_t row = row0 + 8 * p;
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w[p][0]), "=r"(w[p][1]), "=r"(w[p][2]), "=r"(w[p][3])
+                         : "r"(from + row * (kD / 2) + chunk * 16)
+                         : "memory");
+            asm volatile("{\n .reg .u16 x;\n ld.shared.u16 x, [%1];\n cvt.u32.u16 %0, x;\n}\n"
+                         : "=r"(s[p])
+                         : "r"(from + kRawCodes + row * kFp4Scales + chunk * 2)
+                         : "memory");
+        }
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(&sh.raw_empty[place]);
+        if (u >= kFp4Stages && !warp_wait(sh, &sh.kv_empty[st], (u / kFp4Stages - 1) & 1, status))
+            return;
+        const uint32_t dst = ring + st * kAttnStageBytes + half * kHalfBytes;
+        auto rows = [&](auto keys_) {
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                const uint32_t row = row0 + 8 * p;
+                // the lanes of the row's second half begin with their third word: then 8 lanes meet no bank twice
+                const uint32_t s0 = (s[p] & 255u) * 0x00800080u, s1 = (s[p] >> 8) * 0x00800080u;   // fp16, twice
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t h[4];
+                    e2m1x8_halves(half ? w[p][i ^ 2] : w[p][i], h);
+                    const uint32_t scale = (i < 2) == (half == 0) ? s0 : s1;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const __half2 y = __hmul2(reinterpret_cast<const __half2 &>(h[e]), reinterpret_cast<const __half2 &>(scale));
+                        h[e] = reinterpret_cast<const uint32_t &>(y);
+                        if (decltype(keys_)::value) {
+                            const float2 f = __half22float2(y);
+                            h[e] = bf16x2(f.x, f.y);
+                        }
+                    }
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + row * 128 + ((((chunk & 1) * 4 + (i ^ turn)) ^ (row & 7)) << 4)),
+                                 "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3])
+                                 : "memory");
+                }
+            }
+        };
+        if (what == RAW_KEYS)
+            rows(std::true_type{});
+        else
+            rows(std::false_type{});
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(&sh.kv_full[st]);
+    }
 }
 
 // ---- the matrix instructions ------------------------------------------------------------
@@ -1157,6 +1187,10 @@ __global__ void __launch_bounds__(FP4 ? kFp4Threads : kAttnThreads, 1)
         }
         mbar_init(&sh.q_full, 1);
         mbar_init(&sh.q_empty, 1);
+        for (int s = 0; s < kRawTiles; ++s) {
+            mbar_init(&sh.raw_full[s], 33);   // each lane's copies, and the word beside them
+            mbar_init(&sh.raw_empty[s], kExpandWarps);
+        }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.s_full[i], 1);
             mbar_init(&sh.p_full[i][0], 4);
@@ -1165,7 +1199,7 @@ __global__ void __launch_bounds__(FP4 ? kFp4Threads : kAttnThreads, 1)
         }
         for (int s = 0; s < kSegments; ++s) {
             mbar_init(&sh.seg_full[s], 1);
-            mbar_init(&sh.seg_empty[s], kLoadWarp + 1 + (FP4 ? kExpandWarps : 0));
+            mbar_init(&sh.seg_empty[s], kLoadWarp + 1);
         }
         mbar_init(&sh.x_full, 4);
         mbar_init(&sh.x_empty, 4);
@@ -1202,8 +1236,10 @@ __global__ void __launch_bounds__(FP4 ? kFp4Threads : kAttnThreads, 1)
         softmax<TWO, CAP, FP4>(c, sh, reinterpret_cast<float *>(attn_smem + kAttnStageBytes), ring, tmem, warp, lane);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(FP4 ? kFp4OtherRegs : kOtherRegs));
-        if (warp == kLoadWarp)
-            copies<TWO, FP4>(c, sh, qmap, kmap, vmap, qbuf, ring, lane);
+        if (warp == kLoadWarp && FP4)
+            bring<TWO>(c, sh, qmap, qbuf, attn_smem + (2 + kStages) * kAttnStageBytes, lane);
+        else if (warp == kLoadWarp)
+            copies<TWO>(c, sh, qmap, kmap, vmap, qbuf, ring, lane);
         else if (warp == kMmaWarp)
             matrices<TWO, FP4>(c, sh, qbuf, ring, tmem);
         else if (warp == kWalkWarp && lane == 0)
