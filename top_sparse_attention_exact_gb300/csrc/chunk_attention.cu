@@ -591,37 +591,37 @@ __device__ __forceinline__ void expand(const AttnLaunch &c, AttnShared &sh, uint
         const int what = sh.raw_what[place];
         if (what == RAW_END)
             return;
-        // all loads go before the first store, which nothing tells them apart from
+        // the loads of the next rows go before the stores, which nothing tells them apart from
         const uint32_t from = raw + place * kRawBytes;
-        uint32_t w[4][4], s[4];
-#pragma unroll
-        for (int p = 0; p < 4; ++p) {
+        auto load = [&](int p, uint32_t (&w)[4], uint32_t &s) {
             const uint32_t row = row0 + 8 * p;
             asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(w[p][0]), "=r"(w[p][1]), "=r"(w[p][2]), "=r"(w[p][3])
+                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
                          : "r"(from + row * (kD / 2) + chunk * 16)
                          : "memory");
             asm volatile("{\n .reg .u16 x;\n ld.shared.u16 x, [%1];\n cvt.u32.u16 %0, x;\n}\n"
-                         : "=r"(s[p])
+                         : "=r"(s)
                          : "r"(from + kRawCodes + row * kFp4Scales + chunk * 2)
                          : "memory");
-        }
-        __syncwarp();
-        if (lane == 0)
-            mbar_arrive(&sh.raw_empty[place]);
+        };
+        uint32_t w[4], s;
+        load(0, w, s);
         if (u >= kFp4Stages && !warp_wait(sh, &sh.kv_empty[st], (u / kFp4Stages - 1) & 1, status))
             return;
         const uint32_t dst = ring + st * kAttnStageBytes + half * kHalfBytes;
+        // (a loop: short code matters beside the softmax, whose instructions fill the caches near the warps)
         auto rows = [&](auto keys_) {
-#pragma unroll
+#pragma unroll 1
             for (int p = 0; p < 4; ++p) {
                 const uint32_t row = row0 + 8 * p;
+                uint32_t next[4], next_s;
+                load(min(p + 1, 3), next, next_s);
                 // the lanes of the row's second half begin with their third word: then 8 lanes meet no bank twice
-                const uint32_t s0 = (s[p] & 255u) * 0x00800080u, s1 = (s[p] >> 8) * 0x00800080u;   // fp16, twice
+                const uint32_t s0 = (s & 255u) * 0x00800080u, s1 = (s >> 8) * 0x00800080u;   // fp16, twice
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     uint32_t h[4];
-                    e2m1x8_halves(half ? w[p][i ^ 2] : w[p][i], h);
+                    e2m1x8_halves(half ? w[i ^ 2] : w[i], h);
                     const uint32_t scale = (i < 2) == (half == 0) ? s0 : s1;
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
@@ -636,12 +636,19 @@ __device__ __forceinline__ void expand(const AttnLaunch &c, AttnShared &sh, uint
                                  "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3])
                                  : "memory");
                 }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    w[i] = next[i];
+                s = next_s;
             }
         };
         if (what == RAW_KEYS)
             rows(std::true_type{});
         else
             rows(std::false_type{});
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(&sh.raw_empty[place]);
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0)
