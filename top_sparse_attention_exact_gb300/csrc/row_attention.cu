@@ -13,7 +13,7 @@
 //   S^T = K Q^T     a lane's 32 codes of a key, 16 bytes, are its part of 8 steps of the contraction
 //   O^T = V^T P^T   a lane's 16 codes of four keys, one scale block each; codes of two keys are brought side by side
 //                   four bits at a time before they are converted; P^T is a transposed 8 x 8 of half words
-// A warp takes 32 keys of every 128, with a ring of its own: copies bring 32 keys' codes and scales two tiles ahead.  Four
+// A warp takes 32 keys of every 128, with a ring of its own: copies bring 32 keys' codes and scales a tile ahead.  Four
 // warps are a CTA, so that one CTA's end of an item lies beside the others' work.
 //
 // Rounding.  Code times scale is exact in fp16.  A query row is brought to fp16's range by a power of two, so
@@ -31,7 +31,7 @@ namespace {
 
 constexpr int kRowWarps = 4, kRowThreads = kRowWarps * 32;
 constexpr int kWarpKeys = kTile / kRowWarps;
-constexpr int kRowStages = 3;                                  // tiles of a warp's ring
+constexpr int kRowStages = 2;                                  // tiles of a warp's ring (with 3: 61 ragged tokens 84.7 us, 83.1)
 constexpr int kCodeBytes = kWarpKeys * kD / 2, kScaleBytes = kWarpKeys * kFp4Scales;
 constexpr int kStageBytes = 2 * (kCodeBytes + kScaleBytes);    // K's codes, V's codes, K's scales, V's scales
 constexpr int kSumRow = kD + 4;                                // floats of a row where the warps' sums meet
@@ -58,7 +58,6 @@ struct RowLaunch {
     AttnArgs a;
     Plan plan;
     RowParts parts;
-    int step_pages, step_rows;   // pages and rows that a tile's keys are on from the last one's
 };
 
 template <int NT>
@@ -184,7 +183,7 @@ __global__ void __launch_bounds__(kRowThreads, row_blocks(NT)) row_attention_ker
     // values: the 16-byte pieces of keys 2, 3 of every four change places by two
     const uint32_t v_at = kCodeBytes + ((g >> 1 ^ (t4 >> 1) << 1) << 4) + (g & 1) * 8;
     const uint32_t va = key_of(2 * t4) * (kD / 2) + v_at, vb = key_of(2 * t4 + 1) * (kD / 2) + v_at;
-    const uint32_t code_from = lane * 16, v_to = kCodeBytes + (g * 4 + (t4 ^ (g >> 1 & 1) << 1)) * 16;   // of the copies
+    const uint32_t code_from = lane * 16, values_to = kCodeBytes + (g * 4 + (t4 ^ (g >> 1 & 1) << 1)) * 16;   // of the copies
     const uint32_t vs_at = 2 * kCodeBytes + kScaleBytes + g;
     const uint32_t vsa = key_of(2 * t4) * kFp4Scales + vs_at, vsb = key_of(2 * t4 + 1) * kFp4Scales + vs_at;
 
@@ -198,81 +197,66 @@ __global__ void __launch_bounds__(kRowThreads, row_blocks(NT)) row_attention_ker
         const int low = a.window > 0 ? first - a.window + 1 : 0;           // the first key that one sees
         const int pos0 = s.j0 * kTile + warp * kWarpKeys;
 
-        // ---- the copies: this warp's keys of a tile.  Pages are looked up a tile ahead.
-        int index = 0, row = pos0;       // of tile `look` ahead: its place in the table, the row in that page
-        if (a.cache.table) {
-            index = pos0 / a.cache.page_rows;
-            row = pos0 % a.cache.page_rows;
-        }
-        int page[2], at[2];              // of the next tile, for each 16 keys: page, row in it
-        bool asked[2];                   // it has keys to be read
+        // ---- the copies: this warp's keys of a tile.  Where 16 keys lie is looked up by a lane each, for 16 tiles at a
+        // time: the byte of the pool where their codes begin; negative: nowhere
+        long long place = -1;
         auto look = [&](int t) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int pos = pos0 + t * kTile + 16 * i;
-                int x = index, r = row + 16 * i;
-                if (a.cache.table && r >= a.cache.page_rows) {
-                    r -= a.cache.page_rows;
-                    ++x;
+            t += lane >> 1;
+            const int pos = pos0 + t * kTile + (lane & 1) * 16;
+            place = -1;
+            if (t < nt && pos < L && pos <= last && pos + 15 >= low) {
+                int page = s.b, row = pos;
+                if (a.cache.table) {
+                    page = a.cache.table[(long long)s.b * a.cache.table_width + pos / a.cache.page_rows];
+                    row = pos % a.cache.page_rows;
                 }
-                at[i] = r;
-                asked[i] = t < nt && pos < L && pos <= last && pos + 15 >= low;
-                page[i] = s.b;
-                if (asked[i] && a.cache.table)
-                    page[i] = a.cache.table[(long long)s.b * a.cache.table_width + x];
-            }
-            index += c.step_pages;
-            row += c.step_rows;
-            if (a.cache.table && row >= a.cache.page_rows) {
-                row -= a.cache.page_rows;
-                ++index;
+                if ((uint32_t)page < (uint32_t)a.cache.n_pages)
+                    place = (((long long)page * a.cache.n_kv_heads + s.hk) * a.cache.page_rows + row) * (kD / 2);
+                else if (a.status)
+                    atomicOr(a.status, RETOPK_STATUS_BAD_PAGE);
             }
         };
         uint32_t to = ring;
         auto issue = [&](int t) {
             if (t < nt) {
+                if ((t & 15) == 0)
+                    look(t);
                 const int left = L - (pos0 + t * kTile);
-                long long from[2];   // rows
-                bool there[2];
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    there[i] = asked[i] && (uint32_t)page[i] < (uint32_t)a.cache.n_pages;
-                    if (asked[i] && !there[i] && a.status)
-                        atomicOr(a.status, RETOPK_STATUS_BAD_PAGE);
-                    from[i] = there[i] ? ((long long)page[i] * a.cache.n_kv_heads + s.hk) * a.cache.page_rows + at[i] : 0;
-                }
+                const long long from[2] = {__shfl_sync(0xffffffffu, place, (t & 15) * 2), __shfl_sync(0xffffffffu, place, (t & 15) * 2 + 1)};
                 // rows that are not there keep what codes the place held, and get scales of zero
                 constexpr int kEight = 8 * (kD / 2);
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const char *k = static_cast<const char *>(a.cache.k) + from[i] * (kD / 2) + code_from;
-                    const char *v = static_cast<const char *>(a.cache.v) + from[i] * (kD / 2) + code_from;
-                    if (there[i] && 16 * i + 16 <= left) {
-                        copy16<0>(to + 2 * i * kEight + code_from, k);
-                        copy16<kEight>(to + 2 * i * kEight + code_from, k);
-                        copy16<0>(to + 2 * i * kEight + v_to, v);
-                        copy16<kEight>(to + 2 * i * kEight + v_to, v);
-                    } else if (there[i]) {
+                    if (from[i] < 0)
+                        continue;
+                    const char *k = static_cast<const char *>(a.cache.k) + from[i] + code_from;
+                    const char *v = static_cast<const char *>(a.cache.v) + from[i] + code_from;
+                    const uint32_t k_to = to + 2 * i * kEight + code_from, v_to = to + 2 * i * kEight + values_to;
+                    if (16 * i + 16 <= left) {
+                        copy16<0>(k_to, k);
+                        copy16<kEight>(k_to, k);
+                        copy16<0>(v_to, v);
+                        copy16<kEight>(v_to, v);
+                    } else {
                         if (16 * i + g < left) {
-                            copy16<0>(to + 2 * i * kEight + code_from, k);
-                            copy16<0>(to + 2 * i * kEight + v_to, v);
+                            copy16<0>(k_to, k);
+                            copy16<0>(v_to, v);
                         }
                         if (16 * i + 8 + g < left) {
-                            copy16<kEight>(to + 2 * i * kEight + code_from, k);
-                            copy16<kEight>(to + 2 * i * kEight + v_to, v);
+                            copy16<kEight>(k_to, k);
+                            copy16<kEight>(v_to, v);
                         }
                     }
                 }
-                const bool ok = (lane >> 4 ? there[1] : there[0]) && lane < left;
-                const long long x = ok ? ((lane >> 4 ? from[1] : from[0]) + (lane & 15)) * kFp4Scales : 0;
+                const long long mine = lane >> 4 ? from[1] : from[0];
+                const bool ok = mine >= 0 && lane < left;
+                const long long x = ok ? (mine >> 3) + (lane & 15) * kFp4Scales : 0;
                 copy8(to + 2 * kCodeBytes + lane * kFp4Scales, a.cache.k_scale + x, ok);
                 copy8(to + 2 * kCodeBytes + kScaleBytes + lane * kFp4Scales, a.cache.v_scale + x, ok);
-                look(t + 1);
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
             to = to + kStageBytes == ring + kRowStages * kStageBytes ? ring : to + kStageBytes;
         };
-        look(0);
 #pragma unroll
         for (int t = 0; t < kRowStages - 1; ++t)
             issue(t);
@@ -526,20 +510,27 @@ __global__ void __launch_bounds__(kRowThreads, row_blocks(NT)) row_attention_ker
     }
 }
 
-// Joins the parts of an item.  BY_ITEM, for few items: the grid's columns are the cut items, in order; else they are the
-// bounds, and the first that cuts an item has it.  One, two, four or eight warps take a row and share out its parts.
+// Joins the parts of an item.  BY_ITEM, for few items of many parts: the grid's columns are the cut items, in order, and its
+// rows theirs; else the columns are the bounds, and the first that cuts an item has it.  Up to all warps take a row
+// and share out its parts.
 template <bool BY_ITEM>
-__global__ void __launch_bounds__(256) row_join_kernel(const __grid_constant__ RowLaunch c, int shares)
+constexpr int kJoinWarps = BY_ITEM ? 16 : 8;
+
+template <bool BY_ITEM>
+__global__ void __launch_bounds__(kJoinWarps<BY_ITEM> * 32) row_join_kernel(const __grid_constant__ RowLaunch c, int shares)
 {
-    __shared__ float4 sum[8][32];
-    __shared__ float2 ml_of[8];
+    constexpr int kWarps = kJoinWarps<BY_ITEM>, kThreads = kWarps * 32, kFlight = BY_ITEM ? 8 : 4;   // parts on their way at once
+    __shared__ float4 sum[kWarps][32];
+    __shared__ float2 ml_of[kWarps];
+    __shared__ Place places[BY_ITEM ? kMaxRowShares + 1 : 1];
     __shared__ uint16_t list[kMaxRowShares + 1];
-    __shared__ int counts[8], found;
+    __shared__ int counts[kWarps], found;
     pdl_wait();
     pdl_trigger();
     const AttnArgs &a = c.a;
     const Bound *const bound = c.parts.bound;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    auto place = [&](int i) { return BY_ITEM ? places[i] : bound[i].at; };
     // flags before this thread's, and all of them
     auto rank = [&](bool flag, int &total) {
         const uint32_t votes = __ballot_sync(0xffffffffu, flag);
@@ -549,7 +540,7 @@ __global__ void __launch_bounds__(256) row_join_kernel(const __grid_constant__ R
         __syncthreads();
         int before = __popc(votes & ((1u << lane) - 1));
         total = 0;
-        for (int w = 0; w < 8; ++w) {
+        for (int w = 0; w < kWarps; ++w) {
             before += w < warp ? counts[w] : 0;
             total += counts[w];
         }
@@ -559,15 +550,18 @@ __global__ void __launch_bounds__(256) row_join_kernel(const __grid_constant__ R
     auto cuts = [&](int i) {
         if (i < 1 || i >= shares)
             return false;
-        const Place p = bound[i].at, before = bound[i - 1].at;
+        const Place p = place(i), before = place(i - 1);
         return p.cut > 0 && !(same_item(p, before) && before.cut > 0);
     };
     int x = blockIdx.x + 1;
     if constexpr (BY_ITEM) {
+        for (int i = tid; i <= shares; i += kThreads)
+            places[i] = bound[i].at;
         if (tid == 0)
             found = 0;
+        __syncthreads();
         int done = 0;
-        for (int base = 1; base < shares && done <= (int)blockIdx.x; base += 256) {
+        for (int base = 1; base < shares && done <= (int)blockIdx.x; base += kThreads) {
             const bool flag = cuts(base + tid);
             int here;
             if (rank(flag, here) + done == (int)blockIdx.x && flag)
@@ -588,11 +582,11 @@ __global__ void __launch_bounds__(256) row_join_kernel(const __grid_constant__ R
     int n = 1;
     if (tid == 0)
         list[0] = (uint16_t)(2 * (x - 1) + 1);
-    for (int base = x; base < shares; base += 256) {
+    for (int base = x; base < shares; base += kThreads) {
         const int i = base + tid;
         bool in = false;
         if (i < shares) {
-            const Place p = bound[i].at, next = bound[i + 1].at;
+            const Place p = place(i), next = place(i + 1);
             in = same_item(p, at) && (!same_item(next, at) || next.cut > p.cut);
         }
         int more;
@@ -600,15 +594,15 @@ __global__ void __launch_bounds__(256) row_join_kernel(const __grid_constant__ R
         if (in)
             list[slot] = (uint16_t)(2 * i);
         n += more;
-        if (!same_item(bound[min(base + 256, shares)].at, at))
+        if (!same_item(place(min(base + kThreads, shares)), at))
             break;
     }
     __syncthreads();
     const int first = at.k * c.plan.tokens, rows = min(c.plan.tokens, here.n - first) * a.G;
     int crew = 1;   // warps of a row
-    while (crew < 8 && 4 * crew < n && 2 * crew * rows <= 8 * (int)gridDim.y)
+    while (crew < kWarps && 4 * crew < n && 2 * crew * rows <= kWarps * (int)gridDim.y)
         crew *= 2;
-    const int mate = warp % crew, step = 8 / crew;   // rows of the block at a time
+    const int mate = warp % crew, step = kWarps / crew;   // rows of the block at a time
     for (int base = blockIdx.y * step; base < rows; base += gridDim.y * step) {
         const int r = base + warp / crew;
         const bool real = r < rows;
@@ -625,11 +619,11 @@ __global__ void __launch_bounds__(256) row_join_kernel(const __grid_constant__ R
             m = mm;
         };
 #pragma unroll 1
-        for (int i0 = mate; i0 < n && real; i0 += 4 * crew) {   // four parts on their way at once
-            float2 ml[4];
-            float4 o[4];
+        for (int i0 = mate; i0 < n && real; i0 += kFlight * crew) {
+            float2 ml[kFlight];
+            float4 o[kFlight];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+            for (int k = 0; k < kFlight; ++k) {
                 const int i = i0 + k * crew;
                 ml[k] = make_float2(-INFINITY, 0.f);
                 o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -640,7 +634,7 @@ __global__ void __launch_bounds__(256) row_join_kernel(const __grid_constant__ R
                 }
             }
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
+            for (int k = 0; k < kFlight; ++k)
                 add(ml[k].x, ml[k].y, o[k]);
         }
         if (crew > 1) {
@@ -700,19 +694,14 @@ static cudaError_t launch_rows(const AttnArgs &a, cudaStream_t st)
         n = (int)std::min<long long>(n, items);
     c.plan.inverse = ~0ull / (unsigned long long)n;
     carve(NT, static_cast<char *>(a.ws), &c.parts);
-    c.step_rows = kTile;
-    if (a.cache.table) {
-        c.step_pages = kTile / a.cache.page_rows;
-        c.step_rows = kTile % a.cache.page_rows;
-    }
     const size_t smem = kRowWarps * kRowStages * kStageBytes + sizeof(RowShared<NT>);
     cudaError_t e = launch_pdl(a.softcap > 0.f ? row_attention_kernel<NT, true> : row_attention_kernel<NT, false>, dim3(n),
                                dim3(kRowThreads), smem, st, 1, c);
     if (e != cudaSuccess || n < 2 || !cuts)
         return e;
     if (items <= sm_count())
-        return launch_pdl(row_join_kernel<true>, dim3((int)std::min<long long>(n - 1, items), 8 * NT), dim3(256), 0, st, 1, c, n);
-    return launch_pdl(row_join_kernel<false>, dim3(n - 1), dim3(256), 0, st, 1, c, n);
+        return launch_pdl(row_join_kernel<true>, dim3((int)std::min<long long>(n - 1, items), 8 * NT), dim3(kJoinWarps<true> * 32), 0, st, 1, c, n);
+    return launch_pdl(row_join_kernel<false>, dim3(n - 1), dim3(kJoinWarps<false> * 32), 0, st, 1, c, n);
 }
 
 cudaError_t launch_row_attention(const AttnArgs &a, cudaStream_t st)
