@@ -477,6 +477,21 @@ def test_attention(n, lens, Hq, Hkv, page, window, cap):
     assert (wide[T:] == 9).all() and (lse[T:] == 9).all() and (wide[:, Hq:] == 9).all()
 
 
+@pytest.mark.parametrize("Hq,Hkv,n", [(8, 1, 1), (9, 1, 1), (16, 1, 1), (8, 1, 2), (6, 2, 5), (17, 17, 17), (8, 1, 3), (12, 2, 4), (5, 1, 5), (14, 2, 4),
+                                      (32, 2, 2), (2, 1, 16), (11, 1, 3), (1, 1, 32), (1, 1, 33), (1, 1, 7), (10, 10, 9)])
+@pytest.mark.parametrize("page,window,cap", [(0, 0, 0.0), (16, 0, 0.0), (64, 300, 0.0), (48, 0, 20.0)])
+def test_attention_rows_by_the_tile(Hq, Hkv, n, page, window, cap):
+    # 1 to 33 rows a sequence and head: tiles that are full, one row past, ragged by token; histories cut and joined, and
+    # sequences with fewer tokens than the mean, or more
+    n = [n, max(1, n - 1), n, 1, n + 2, 0]
+    lens = [5003, 40, 1300, 7001, 1030, 77]
+    q, c = setup(n, lens, Hq, Hkv, page, Hq + sum(n))
+    lse = torch.full((sum(n) + 2, Hq), 9.0, device="cuda")
+    out = retopk.chunk_attention(q, c.h, i32(lens), cu_tokens=offsets(n), softcap=cap, window=window, lse=lse)
+    check(q, n, lens, c, out, lse, 1 / math.sqrt(D), cap, window)
+    assert (lse[sum(n):] == 9).all()
+
+
 @pytest.mark.parametrize("B,L", [(1, 260), (6, 1000)])
 def test_attention_one_token_each_without_offsets(B, L):
     q, c = setup([1] * B, [L] * B, 8, 2, 0, B, pad=0, strided=False)

@@ -31,15 +31,19 @@ namespace {
 
 constexpr int kRowWarps = 4, kRowThreads = kRowWarps * 32;
 constexpr int kWarpKeys = kTile / kRowWarps;
-constexpr int kRowStages = 2;                                  // tiles of a warp's ring (with 3: 61 ragged tokens 84.7 us, 83.1)
 constexpr int kCodeBytes = kWarpKeys * kD / 2, kScaleBytes = kWarpKeys * kFp4Scales;
 constexpr int kStageBytes = 2 * (kCodeBytes + kScaleBytes);    // K's codes, V's codes, K's scales, V's scales
 constexpr int kSumRow = kD + 4;                                // floats of a row where the warps' sums meet
 constexpr float kLift = 7.f, kLazy = 8.f;                      // as in chunk_attention.cu
 constexpr int kMaxRowShares = 1024;
+constexpr int kMaxRowTiles = 4;                                // of 8 query rows
 
-// CTAs of an SM, by the tiles of 8 query rows.
-__host__ __device__ constexpr int row_blocks(int nt) { return nt == 1 ? 4 : 3; }
+// CTAs of an SM, by the tiles of 8 query rows, and tiles of a warp's ring (61 ragged tokens 83.1 us with 2, 84.7 with 3; where
+// few warps share an SM each has more on its way).
+__host__ __device__ constexpr int row_blocks(int nt) { return nt == 1 ? 4 : nt == 2 ? 3 : 2; }
+__host__ __device__ constexpr int row_stages(int nt) { return nt <= 2 ? 2 : 4; }
+// The queries stay in registers, or, where the sums take those, in shared memory.
+__host__ __device__ constexpr bool shared_queries(int nt) { return nt > 1; }
 
 struct RowCost {
     static constexpr int kItem = 256;
@@ -66,6 +70,8 @@ struct RowShared {
     Walk walk;
     Segment segments[2];
     float2 ml[kRowWarps][8 * NT];
+    int exponent[8 * NT];                                       // of the queries' rows
+    uint4 q[shared_queries(NT) ? 4 : 1][shared_queries(NT) ? NT : 1][32];
 };
 
 __device__ __forceinline__ float ex2(float x)
@@ -156,6 +162,8 @@ __device__ __forceinline__ float tanh_of(float y)
 template <int NT, bool CAP>
 __global__ void __launch_bounds__(kRowThreads, row_blocks(NT)) row_attention_kernel(const __grid_constant__ RowLaunch c)
 {
+    constexpr int kRowStages = row_stages(NT);
+    constexpr bool kShared = shared_queries(NT);
     extern __shared__ __align__(16) unsigned char row_smem[];
     RowShared<NT> &sh = *reinterpret_cast<RowShared<NT> *>(row_smem + kRowWarps * kRowStages * kStageBytes);
     const AttnArgs &a = c.a;
@@ -264,11 +272,10 @@ __global__ void __launch_bounds__(kRowThreads, row_blocks(NT)) row_attention_ker
             sh.segments[(n + 1) & 1].more = next_segment(a, c.plan, sh.walk, sh.segments[(n + 1) & 1]);
 
         // ---- the queries: column g of each 8, this lane's 32 elements, as fp16 of at most 2^15
-        uint32_t q[NT][16];
+        uint32_t q[kShared ? 1 : NT][16];
         float factor[NT][2];             // of a column's scores: in powers of two, or over the cap
         int hi[NT][2];                   // the last key that a column sees
-#pragma unroll
-        for (int x = 0; x < NT; ++x) {
+        auto query = [&](int x, uint32_t (&q)[16]) {
             const int r = 8 * x + g, tok = r / G;
             uint32_t w[16];
 #pragma unroll
@@ -293,17 +300,40 @@ __global__ void __launch_bounds__(kRowThreads, row_blocks(NT)) row_attention_ker
             const float down = __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-                q[x][i] = f16x2(bf16lo(w[i]) * down, bf16hi(w[i]) * down);
+                q[i] = f16x2(bf16lo(w[i]) * down, bf16hi(w[i]) * down);
+            return e;
+        };
+        auto columns = [&](int x, int k, int e) {
+            const int col = 8 * x + 2 * t4 + k;
+            const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+            // (never zero, as a hidden score is -inf and has to stay so)
+            factor[x][k] = CAP ? fminf(a.scale * up / a.softcap, 3e38f) : fmaxf(a.scale * 1.4426950408889634f * up, 1e-38f);
+            hi[x][k] = min(first + col / G, last);
+        };
+        if constexpr (kShared) {
+            for (int x = warp; x < NT; x += kRowWarps) {
+                const int e = query(x, q[0]);
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int col = 2 * t4 + k;
-                const float up = __uint_as_float((uint32_t)(127 + __shfl_sync(0xffffffffu, e, col * 4)) << 23);
-                // (never zero, as a hidden score is -inf and has to stay so)
-                factor[x][k] = CAP ? fminf(a.scale * up / a.softcap, 3e38f) : fmaxf(a.scale * 1.4426950408889634f * up, 1e-38f);
-                hi[x][k] = min(first + (8 * x + col) / G, last);
+                for (int i = 0; i < 4; ++i)
+                    sh.q[i][x][lane] = make_uint4(q[0][4 * i], q[0][4 * i + 1], q[0][4 * i + 2], q[0][4 * i + 3]);
+                if (t4 == 0)
+                    sh.exponent[8 * x + g] = e;
+            }
+            __syncthreads();
+#pragma unroll
+            for (int x = 0; x < NT; ++x)
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    columns(x, k, sh.exponent[8 * x + 2 * t4 + k]);
+        } else {
+#pragma unroll
+            for (int x = 0; x < NT; ++x) {
+                const int e = query(x, q[x]);
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    columns(x, k, __shfl_sync(0xffffffffu, e, (2 * t4 + k) * 4));
             }
         }
-
         // what the scores that the softmax sees are multiplied by, to be in powers of two
         const float cap2 = fmaxf(a.softcap * 1.4426950408889634f, 1e-38f);
         auto unit = [&](int x, int k) { return CAP ? cap2 : factor[x][k]; };
@@ -326,32 +356,44 @@ __global__ void __launch_bounds__(kRowThreads, row_blocks(NT)) row_attention_ker
             const int pos = pos0 + t * kTile;
             if (pos <= last && pos + kWarpKeys > low) {
                 float sc[2][NT][4];
+                uint32_t w0[2][4], w1[2][4], s0[2], s1[2];
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
 #pragma unroll
                     for (int x = 0; x < NT; ++x)
                         sc[half][x][0] = sc[half][x][1] = sc[half][x][2] = sc[half][x][3] = 0.f;
                     const uint32_t base = from + half * 16 * (kD / 2), sbase = from + half * 16 * kFp4Scales;
-                    uint32_t w0[4], w1[4];
-                    lds128(base + k_at, w0);
-                    lds128(base + k_at + 8 * (kD / 2), w1);
-                    const uint32_t s0 = lds16(sbase + ks_at), s1 = lds16(sbase + ks_at + 8 * kFp4Scales);
-                    const uint32_t s0a = (s0 & 255u) * 0x00800080u, s0b = (s0 >> 8) * 0x00800080u;   // fp16, twice
-                    const uint32_t s1a = (s1 & 255u) * 0x00800080u, s1b = (s1 >> 8) * 0x00800080u;
+                    lds128(base + k_at, w0[half]);
+                    lds128(base + k_at + 8 * (kD / 2), w1[half]);
+                    s0[half] = lds16(sbase + ks_at);
+                    s1[half] = lds16(sbase + ks_at + 8 * kFp4Scales);
+                }
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint32_t h0[4], h1[4];
-                        e2m1x8_halves(w0[i], h0);
-                        e2m1x8_halves(w1[i], h1);
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t h0[2][4], h1[2][4];
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const uint32_t z0 = (i < 2 ? s0[half] & 255u : s0[half] >> 8) * 0x00800080u;   // fp16, twice
+                        const uint32_t z1 = (i < 2 ? s1[half] & 255u : s1[half] >> 8) * 0x00800080u;
+                        e2m1x8_halves(w0[half][i], h0[half]);
+                        e2m1x8_halves(w1[half][i], h1[half]);
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            h0[k] = mul_halves(h0[k], i < 2 ? s0a : s0b);
-                            h1[k] = mul_halves(h1[k], i < 2 ? s1a : s1b);
+                            h0[half][k] = mul_halves(h0[half][k], z0);
+                            h1[half][k] = mul_halves(h1[half][k], z1);
                         }
+                    }
 #pragma unroll
-                        for (int x = 0; x < NT; ++x) {
-                            mma_f16_16816(sc[half][x], h0[0], h1[0], h0[1], h1[1], q[x][4 * i], q[x][4 * i + 1]);
-                            mma_f16_16816(sc[half][x], h0[2], h1[2], h0[3], h1[3], q[x][4 * i + 2], q[x][4 * i + 3]);
+                    for (int x = 0; x < NT; ++x) {
+                        uint4 b;
+                        if constexpr (kShared)
+                            b = sh.q[i][x][lane];
+                        else
+                            b = make_uint4(q[x][4 * i], q[x][4 * i + 1], q[x][4 * i + 2], q[x][4 * i + 3]);
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            mma_f16_16816(sc[half][x], h0[half][0], h1[half][0], h0[half][1], h1[half][1], b.x, b.y);
+                            mma_f16_16816(sc[half][x], h0[half][2], h1[half][2], h0[half][3], h1[half][3], b.z, b.w);
                         }
                     }
                 }
@@ -510,153 +552,159 @@ __global__ void __launch_bounds__(kRowThreads, row_blocks(NT)) row_attention_ker
     }
 }
 
-// Joins the parts of an item.  BY_ITEM, for few items of many parts: the grid's columns are the cut items, in order, and its
-// rows theirs; else the columns are the bounds, and the first that cuts an item has it.  Up to all warps take a row
-// and share out its parts.
-template <bool BY_ITEM>
-constexpr int kJoinWarps = BY_ITEM ? 16 : 8;
-
-template <bool BY_ITEM>
-__global__ void __launch_bounds__(kJoinWarps<BY_ITEM> * 32) row_join_kernel(const __grid_constant__ RowLaunch c, int shares)
+// One more part (m2, l2, o) of a row's sums.
+__device__ __forceinline__ void add_part(float &m, float &l, float4 &acc, float m2, float l2, float4 o)
 {
-    constexpr int kWarps = kJoinWarps<BY_ITEM>, kThreads = kWarps * 32, kFlight = BY_ITEM ? 8 : 4;   // parts on their way at once
-    __shared__ float4 sum[kWarps][32];
-    __shared__ float2 ml_of[kWarps];
-    __shared__ Place places[BY_ITEM ? kMaxRowShares + 1 : 1];
-    __shared__ uint16_t list[kMaxRowShares + 1];
-    __shared__ int counts[kWarps], found;
+    const float mm = fmaxf(m, m2), zero = mm == -INFINITY ? 0.f : mm;
+    const float f1 = ex2(m - zero), f2 = ex2(m2 - zero);
+    l = l * f1 + l2 * f2;
+    acc.x = fmaf(acc.x, f1, o.x * f2);
+    acc.y = fmaf(acc.y, f1, o.y * f2);
+    acc.z = fmaf(acc.z, f1, o.z * f2);
+    acc.w = fmaf(acc.w, f1, o.w * f2);
+    m = mm;
+}
+
+// A row's end: four columns a lane.
+__device__ __forceinline__ void write_row(const AttnArgs &a, size_t t, int head, int lane, float m, float l, float4 acc)
+{
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    *reinterpret_cast<uint2 *>(a.out + t * a.out_stride + head * kD + lane * 4) =
+        make_uint2(bf16x2(acc.x * inv, acc.y * inv), bf16x2(acc.z * inv, acc.w * inv));
+    if (a.lse && lane == 0)
+        a.lse[t * a.Hq + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+}
+
+// Parts `from`, `from` + `step`, ... of n, kFlight of them on their way at once; part_of(i): its number, negative for none.
+template <int kFlight, class Part>
+__device__ __forceinline__ void add_parts(const RowParts &p, int row, int lane, int from, int step, int n, Part part_of, float &m, float &l,
+                                          float4 &acc)
+{
+#pragma unroll 1
+    for (int i0 = from; i0 < n; i0 += kFlight * step) {
+        float2 ml[kFlight];
+        float4 o[kFlight];
+#pragma unroll
+        for (int k = 0; k < kFlight; ++k) {
+            const int i = i0 + k * step, part = i < n ? part_of(i) : -1;
+            ml[k] = make_float2(-INFINITY, 0.f);
+            o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (part >= 0) {
+                ml[k] = p.ml[(size_t)part * p.rows + row];
+                o[k] = reinterpret_cast<const float4 *>(p.o + ((size_t)part * p.rows + row) * kD)[lane];
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kFlight; ++k)
+            add_part(m, l, acc, ml[k].x, ml[k].y, o[k]);
+    }
+}
+
+// Joins the parts of items.  An item's parts are the end of the share before the first bound in it, and the shares that
+// begin at its bounds (but between two equal ones).  Few items, of many parts each: a block takes a row of a sequence
+// and head; its 16 warps share out the parts.
+constexpr int kJoinWarps = 16;
+
+__global__ void __launch_bounds__(kJoinWarps * 32) row_join_kernel(const __grid_constant__ RowLaunch c, int shares)
+{
+    __shared__ float4 sum[kJoinWarps][32];
+    __shared__ float2 ml_of[kJoinWarps];
+    __shared__ Place places[kMaxRowShares + 1];
+    __shared__ int lowest, highest;
     pdl_wait();
     pdl_trigger();
     const AttnArgs &a = c.a;
-    const Bound *const bound = c.parts.bound;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    auto place = [&](int i) { return BY_ITEM ? places[i] : bound[i].at; };
-    // flags before this thread's, and all of them
-    auto rank = [&](bool flag, int &total) {
-        const uint32_t votes = __ballot_sync(0xffffffffu, flag);
-        __syncthreads();
-        if (lane == 0)
-            counts[warp] = __popc(votes);
-        __syncthreads();
-        int before = __popc(votes & ((1u << lane) - 1));
-        total = 0;
-        for (int w = 0; w < kWarps; ++w) {
-            before += w < warp ? counts[w] : 0;
-            total += counts[w];
-        }
-        return before;
-    };
-    // bound i is the first that cuts its item
-    auto cuts = [&](int i) {
-        if (i < 1 || i >= shares)
-            return false;
-        const Place p = place(i), before = place(i - 1);
-        return p.cut > 0 && !(same_item(p, before) && before.cut > 0);
-    };
-    int x = blockIdx.x + 1;
-    if constexpr (BY_ITEM) {
-        for (int i = tid; i <= shares; i += kThreads)
-            places[i] = bound[i].at;
-        if (tid == 0)
-            found = 0;
-        __syncthreads();
-        int done = 0;
-        for (int base = 1; base < shares && done <= (int)blockIdx.x; base += kThreads) {
-            const bool flag = cuts(base + tid);
-            int here;
-            if (rank(flag, here) + done == (int)blockIdx.x && flag)
-                found = base + tid;
-            done += here;
+    const int b = blockIdx.x / a.cache.n_kv_heads, hk = blockIdx.x % a.cache.n_kv_heads;
+    for (int i = tid; i <= shares; i += kJoinWarps * 32)
+        places[i] = c.parts.bound[i].at;
+    const Seq s = sequence(a, b);
+    for (int k = 0; k < blocks_of(c.plan, s); ++k) {
+        if (tid == 0) {
+            lowest = shares;
+            highest = 0;
         }
         __syncthreads();
-        x = found;
-        if (x == 0)
-            return;
-    } else if (!cuts(x)) {
-        return;
-    }
-    // parts: share x - 1's part 1, then part 0 of shares x, x + 1, ... while they begin in the item (a
-    // share between two equal cuts has none)
-    const Bound here = bound[x];
-    const Place at = here.at;
-    int n = 1;
-    if (tid == 0)
-        list[0] = (uint16_t)(2 * (x - 1) + 1);
-    for (int base = x; base < shares; base += kThreads) {
-        const int i = base + tid;
-        bool in = false;
-        if (i < shares) {
-            const Place p = place(i), next = place(i + 1);
-            in = same_item(p, at) && (!same_item(next, at) || next.cut > p.cut);
-        }
-        int more;
-        const int slot = n + rank(in, more);
-        if (in)
-            list[slot] = (uint16_t)(2 * i);
-        n += more;
-        if (!same_item(place(min(base + kThreads, shares)), at))
-            break;
-    }
-    __syncthreads();
-    const int first = at.k * c.plan.tokens, rows = min(c.plan.tokens, here.n - first) * a.G;
-    int crew = 1;   // warps of a row
-    while (crew < kWarps && 4 * crew < n && 2 * crew * rows <= kWarps * (int)gridDim.y)
-        crew *= 2;
-    const int mate = warp % crew, step = kWarps / crew;   // rows of the block at a time
-    for (int base = blockIdx.y * step; base < rows; base += gridDim.y * step) {
-        const int r = base + warp / crew;
-        const bool real = r < rows;
-        float m = -INFINITY, l = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        auto add = [&](float m2, float l2, float4 o) {
-            const float mm = fmaxf(m, m2), zero = mm == -INFINITY ? 0.f : mm;
-            const float f1 = ex2(m - zero), f2 = ex2(m2 - zero);
-            l = l * f1 + l2 * f2;
-            acc.x = fmaf(acc.x, f1, o.x * f2);
-            acc.y = fmaf(acc.y, f1, o.y * f2);
-            acc.z = fmaf(acc.z, f1, o.z * f2);
-            acc.w = fmaf(acc.w, f1, o.w * f2);
-            m = mm;
-        };
-#pragma unroll 1
-        for (int i0 = mate; i0 < n && real; i0 += kFlight * crew) {
-            float2 ml[kFlight];
-            float4 o[kFlight];
-#pragma unroll
-            for (int k = 0; k < kFlight; ++k) {
-                const int i = i0 + k * crew;
-                ml[k] = make_float2(-INFINITY, 0.f);
-                o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (i < n) {
-                    const size_t part = list[i];
-                    ml[k] = c.parts.ml[part * c.parts.rows + r];
-                    o[k] = reinterpret_cast<const float4 *>(c.parts.o + (part * c.parts.rows + r) * kD)[lane];
-                }
+        for (int i = tid + 1; i < shares; i += kJoinWarps * 32) {
+            if (places[i].cut > 0 && same_item(places[i], Place{b, hk, k, 0})) {
+                atomicMin(&lowest, i);
+                atomicMax(&highest, i);
             }
-#pragma unroll
-            for (int k = 0; k < kFlight; ++k)
-                add(ml[k].x, ml[k].y, o[k]);
         }
-        if (crew > 1) {
+        __syncthreads();
+        const int x = lowest, n = highest - x + 2;   // bounds in the item, and one more part
+        const int rows = min(c.plan.tokens, s.n - k * c.plan.tokens) * a.G;
+        for (int r = blockIdx.y; r < rows && x < shares; r += gridDim.y) {
+            float m = -INFINITY, l = 0.f;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            add_parts<8>(c.parts, r, lane, warp, kJoinWarps, n, [&](int i) {
+                const int share = x - 1 + i;
+                if (i == 0)
+                    return 2 * share + 1;
+                return same_item(places[share], places[share + 1]) && places[share].cut == places[share + 1].cut ? -1 : 2 * share;
+            }, m, l, acc);
             sum[warp][lane] = acc;
             if (lane == 0)
                 ml_of[warp] = make_float2(m, l);
             __syncthreads();
-            if (mate == 0)
-#pragma unroll 1
-                for (int i = 1; i < crew; ++i)
-                    add(ml_of[warp + i].x, ml_of[warp + i].y, sum[warp + i][lane]);
+            if (warp == 0) {
+                float top = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < kJoinWarps; ++i)
+                    top = fmaxf(top, ml_of[i].x);
+                const float zero = top == -INFINITY ? 0.f : top;
+                l = 0.f;
+                acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int i = 0; i < kJoinWarps; ++i) {
+                    const float f = ex2(ml_of[i].x - zero);
+                    const float4 o = sum[i][lane];
+                    l = fmaf(ml_of[i].y, f, l);
+                    acc.x = fmaf(o.x, f, acc.x);
+                    acc.y = fmaf(o.y, f, acc.y);
+                    acc.z = fmaf(o.z, f, acc.z);
+                    acc.w = fmaf(o.w, f, acc.w);
+                }
+                write_row(a, s.t0 + k * c.plan.tokens + r / a.G, hk * a.G + r % a.G, lane, top, l, acc);
+            }
             __syncthreads();
         }
-        if (mate != 0 || !real)
-            continue;
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        const size_t t = here.t0 + first + r / a.G;
-        const int h = at.hk * a.G + r % a.G;
-        *reinterpret_cast<uint2 *>(a.out + t * a.out_stride + h * kD + lane * 4) =
-            make_uint2(bf16x2(acc.x * inv, acc.y * inv), bf16x2(acc.z * inv, acc.w * inv));
-        if (a.lse && lane == 0)
-            a.lse[t * a.Hq + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+        __syncthreads();
+    }
+}
+
+// Many items, of few parts each: a block takes the item that its bound is the first in; a warp takes a row.
+__global__ void __launch_bounds__(256) row_joins_kernel(const __grid_constant__ RowLaunch c, int shares)
+{
+    pdl_wait();
+    pdl_trigger();
+    const AttnArgs &a = c.a;
+    const Bound *const bound = c.parts.bound;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, x = blockIdx.x + 1;
+    const Bound here = bound[x];
+    const Place at = here.at, before = bound[x - 1].at;
+    if (at.cut == 0 || (same_item(at, before) && before.cut > 0))
+        return;
+    int n = 2;   // parts: a lane looks at a bound
+    for (int base = x + 1; base < shares; base += 32) {
+        const int i = base + lane;
+        const int more = __popc(__ballot_sync(0xffffffffu, i < shares && same_item(bound[min(i, shares)].at, at)));
+        n += more;
+        if (more < 32)
+            break;
+    }
+    const int first = at.k * c.plan.tokens, rows = min(c.plan.tokens, here.n - first) * a.G;
+    for (int r = warp; r < rows; r += 8) {
+        float m = -INFINITY, l = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        add_parts<4>(c.parts, r, lane, 0, 1, n, [&](int i) {
+            const int share = x - 1 + i;
+            if (i == 0)
+                return 2 * share + 1;
+            const Place p = bound[share].at, next = bound[share + 1].at;
+            return same_item(p, next) && p.cut == next.cut ? -1 : 2 * share;
+        }, m, l, acc);
+        write_row(a, here.t0 + first + r / a.G, at.hk * a.G + r % a.G, lane, m, l, acc);
     }
 }
 
@@ -675,10 +723,24 @@ static size_t carve(int nt, char *ws, RowParts *p)
     return o_o + 2 * n * (size_t)rows * kD * sizeof(float);
 }
 
-size_t row_attention_ws() { return std::max(carve(1, nullptr, nullptr), carve(2, nullptr, nullptr)); }
+size_t row_attention_ws()
+{
+    size_t n = 0;
+    for (int nt = 1; nt <= kMaxRowTiles; ++nt)
+        n = std::max(n, carve(nt, nullptr, nullptr));
+    return n;
+}
 
-// Up to 16 rows a sequence and KV head on average.
-bool takes_rows(int T, int B, int G) { return (long long)T * G <= 16ll * B; }
+// Tiles of 8 rows that hold a sequence's tokens by the group's heads, by the mean of tokens (the lengths are the device's).
+static int row_tiles(int T, int B, int G) { return (int)(((T + (long long)B - 1) / B * G + 7) / 8); }
+
+bool takes_rows(int T, int B, int G) { return row_tiles(T, B, G) <= kMaxRowTiles; }
+
+template <int NT>
+static constexpr size_t row_smem_bytes()
+{
+    return kRowWarps * row_stages(NT) * kStageBytes + sizeof(RowShared<NT>);
+}
 
 template <int NT>
 static cudaError_t launch_rows(const AttnArgs &a, cudaStream_t st)
@@ -694,36 +756,48 @@ static cudaError_t launch_rows(const AttnArgs &a, cudaStream_t st)
         n = (int)std::min<long long>(n, items);
     c.plan.inverse = ~0ull / (unsigned long long)n;
     carve(NT, static_cast<char *>(a.ws), &c.parts);
-    const size_t smem = kRowWarps * kRowStages * kStageBytes + sizeof(RowShared<NT>);
     cudaError_t e = launch_pdl(a.softcap > 0.f ? row_attention_kernel<NT, true> : row_attention_kernel<NT, false>, dim3(n),
-                               dim3(kRowThreads), smem, st, 1, c);
+                               dim3(kRowThreads), row_smem_bytes<NT>(), st, 1, c);
     if (e != cudaSuccess || n < 2 || !cuts)
         return e;
-    if (items <= sm_count())
-        return launch_pdl(row_join_kernel<true>, dim3((int)std::min<long long>(n - 1, items), 8 * NT), dim3(kJoinWarps<true> * 32), 0, st, 1, c, n);
-    return launch_pdl(row_join_kernel<false>, dim3(n - 1), dim3(kJoinWarps<false> * 32), 0, st, 1, c, n);
+    if ((long long)a.B * Hkv <= sm_count())
+        return launch_pdl(row_join_kernel, dim3(a.B * Hkv, 8 * NT), dim3(kJoinWarps * 32), 0, st, 1, c, n);
+    return launch_pdl(row_joins_kernel, dim3(n - 1), dim3(256), 0, st, 1, c, n);
 }
 
 cudaError_t launch_row_attention(const AttnArgs &a, cudaStream_t st)
 {
-    return a.G <= 8 && (long long)a.T * a.G <= 8ll * a.B ? launch_rows<1>(a, st) : launch_rows<2>(a, st);
+    switch (row_tiles(a.T, a.B, a.G)) {
+    case 1:
+        return launch_rows<1>(a, st);
+    case 2:
+        return launch_rows<2>(a, st);
+    case 3:
+        return launch_rows<3>(a, st);
+    default:
+        return launch_rows<4>(a, st);
+    }
+}
+
+template <int NT>
+static cudaError_t configure_rows()
+{
+    for (const void *f : {(const void *)row_attention_kernel<NT, false>, (const void *)row_attention_kernel<NT, true>}) {
+        cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)row_smem_bytes<NT>());
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(f, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+        if (e != cudaSuccess)
+            return e;
+    }
+    return cudaSuccess;
 }
 
 cudaError_t configure_row_attention()
 {
-    cudaError_t e = cudaSuccess;
-    auto set = [&](const void *f, size_t shared) {
-        const size_t smem = kRowWarps * kRowStages * kStageBytes + shared;
-        if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(f, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
-    };
-    set((const void *)row_attention_kernel<1, false>, sizeof(RowShared<1>));
-    set((const void *)row_attention_kernel<1, true>, sizeof(RowShared<1>));
-    set((const void *)row_attention_kernel<2, false>, sizeof(RowShared<2>));
-    set((const void *)row_attention_kernel<2, true>, sizeof(RowShared<2>));
-    return e;
+    for (auto f : {configure_rows<1>, configure_rows<2>, configure_rows<3>, configure_rows<4>})
+        if (cudaError_t e = f())
+            return e;
+    return cudaSuccess;
 }
 
 }  // namespace retopk
