@@ -601,11 +601,11 @@ __device__ __forceinline__ void add_parts(const RowParts &p, int row, int lane, 
 }
 
 // Joins the parts of items.  An item's parts are the end of the share before the first bound in it, and the shares that
-// begin at its bounds (but between two equal ones).  Few items, of many parts each: a block takes a row of a sequence
-// and head; its 16 warps share out the parts.
+// begin at its bounds (but between two equal ones).  Few items, of many parts each: a block takes rows of a sequence
+// and head, `crew` of its 16 warps a row, which share out the parts.
 constexpr int kJoinWarps = 16;
 
-__global__ void __launch_bounds__(kJoinWarps * 32) row_join_kernel(const __grid_constant__ RowLaunch c, int shares)
+__global__ void __launch_bounds__(kJoinWarps * 32) row_join_kernel(const __grid_constant__ RowLaunch c, int shares, int crew)
 {
     __shared__ float4 sum[kJoinWarps][32];
     __shared__ float2 ml_of[kJoinWarps];
@@ -634,10 +634,12 @@ __global__ void __launch_bounds__(kJoinWarps * 32) row_join_kernel(const __grid_
         __syncthreads();
         const int x = lowest, n = highest - x + 2;   // bounds in the item, and one more part
         const int rows = min(c.plan.tokens, s.n - k * c.plan.tokens) * a.G;
-        for (int r = blockIdx.y; r < rows && x < shares; r += gridDim.y) {
+        const int step = kJoinWarps / crew, mate = warp % crew;   // rows of the block at a time
+        for (int base = blockIdx.y * step; base < rows && x < shares; base += gridDim.y * step) {
+            const int r = base + warp / crew;
             float m = -INFINITY, l = 0.f;
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-            add_parts<8>(c.parts, r, lane, warp, kJoinWarps, n, [&](int i) {
+            add_parts<8>(c.parts, r, lane, mate, crew, r < rows ? n : 0, [&](int i) {
                 const int share = x - 1 + i;
                 if (i == 0)
                     return 2 * share + 1;
@@ -647,19 +649,19 @@ __global__ void __launch_bounds__(kJoinWarps * 32) row_join_kernel(const __grid_
             if (lane == 0)
                 ml_of[warp] = make_float2(m, l);
             __syncthreads();
-            if (warp == 0) {
+            if (mate == 0 && r < rows) {
                 float top = -INFINITY;
-#pragma unroll
-                for (int i = 0; i < kJoinWarps; ++i)
-                    top = fmaxf(top, ml_of[i].x);
+#pragma unroll 4
+                for (int i = 0; i < crew; ++i)
+                    top = fmaxf(top, ml_of[warp + i].x);
                 const float zero = top == -INFINITY ? 0.f : top;
                 l = 0.f;
                 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                for (int i = 0; i < kJoinWarps; ++i) {
-                    const float f = ex2(ml_of[i].x - zero);
-                    const float4 o = sum[i][lane];
-                    l = fmaf(ml_of[i].y, f, l);
+#pragma unroll 4
+                for (int i = 0; i < crew; ++i) {
+                    const float f = ex2(ml_of[warp + i].x - zero);
+                    const float4 o = sum[warp + i][lane];
+                    l = fmaf(ml_of[warp + i].y, f, l);
                     acc.x = fmaf(o.x, f, acc.x);
                     acc.y = fmaf(o.y, f, acc.y);
                     acc.z = fmaf(o.z, f, acc.z);
@@ -760,8 +762,13 @@ static cudaError_t launch_rows(const AttnArgs &a, cudaStream_t st)
                                dim3(kRowThreads), row_smem_bytes<NT>(), st, 1, c);
     if (e != cudaSuccess || n < 2 || !cuts)
         return e;
-    if ((long long)a.B * Hkv <= sm_count())
-        return launch_pdl(row_join_kernel, dim3(a.B * Hkv, 8 * NT), dim3(kJoinWarps * 32), 0, st, 1, c, n);
+    if ((long long)a.B * Hkv <= sm_count()) {
+        // (eight parts of a warp are on their way at once)
+        int crew = 1;
+        while (crew < kJoinWarps && 8 * crew * a.B * Hkv < n)
+            crew *= 2;
+        return launch_pdl(row_join_kernel, dim3(a.B * Hkv, 8 * NT * crew / kJoinWarps + 1), dim3(kJoinWarps * 32), 0, st, 1, c, n, crew);
+    }
     return launch_pdl(row_joins_kernel, dim3(n - 1), dim3(256), 0, st, 1, c, n);
 }
 
