@@ -13,7 +13,14 @@ constexpr int kCopyThreads = 128;
 // read back: 474, with 3 488, with 4 489; small blocks also start sooner: 3 x 4099 rows 7.5 us, 10.1 in blocks of 128 rows)
 __host__ __device__ constexpr int copy_rows(int src, int dst)
 {
-    return src == RETOPK_CACHE_BF16 && dst != RETOPK_CACHE_BF16 ? 3 : 2;
+    return src == RETOPK_CACHE_BF16 && dst == RETOPK_CACHE_FP4 ? 4 : src == RETOPK_CACHE_BF16 && dst == RETOPK_CACHE_MX8 ? 3 : 2;
+}
+
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b)
+{
+    uint32_t d;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
 }
 
 // Sixteen elements of a row as they are read: bf16, 8-bit or 4-bit codes.
@@ -45,6 +52,21 @@ struct Piece {
                     make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
         }
     }
+    // the largest size's fp32 bits
+    __device__ __forceinline__ uint32_t top(const float (&x)[16]) const
+    {
+        uint32_t m = 0;
+        if constexpr (FORMAT == RETOPK_CACHE_BF16) {   // two at a time, as they are
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                m = max_u16x2(m, w[i] & 0x7fff7fffu);
+            return max(m << 16, m & 0xffff0000u);
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+            m = max(m, __float_as_uint(x[e]) & 0x7fffffffu);
+        return m;
+    }
     // the elements, with the scale byte that they share
     __device__ __forceinline__ void values(uint32_t scale, float (&x)[16]) const
     {
@@ -60,7 +82,7 @@ struct Piece {
                 x[2 * i] = v.x * s, x[2 * i + 1] = v.y * s;
             }
         } else {
-            const float s = fp4_value(scale);
+            const float s = fp4_value(scale);   // (not in fp16, where scales that no call writes overflow)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 uint32_t h[4];
@@ -141,11 +163,7 @@ __global__ void __launch_bounds__(kCopyThreads)
             for (int i = 0; i < 8; ++i)
                 out.w[i] = bf16x2(x[2 * i], x[2 * i + 1]);
         } else {
-            uint32_t m = 0;
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-                m = max(m, __float_as_uint(x[e]) & 0x7fffffffu);
-            uint32_t s;
+            uint32_t m = in[u].top(x), s;
             if constexpr (DST == RETOPK_CACHE_MX8) {
                 m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
                 s = mx_scale(m);

@@ -125,7 +125,9 @@ __device__ __forceinline__ uint32_t fp4_scale(uint32_t amax_bits)
 {
     if (amax_bits >= 0x7f800000u)
         return 255u;
-    const float s = __uint_as_float(amax_bits) / 6.f;
+    const float x = __uint_as_float(amax_bits);
+    float s = x * (1.f / 6.f);
+    s = fmaf(fmaf(-6.f, s, x), 1.f / 6.f, s);   // (a sixth itself, where it has one: see below)
     const uint32_t u = __float_as_uint(s);
     const uint32_t byte = s < 0x1p-14f ? (uint32_t)rintf(s * 0x1p17f) : ((u + 0x7ffffu + (u >> 20 & 1u)) >> 20) - (112u << 3);
     return min(byte, kFp4Top);
@@ -142,20 +144,20 @@ __device__ __forceinline__ float fp4_value(uint32_t byte)
 // the product leaves, x - q s, is exact, and adding its quotient brings q to the border itself.
 __device__ __forceinline__ uint32_t e2m1x8(const float *x, float s)
 {
-    const float r = s > 0.f ? 1.f / s : 0.f;
-    uint32_t w = 0;
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+    r = s > 0.f ? r : 0.f;
+    float q[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        float q[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            q[k] = x[2 * i + k] * r;
-            q[k] = fmaf(fmaf(-q[k], s, x[2 * i + k]), r, q[k]);
-        }
-        uint32_t c;
-        asm("{\n .reg .b8 b;\n cvt.rn.satfinite.e2m1x2.f32 b, %1, %2;\n cvt.u32.u8 %0, b;\n}\n" : "=r"(c) : "f"(q[1]), "f"(q[0]));
-        w |= c << 8 * i;
+    for (int i = 0; i < 8; ++i) {
+        q[i] = x[i] * r;
+        q[i] = fmaf(fmaf(-q[i], s, x[i]), r, q[i]);
     }
+    uint32_t w;
+    asm("{\n .reg .b8 a, b, c, d;\n cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
+        " cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n mov.b32 %0, {a, b, c, d};\n}\n"
+        : "=r"(w)
+        : "f"(q[0]), "f"(q[1]), "f"(q[2]), "f"(q[3]), "f"(q[4]), "f"(q[5]), "f"(q[6]), "f"(q[7]));
     return w;
 }
 
