@@ -265,23 +265,16 @@ __global__ void __launch_bounds__(kRowThreads, row_blocks(NT)) row_attention_ker
             asm volatile("cp.async.commit_group;" ::: "memory");
             to = to + kStageBytes == ring + kRowStages * kStageBytes ? ring : to + kStageBytes;
         };
-#pragma unroll
-        for (int t = 0; t < kRowStages - 1; ++t)
-            issue(t);
-        if (tid == 0)
-            sh.segments[(n + 1) & 1].more = next_segment(a, c.plan, sh.walk, sh.segments[(n + 1) & 1]);
-
         // ---- the queries: column g of each 8, this lane's 32 elements, as fp16 of at most 2^15
         uint32_t q[kShared ? 1 : NT][16];
         float factor[NT][2];             // of a column's scores: in powers of two, or over the cap
         int hi[NT][2];                   // the last key that a column sees
-        auto query = [&](int x, uint32_t (&q)[16]) {
+        auto ask = [&](int x, uint32_t (&w)[16]) {
             const int r = 8 * x + g, tok = r / G;
-            uint32_t w[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i)
                 w[i] = 0;
-            if (tok < tokens) {
+            if (x < NT && tok < tokens) {
                 const uint4 *src = reinterpret_cast<const uint4 *>(a.q + (long long)(s.seq.t0 + tok0 + tok) * a.q_stride +
                                                                    (s.hk * G + r % G) * kD + t4 * 32);
 #pragma unroll
@@ -290,17 +283,19 @@ __global__ void __launch_bounds__(kRowThreads, row_blocks(NT)) row_attention_ker
                     w[4 * i] = y.x, w[4 * i + 1] = y.y, w[4 * i + 2] = y.z, w[4 * i + 3] = y.w;
                 }
             }
+        };
+        auto scaled = [&](uint32_t (&q)[16]) {   // in place; the power of two
             uint32_t top = 0;
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-                top = max(top, max(w[i] << 16 & 0x7fffffffu, w[i] & 0x7fff0000u));
+                top = max(top, max(q[i] << 16 & 0x7fffffffu, q[i] & 0x7fff0000u));
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
             const int e = top == 0 ? 0 : max((int)(top >> 23) - 127 - 14, -100);
             const float down = __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-                q[i] = f16x2(bf16lo(w[i]) * down, bf16hi(w[i]) * down);
+                q[i] = f16x2(bf16lo(q[i]) * down, bf16hi(q[i]) * down);
             return e;
         };
         auto columns = [&](int x, int k, int e) {
@@ -310,14 +305,29 @@ __global__ void __launch_bounds__(kRowThreads, row_blocks(NT)) row_attention_ker
             factor[x][k] = CAP ? fminf(a.scale * up / a.softcap, 3e38f) : fmaxf(a.scale * 1.4426950408889634f * up, 1e-38f);
             hi[x][k] = min(first + col / G, last);
         };
+        // they are asked for before the keys, whose copies would hold them up
+        static_assert(NT <= kRowWarps, "a warp makes one tile of shared queries");
         if constexpr (kShared) {
-            for (int x = warp; x < NT; x += kRowWarps) {
-                const int e = query(x, q[0]);
+            ask(warp, q[0]);
+        } else {
+#pragma unroll
+            for (int x = 0; x < NT; ++x)
+                ask(x, q[x]);
+        }
+#pragma unroll
+        for (int t = 0; t < kRowStages - 1; ++t)
+            issue(t);
+        if (tid == 0)
+            sh.segments[(n + 1) & 1].more = next_segment(a, c.plan, sh.walk, sh.segments[(n + 1) & 1]);
+
+        if constexpr (kShared) {
+            const int e = scaled(q[0]);
+            if (warp < NT) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    sh.q[i][x][lane] = make_uint4(q[0][4 * i], q[0][4 * i + 1], q[0][4 * i + 2], q[0][4 * i + 3]);
+                    sh.q[i][warp][lane] = make_uint4(q[0][4 * i], q[0][4 * i + 1], q[0][4 * i + 2], q[0][4 * i + 3]);
                 if (t4 == 0)
-                    sh.exponent[8 * x + g] = e;
+                    sh.exponent[8 * warp + g] = e;
             }
             __syncthreads();
 #pragma unroll
@@ -328,12 +338,13 @@ __global__ void __launch_bounds__(kRowThreads, row_blocks(NT)) row_attention_ker
         } else {
 #pragma unroll
             for (int x = 0; x < NT; ++x) {
-                const int e = query(x, q[x]);
+                const int e = scaled(q[x]);
 #pragma unroll
                 for (int k = 0; k < 2; ++k)
                     columns(x, k, __shfl_sync(0xffffffffu, e, (2 * t4 + k) * 4));
             }
         }
+
         // what the scores that the softmax sees are multiplied by, to be in powers of two
         const float cap2 = fmaxf(a.softcap * 1.4426950408889634f, 1e-38f);
         auto unit = [&](int x, int k) { return CAP ? cap2 : factor[x][k]; };
@@ -602,8 +613,8 @@ __device__ __forceinline__ void add_parts(const RowParts &p, int row, int lane, 
 
 // Joins the parts of items.  An item's parts are the end of the share before the first bound in it, and the shares that
 // begin at its bounds (but between two equal ones).  Few items, of many parts each: a block takes rows of a sequence
-// and head, `crew` of its 16 warps a row, which share out the parts.
-constexpr int kJoinWarps = 16;
+// and head, `crew` of its 32 warps a row, which share out the parts.
+constexpr int kJoinWarps = 32;
 
 __global__ void __launch_bounds__(kJoinWarps * 32) row_join_kernel(const __grid_constant__ RowLaunch c, int shares, int crew)
 {
@@ -625,10 +636,12 @@ __global__ void __launch_bounds__(kJoinWarps * 32) row_join_kernel(const __grid_
             highest = 0;
         }
         __syncthreads();
-        for (int i = tid + 1; i < shares; i += kJoinWarps * 32) {
-            if (places[i].cut > 0 && same_item(places[i], Place{b, hk, k, 0})) {
-                atomicMin(&lowest, i);
-                atomicMax(&highest, i);
+        for (int base = 0; base < shares; base += kJoinWarps * 32) {
+            const int i = base + tid;
+            const uint32_t in = __ballot_sync(0xffffffffu, i > 0 && i < shares && places[i].cut > 0 && same_item(places[i], Place{b, hk, k, 0}));
+            if (in && lane == 0) {
+                atomicMin(&lowest, i + __ffs(in) - 1);
+                atomicMax(&highest, i + 31 - __clz(in));
             }
         }
         __syncthreads();
@@ -639,7 +652,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) row_join_kernel(const __grid_
             const int r = base + warp / crew;
             float m = -INFINITY, l = 0.f;
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-            add_parts<8>(c.parts, r, lane, mate, crew, r < rows ? n : 0, [&](int i) {
+            add_parts<5>(c.parts, r, lane, mate, crew, r < rows ? n : 0, [&](int i) {
                 const int share = x - 1 + i;
                 if (i == 0)
                     return 2 * share + 1;
@@ -763,9 +776,9 @@ static cudaError_t launch_rows(const AttnArgs &a, cudaStream_t st)
     if (e != cudaSuccess || n < 2 || !cuts)
         return e;
     if ((long long)a.B * Hkv <= sm_count()) {
-        // (eight parts of a warp are on their way at once)
+        // (five parts of a warp are on their way at once)
         int crew = 1;
-        while (crew < kJoinWarps && 8 * crew * a.B * Hkv < n)
+        while (crew < kJoinWarps && 5 * crew * a.B * Hkv < n)
             crew *= 2;
         return launch_pdl(row_join_kernel, dim3(a.B * Hkv, 8 * NT * crew / kJoinWarps + 1), dim3(kJoinWarps * 32), 0, st, 1, c, n, crew);
     }
