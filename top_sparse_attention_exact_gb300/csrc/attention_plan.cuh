@@ -6,8 +6,8 @@
 // the device.  A CTA that has a part of an item leaves its rows, unnormalised, in the
 // workspace for a join.  Shares, and with them the order of every sum, depend on the lengths alone.
 //
-// `Cost` is the kernel's: kItem, the weight of an item beside its keys, and grain(tiles), the number of
-// tiles that an item of so many is cut by.
+// `Cost` is the kernel's: kItem, the weight of an item beside its keys, and grain(plan, tiles), the number
+// of tiles that an item of so many is cut by.
 #pragma once
 
 #include "prompt.cuh"
@@ -30,6 +30,7 @@ __device__ __forceinline__ bool same_item(const Place &x, const Place &y)
 struct Plan {
     int tokens;                    // tokens of a block (two tiles', or one tile's)
     unsigned long long inverse;    // 2^64 / shares
+    int uncut;                     // tiles of an item that is not cut (row attention)
 };
 
 // Tokens, first token and rows of a sequence.
@@ -102,7 +103,7 @@ __device__ __forceinline__ Place place_in(const AttnArgs &a, const Plan &p, cons
     int lo, hi;
     tiles_of(a, p, s, r.k, lo, hi);
     const long long begin = weight<Cost>(a, p, s, r.k);
-    const int nt = hi - lo, grain = Cost::grain(nt);
+    const int nt = hi - lo, grain = Cost::grain(p, nt);
     // (half the item's own weight lies before its first tile, half behind its last)
     const int in = (int)(u - begin) - Cost::kItem / 2, keys = (int)(weight<Cost>(a, p, s, r.k + 1) - begin) - Cost::kItem;
     const int x = (int)(__fdividef((float)max(in, 0), (float)keys) * nt);

@@ -77,7 +77,7 @@ struct ChunkCost {
     static constexpr int kItem = 512;
     // short items are cut into no small parts: joining costs more than it gives (8 sequences of 50 tokens over 1000
     // keys 29 us, cut anywhere 32); long ones anywhere (4 of 19 over 9000 keys 32 us, by fours 34)
-    static __device__ __forceinline__ int grain(int nt) { return nt >= 64 ? 1 : nt >= 16 ? 2 : 4; }
+    static __device__ __forceinline__ int grain(const Plan &, int nt) { return nt >= 64 ? 1 : nt >= 16 ? 2 : 4; }
 };
 constexpr float kLazy = 8.f;                     // growth of m, in powers of two, that is left to the accumulators
 // Over 4-bit rows V is fp16 and so is P: m lies 2^7 below the maximum, so that weights reach from 2^15 down to fp16's 2^-24
