@@ -1269,8 +1269,8 @@ __global__ void __launch_bounds__(FP4 ? kFp4Threads : kAttnThreads, 1)
 template <bool TWO>
 __global__ void __launch_bounds__(256) join_kernel(const AttnLaunch c, int shares)
 {
-    __shared__ float4 sum[8][32];
-    __shared__ float2 ml_of[8];
+    __shared__ float4 sum[8][8][32];
+    __shared__ float2 ml_of[8][8];
     __shared__ Bound bounds[kMaxShares + 1];
     __shared__ uint16_t list[kMaxShares + 1];   // the item's parts
     __shared__ int counts[8], first_cut;
@@ -1328,69 +1328,103 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnLaunch c, int share
     if (in)
         list[slot] = (uint16_t)(2 * tid + (tid == x - 1));
     __syncthreads();
+    // Eight rows lie side by side in a part, so a warp takes them together, all columns: lane (r, q) those of four numbered
+    // 4 k + q of row r.  (A row a warp: a prompt of 2000 tokens over 4-bit rows 71 us, 67; 64 tokens over 8000 32, 25; 36 over 17663 bf16 ones, 16 over 2 heads, 39, 25.)
+    constexpr int kUnit = 8;
     const int tile_tokens = kTile / a.G, per_tile = tile_tokens * a.G, first = at.k * c.plan.tokens;
-    const int rows = min(TWO ? 2 * per_tile : per_tile, (here.n - first) * a.G);
-    int crew = 1;   // warps of a row
-    while (crew < 8 && 4 * crew < n && 2 * crew * rows <= 8 * (int)gridDim.y)
+    const int units = TWO ? 2 * kTile / kUnit : (min(per_tile, (here.n - first) * a.G) + kUnit - 1) / kUnit;
+    int crew = 1;   // warps of a unit
+    while (crew < 8 && 2 * crew < n && 2 * crew * units <= 8 * (int)gridDim.y)
         crew *= 2;
-    const int mate = warp % crew, step = 8 / crew;   // rows of the block at a time
-    for (int base = blockIdx.y * step; base < rows; base += gridDim.y * step) {
-        const int r0 = base + warp / crew;
-        const bool real = r0 < rows;
-        const int second = r0 >= per_tile, in_tile = r0 - second * per_tile;
-        const int r = second * kTile + in_tile;
+    const int mate = warp % crew, step = 8 / crew, q = lane / kUnit;   // step: units of the block at a time
+    for (int base = blockIdx.y * step; base < units; base += gridDim.y * step) {
+        const int unit = base + warp / crew, r = unit * kUnit + lane % kUnit, in_tile = r % kTile;
+        const int tok = first + r / kTile * tile_tokens + in_tile / a.G;
+        const bool valid = unit < units && in_tile < per_tile && tok < here.n;
+        const bool real = __any_sync(0xffffffffu, valid);
         float m = -INFINITY, l = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        auto add = [&](float m2, float l2, float4 o) {
-            const float mm = fmaxf(m, m2), zero = mm == -INFINITY ? 0.f : mm;
-            const float f1 = ex2(m - zero), f2 = m2 == -INFINITY ? 0.f : ex2(m2 - zero);
-            l = l * f1 + l2 * f2;
+        float4 acc[kUnit];
+#pragma unroll
+        for (int k = 0; k < kUnit; ++k)
+            acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        auto add = [](float4 &sum, float f1, float f2, float4 o) {
             // (a part without a row's keys may hold anything)
-            acc.x = fmaf(acc.x, f1, f2 != 0.f ? o.x * f2 : 0.f);
-            acc.y = fmaf(acc.y, f1, f2 != 0.f ? o.y * f2 : 0.f);
-            acc.z = fmaf(acc.z, f1, f2 != 0.f ? o.z * f2 : 0.f);
-            acc.w = fmaf(acc.w, f1, f2 != 0.f ? o.w * f2 : 0.f);
+            sum.x = fmaf(sum.x, f1, f2 != 0.f ? o.x * f2 : 0.f);
+            sum.y = fmaf(sum.y, f1, f2 != 0.f ? o.y * f2 : 0.f);
+            sum.z = fmaf(sum.z, f1, f2 != 0.f ? o.z * f2 : 0.f);
+            sum.w = fmaf(sum.w, f1, f2 != 0.f ? o.w * f2 : 0.f);
+        };
+        auto factors = [](float &m, float m2, float &f1, float &f2) {
+            const float mm = fmaxf(m, m2), zero = mm == -INFINITY ? 0.f : mm;
+            f1 = ex2(m - zero);
+            f2 = m2 == -INFINITY ? 0.f : ex2(m2 - zero);
             m = mm;
         };
 #pragma unroll 1
-        for (int i0 = mate; i0 < n && real; i0 += 4 * crew) {   // four parts on their way at once
-            float2 ml[4];
-            float4 o[4];
+        for (int i0 = mate; i0 < n && real; i0 += 2 * crew) {   // two parts on their way at once
+            float2 ml[2];
+            float4 o[2][kUnit];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int i = i0 + k * crew;
-                ml[k] = make_float2(-INFINITY, 0.f);
-                o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int x = 0; x < 2; ++x) {
+                const int i = i0 + x * crew;
+                ml[x] = make_float2(-INFINITY, 0.f);
                 if (i < n) {
                     const size_t part = list[i];
-                    ml[k] = c.parts.ml[part * c.parts.rows + r];
-                    o[k] = c.parts.o[(part * (kD / 4) + lane) * c.parts.rows + r];
+                    ml[x] = c.parts.ml[part * c.parts.rows + r];
+#pragma unroll
+                    for (int k = 0; k < kUnit; ++k)
+                        o[x][k] = c.parts.o[(part * (kD / 4) + 4 * k + q) * c.parts.rows + r];
                 }
             }
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                add(ml[k].x, ml[k].y, o[k]);
+            for (int x = 0; x < 2; ++x) {
+                if (i0 + x * crew >= n)
+                    break;
+                float f1, f2;
+                factors(m, ml[x].x, f1, f2);
+                l = l * f1 + ml[x].y * f2;
+#pragma unroll
+                for (int k = 0; k < kUnit; ++k)
+                    add(acc[k], f1, f2, o[x][k]);
+            }
         }
-        if (crew > 1) {
-            sum[warp][lane] = acc;
-            if (lane == 0)
-                ml_of[warp] = make_float2(m, l);
-            __syncthreads();
-            if (mate == 0)
-#pragma unroll 1
-                for (int i = 1; i < crew; ++i)
-                    add(ml_of[warp + i].x, ml_of[warp + i].y, sum[warp + i][lane]);
-            __syncthreads();
-        }
-        if (mate != 0 || !real)
-            continue;
-        const int tok = first + second * tile_tokens + in_tile / a.G;
-        const float inv = l == 0.f ? 0.f : 1.f / l;
         const size_t t = here.t0 + tok;
         const int h = at.hk * a.G + in_tile % a.G;
-        *reinterpret_cast<uint2 *>(a.out + t * a.out_stride + h * kD + lane * 4) =
-            make_uint2(bf16x2(acc.x * inv, acc.y * inv), bf16x2(acc.z * inv, acc.w * inv));
-        if (a.lse && lane == 0)
+        auto write = [&](int k, float4 y, float l) {
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            if (valid)
+                *reinterpret_cast<uint2 *>(a.out + t * a.out_stride + h * kD + (4 * k + q) * 4) =
+                    make_uint2(bf16x2(y.x * inv, y.y * inv), bf16x2(y.z * inv, y.w * inv));
+        };
+        if (crew > 1) {   // the crew's sums meet, and each mate ends its columns
+#pragma unroll
+            for (int k = 0; k < kUnit; ++k)
+                sum[warp][k][lane] = acc[k];
+            if (q == 0)
+                ml_of[warp][lane] = make_float2(m, l);
+            __syncthreads();
+            const int w0 = warp - mate;
+#pragma unroll 1
+            for (int k = mate; k < kUnit; k += crew) {
+                m = -INFINITY, l = 0.f;
+                float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+                for (int i = 0; i < crew; ++i) {
+                    const float2 ml = ml_of[w0 + i][lane % kUnit];
+                    float f1, f2;
+                    factors(m, ml.x, f1, f2);
+                    l = l * f1 + ml.y * f2;
+                    add(y, f1, f2, sum[w0 + i][k][lane]);
+                }
+                write(k, y, l);
+            }
+            __syncthreads();
+        } else {
+#pragma unroll
+            for (int k = 0; k < kUnit; ++k)
+                write(k, acc[k], l);
+        }
+        if (a.lse && valid && mate == 0 && q == 0)
             a.lse[t * a.Hq + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
     }
 }
@@ -1461,7 +1495,7 @@ static cudaError_t launch_mode(const CUtensorMap &qm, const CUtensorMap &km, con
         return e;
     // the items that may be cut, and blocks for each: few items have many parts
     const int cut = TWO ? (int)std::min<long long>(n - 1, c.items) : n - 1;
-    const int each = TWO ? std::max(8, std::min(64, 1216 / cut)) : 8;
+    const int each = TWO ? std::max(8, std::min(32, 1216 / cut)) : 8;
     return launch_pdl(join_kernel<TWO>, dim3(cut, each), dim3(256), 0, st, 1, c, n);
 }
 
