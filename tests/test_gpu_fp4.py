@@ -447,6 +447,9 @@ ATTEND = [  # tokens of each sequence, rows in all, Hq, Hkv, page, window, cap
     ([2, 90], [800, 700], 8, 2, 0, 0, 1e-3),                        # and far below
     ([1, 1], [800, 700], 8, 2, 0, 0, 1e6),
     ([1, 1], [800, 700], 8, 2, 0, 0, 1e-3),
+    ([1, 2], [800, 700], 8, 2, 0, 200, 1e-30),
+    ([1, 2], [800, 700], 8, 2, 0, 0, 3e38),
+    ([2, 90], [800, 700], 8, 2, 0, 200, 1e-30),
     ([2, 90], [800, 700], 8, 2, 0, (1 << 31) - 1, 0.0),             # a window wider than any history
     ([1, 1], [800, 700], 8, 2, 0, 1 << 23, 12.0),
 ]
@@ -500,6 +503,16 @@ def test_attention_one_token_each_without_offsets(B, L):
     same = q.clone()
     assert retopk.chunk_attention(same, c.h, i32([L] * B), same, scale=0.3) is same      # out may be q
     assert torch.equal(same, out)
+
+
+@pytest.mark.parametrize("n", [[1, 1], [1, 40]])
+def test_attention_zero_scores_under_any_cap(n):
+    L = [300, 600]
+    q, c = setup(n, L, 8, 2, 0, 25)
+    q.zero_()
+    for cap in (1e-38, 1e-30, 1e-8, 3.0, 1e30, 3e38):
+        out = retopk.chunk_attention(q, c.h, i32(L), cu_tokens=offsets(n), softcap=cap)
+        check(q, n, L, c, out, None, 1 / math.sqrt(D), 0.0, 0)     # all weights equal
 
 
 @pytest.mark.parametrize("n", [[1, 1], [3, 2], [1, 40]])

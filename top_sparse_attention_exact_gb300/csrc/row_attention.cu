@@ -148,12 +148,13 @@ __device__ __forceinline__ void copy8(uint32_t dst, const void *src, bool there)
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(there ? 8 : 0) : "memory");
 }
 
-// tanh(y), |y| < 1/2 by the polynomial of chunk_attention.cu (6.4e-7 of the value).
-__device__ __forceinline__ float tanh_of(float y)
+// cap tanh(x / cap), up to half the cap by the polynomial of chunk_attention.cu (6.4e-7 of the value): a cap far above the
+// scores leaves them as they are.
+__device__ __forceinline__ float capped(float x, float cap, float inverse)
 {
-    const float t = y * y;
-    const float small = y * fmaf(fmaf(fmaf(-0.04475064703577332f, t, 0.132053598066859f), t, -0.3332815934197915f), t, 1.f);
-    const float large = fmaf(-2.f, rcp(1.f + ex2(y * 2.885390081777927f)), 1.f);
+    const float y = x * inverse, t = y * y;
+    const float small = x * fmaf(fmaf(fmaf(-0.04475064703577332f, t, 0.132053598066859f), t, -0.3332815934197915f), t, 1.f);
+    const float large = fmaf(-2.f * cap, rcp(1.f + ex2(y * 2.885390081777927f)), cap);
     return fabsf(y) < 0.5f ? small : large;
 }
 
@@ -267,7 +268,7 @@ __global__ void __launch_bounds__(kRowThreads, row_blocks(NT)) row_attention_ker
         };
         // ---- the queries: column g of each 8, this lane's 32 elements, as fp16 of at most 2^15
         uint32_t q[kShared ? 1 : NT][16];
-        float factor[NT][2];             // of a column's scores: in powers of two, or over the cap
+        float factor[NT][2];             // of a column's scores, to be in powers of two
         int hi[NT][2];                   // the last key that a column sees
         auto ask = [&](int x, uint32_t (&w)[16]) {
             const int r = 8 * x + g, tok = r / G;
@@ -302,7 +303,7 @@ __global__ void __launch_bounds__(kRowThreads, row_blocks(NT)) row_attention_ker
             const int col = 8 * x + 2 * t4 + k;
             const float up = __uint_as_float((uint32_t)(127 + e) << 23);
             // (never zero, as a hidden score is -inf and has to stay so)
-            factor[x][k] = CAP ? fminf(a.scale * up / a.softcap, 3e38f) : fmaxf(a.scale * 1.4426950408889634f * up, 1e-38f);
+            factor[x][k] = fmaxf(a.scale * 1.4426950408889634f * up, 1e-38f);
             hi[x][k] = min(first + col / G, last);
         };
         // they are asked for before the keys, whose copies would hold them up
@@ -345,9 +346,9 @@ __global__ void __launch_bounds__(kRowThreads, row_blocks(NT)) row_attention_ker
             }
         }
 
-        // what the scores that the softmax sees are multiplied by, to be in powers of two
-        const float cap2 = fmaxf(a.softcap * 1.4426950408889634f, 1e-38f);
-        auto unit = [&](int x, int k) { return CAP ? cap2 : factor[x][k]; };
+        // (capped scores have that factor before the softmax sees them)
+        const float cap2 = a.softcap * 1.4426950408889634f, over_cap = fminf(1.f / cap2, 3e38f);
+        auto unit = [&](int x, int k) { return CAP ? 1.f : factor[x][k]; };
 
         // ---- the tiles
         float o[NT][8][4], m[NT][2], l[NT][2];
@@ -408,13 +409,13 @@ __global__ void __launch_bounds__(kRowThreads, row_blocks(NT)) row_attention_ker
                         }
                     }
                 }
-                // capped scores over the cap; hidden ones -inf
+                // capped; hidden ones -inf
                 if (CAP) {
 #pragma unroll
                     for (int x = 0; x < NT; ++x)
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
-                            sc[i >> 2][x][i & 3] = tanh_of(sc[i >> 2][x][i & 3] * factor[x][i & 1]);
+                            sc[i >> 2][x][i & 3] = capped(sc[i >> 2][x][i & 3] * factor[x][i & 1], cap2, over_cap);
                 }
                 if (pos + kWarpKeys - 1 > first || (a.window > 0 && pos < last - a.window + 1)) {
 #pragma unroll
