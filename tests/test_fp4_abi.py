@@ -46,6 +46,35 @@ def test_copies_between_pools_that_overlap_are_refused(lib):
         assert copy(lib, a, b) == -1 and copy(lib, b, a) == -1
 
 
+def test_copies_between_scales_that_overlap_are_refused(lib):
+    a, far = cache(), dict(k=P + (1 << 27), v=P + (1 << 28), k_scale=P + (1 << 29), v_scale=P + (1 << 30))   # scales of 6400 bytes
+    for kw in (dict(k_scale=P + (1 << 25) + 6392), dict(v_scale=P + (1 << 25)), dict(v_scale=P + (1 << 26) - 6392), dict(k_scale=P + 51192),
+               dict(v=P + (1 << 25) - 51184)):
+        b = cache(**{**far, **kw})
+        assert copy(lib, a, b) == -1 and copy(lib, b, a) == -1
+    b = cache(format=1, **{**far, "k_scale": P + (1 << 26) + 3196})       # of 3200 bytes
+    assert copy(lib, a, b) == -1 and copy(lib, b, a) == -1
+
+
+def test_attention_takes_4_bit_caches_and_checks_them(lib):
+    n = lib.retopk_chunk_attention_workspace_bytes(2, 2, 8, 4)
+
+    def attend(c, q=P + (1 << 27), ws=P + (1 << 28), size=n):
+        return lib.retopk_chunk_attention(q, 1024, ctypes.addressof(c), None, 2, 2, 8, P, 0.0, 0.0, 0, P + (1 << 29), 1024, None, ws, size, None, None)
+    for kw, rc in ((dict(k_scale=None), -1), (dict(v_scale=P + 4), -5), (dict(k=P + 8), -5), (dict(page_rows=0), -1), (dict(format=1), -2)):
+        assert attend(cache(**kw)) == rc
+    assert attend(cache(), q=P + 2) == -5 and attend(cache(), size=n - 1) == -3 and attend(cache(), ws=P + 128) == -3
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(28, 4), (32, 8), (16, 1), (8, 8), (7, 1)])
+def test_a_workspace_of_the_largest_call_is_enough_for_smaller_ones(lib, Hq, Hkv):
+    n = lib.retopk_chunk_attention_workspace_bytes
+    sizes = [1, 2, 5, 64, 608, 4096]
+    at = {(T, B): n(T, B, Hq, Hkv) for T in sizes for B in sizes}
+    for (T, B), most in at.items():
+        assert all(size <= most for (T2, _), size in at.items() if T2 <= T)
+
+
 def test_python_handles_check_their_tensors():
     z = lambda *s: torch.zeros(s, dtype=torch.uint8)  # noqa: E731
     c, s = z(2, 4, 32, 64), z(2, 4, 32, 8)

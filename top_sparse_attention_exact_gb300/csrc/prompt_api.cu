@@ -55,6 +55,11 @@ size_t pool_bytes(const retopk_cache &c)
     return (size_t)c.n_pages * c.n_kv_heads * c.page_rows * row_bytes(c.format);
 }
 
+size_t scale_bytes(const retopk_cache &c)
+{
+    return (size_t)c.n_pages * c.n_kv_heads * c.page_rows * row_scales(c.format);
+}
+
 // A strided [T, heads, 128] tensor.
 int check_rows(const void *p, int64_t stride, int heads)
 {
@@ -66,7 +71,7 @@ int check_rows(const void *p, int64_t stride, int heads)
 // Bytes [p, p + n) and [q, q + m).
 bool meet(const void *p, size_t n, const void *q, size_t m)
 {
-    return (uintptr_t)p < (uintptr_t)q + m && (uintptr_t)q < (uintptr_t)p + n;
+    return n && m && (uintptr_t)p < (uintptr_t)q + m && (uintptr_t)q < (uintptr_t)p + n;
 }
 
 // Whether two strided [T, heads, 128] tensors share an element; of two whose rows lie between each other's, those of one
@@ -225,6 +230,18 @@ int retopk_cache_copy(const retopk_cache *src, const retopk_cache *dst, const in
     for (const void *x : {src->k, src->v})
         for (const void *y : {dst->k, dst->v})
             if (meet(x, pool_bytes(*src), y, pool_bytes(*dst)))
+                return RETOPK_ERR_INVALID;
+    for (const void *y : {(const void *)dst->k_scale, (const void *)dst->v_scale}) {   // (no bytes of bf16 rows)
+        for (const void *x : {(const void *)src->k_scale, (const void *)src->v_scale})
+            if (meet(x, scale_bytes(*src), y, scale_bytes(*dst)))
+                return RETOPK_ERR_INVALID;
+        for (const void *x : {src->k, src->v})
+            if (meet(x, pool_bytes(*src), y, scale_bytes(*dst)))
+                return RETOPK_ERR_INVALID;
+    }
+    for (const void *x : {(const void *)src->k_scale, (const void *)src->v_scale})
+        for (const void *y : {dst->k, dst->v})
+            if (meet(x, scale_bytes(*src), y, pool_bytes(*dst)))
                 return RETOPK_ERR_INVALID;
     return cuda_rc(launch_cache_copy(*src, *dst, first, last, B, max_rows, d_status, (cudaStream_t)stream));
 }
