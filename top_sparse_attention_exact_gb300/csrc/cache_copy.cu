@@ -89,13 +89,34 @@ struct Piece {
                 e2m1x8_halves(w[i], h);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const float2 v = __half22float2(reinterpret_cast<const __half2 &>(h[k]));
-                    x[8 * i + 2 * k] = v.x * s, x[8 * i + 2 * k + 1] = v.y * s;
+                    const float2 v = mul2(__half22float2(reinterpret_cast<const __half2 &>(h[k])), make_float2(s, s));
+                    x[8 * i + 2 * k] = v.x, x[8 * i + 2 * k + 1] = v.y;
                 }
             }
         }
     }
 };
+
+// cache_row with a division by the page's rows that is a product: both are below 2^23, so it is off by one at most.
+__device__ __forceinline__ long long row_of(const retopk_cache &c, float inverse, int b, int hk, int pos, uint32_t *status)
+{
+    int page = b, r = pos;
+    if (c.table) {
+        int i = (int)((float)pos * inverse);
+        r -= i * c.page_rows;
+        if (r < 0)
+            r += c.page_rows, --i;
+        else if (r >= c.page_rows)
+            r -= c.page_rows, ++i;
+        page = c.table[(long long)b * c.table_width + i];
+        if ((uint32_t)page >= (uint32_t)c.n_pages) {
+            if (status)
+                atomicOr(status, RETOPK_STATUS_BAD_PAGE);
+            return -1;
+        }
+    }
+    return ((long long)page * c.n_kv_heads + hk) * c.page_rows + r;
+}
 
 // 8 lanes a row, 16 elements a lane.
 template <int SRC, int DST>
@@ -120,6 +141,7 @@ __global__ void __launch_bounds__(kCopyThreads)
     char *dk = static_cast<char *>(isv ? dst.v : dst.k);
     const uint8_t *ss = isv ? src.v_scale : src.k_scale;
     uint8_t *ds = isv ? dst.v_scale : dst.k_scale;
+    const float src_inverse = 1.f / src.page_rows, dst_inverse = 1.f / dst.page_rows;
     // all rows of the block are on their way before the first is written
     long long rd[kCopyRows];
     Piece<SRC> in[kCopyRows];
@@ -130,8 +152,8 @@ __global__ void __launch_bounds__(kCopyThreads)
         long long rs = -1;
         rd[u] = -1;
         if (pos >= 0 && pos < end) {
-            rs = cache_row(src, b, hk, (int)pos, status);
-            rd[u] = cache_row(dst, b, hk, (int)pos, status);
+            rs = row_of(src, src_inverse, b, hk, (int)pos, status);
+            rd[u] = row_of(dst, dst_inverse, b, hk, (int)pos, status);
         }
         if (rs < 0 || rd[u] < 0) {
             rd[u] = -1;
@@ -174,8 +196,8 @@ __global__ void __launch_bounds__(kCopyThreads)
             } else {
                 s = fp4_scale(m);
                 const float f = fp4_value(s);
-                out.w[0] = e2m1x8(x, f);
-                out.w[1] = e2m1x8(x + 8, f);
+                out.w[0] = e2m1x8<true>(x, f);
+                out.w[1] = e2m1x8<true>(x + 8, f);
             }
             if (ok && lane % (8 / kDstScales) == 0)
                 ds[rd[u] * kDstScales + lane / (8 / kDstScales)] = (uint8_t)s;

@@ -138,29 +138,6 @@ __device__ __forceinline__ float fp4_value(uint32_t byte)
     return __half2float(__ushort_as_half((unsigned short)(byte << 7)));
 }
 
-// Eight elements as codes, the first in the low bits: x / s rounded once to the nearest
-// code, ties to the even one.  s has 4 significant bits and a border between two codes at most 3,
-// so bf16 elements do lie on borders, where a product with 1 / s would fall to either side.  What
-// the product leaves, x - q s, is exact, and adding its quotient brings q to the border itself.
-__device__ __forceinline__ uint32_t e2m1x8(const float *x, float s)
-{
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
-    r = s > 0.f ? r : 0.f;
-    float q[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        q[i] = x[i] * r;
-        q[i] = fmaf(fmaf(-q[i], s, x[i]), r, q[i]);
-    }
-    uint32_t w;
-    asm("{\n .reg .b8 a, b, c, d;\n cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
-        " cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n mov.b32 %0, {a, b, c, d};\n}\n"
-        : "=r"(w)
-        : "f"(q[0]), "f"(q[1]), "f"(q[2]), "f"(q[3]), "f"(q[4]), "f"(q[5]), "f"(q[6]), "f"(q[7]));
-    return w;
-}
-
 // Eight codes as fp16, two a register.
 __device__ __forceinline__ void e2m1x8_halves(uint32_t codes, uint32_t (&h)[4])
 {
@@ -203,6 +180,39 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b)
         : "=l"(reinterpret_cast<uint64_t &>(d))
         : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)));
     return d;
+}
+
+// Eight elements as codes, the first in the low bits: x / s rounded once to the nearest
+// code, ties to the even one.  s has 4 significant bits and a border between two codes at most 3,
+// so bf16 elements do lie on borders, where a product with 1 / s would fall to either side.  What
+// the product leaves, x - q s, is exact, and adding its quotient brings q to the border itself.  PACKED: two elements an
+// instruction (7 x 40000 rows parked: 181 us, 212 one by one; in the append, whose warps have no registers to spare for
+// pairs, 131072 tokens 415, 385 one by one).
+template <bool PACKED>
+__device__ __forceinline__ uint32_t e2m1x8(const float *x, float s)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+    r = s > 0.f ? r : 0.f;
+    float2 q[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (PACKED) {
+            const float2 y = make_float2(x[2 * i], x[2 * i + 1]), r2 = make_float2(r, r);
+            q[i] = mul2(y, r2);
+            q[i] = fma2(fma2(q[i], make_float2(-s, -s), y), r2, q[i]);
+        } else {
+            q[i] = make_float2(x[2 * i] * r, x[2 * i + 1] * r);
+            q[i].x = fmaf(fmaf(-q[i].x, s, x[2 * i]), r, q[i].x);
+            q[i].y = fmaf(fmaf(-q[i].y, s, x[2 * i + 1]), r, q[i].y);
+        }
+    }
+    uint32_t w;
+    asm("{\n .reg .b8 a, b, c, d;\n cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
+        " cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n mov.b32 %0, {a, b, c, d};\n}\n"
+        : "=r"(w)
+        : "f"(q[0].x), "f"(q[0].y), "f"(q[1].x), "f"(q[1].y), "f"(q[2].x), "f"(q[2].y), "f"(q[3].x), "f"(q[3].y));
+    return w;
 }
 
 __device__ __forceinline__ void unpack8(const uint4 &u, float (&x)[8])

@@ -295,8 +295,8 @@ __global__ void __launch_bounds__(kRopeWarps * 32, kRopeBlocks) rope_kernel(cons
                     const uint32_t s0 = scale(c0), s1 = scale(c1);
                     const float f0 = fp4 ? fp4_value(s0) : mx_inverse(s0), f1 = fp4 ? fp4_value(s1) : mx_inverse(s1);
                     if (real && fp4) {
-                        *reinterpret_cast<uint32_t *>(to) = e2m1x8(y, f0);
-                        *reinterpret_cast<uint32_t *>(to + 4 * (c1 - c0)) = e2m1x8(y + 8, f1);
+                        *reinterpret_cast<uint32_t *>(to) = e2m1x8<false>(y, f0);
+                        *reinterpret_cast<uint32_t *>(to + 4 * (c1 - c0)) = e2m1x8<false>(y + 8, f1);
                         if ((c0 & 1) == 0)
                             sc[c0 / 2] = (uint8_t)s0;
                         if ((c1 & 1) == 0)
