@@ -463,6 +463,7 @@ __device__ __forceinline__ void copies(const AttnLaunch &c, AttnShared &sh, cons
 // the ring's places, so the warps that expand them need to be told keys from values only.  Codes come by bulk copies
 // (4096 tokens over 32768 keys: 2812 us with 16 bytes a lane, as one warp cannot ask for more than that brings), scales, which
 // may lie at any multiple of 8 bytes, 8 bytes a lane.  Rows past the length, or in a bad page, get scales of zero.
+// Its loops are not unrolled, as what all warps run has to stay near (a prompt of 8192 tokens 504 us, 423).
 constexpr int kRawTiles = 3, kRawCodes = kTile * kD / 2, kRawBytes = kRawCodes + kTile * kFp4Scales;
 static_assert(kRawTiles * kRawBytes <= (kAttnStages - kFp4Stages) * kAttnStageBytes, "the ring's last place");
 enum { RAW_VALUES = 0, RAW_KEYS = 1, RAW_END = 2 };
@@ -522,10 +523,11 @@ __device__ __forceinline__ void bring(const AttnLaunch &c, AttnShared &sh, const
             return at;
         };
         constexpr int ahead = TWO ? 1 : 2;   // the ring's order, as in copies()
-        long long at[3] = {look(0), look(0), look(0)};
-        for (int x = -ahead; x < nt && ok; ++x) {
+        long long at[3] = {-1, -1, -1};
+#pragma unroll 1
+        for (int x = -ahead - 1; x < nt && ok; ++x) {
             const long long next = look(x + ahead + 1);
-#pragma unroll
+#pragma unroll 1
             for (int isk = 0; isk < 2; ++isk) {
                 const int t = isk ? x + ahead : x;
                 if (t < 0 || t >= nt || !ok)
@@ -533,7 +535,7 @@ __device__ __forceinline__ void bring(const AttnLaunch &c, AttnShared &sh, const
                 ok = begin();
                 if (!ok)
                     break;
-                const long long mine = at[isk ? ahead : 0];
+                const long long mine = isk ? at[ahead] : at[0];
                 const uint8_t *codes = static_cast<const uint8_t *>(isk ? a.cache.k : a.cache.v), *scales = isk ? a.cache.k_scale : a.cache.v_scale;
                 const int left = L - (j0 + t) * kTile;
                 unsigned char *place = raw + used % kRawTiles * kRawBytes;
@@ -545,7 +547,7 @@ __device__ __forceinline__ void bring(const AttnLaunch &c, AttnShared &sh, const
                     asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
                     bulk_load(reinterpret_cast<void *>(place + (lane << shift) * (kD / 2)), codes + mine * (kD / 2), bytes, bar);
                 }
-#pragma unroll
+#pragma unroll 1
                 for (int i = 0; i < kTile / 32; ++i) {
                     const int r = 32 * i + lane;
                     const long long first = __shfl_sync(0xffffffffu, mine, r >> shift);
