@@ -1,7 +1,8 @@
 // cache_copy.cu -- rows of one cache into another: 8-bit and 4-bit rows read back,
 // bf16 rows quantised, pages gathered or scattered.  Memory bound: each row is
-// read and written once.  4 heads: 1048576 8-bit rows read back 476 us, 6.8 TB/s; 8 heads:
-// 7 x 40000 rows quantised to 8 bits 202 us, 6.6 TB/s; a plain copy reaches 6.8.
+// read and written once.  4 heads: 1048576 8-bit rows read back 475 us, 6.8 TB/s, 4-bit ones 440 us, 6.2 TB/s, of which
+// 4.9 are writes (a fill, which writes alone, reaches 4.05); 8 heads: 7 x 40000 rows quantised to 8 bits 187 us, 7.1 TB/s, to 4
+// bits 181 us, 6.2 TB/s, issue slots 68 %; a plain copy reaches 6.8.
 #include <algorithm>
 
 #include "prompt.cuh"
@@ -9,8 +10,9 @@
 namespace retopk {
 
 constexpr int kCopyThreads = 128;
-// rows in flight per 8 lanes (7 x 40000 rows quantised to 8 bits: 201 us with 3, 210 with 2, 206 with 4; 1048576 8-bit rows
-// read back: 474, with 3 488, with 4 489; small blocks also start sooner: 3 x 4099 rows 7.5 us, 10.1 in blocks of 128 rows)
+// rows in flight per 8 lanes (7 x 40000 rows quantised to 8 bits: 201 us with 3, 210 with 2, 206 with 4, to 4 bits 225 with 3, 221
+// with 4, 230 with 6, all before pages were found by products; 1048576 8-bit rows read back: 474, with 3 488, with 4 489, 4-bit
+// ones 454, 457, 451; small blocks also start sooner: 3 x 4099 rows 7.5 us, 10.1 in blocks of 128 rows)
 __host__ __device__ constexpr int copy_rows(int src, int dst)
 {
     return src == RETOPK_CACHE_BF16 && dst == RETOPK_CACHE_FP4 ? 4 : src == RETOPK_CACHE_BF16 && dst == RETOPK_CACHE_MX8 ? 3 : 2;

@@ -11,7 +11,10 @@
 // one KV head (the row of token t, head g is t G + g), so every head of the group uses
 // the K / V rows that were loaded once.
 //
-// Roles (12 warps, one CTA per SM; one of them idle): two groups of four softmax
+// 4-bit rows.  Sequences with few rows go to row_attention.cu.  Here four more warps expand codes into the ring's tiles: bf16
+// keys, as Q is bf16, and fp16 values, both exact; P is then fp16 too.  One warp brings the codes in bulk.
+//
+// Roles (12 warps, 16 over 4-bit rows, one CTA per SM; one of them idle): two groups of four softmax
 // warps, each thread one row of its tile, whose 128 scores stay in registers; one
 // thread that issues the matrix instructions (S = Q K^T from shared memory, O += P V
 // with P in tensor memory); one warp that issues the copies; one that walks the
@@ -35,15 +38,20 @@
 // Rounding.  Scores, maxima, sums, parts and accumulators have 32 bits.  P is rounded to bf16, as the matrix
 // instruction takes both operands in one type and V is bf16: an output is off by up to 2^-8 sum_j p_j |v_j| for it
 // (against 64 bits 0.0019 to 0.0023 of the outputs' size, where 32-bit weights give 0.0017, the output's own rounding).
+// Over 4-bit rows it is rounded to fp16, by 2^-11 of a weight or 2^-32 of the row's largest (0.0017 too).
 //
 // Measured (28 query heads over 4 KV heads but where said).  4096 tokens over 32768 keys: 1233 us,
 // 1.47 PFLOP/s, held by the GPU's power limit (1133 us in short bursts, held by the chain softmax -> P V ->
 // Q K of each group).  One token over 131072 keys: 51 us, 5.2 TB/s, of which the stream
 // takes 40.  61 ragged sequences of 9000 keys, 32 over 8 heads: 219 us, 6.7 TB/s, 98 % of a plain copy's rate.  3 x 333
 // tokens in windows of 4096 keys, 16 over 2 heads: 53 us; capped, 65 us, and 80 with scores past half the cap.
-// What an item costs beside its tiles shows where items are short or shares small: a prompt of 2048 tokens 60 us and
-// of 8192 388 (0.50 and 1.24 PFLOP/s), 128 sequences of 1500 keys, 32 over 8 heads, 130 us (3.9 TB/s), 36 tokens over
-// 17663 keys, 16 over 2 heads, 39 us (0.13 PFLOP/s), one token over 300 keys 11.7 us.
+// What an item costs beside its tiles shows where items are short or shares small: a prompt of 2048 tokens 57 us and
+// of 8192 385 (0.53 and 1.25 PFLOP/s), 128 sequences of 1500 keys, 32 over 8 heads, 130 us (3.9 TB/s), 36 tokens over
+// 17663 keys, 16 over 2 heads, 25 us (0.20 PFLOP/s), one token over 300 keys 11.7 us.
+// Over 4-bit rows: 4096 tokens over 32768 keys 1317 us, prompts of 2048 and 8192 65 and 423 us, 3 x 333 capped tokens 73, 20 sequences of 45
+// tokens over 3000 keys 60.  A tile of keys and one of values take the four warps ~1.1 us beside the softmax of eight, and all
+// code has to stay in caches that hold less than it: what the warps that bring and expand run is kept in short loops (unrolled,
+// 4096 over 32768 1570 us, the prompt of 8192 504).
 #include <math.h>
 
 #include <algorithm>
@@ -68,7 +76,7 @@ constexpr int kHalf = kTile / 2;                 // keys of half a tile
 // registers of a thread after the split: 2 x 128 x 208 + 128 x 88 = 384 x 168, what the block is launched with
 // (4096 tokens over 32768 keys in short bursts: 1133 us; with 216 and 72 or 224 and 56, 1190)
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
-// over 4-bit rows: 2 x 128 x 200 + 2 x 128 x 56 = 512 x 128
+// over 4-bit rows: 2 x 128 x 200 + 2 x 128 x 56 = 512 x 128 (1024 tokens over 32768 keys 354 us; with 208 and 48 394, 192 and 64 494)
 constexpr int kFp4SoftmaxRegs = 200, kFp4OtherRegs = 56;
 struct ChunkCost {
     // Weight of an item beside its keys: what beginning and ending it costs, in keys.  (A prompt

@@ -15,8 +15,8 @@
 // pairs through shared memory.
 //
 // Measured (28 query, 4 KV heads): 131072 tokens into 8-bit pages 366 us, 6.2 TB/s, 92 % of a
-// plain copy; 8191 ragged tokens into bf16 pages 30 us, 5.0 TB/s (5 us of it start and end); one
-// token 3.8 us.  The large call was 443 us while every lane made the factors that it used from the
+// plain copy, into 4-bit ones 386 us, 5.8 TB/s (quotients and codes take the issue slots that loads wait in); 8191 ragged
+// tokens into bf16 pages 30 us, 5.0 TB/s (5 us of it start and end), into 4-bit ones 34 us; one token 3.8 us.  The large call was 443 us while every lane made the factors that it used from the
 // weights anew, 403 with the factors in rows of 128 bytes that share their banks.
 //
 // Angles.  pos is whole, so only the fraction of inv_freq / 2 pi counts: it is kept

@@ -19,6 +19,18 @@
 // Rounding.  Code times scale is exact in fp16.  A query row is brought to fp16's range by a power of two, so
 // its elements are exact down to 2^-28 of the largest.  P is rounded to fp16 (m lies 2^7 below the maximum when
 // it is taken and is raised when that has grown by 2^8 more, so weights reach from 2^15 down to 2^-24).  All else has 32 bits.
+//
+// Measured (28 query heads over 4 KV heads but where said).  61 ragged sequences of up to 9000 keys, 32 over 8 heads: 81 us,
+// 5.1 TB/s (over bf16 rows 217 us): the stream runs at nine tenths of a plain copy's rate, with ~5 us of start before it and ~5 of the
+// slowest warps and the join behind.  One token over 131072 keys 26 us (bf16 51), over 500000 60 (155): 4 us of start, the
+// stream, 6 of end and join.  128 sequences of 1500 keys, 32 over 8 heads, 40 us (130).  16 sequences of 2, 3 and 4 tokens
+// over 20000 keys 45, 47 and 63 us (bf16 78, 79, 69): registers leave 12 and then 8 warps an SM, which issue in two
+// cycles of five.  One token over 300 keys 7.3 us of a graph of such calls, 9.7 called from Python.
+// A tile of a warp, 32 keys, is 640 instructions: 128 conversions, 128 products with the scales, 32 matrix products, 32 to bring codes
+// of two keys together, 24 loads, ~70 of softmax, the rest copies, scales and the loop.
+// Not kept: one CTA of all the SM's warps (61 sequences 78 us, one token over 131072 27.5; with a limit on how far its groups of
+// four run apart 80), the same only where items are few (16 x 3 47.4 of a graph, 45.0 as it is), codes made fp16 by shifts and masks
+// (1.4 cycles of an SM for two codes of 32 lanes, a conversion takes 0.5).
 #include <math.h>
 
 #include <algorithm>
