@@ -99,18 +99,12 @@ struct Piece {
     }
 };
 
-// cache_row with a division by the page's rows that is a product: both are below 2^23, so it is off by one at most.
+// cache_row with the page found by a product.
 __device__ __forceinline__ long long row_of(const retopk_cache &c, float inverse, int b, int hk, int pos, uint32_t *status)
 {
     int page = b, r = pos;
     if (c.table) {
-        int i = (int)((float)pos * inverse);
-        r -= i * c.page_rows;
-        if (r < 0)
-            r += c.page_rows, --i;
-        else if (r >= c.page_rows)
-            r -= c.page_rows, ++i;
-        page = c.table[(long long)b * c.table_width + i];
+        page = c.table[(long long)b * c.table_width + page_of(pos, c.page_rows, inverse, r)];
         if ((uint32_t)page >= (uint32_t)c.n_pages) {
             if (status)
                 atomicOr(status, RETOPK_STATUS_BAD_PAGE);

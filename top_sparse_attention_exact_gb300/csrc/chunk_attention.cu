@@ -482,6 +482,7 @@ __device__ __forceinline__ void bring(const AttnLaunch &c, AttnShared &sh, const
 {
     const AttnArgs &a = c.a;
     const int Hkv = a.cache.n_kv_heads, tile_tokens = kTile / a.G, shift = 31 - __clz(c.chunk);
+    const float inverse = 1.f / a.cache.page_rows;
     bool ok = true;
     uint32_t segs = 0, used = 0, q_copies = 0;
     // place `used` is free, and once what was copied to it is there it holds `what`
@@ -520,8 +521,7 @@ __device__ __forceinline__ void bring(const AttnLaunch &c, AttnShared &sh, const
             if (lane < kTile >> shift && t < nt && pos < L) {
                 int page = b, row = pos;
                 if (a.cache.table) {
-                    page = a.cache.table[(long long)b * a.cache.table_width + pos / a.cache.page_rows];
-                    row = pos % a.cache.page_rows;
+                    page = a.cache.table[(long long)b * a.cache.table_width + page_of(pos, a.cache.page_rows, inverse, row)];
                 }
                 if ((uint32_t)page < (uint32_t)a.cache.n_pages)
                     at = ((long long)page * Hkv + hk) * a.cache.page_rows + row;

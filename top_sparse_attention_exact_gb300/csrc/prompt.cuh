@@ -30,6 +30,19 @@ inline long long cache_capacity(const retopk_cache &c)
     return c.table ? (long long)c.table_width * c.page_rows : c.page_rows;
 }
 
+// Place in the table of position pos, and its row there: a division by the page's rows as a product with 1 / rows.  Both
+// are at most 2^23, so it is off by one at most.
+__device__ __forceinline__ int page_of(int pos, int page_rows, float inverse, int &row)
+{
+    int i = (int)((float)pos * inverse);
+    row = pos - i * page_rows;
+    if (row < 0)
+        row += page_rows, --i;
+    else if (row >= page_rows)
+        row -= page_rows, ++i;
+    return i;
+}
+
 // Row (page, head, row in page) of sequence b, head hk, position pos, as an
 // index into [n_pages, Hkv, page_rows]; -1 (and RETOPK_STATUS_BAD_PAGE) for a
 // table entry outside the pool.  pos is within the capacity.

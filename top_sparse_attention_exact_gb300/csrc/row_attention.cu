@@ -228,8 +228,7 @@ __global__ void __launch_bounds__(kRowThreads, row_blocks(NT)) row_attention_ker
             if (t < nt && pos < L && pos <= last && pos + 15 >= low) {
                 int page = s.b, row = pos;
                 if (a.cache.table) {
-                    page = a.cache.table[(long long)s.b * a.cache.table_width + pos / a.cache.page_rows];
-                    row = pos % a.cache.page_rows;
+                    page = a.cache.table[(long long)s.b * a.cache.table_width + page_of(pos, a.cache.page_rows, 1.f / a.cache.page_rows, row)];
                 }
                 if ((uint32_t)page < (uint32_t)a.cache.n_pages)
                     place = (((long long)page * a.cache.n_kv_heads + s.hk) * a.cache.page_rows + row) * (kD / 2);
