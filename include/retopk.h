@@ -401,7 +401,8 @@ int retopk_support_overlap(const int32_t *S, const int32_t *others, int rows, in
                                  once.  A block with a NaN or an infinity gets scale 255 and
                                  reads back as NaN.  retopk_qkv_append and retopk_cache_copy
                                  write such rows, retopk_cache_copy and
-                                 retopk_chunk_attention read them. */
+                                 retopk_chunk_attention read them (the latter holds code *
+                                 scale in fp16, which scales above 10240 can overflow). */
 
 /* The keys and values of B sequences: k and v are [n_pages, n_kv_heads,
  * page_rows, 128] (bf16, or e4m3 bytes with k_scale / v_scale [n_pages,

@@ -440,6 +440,7 @@ ATTEND = [  # tokens of each sequence, rows in all, Hq, Hkv, page, window, cap
     ([i % 3 for i in range(900)], [(53 * i) % 300 for i in range(900)], 2, 1, 16, 0, 0.0),
     ([40] * 400, [40 + i % 90 for i in range(400)], 8, 8, 0, 0, 0.0),
     ([1] * 63 + [900], [700 + 9 * i for i in range(63)] + [900], 28, 4, 64, 0, 0.0),     # a prompt among single tokens
+    ([1] * 90 + [70] + [1] * 20, [300 + 31 * i for i in range(90)] + [2000] + [1500] * 20, 28, 4, 16, 0, 0.0),     # the mean is below two
     ([3, 70], [600, 1500], 40, 40, 0, 0, 0.0),                      # many KV heads
     ([1], [512], 6, 2, 0, 0, 0.0),                                  # a cache of a few tiles, with rows past the length
     ([130], [515], 3, 3, 64, 0, 0.0),

@@ -48,8 +48,8 @@
 // What an item costs beside its tiles shows where items are short or shares small: a prompt of 2048 tokens 57 us and
 // of 8192 385 (0.53 and 1.25 PFLOP/s), 128 sequences of 1500 keys, 32 over 8 heads, 130 us (3.9 TB/s), 36 tokens over
 // 17663 keys, 16 over 2 heads, 25 us (0.20 PFLOP/s), one token over 300 keys 11.7 us.
-// Over 4-bit rows: 4096 tokens over 32768 keys 1317 us, prompts of 2048 and 8192 65 and 423 us, 3 x 333 capped tokens 73, 20 sequences of 45
-// tokens over 3000 keys 60.  A tile of keys and one of values take the four warps ~1.1 us beside the softmax of eight, and all
+// Over 4-bit rows: 4096 tokens over 32768 keys 1320 us, prompts of 2048 and 8192 64 and 423 us (in pages of 64 rows 440), 3 x 333 capped
+// tokens 72, 20 sequences of 45 tokens over 3000 keys 62.  A tile of keys and one of values take the four warps ~1.1 us beside the softmax of eight, and all
 // code has to stay in caches that hold less than it: what the warps that bring and expand run is kept in short loops (unrolled,
 // 4096 over 32768 1570 us, the prompt of 8192 504).
 #include <math.h>
@@ -520,9 +520,8 @@ __device__ __forceinline__ void bring(const AttnLaunch &c, AttnShared &sh, const
             long long at = -1;
             if (lane < kTile >> shift && t < nt && pos < L) {
                 int page = b, row = pos;
-                if (a.cache.table) {
+                if (a.cache.table)
                     page = a.cache.table[(long long)b * a.cache.table_width + page_of(pos, a.cache.page_rows, inverse, row)];
-                }
                 if ((uint32_t)page < (uint32_t)a.cache.n_pages)
                     at = ((long long)page * Hkv + hk) * a.cache.page_rows + row;
                 else if (a.status)

@@ -20,11 +20,11 @@
 // its elements are exact down to 2^-28 of the largest.  P is rounded to fp16 (m lies 2^7 below the maximum when
 // it is taken and is raised when that has grown by 2^8 more, so weights reach from 2^15 down to 2^-24).  All else has 32 bits.
 //
-// Measured (28 query heads over 4 KV heads but where said).  61 ragged sequences of up to 9000 keys, 32 over 8 heads: 81 us,
+// Measured (28 query heads over 4 KV heads but where said).  61 ragged sequences of up to 9000 keys, 32 over 8 heads: 80 us,
 // 5.1 TB/s (over bf16 rows 217 us): the stream runs at nine tenths of a plain copy's rate, with ~5 us of start before it and ~5 of the
-// slowest warps and the join behind.  One token over 131072 keys 26 us (bf16 51), over 500000 60 (155): 4 us of start, the
+// slowest warps and the join behind.  One token over 131072 keys 26 us (bf16 51), over 500000 60 (153): 4 us of start, the
 // stream, 6 of end and join.  128 sequences of 1500 keys, 32 over 8 heads, 40 us (130).  16 sequences of 2, 3 and 4 tokens
-// over 20000 keys 45, 47 and 63 us (bf16 78, 79, 69): registers leave 12 and then 8 warps an SM, which issue in two
+// over 20000 keys 44, 47 and 64 us (bf16 77, 79, 68): registers leave 12 and then 8 warps an SM, which issue in two
 // cycles of five.  One token over 300 keys 7.3 us of a graph of such calls, 9.7 called from Python.
 // A tile of a warp, 32 keys, is 640 instructions: 128 conversions, 128 products with the scales, 32 matrix products, 32 to bring codes
 // of two keys together, 24 loads, ~70 of softmax, the rest copies, scales and the loop.
@@ -227,9 +227,8 @@ __global__ void __launch_bounds__(kRowThreads, row_blocks(NT)) row_attention_ker
             place = -1;
             if (t < nt && pos < L && pos <= last && pos + 15 >= low) {
                 int page = s.b, row = pos;
-                if (a.cache.table) {
+                if (a.cache.table)
                     page = a.cache.table[(long long)s.b * a.cache.table_width + page_of(pos, a.cache.page_rows, 1.f / a.cache.page_rows, row)];
-                }
                 if ((uint32_t)page < (uint32_t)a.cache.n_pages)
                     place = (((long long)page * a.cache.n_kv_heads + s.hk) * a.cache.page_rows + row) * (kD / 2);
                 else if (a.status)
