@@ -428,6 +428,9 @@ ATTEND = [  # tokens of each sequence, rows in all, Hq, Hkv, page, window, cap
     ([1], [20000], 28, 4, 64, 5000, 0.0),                           # a window of a long history
     ([1, 1], [2000, 50], 9, 1, 0, 1, 2.0),
     ([77], [77], 4, 2, 0, 0, 0.0),
+    ([9, 12, 11], [4000, 12, 700], 28, 4, 64, 0, 0.0),              # around half a tile of tokens
+    ([10, 9, 8], [4000, 12, 700], 28, 4, 16, 0, 7.0),
+    ([65, 66], [3000, 66], 2, 2, 0, 0, 0.0),
     ([300], [300], 28, 4, 128, 0, 0.0),
     ([129], [1300], 16, 1, 16, 0, 0.0),
     ([64, 0, 1, 200], [64, 50, 700, 900], 10, 2, 48, 0, 0.0),

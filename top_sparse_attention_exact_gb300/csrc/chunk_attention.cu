@@ -1447,7 +1447,10 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnLaunch c, int share
 // in one and the tokens in the other, 4096 tokens over 32768 keys beside 200 single tokens over 9000 take 2064 us
 // (two calls 1729), 4096 over 4096 beside 200 over 1500 274 (259); with fewer tokens beside it one call is the faster:
 // 512 over 9000 beside 63 over 9000 221 (254), 4096 over 32768 beside 63 over 9000 1350 (1382, in two tiles).
-static bool two_tiles(int T, int B, int G) { return T / B > kTile / G * 3 / 2; }
+// Over 4-bit rows, where two tiles share what was expanded, from half a tile on (18 tokens a tile; streams against two tiles: 16 x 10
+// tokens over 9000 keys 62 us against 59, 8 x 20 over 20000 96 against 74, 4 x 24 over 9000 38 against 34; 16 x 5 over 20000
+// 100 against 101).
+static bool two_tiles(int T, int B, int G, bool fp4) { return T / B > (fp4 ? kTile / G / 2 : kTile / G * 3 / 2); }
 
 // Rows of a part.
 static int part_rows(int T, int G, bool two)
@@ -1469,12 +1472,12 @@ static size_t carve(int rows, char *ws, Parts *p)
     return o_o + 2 * n * (size_t)rows * kD * sizeof(float);
 }
 
-// Enough for fewer tokens and any number of sequences as well: of all batches of T tokens, the one of a single sequence
+// Enough for fewer tokens, any number of sequences and either form as well: of all batches of T tokens, the one of a single sequence
 // has the most rows a part.
 size_t chunk_attention_ws(int T, int Hq, int Hkv)
 {
     const int G = Hq / Hkv;
-    return carve(part_rows(T, G, two_tiles(T, 1, G)), nullptr, nullptr);
+    return carve(part_rows(T, G, two_tiles(T, 1, G, true)), nullptr, nullptr);
 }
 
 static bool make_map(CUtensorMap *map, const void *p, cuuint64_t d1, cuuint64_t d2, cuuint64_t s1, cuuint64_t s2, int b1,
@@ -1513,7 +1516,7 @@ cudaError_t launch_chunk_attention(const AttnArgs &a, cudaStream_t st)
     AttnLaunch c{};
     c.a = a;
     const int Hkv = a.cache.n_kv_heads, tokens = kTile / a.G;
-    const bool two = two_tiles(a.T, a.B, a.G);
+    const bool two = two_tiles(a.T, a.B, a.G, a.cache.format == RETOPK_CACHE_FP4);
     c.plan.tokens = two ? 2 * tokens : tokens;
     c.shares = std::min(sm_count(), kMaxShares);
     c.items = std::min<long long>(a.T, a.T / c.plan.tokens + a.B) * Hkv;
