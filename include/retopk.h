@@ -489,7 +489,8 @@ int retopk_cache_copy(const retopk_cache *src, const retopk_cache *dst, const in
  * may reach every token of its sequence; a query that is not stays in its row.  Lengths beyond the cache's capacity
  * are clamped to it.  scale 0 means 1/sqrt(128).
  * d_workspace: >= retopk_chunk_attention_workspace_bytes, 256-byte aligned; what
- * it gives for T tokens is enough for fewer of the same heads, whatever their sequences
+ * it gives for T tokens is enough for fewer of the same heads, whatever their sequences, and for either
+ * format (a call over bf16 rows needs less of it, and takes a buffer of that much)
  * (on the device that was current: it counts the SMs); concurrent calls need one each.  Long histories of few tokens are split over the GPU
  * and joined from it.  Results do not depend on the other sequences of the call beyond
  * rounding; the weights are rounded to bf16 once, which out carries (2^-8 sum_j p_j |v_j|), over 4-bit rows to

@@ -789,6 +789,23 @@ def test_attention_of_several_batches_in_one_workspace():
             assert torch.equal(out, call[4])
 
 
+@pytest.mark.parametrize("n,L", [([1], [9000]), ([12], [5000]), ([19], [3000]), ([40], [4000]), ([1] * 30, [700] * 30), ([2, 30], [3000, 900])])
+@pytest.mark.parametrize("Hq,Hkv", [(28, 4), (16, 1)])
+def test_attention_stays_within_the_workspace_that_bf16_rows_need(n, L, Hq, Hkv):
+    # two parts an SM of min(128, T G) rows, or of 256 from one and a half tiles of tokens on
+    T, G = sum(n), Hq // Hkv
+    shares = min(torch.cuda.get_device_properties(0).multi_processor_count, 255)
+    rows = 256 if T > 128 // G * 3 // 2 else min(128, (T * G + 7) // 8 * 8)
+    up = lambda x: (x + 255) // 256 * 256  # noqa: E731
+    size = up((shares + 1) * 24) + up(2 * shares * rows * 8) + 2 * shares * rows * 512
+    q, c = setup(n, L, Hq, Hkv, 64, 70 + T, pad=0)
+    ws = torch.full((size + 4096,), 0x5a, dtype=torch.uint8, device="cuda")
+    assert ws.data_ptr() % 256 == 0
+    out = retopk.chunk_attention(q, c.h, i32(L), cu_tokens=offsets(n), workspace=ws[:size])
+    check(q, 0, n, L, c, out, None, 1 / math.sqrt(D), 0.0, 0)
+    assert (ws[size:] == 0x5a).all()
+
+
 def test_calls_refuse_tensors_elsewhere():
     q, c = setup([1], [10], 4, 1, 0, 19, pad=0)
     with pytest.raises(retopk.RetopkError):

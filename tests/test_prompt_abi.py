@@ -110,6 +110,25 @@ def test_a_workspace_of_the_largest_call_is_enough_for_smaller_ones(lib, Hq, Hkv
         assert most > 0 and all(size <= most for (T2, _), size in at.items() if T2 <= T)
 
 
+def bf16_workspace(T, G):
+    """Bytes that attention of T tokens over bf16 rows lays out: places of the shares' bounds (24 bytes each), then two parts a
+    share of (m, l) pairs and 128 sums a row, a share for each SM; 256 rows a part from one and a half tiles of tokens on."""
+    shares = min(torch.cuda.get_device_properties(0).multi_processor_count if torch.cuda.is_available() else 1, 255)
+    rows = 256 if T > 128 // G * 3 // 2 else min(128, (T * G + 7) // 8 * 8)
+    up = lambda n: (n + 255) // 256 * 256  # noqa: E731
+    return up((shares + 1) * 24) + up(2 * shares * rows * 8) + 2 * shares * rows * 512
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(28, 4), (32, 8), (16, 1), (8, 8), (7, 1)])
+@pytest.mark.parametrize("T", [1, 2, 8, 9, 12, 18, 19, 27, 28, 64, 192, 193, 4096])
+def test_a_bf16_call_takes_the_workspace_that_bf16_rows_need(lib, T, Hq, Hkv):
+    # (an output that overlaps the queries is what refuses the call once its workspace has been taken)
+    n = bf16_workspace(T, Hq // Hkv)
+    kw = dict(c=cache(n_kv_heads=Hkv), T=T, B=1, cu=P, Hq=Hq, qs=Hq * 128, os=Hq * 128, out=P + 16)
+    assert n <= lib.retopk_chunk_attention_workspace_bytes(T, 1, Hq, Hkv)
+    assert attend(lib, n=n, **kw) == -1 and attend(lib, n=n - 1, **kw) == -3
+
+
 def test_outputs_that_overlap_what_is_read_are_refused(lib):
     far, c = P + (1 << 20), cache(k=P + (1 << 24), v=P + (1 << 25))
     ok = dict(c=c, q=P, k=P + 65536, v=P + 131072, qo=far, sl=P + 262144, so=P + 262144)

@@ -1472,12 +1472,12 @@ static size_t carve(int rows, char *ws, Parts *p)
     return o_o + 2 * n * (size_t)rows * kD * sizeof(float);
 }
 
-// Enough for fewer tokens, any number of sequences and either form as well: of all batches of T tokens, the one of a single sequence
-// has the most rows a part.
-size_t chunk_attention_ws(int T, int Hq, int Hkv)
+// Enough for fewer tokens and any number of sequences as well: of all batches of T tokens, the one of a single sequence
+// has the most rows a part.  (4-bit rows want two tiles, and so as much or more, from fewer tokens on.)
+size_t chunk_attention_ws(int T, int Hq, int Hkv, bool fp4)
 {
     const int G = Hq / Hkv;
-    return carve(part_rows(T, G, two_tiles(T, 1, G, true)), nullptr, nullptr);
+    return carve(part_rows(T, G, two_tiles(T, 1, G, fp4)), nullptr, nullptr);
 }
 
 static bool make_map(CUtensorMap *map, const void *p, cuuint64_t d1, cuuint64_t d2, cuuint64_t s1, cuuint64_t s2, int b1,

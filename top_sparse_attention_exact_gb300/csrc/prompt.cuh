@@ -265,7 +265,7 @@ struct AttnArgs {
     float scale, softcap;
     void *ws;
 };
-size_t chunk_attention_ws(int T, int Hq, int Hkv);
+size_t chunk_attention_ws(int T, int Hq, int Hkv, bool fp4);
 cudaError_t launch_chunk_attention(const AttnArgs &a, cudaStream_t st);
 // over 4-bit rows, where sequences have few of them
 bool takes_rows(int T, int B, int G);

@@ -94,6 +94,13 @@ bool may_write(const void *out, int64_t out_stride, const void *in, int64_t in_s
            !rows_meet(out, out_stride, heads, in, in_stride, heads, T);
 }
 
+// Workspace of attention over rows of a format: over bf16 ones less, as fewer kernels take them.
+size_t attention_ws(int T, int Hq, int Hkv, int format)
+{
+    return format == RETOPK_CACHE_FP4 ? std::max(chunk_attention_ws(T, Hq, Hkv, true), row_attention_ws())
+                                      : chunk_attention_ws(T, Hq, Hkv, false);
+}
+
 int check_rope(const retopk_rope *r)
 {
     if (!r || r->rot_dim < 0 || (r->rot_dim > 0 && !r->inv_freq) || !(r->eps >= 0.f) || isinf(r->eps))
@@ -251,7 +258,7 @@ size_t retopk_chunk_attention_workspace_bytes(int T, int B, int Hq, int Hkv)
     if (T < 0 || B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || T > kMaxTokens || B > kMaxBatch ||
         Hq > kMaxHeads || Hq / Hkv > kMaxGroup)
         return 0;
-    return std::max(chunk_attention_ws(T, Hq, Hkv), row_attention_ws());
+    return attention_ws(T, Hq, Hkv, RETOPK_CACHE_FP4);   // (enough for either format)
 }
 
 int retopk_chunk_attention(const retopk_bf16 *q, int64_t q_stride, const retopk_cache *cache,
@@ -272,8 +279,7 @@ int retopk_chunk_attention(const retopk_bf16 *q, int64_t q_stride, const retopk_
         return e;
     if (!aligned(lse, 4) || !aligned(d_status, 4))
         return RETOPK_ERR_ALIGN;
-    if (!d_workspace || !aligned(d_workspace, 256) ||
-        bytes < retopk_chunk_attention_workspace_bytes(T, B, Hq, cache->n_kv_heads))
+    if (!d_workspace || !aligned(d_workspace, 256) || bytes < attention_ws(T, Hq, cache->n_kv_heads, cache->format))
         return RETOPK_ERR_WORKSPACE;
     if (!may_write(out, out_stride, q, q_stride, Hq, T))
         return RETOPK_ERR_INVALID;
