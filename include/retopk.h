@@ -398,7 +398,8 @@ int retopk_support_overlap(const int32_t *S, const int32_t *others, int rows, in
                                  fp16: 5 of exponent, 3 of mantissa.  Written with
                                  the largest size over 6 rounded to nearest, at most 10240 (so
                                  values beyond 61440 saturate), codes rounded to nearest even
-                                 once.  A block with a NaN or an infinity gets scale 255 and
+                                 once.  Scales have all their bits for sizes from 6 * 2^-14 (3.7e-4)
+                                 on; a block whose largest is at most 6 * 2^-18 (2.3e-5) becomes zeros.  A block with a NaN or an infinity gets scale 255 and
                                  reads back as NaN.  retopk_qkv_append and retopk_cache_copy
                                  write such rows, retopk_cache_copy and
                                  retopk_chunk_attention read them (the latter holds code *

@@ -248,6 +248,36 @@ def test_blocks_that_are_not_finite():
     assert not back.k[0, 0, 3].isnan().any()
 
 
+@pytest.mark.parametrize("by", ["copy", "append"])
+def test_blocks_at_the_ends_of_the_scales(by):
+    # (largest of a block, its scale byte, what comes back of it), by hand.  Below 6 x 2^-14 scales are 2^-17 apart, ties go to even
+    u = 2.0 ** -17                                                   # the smallest scale
+    cases = [(0.0, 0, 0.0), (2.0 ** -133, 0, 0.0), (2.0 ** -19, 0, 0.0), (2.0 ** -16, 0, 0.0),
+             (3 * u, 0, 0.0),                                        # 6 x 2^-18: the tie between no scale and the smallest
+             ((1.5 + 2.0 ** -7) * 2 * u, 1, 3 * u),                  # the next bf16
+             (6 * u, 1, 6 * u), (8.9375 * u, 1, 6 * u),              # (1.49 of it: the code is held at 6)
+             (9 * u, 2, 8 * u),                                      # the tie between 1 and 2; 4.5 of 2, nearest code 4
+             (15 * u, 2, 12 * u), (6 * 8 * u, 8, 6 * 8 * u),         # 2.5: a tie to 2; 6 x 2^-14, the smallest normal scale
+             (48.25 * u, 8, 6 * 8 * u), (61440.0, 226, 61440.0), (61440.0 + 256, 226, 61440.0), (3e38, 226, 61440.0)]
+    g = gen(77)
+    x = torch.zeros((len(cases), 1, D), dtype=torch.bfloat16, device="cuda")
+    for r, (top, byte, back) in enumerate(cases):
+        at = torch.randint(0, 16, (8,), generator=g, device="cuda") + 16 * torch.arange(8, device="cuda")
+        x[r, 0, at] = torch.tensor([top, -top] * 4, dtype=torch.bfloat16, device="cuda")
+    n = len(cases)
+    c, flat = Cache(1, 1, n), Cache(1, 1, n, 0, "bf16")
+    if by == "copy":
+        flat.put(0, x, x)
+        retopk.cache_copy(flat.h, c.h, i32([0]), i32([n]))
+    else:
+        retopk.qkv_append(retopk.QKRope(), x, x, x, c.h, i32([0]), cu_tokens=offsets([n]))
+    retopk.cache_copy(c.h, flat.h, i32([0]), i32([n]))
+    for r, (top, byte, back) in enumerate(cases):
+        for scales, rows in ((c.ks, flat.k), (c.vs, flat.v)):
+            assert scales[0, 0, r].tolist() == [byte] * 8, (top, scales[0, 0, r])
+            assert torch.equal(rows[0, 0, r].double(), back * x[r, 0].double().sign()), top
+
+
 def test_a_pool_past_2_31_elements():
     pages, g = 70000, gen(2)                              # 64 bytes x 512 rows a page: 2.3e9
     k, v = (torch.zeros((pages, 1, 512, 64), dtype=torch.uint8, device="cuda") for _ in range(2))

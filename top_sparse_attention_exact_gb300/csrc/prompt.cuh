@@ -128,8 +128,10 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi)
 // ---- 4-bit rows: e2m1 codes with one scale for 16 elements --------------------
 // A scale byte is the upper bits of an fp16 (5 of exponent, 3 of mantissa, no sign).
 // With 3 mantissa bits a block's largest element lies within 2^-4 of the code 6 (a
-// power of two would leave it anywhere in (3, 6]), and 16 elements of any size down
-// to 2^-19 find a scale without a second one for the tensor.  Code times scale has at
+// power of two would leave it anywhere in (3, 6]), without a second scale for the tensor,
+// where that element is 6 * 2^-14 (3.7e-4) or more.  Below, scales are 2^-17 apart: byte n
+// stands for largest elements of 6 n - 3 to 6 n + 3 times 2^-17, and a block of at most
+// 6 * 2^-18 (2.3e-5) becomes zeros.  Code times scale has at
 // most 6 significant bits and is exact in fp16 and in bf16.
 constexpr uint32_t kFp4Top = 226;   // the largest that is written, 10240: six times it is an fp16
 
