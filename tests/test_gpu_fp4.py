@@ -278,6 +278,24 @@ def test_blocks_at_the_ends_of_the_scales(by):
             assert torch.equal(rows[0, 0, r].double(), back * x[r, 0].double().sign()), top
 
 
+@pytest.mark.parametrize("form", ["fp4", "mx8"])
+def test_keys_that_are_the_values_keep_one_pool(form):
+    src, two, one = Cache(2, 2, 40, 16, "bf16"), Cache(2, 2, 40, 48, form), Cache(2, 2, 40, 48, form)
+    for b in range(2):
+        x = normal(gen(80 + b), 40, 2, D)
+        src.put(b, x, x)
+    one.h = retopk.KVCache(one.k, one.k, table=one.table, k_scale=one.ks, v_scale=one.ks)
+    for c in (one, two):
+        retopk.cache_copy(src.h, c.h, i32([0, 3]), i32([40, 17]))
+    assert torch.equal(one.k, two.k) and torch.equal(one.ks, two.ks)
+    for half in (one.ks.view(-1)[:one.ks.numel() // 2], one.ks.view(-1)[one.ks.numel() // 2:]):     # a pool within the other is refused
+        half = half.view(one.ks.shape[0] // 2, *one.ks.shape[1:])
+        k, v = one.k[:half.shape[0]], one.k[half.shape[0]:2 * half.shape[0]]
+        bad = retopk.KVCache(k, v, k_scale=half, v_scale=half)
+        with pytest.raises(retopk.RetopkError):
+            retopk.cache_copy(src.h, bad, i32([0]), i32([1]))
+
+
 def test_a_pool_past_2_31_elements():
     pages, g = 70000, gen(2)                              # 64 bytes x 512 rows a page: 2.3e9
     k, v = (torch.zeros((pages, 1, 512, 64), dtype=torch.uint8, device="cuda") for _ in range(2))

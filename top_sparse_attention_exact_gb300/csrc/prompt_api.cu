@@ -74,6 +74,18 @@ bool meet(const void *p, size_t n, const void *q, size_t m)
     return n && m && (uintptr_t)p < (uintptr_t)q + m && (uintptr_t)q < (uintptr_t)p + n;
 }
 
+// Whether a cache's codes and scales lie over one another, so that a call that writes rows would lose some.  (Keys and values
+// may be one pool with one of scales, of a model whose values are its keys.)
+bool folded(const retopk_cache &c)
+{
+    const size_t n = pool_bytes(c), m = scale_bytes(c);
+    if (m == 0)
+        return false;
+    const bool one = c.k == c.v && c.k_scale == c.v_scale;
+    return (!one && (meet(c.k, n, c.v, n) || meet(c.k_scale, m, c.v_scale, m))) || meet(c.k, n, c.k_scale, m) ||
+           meet(c.k, n, c.v_scale, m) || meet(c.v, n, c.k_scale, m) || meet(c.v, n, c.v_scale, m);
+}
+
 // Whether two strided [T, heads, 128] tensors share an element; of two whose rows lie between each other's, those of one
 // stride are told apart, others count as sharing.
 bool rows_meet(const void *p, int64_t ps, int pheads, const void *q, int64_t qs, int qheads, int T)
@@ -179,7 +191,7 @@ int retopk_qkv_append(const retopk_rope *rope, const retopk_bf16 *q, int64_t q_s
             return RETOPK_ERR_ALIGN;
         const int64_t qw = (int64_t)Hq * kD;
         if (!may_write(q_out, qw, q, q_stride, Hq, T) || rows_meet(q_out, qw, Hq, k, k_stride, Hkv, T) ||
-            rows_meet(q_out, qw, Hq, v, v_stride, Hkv, T))
+            rows_meet(q_out, qw, Hq, v, v_stride, Hkv, T) || folded(*cache))
             return RETOPK_ERR_INVALID;
     }
     if (seqlens_out != seqlens && meet(seqlens_out, B * sizeof(int32_t), seqlens, B * sizeof(int32_t)))
@@ -250,6 +262,8 @@ int retopk_cache_copy(const retopk_cache *src, const retopk_cache *dst, const in
         for (const void *y : {dst->k, dst->v})
             if (meet(x, scale_bytes(*src), y, pool_bytes(*dst)))
                 return RETOPK_ERR_INVALID;
+    if (folded(*dst))
+        return RETOPK_ERR_INVALID;
     return cuda_rc(launch_cache_copy(*src, *dst, first, last, B, max_rows, d_status, (cudaStream_t)stream));
 }
 
