@@ -47,11 +47,12 @@
 // tokens in windows of 4096 keys, 16 over 2 heads: 53 us; capped, 65 us, and 80 with scores past half the cap.
 // What an item costs beside its tiles shows where items are short or shares small: a prompt of 2048 tokens 57 us and
 // of 8192 385 (0.53 and 1.25 PFLOP/s), 128 sequences of 1500 keys, 32 over 8 heads, 130 us (3.9 TB/s), 36 tokens over
-// 17663 keys, 16 over 2 heads, 25 us (0.20 PFLOP/s), one token over 300 keys 11.7 us.
+// 17663 keys, 16 over 2 heads, 25 us (0.20 PFLOP/s), one token over 300 keys 11.7 us (14.4 in a cache of more than 512 rows,
+// whose call takes all shares and a join).
 // Over 4-bit rows: 4096 tokens over 32768 keys 1320 us, prompts of 2048 and 8192 64 and 423 us (in pages of 64 rows 440), 3 x 333 capped
 // tokens 72, 20 sequences of 45 tokens over 3000 keys 62.  A tile of keys and one of values take the four warps ~1.1 us beside the softmax of eight, and all
 // code has to stay in caches that hold less than it: what the warps that bring and expand run is kept in short loops (unrolled,
-// 4096 over 32768 1570 us, the prompt of 8192 504).
+// 4096 over 32768 1570 us, the prompt of 8192 504).  32 to 64 bytes a thread are spilled there (two tiles over bf16 rows: 8).
 #include <math.h>
 
 #include <algorithm>
@@ -1449,7 +1450,8 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnLaunch c, int share
 // 512 over 9000 beside 63 over 9000 221 (254), 4096 over 32768 beside 63 over 9000 1350 (1382, in two tiles).
 // Over 4-bit rows, where two tiles share what was expanded, from half a tile on (18 tokens a tile; streams against two tiles: 16 x 10
 // tokens over 9000 keys 62 us against 59, 8 x 20 over 20000 96 against 74, 4 x 24 over 9000 38 against 34; 16 x 5 over 20000
-// 100 against 101).
+// 100 against 101).  A call of many single tokens and a chunk is slower than two calls there, as the single ones are what the
+// row kernel is for: 512 over 9000 beside 63 over 9000 323 us (two calls 154), 4096 over 32768 beside 200 over 9000 2158 (1610).
 static bool two_tiles(int T, int B, int G, bool fp4) { return T / B > (fp4 ? kTile / G / 2 : kTile / G * 3 / 2); }
 
 // Rows of a part.

@@ -25,7 +25,10 @@
 // slowest warps and the join behind.  One token over 131072 keys 26 us (bf16 51), over 500000 60 (153): 4 us of start, the
 // stream, 6 of end and join.  128 sequences of 1500 keys, 32 over 8 heads, 40 us (130).  16 sequences of 2, 3 and 4 tokens
 // over 20000 keys 44, 47 and 64 us (bf16 77, 79, 68): registers leave 12 and then 8 warps an SM, which issue in two
-// cycles of five.  One token over 300 keys 7.3 us of a graph of such calls, 9.7 called from Python.
+// cycles of five.  One token over 300 keys 7.2 us of a graph of such calls and 9.8 called from Python where the cache holds
+// up to 512 rows; 9.9 and 11.3 where it holds more, as such a call is cut and joined whatever its length.
+// Registers of a thread are 128, 168, 255 and 255 with one to four tiles of rows; 36, 8 and 108 bytes of it are spilled with two, three
+// and four (capped: 44, 0 and 108).
 // A tile of a warp, 32 keys, is 640 instructions: 128 conversions, 128 products with the scales, 32 matrix products, 32 to bring codes
 // of two keys together, 24 loads, ~70 of softmax, the rest copies, scales and the loop.
 // Not kept: one CTA of all the SM's warps (61 sequences 78 us, one token over 131072 27.5; with a limit on how far its groups of
@@ -757,7 +760,10 @@ size_t row_attention_ws()
     return n;
 }
 
-// Tiles of 8 rows that hold a sequence's tokens by the group's heads, by the mean of tokens (the lengths are the device's).
+// Tiles of 8 rows that hold a sequence's tokens by the group's heads, by the mean of tokens (the lengths are the device's).  So a
+// chunk among many single tokens comes here with them, in blocks of as few tokens, each of which reads every key that it sees
+// again: 440 tokens beside 64 single ones over 1500 keys, 32 over 8 heads, 120 us, in a call of their own and one for the tokens 60; 3000
+// beside 512, 933 against 282; 32 over 4000 beside 31 over 4000 49 against 63.
 static int row_tiles(int T, int B, int G) { return (int)(((T + (long long)B - 1) / B * G + 7) / 8); }
 
 bool takes_rows(int T, int B, int G) { return row_tiles(T, B, G) <= kMaxRowTiles; }
