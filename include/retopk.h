@@ -412,8 +412,8 @@ int retopk_support_overlap(const int32_t *S, const int32_t *others, int rows, in
  * b whole (n_pages >= B, page_rows = max_len) -- the contiguous layout of the
  * calls above.  With a table, page_rows is a multiple of 16.  Sequences may share
  * pages that no call writes.  The struct is host memory, read during the call; all its pointers
- * are device memory, 16-byte aligned (table: 4-byte, scales: as many bytes as a row has).  Calls that write a cache with scales
- * refuse one whose pools share memory, but for k and v in one pool with one of scales. */
+ * are device memory, 16-byte aligned (table: 4-byte, scales: as many bytes as a row has).  Calls that write a cache
+ * refuse one whose k_scale is its v_scale where k is not v; other pools may overlap as long as no two rows that are used do. */
 typedef struct retopk_cache {
     void *k, *v;
     uint8_t *k_scale, *v_scale;   /* RETOPK_CACHE_MX8 and RETOPK_CACHE_FP4 only   */

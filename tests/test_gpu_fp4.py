@@ -288,12 +288,34 @@ def test_keys_that_are_the_values_keep_one_pool(form):
     for c in (one, two):
         retopk.cache_copy(src.h, c.h, i32([0, 3]), i32([40, 17]))
     assert torch.equal(one.k, two.k) and torch.equal(one.ks, two.ks)
-    for half in (one.ks.view(-1)[:one.ks.numel() // 2], one.ks.view(-1)[one.ks.numel() // 2:]):     # a pool within the other is refused
-        half = half.view(one.ks.shape[0] // 2, *one.ks.shape[1:])
-        k, v = one.k[:half.shape[0]], one.k[half.shape[0]:2 * half.shape[0]]
-        bad = retopk.KVCache(k, v, k_scale=half, v_scale=half)
-        with pytest.raises(retopk.RetopkError):
-            retopk.cache_copy(src.h, bad, i32([0]), i32([1]))
+    bad = retopk.KVCache(one.k, two.k, table=one.table, k_scale=one.ks, v_scale=one.ks)      # one's scales for both are refused
+    with pytest.raises(retopk.RetopkError):
+        retopk.cache_copy(src.h, bad, i32([0]), i32([1]))
+
+
+@pytest.mark.parametrize("form", ["fp4", "mx8"])
+def test_keys_and_values_by_turns_in_one_pool(form):
+    # pages 2 i of a pool are keys, pages 2 i + 1 values: the pools overlap, no row does
+    g, B, rows = gen(81), 2, 40
+    src, c, near = Cache(B, 2, rows, 16, "bf16"), Cache(2 * B, 2, rows, 16, form), Cache(B, 2, rows, 16, form)
+    for b in range(B):
+        src.put(b, normal(g, rows, 2, D), normal(g, rows, 2, D))
+    pages = c.k.shape[0] // 2 * 2
+    table = 2 * torch.randperm(pages // 2, generator=torch.Generator().manual_seed(3))[:B * 3].view(B, 3).to(torch.int32).cuda()
+    h = retopk.KVCache(c.k[:pages - 1], c.k[1:pages], table=table, k_scale=c.ks[:pages - 1], v_scale=c.ks[1:pages])
+    x = normal(g, B, 8, D)
+    for to in (h, near.h):
+        retopk.cache_copy(src.h, to, i32([0] * B), i32([rows - 2] * B))
+        retopk.qkv_append(retopk.QKRope(), x, x[:, :2], x[:, 2:4], to, i32([rows - 2, 20]))
+    for b in range(B):
+        pos = torch.arange(rows - 2 + (b == 0), device="cuda")
+        p, r = table[b, pos // 16].long(), pos % 16
+        pn, rn = near.at(b, len(pos))
+        for codes, scales, want, want_scales, odd in ((c.k, c.ks, near.k, near.ks, 0), (c.k, c.ks, near.v, near.vs, 1)):
+            assert torch.equal(codes[p + odd, :, r], want[pn, :, rn]) and torch.equal(scales[p + odd, :, r], want_scales[pn, :, rn])
+    if form == "fp4":
+        q = normal(g, B, 8, D)
+        assert torch.equal(retopk.chunk_attention(q, h, i32([rows - 1, 30])), retopk.chunk_attention(q, near.h, i32([rows - 1, 30])))
 
 
 def test_a_pool_past_2_31_elements():

@@ -74,16 +74,12 @@ bool meet(const void *p, size_t n, const void *q, size_t m)
     return n && m && (uintptr_t)p < (uintptr_t)q + m && (uintptr_t)q < (uintptr_t)p + n;
 }
 
-// Whether a cache's codes and scales lie over one another, so that a call that writes rows would lose some.  (Keys and values
-// may be one pool with one of scales, of a model whose values are its keys.)
-bool folded(const retopk_cache &c)
+// Whether keys and values of a cache have one place for the scales of a row, so that a call that writes it would lose one's.  (Both in
+// one pool, codes and scales, is what a model has whose values are its keys.  Pools that overlap in any other way may still share no row:
+// pages of keys and of values by turns in one pool, scales in pages that no table names.)
+bool one_scale(const retopk_cache &c)
 {
-    const size_t n = pool_bytes(c), m = scale_bytes(c);
-    if (m == 0)
-        return false;
-    const bool one = c.k == c.v && c.k_scale == c.v_scale;
-    return (!one && (meet(c.k, n, c.v, n) || meet(c.k_scale, m, c.v_scale, m))) || meet(c.k, n, c.k_scale, m) ||
-           meet(c.k, n, c.v_scale, m) || meet(c.v, n, c.k_scale, m) || meet(c.v, n, c.v_scale, m);
+    return row_scales(c.format) && c.k_scale == c.v_scale && c.k != c.v;
 }
 
 // Whether two strided [T, heads, 128] tensors share an element; of two whose rows lie between each other's, those of one
@@ -191,7 +187,7 @@ int retopk_qkv_append(const retopk_rope *rope, const retopk_bf16 *q, int64_t q_s
             return RETOPK_ERR_ALIGN;
         const int64_t qw = (int64_t)Hq * kD;
         if (!may_write(q_out, qw, q, q_stride, Hq, T) || rows_meet(q_out, qw, Hq, k, k_stride, Hkv, T) ||
-            rows_meet(q_out, qw, Hq, v, v_stride, Hkv, T) || folded(*cache))
+            rows_meet(q_out, qw, Hq, v, v_stride, Hkv, T) || one_scale(*cache))
             return RETOPK_ERR_INVALID;
     }
     if (seqlens_out != seqlens && meet(seqlens_out, B * sizeof(int32_t), seqlens, B * sizeof(int32_t)))
@@ -262,7 +258,7 @@ int retopk_cache_copy(const retopk_cache *src, const retopk_cache *dst, const in
         for (const void *y : {dst->k, dst->v})
             if (meet(x, scale_bytes(*src), y, pool_bytes(*dst)))
                 return RETOPK_ERR_INVALID;
-    if (folded(*dst))
+    if (one_scale(*dst))
         return RETOPK_ERR_INVALID;
     return cuda_rc(launch_cache_copy(*src, *dst, first, last, B, max_rows, d_status, (cudaStream_t)stream));
 }
